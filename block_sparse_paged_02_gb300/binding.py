@@ -24,7 +24,9 @@ MSA_DEV_BAD_PAGE, MSA_DEV_BAD_LEN, MSA_DEV_MALFORMED, MSA_DEV_BAD_TABLE, MSA_DEV
 
 EXPORTED = ("msa_index_score", "msa_topk_build_table", "msa_sparse_paged_attn", "msa_decode",
             "msa_kv_insert", "msa_sparse_mla_decode", "msa_sparse_mla_workspace_size",
-            "msa_workspace_size", "msa_status_string", "msa_check_bounded_wait")
+            "msa_workspace_size", "msa_status_string", "msa_check_bounded_wait",
+            "msa_tree_attn_workspace_size", "msa_tree_attn", "msa_attn_mass", "msa_evict_select",
+            "msa_kv_compact")
 MSA_CHECK_WAIT_TMEM, MSA_CHECK_WAIT_COPY = 1, 2
 
 
@@ -69,6 +71,25 @@ class msa_mla_args(ctypes.Structure):
                 ("lse", ctypes.c_void_p), ("q_dtype", ctypes.c_int32),
                 ("kv_dtype", ctypes.c_int32), ("q_scale", ctypes.c_void_p),
                 ("kv_scale", ctypes.c_void_p)]
+
+
+class msa_tree(ctypes.Structure):
+    _fields_ = [("mask", ctypes.c_void_p), ("mask_words", ctypes.c_int32),
+                ("topk_idx", ctypes.c_void_p), ("topk", ctypes.c_int32)]
+
+
+class msa_cache_view(ctypes.Structure):
+    _fields_ = [("lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("bt_stride", ctypes.c_int32), ("num_reqs", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32)]
+
+
+class msa_kv_pools(ctypes.Structure):
+    _fields_ = [("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+                ("kv_dtype", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("scale_mode", ctypes.c_int32),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("index", ctypes.c_void_p), ("mass", ctypes.c_void_p)]
 
 
 class msa_trace(ctypes.Structure):
@@ -116,6 +137,16 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
             L.msa_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
             L.msa_check_bounded_wait.restype = ctypes.c_int
             L.msa_check_bounded_wait.argtypes = [P, ctypes.c_uint32, i32, P, P]
+            L.msa_tree_attn_workspace_size.restype = ctypes.c_size_t
+            L.msa_tree_attn_workspace_size.argtypes = [i32] * 6
+            L.msa_tree_attn.restype = ctypes.c_int
+            L.msa_tree_attn.argtypes = [P, P, P, P, ctypes.c_size_t, P, P]
+            L.msa_attn_mass.restype = ctypes.c_int
+            L.msa_attn_mass.argtypes = [P, P, P, P, P, ctypes.c_size_t, P, P]
+            L.msa_evict_select.restype = ctypes.c_int
+            L.msa_evict_select.argtypes = [P, P, i32, i32, i32, P, P, P, P]
+            L.msa_kv_compact.restype = ctypes.c_int
+            L.msa_kv_compact.argtypes = [P, P, P, i32, P, P, P, P]
             L.msa_status_string.restype = ctypes.c_char_p
             L.msa_status_string.argtypes = [ctypes.c_int]
             _lib = L
@@ -287,6 +318,139 @@ def msa_check_bounded_wait(dev_status, limit_us: int, flags: int = 0, copy_src=N
     gives up after limit_us and sets MSA_DEV_TIMEOUT in dev_status."""
     _check("msa_check_bounded_wait", lib().msa_check_bounded_wait(
         _p(dev_status), int(limit_us), int(flags), _p(copy_src), _stream(stream)))
+
+
+# ------------------------------------ draft trees and eviction (msa_cache.h)
+
+def _typed(name: str, t: Optional[torch.Tensor], dtypes, shape=None):
+    """The tensor's type and shape (None: any extent), which a C ABI cannot see."""
+    if t is None:
+        return
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if shape is not None and (t.ndim != len(shape) or
+                              any(w is not None and w != n for w, n in zip(shape, t.shape))):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _here(*tensors: Optional[torch.Tensor]):
+    """The tensors live on the current device, on which the call is enqueued."""
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
+            raise ValueError(f"tensor on {t.device}, but cuda:{torch.cuda.current_device()} is current")
+
+
+def make_tree(mask: Optional[torch.Tensor] = None,
+              topk_idx: Optional[torch.Tensor] = None) -> msa_tree:
+    """What the drafted rows see: `mask` int32 or uint32 [num_rows, words] (bit i of a row: it
+    sees drafted token i; None: a causal chain) and `topk_idx` int32 [num_rows, topk] (the
+    row's selected blocks; None: the whole context)."""
+    _typed("mask", mask, (torch.int32, torch.uint32), (None, None))
+    _typed("topk_idx", topk_idx, (torch.int32,), (None, None))
+    t = msa_tree(_p(mask), int(mask.shape[1]) if mask is not None else 0, _p(topk_idx),
+                 int(topk_idx.shape[1]) if topk_idx is not None else 0)
+    t._keep = (mask, topk_idx)
+    return t
+
+
+def _tree_rows(batch: msa_batch, tree: msa_tree):
+    for name, t in zip(("mask", "topk_idx"), tree._keep):
+        if t is not None and int(t.shape[0]) != batch.num_rows:
+            raise ValueError(f"{name} has {t.shape[0]} rows, the batch {batch.num_rows}")
+
+
+def msa_tree_attn_workspace_size(num_reqs, num_rows, bt_stride, num_heads, max_q_len=0,
+                                 topk=0) -> int:
+    return int(lib().msa_tree_attn_workspace_size(int(num_reqs), int(num_rows), int(bt_stride),
+                                                  int(num_heads), int(max_q_len), int(topk)))
+
+
+def _bytes(t: Optional[torch.Tensor]) -> int:
+    return int(t.numel() * t.element_size()) if t is not None else 0
+
+
+def msa_tree_attn(batch: msa_batch, tree: msa_tree, attn: msa_attn_args, workspace, dev_status,
+                  stream=None):
+    """Attention of every drafted row over its request's cache (see msa_cache.h)."""
+    _tree_rows(batch, tree)
+    _here(dev_status, workspace)
+    _check("msa_tree_attn", lib().msa_tree_attn(
+        ctypes.byref(batch), ctypes.byref(tree), ctypes.byref(attn), _p(workspace),
+        _bytes(workspace), _p(dev_status), _stream(stream)))
+
+
+def msa_attn_mass(batch: msa_batch, tree: msa_tree, attn: msa_attn_args, mass, workspace,
+                  dev_status, stream=None):
+    """Add the weight that each cached token received to `mass` fp32 [num_pages, 128]; the rows'
+    log-sum-exps are read from the attention arguments' lse."""
+    _tree_rows(batch, tree)
+    _typed("mass", mass, (torch.float32,), (batch.num_pages, 128))
+    _here(dev_status, workspace, mass)
+    _check("msa_attn_mass", lib().msa_attn_mass(
+        ctypes.byref(batch), ctypes.byref(tree), ctypes.byref(attn), _p(mass), _p(workspace),
+        _bytes(workspace), _p(dev_status), _stream(stream)))
+
+
+def make_cache_view(lens, block_table, num_pages: int) -> msa_cache_view:
+    """The cached tokens of a set of requests: int32 lens [R], block_table [R, bt_stride]."""
+    _typed("lens", lens, (torch.int32,), (None,))
+    _typed("block_table", block_table, (torch.int32,), (int(lens.shape[0]), None))
+    c = msa_cache_view(_p(lens), _p(block_table), int(block_table.shape[1]), int(lens.shape[0]),
+                       int(num_pages))
+    c._keep = (lens, block_table)
+    return c
+
+
+def msa_evict_select(cache: msa_cache_view, mass, budget: int, keep_first: int, keep_recent: int,
+                     keep, keep_len, dev_status, stream=None):
+    """The positions each request keeps under the budget, into keep int32 [R, budget] (ascending,
+    then -1) and keep_len int32 [R]."""
+    _typed("mass", mass, (torch.float32,), (cache.num_pages, 128))
+    _typed("keep", keep, (torch.int32,), (cache.num_reqs, int(budget)))
+    _typed("keep_len", keep_len, (torch.int32,), (cache.num_reqs,))
+    _here(dev_status, mass, keep, keep_len)
+    _check("msa_evict_select", lib().msa_evict_select(
+        ctypes.byref(cache), _p(mass), int(budget), int(keep_first), int(keep_recent), _p(keep),
+        _p(keep_len), _p(dev_status), _stream(stream)))
+
+
+def make_kv_pools(k_cache, v_cache, kv_dtype: int, *, scale_mode: int = MSA_SCALE_NONE,
+                  k_scale=None, v_scale=None, index: Optional[msa_index_cache] = None,
+                  mass=None) -> msa_kv_pools:
+    """The pools whose tokens move together: K and V [P, 128, Hkv, 128], per-token-head scales
+    [P, 128, Hkv], an index cache of make_index_cache, accumulated weights [P, 128]."""
+    pages, _, hkv, dim = (int(x) for x in k_cache.shape)
+    of = (torch.uint8, torch.float8_e4m3fn) if kv_dtype == MSA_KV_FP8_E4M3 else (torch.bfloat16,)
+    _typed("k_cache", k_cache, of, (pages, 128, hkv, dim))
+    _typed("v_cache", v_cache, of, (pages, 128, hkv, dim))
+    if scale_mode == MSA_SCALE_PER_TOKEN_HEAD:
+        _typed("k_scale", k_scale, (torch.float32,), (pages, 128, hkv))
+        _typed("v_scale", v_scale, (torch.float32,), (pages, 128, hkv))
+    _typed("mass", mass, (torch.float32,), (pages, 128))
+    if index is not None and int(index._keep[0].shape[0]) != pages:
+        raise ValueError(f"the index cache has {index._keep[0].shape[0]} pages, K has {pages}")
+    x = msa_kv_pools(_p(k_cache), _p(v_cache), int(kv_dtype), hkv, dim, int(scale_mode),
+                     _p(k_scale), _p(v_scale),
+                     ctypes.cast(ctypes.pointer(index), ctypes.c_void_p) if index is not None else None,
+                     _p(mass))
+    x._keep = (k_cache, v_cache, k_scale, v_scale, index, mass)
+    x._pages = pages
+    return x
+
+
+def msa_kv_compact(cache: msa_cache_view, base, keep, keep_len, pools: msa_kv_pools, dev_status,
+                   stream=None):
+    """Move the tokens at base + keep[r, i] to base + i, i < keep_len[r], in every pool (base
+    int32 [R] or None for 0; keep int32 [R, stride], strictly ascending; keep_len int32 [R])."""
+    _typed("base", base, (torch.int32,), (cache.num_reqs,))
+    _typed("keep", keep, (torch.int32,), (cache.num_reqs, None))
+    _typed("keep_len", keep_len, (torch.int32,), (cache.num_reqs,))
+    if pools._pages != cache.num_pages:
+        raise ValueError(f"the pools have {pools._pages} pages, the cache view {cache.num_pages}")
+    _here(dev_status, base, keep, keep_len, pools._keep[0])
+    _check("msa_kv_compact", lib().msa_kv_compact(
+        ctypes.byref(cache), _p(base), _p(keep), int(keep.shape[1]), _p(keep_len),
+        ctypes.byref(pools), _p(dev_status), _stream(stream)))
 
 
 def make_trace(after_score=None, after_topk=None, after_attn=None) -> msa_trace:

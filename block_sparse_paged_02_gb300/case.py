@@ -73,6 +73,7 @@ class DeviceCase:
         self.workspace = torch.zeros((ws,), dtype=torch.uint8, device=device)
         ws_a = B.msa_workspace_size(N, 0, 0, hq, d, self.tbl_stride)
         self.attn_workspace = torch.zeros((ws_a,), dtype=torch.uint8, device=device)
+        self._tree_ws = {}
         self.step_inputs = None
         self.step_outputs = None
         self._args()
@@ -157,6 +158,48 @@ class DeviceCase:
         B.msa_kv_insert(self.batch, k_new, v_new, self.w.hkv, self.w.head_dim, self.k, self.v,
                         self.w.kv_dtype, self.w.scale_mode, self.k_scale, self.v_scale,
                         idx_new, self.index, skip_index, self.status, stream)
+
+    # -- the batch's rows as drafts, and the cache's eviction
+    def tree_attn(self, mask=None, topk_idx=None, stream=None):
+        """msa_tree_attn of the batch's rows over the whole context (or the blocks of topk_idx,
+        device int32 [num_rows, k]) and each other (mask: device int32 [num_rows, words])."""
+        tree = B.make_tree(mask, topk_idx)
+        B.msa_tree_attn(self.batch, tree, self.attn, self._tree_workspace(tree), self.status, stream)
+
+    def attn_mass(self, mass, mask=None, topk_idx=None, stream=None):
+        """msa_attn_mass of the rows whose lse a call of tree_attn wrote."""
+        tree = B.make_tree(mask, topk_idx)
+        B.msa_attn_mass(self.batch, tree, self.attn, mass, self._tree_workspace(tree), self.status,
+                        stream)
+
+    def _tree_workspace(self, tree):
+        # one per selection width, kept for the life of the case
+        if tree.topk not in self._tree_ws:
+            need = B.msa_tree_attn_workspace_size(self.w.num_reqs, self.num_rows, self.w.bt_stride,
+                                                  self.w.hq, self.max_q_len, tree.topk)
+            self._tree_ws[tree.topk] = torch.empty((max(need, 16),), dtype=torch.uint8,
+                                                   device=self.device)
+        return self._tree_ws[tree.topk]
+
+    def kv_pools(self, mass=None):
+        """The pools whose tokens msa_kv_compact moves together."""
+        return B.make_kv_pools(self.k, self.v, self.w.kv_dtype, scale_mode=self.w.scale_mode,
+                               k_scale=self.k_scale, v_scale=self.v_scale, index=self.index,
+                               mass=mass)
+
+    def evict_select(self, lens, mass, budget: int, keep_first: int = 0, keep_recent: int = 0,
+                     stream=None):
+        """The kept positions [R, budget] and their counts [R] of requests holding `lens` tokens."""
+        keep = torch.empty((self.w.num_reqs, budget), dtype=torch.int32, device=self.device)
+        keep_len = torch.empty((self.w.num_reqs,), dtype=torch.int32, device=self.device)
+        B.msa_evict_select(B.make_cache_view(lens, self.bt, self.w.num_pages), mass, budget,
+                           keep_first, keep_recent, keep, keep_len, self.status, stream)
+        return keep, keep_len
+
+    def kv_compact(self, lens, keep, keep_len, base=None, mass=None, stream=None):
+        """Move the kept tokens together in every pool of the case (and `mass`)."""
+        B.msa_kv_compact(B.make_cache_view(lens, self.bt, self.w.num_pages), base, keep, keep_len,
+                         self.kv_pools(mass), self.status, stream)
 
     def fetch(self):
         torch.cuda.synchronize()

@@ -1,0 +1,287 @@
+"""Draft-tree attention and weight accumulation on the GPU against the 64-bit
+plain forms of tree_ref (their tolerances are derived there)."""
+import numpy as np
+import pytest
+import torch
+
+import workloads as W
+from tests import tree_ref as T
+
+pytestmark = pytest.mark.gpu
+
+BF, F8 = W.KV_BF16, W.KV_FP8
+NONE, SCALAR, TOKEN = W.SCALE_NONE, W.SCALE_SCALAR, W.SCALE_PER_TOKEN_HEAD
+
+
+def case(w, **kw):
+    from block_sparse_paged_02_gb300 import DeviceCase
+    return DeviceCase(w, **kw)
+
+
+def make(seed, q_lens, ctxs, hq=16, kv=BF, scale=NONE, sink=False, **kw):
+    return W.custom(seed, q_lens, [c + q for c, q in zip(ctxs, q_lens)], hq=hq, kv_dtype=kv,
+                    scale_mode=scale, with_sink=sink, fill_unused_nan=True, **kw)
+
+
+def words_of(q_lens):
+    return max(1, (max(q_lens) + 31) // 32)
+
+
+def check_attn(c, ref, rows=slice(None)):
+    out, lse, ot, lt = ref
+    got, gl = c.out.double().cpu().numpy(), c.lse.double().cpu().numpy()
+    err = np.abs(got - out)[rows]
+    assert not np.isnan(got[rows]).any()
+    assert (err <= ot[rows]).all(), (np.argwhere(err > ot[rows])[:4].tolist(), (err / (ot[rows] + 1e-300)).max())
+    inf = np.isneginf(lse)
+    assert np.array_equal(inf[rows], np.isneginf(gl)[rows])
+    with np.errstate(invalid="ignore"):
+        e = np.where(inf, 0.0, np.abs(gl - lse))[rows]
+    # a sink returned by itself is exact up to one rounding
+    assert (e <= lt[rows] + 1e-6 * (np.abs(np.where(inf, 0, lse))[rows] + 1)).all(), e.max()
+
+
+def run_both(w, mask=None, topk=None, bad=(), status=0):
+    c = case(w)
+    c.tree_attn(mask=None if mask is None else T.dev(mask), topk_idx=None if topk is None else T.dev(topk))
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == status
+    check_attn(c, T.tree_attn(w, mask, topk, bad))
+    # the weights, from the lse that the call wrote
+    rng = np.random.default_rng(5)
+    mass = rng.random((w.num_pages, 128)).astype(np.float32)
+    m = torch.from_numpy(mass).cuda()
+    c.attn_mass(m, mask=None if mask is None else T.dev(mask), topk_idx=None if topk is None else T.dev(topk))
+    torch.cuda.synchronize()
+    want, tol = T.attn_mass(w, c.lse.cpu().numpy(), mass, mask, topk, bad)
+    got = m.double().cpu().numpy()
+    assert (np.abs(got - want) <= tol).all(), np.max(np.abs(got - want) / (tol + 1e-300))
+    return c
+
+
+@pytest.mark.parametrize("kv,scale", [(BF, NONE), (BF, SCALAR), (BF, TOKEN), (F8, NONE), (F8, SCALAR), (F8, TOKEN)])
+@pytest.mark.parametrize("hq,q_lens", [(16, [1]), (1, [1, 3, 2]), (8, [4, 2, 1]), (16, [2, 1]), (12, [5, 3]),
+                                       (16, [8, 4]), (5, [33, 7]), (16, [40, 64])])
+def test_chain(kv, scale, hq, q_lens):
+    ctxs = [700, 129, 1][:len(q_lens)]
+    run_both(make(11, q_lens, ctxs, hq, kv, scale, sink=hq % 2 == 0))
+
+
+@pytest.mark.parametrize("kv,scale", [(BF, NONE), (F8, TOKEN)])
+@pytest.mark.parametrize("kind", ["tree", "any"])
+@pytest.mark.parametrize("hq,q_lens,ctxs", [
+    (16, [7, 16, 1], [0, 250, 383]), (3, [31, 32, 33], [5, 127, 128]), (16, [64], [1000]),
+    (4, [100, 130], [77, 513]), (16, [1, 1, 1, 1], [0, 1, 127, 640]), (7, [256], [300])])
+def test_masks(kv, scale, kind, hq, q_lens, ctxs):
+    rng = np.random.default_rng(3)
+    run_both(make(12, q_lens, ctxs, hq, kv, scale, sink=True), T.random_mask(rng, q_lens, words_of(q_lens), kind))
+
+
+@pytest.mark.parametrize("sink", [False, True])
+def test_rows_that_see_nothing(sink):
+    # no context and an empty mask: out 0, lse the sink's or -inf
+    w = make(13, [4, 20, 3], [0, 0, 200], 8, BF, NONE, sink)
+    mask = np.zeros((27, 1), np.uint32)
+    mask[5] = 1 << 5
+    c = run_both(w, mask)
+    assert (c.out[0].float() == 0).all()
+
+
+@pytest.mark.parametrize("ctx", [1, 63, 64, 65, 127, 128, 129, 255, 257])
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_block_edges(ctx, kv):
+    run_both(make(14, [3, 6], [ctx, ctx + 64], 16, kv, SCALAR))
+
+
+@pytest.mark.parametrize("kv,scale", [(BF, NONE), (BF, SCALAR), (F8, TOKEN)])
+@pytest.mark.parametrize("hq,q_lens,ctxs", [(16, [1, 1], [5000, 900]), (16, [9, 40], [4100, 2600]),
+                                            (2, [70, 3], [3333, 128 * 9]), (16, [64, 50], [20000, 3000])])
+def test_split_tiles(kv, scale, hq, q_lens, ctxs):
+    # long enough that tiles are shared by CTAs and joined
+    run_both(make(15, q_lens, ctxs, hq, kv, scale, sink=True))
+
+
+@pytest.mark.parametrize("kv,scale", [(BF, NONE), (F8, TOKEN)])
+@pytest.mark.parametrize("hq,q_lens,ctxs,topk", [
+    (16, [1, 1], [3000, 100], 4), (16, [20, 7], [2500, 1280], 3), (4, [65, 40], [128 * 12 + 5, 128 * 7], 2),
+    (16, [3, 30], [60, 9000], 16)])
+def test_selected_blocks(kv, scale, hq, q_lens, ctxs, topk):
+    # each row its own blocks, with repeats, -1 and numbers out of range
+    w = make(16, q_lens, ctxs, hq, kv, scale, sink=True)
+    rng = np.random.default_rng(7)
+    sel = np.full((w.num_rows, topk), -1, np.int32)
+    for r in range(w.num_reqs):
+        for j in range(int(w.cu_seqlens_q[r]), int(w.cu_seqlens_q[r + 1])):
+            sel[j] = rng.integers(-1, ctxs[r] // 128 + 2, topk)
+    sel[0, -1] = 1 << 30
+    run_both(w, T.random_mask(rng, q_lens, words_of(q_lens)), sel)
+
+
+@pytest.mark.parametrize("kv,scale", [(BF, NONE), (F8, TOKEN)])
+@pytest.mark.parametrize("q_lens", [[5, 2], [64, 20]])
+def test_hidden_values_do_not_leak(kv, scale, q_lens):
+    # NaN (and infinities) in drafted tokens and selected blocks that some rows do not see
+    ctxs = [700, 300]
+    w = make(17, q_lens, ctxs, 16, kv, scale)
+    rng = np.random.default_rng(9)
+    mask = T.random_mask(rng, q_lens, words_of(q_lens), "tree")
+    nan, inf = (0x7f, 0x7f) if kv == F8 else (0x7fc0, 0xff80)
+    hidden = {}
+    for r in range(2):
+        q0, q1 = int(w.cu_seqlens_q[r]), int(w.cu_seqlens_q[r + 1])
+        i = q1 - q0 - 1  # seen only by itself
+        pos = ctxs[r] + i
+        page = w.block_table[r, pos // 128]
+        w.v_cache[page, pos % 128, 0, ::3] = nan
+        w.v_cache[page, pos % 128, 0, 1::3] = inf
+        w.k_cache[page, pos % 128, 0, 5] = nan
+        hidden[r] = q1 - 1
+    sel = np.full((w.num_rows, 2), -1, np.int32)
+    sel[:, 0] = 1
+    sel[0, 1] = 0  # row 0 alone reads block 0 of request 0
+    for b, seq in ((0, 700),):
+        w.v_cache[w.block_table[0, b], 3] = nan
+    c = case(w)
+    c.tree_attn(mask=T.dev(mask), topk_idx=T.dev(sel))
+    torch.cuda.synchronize()
+    keep = [r for r in range(w.num_rows) if r not in hidden.values() and r != 0]
+    clean = W.custom(17, q_lens, [x + y for x, y in zip(ctxs, q_lens)], hq=16, kv_dtype=kv, scale_mode=scale)
+    check_attn(c, T.tree_attn(clean, mask, sel), keep)
+    got = c.out.float().cpu().numpy()
+    assert np.isnan(got[0]).all()
+    for r in hidden.values():
+        assert np.isnan(got[r]).any()
+    m = torch.zeros((w.num_pages, 128), device="cuda")
+    lse = np.nan_to_num(c.lse.cpu().numpy(), nan=0.0)
+    c.lse.copy_(torch.from_numpy(lse))
+    c.attn_mass(m, mask=T.dev(mask), topk_idx=T.dev(sel))
+    m = m.cpu().numpy()
+    # only the drafted token that holds a NaN key, as seen by itself, has a NaN weight
+    assert np.isnan(m).sum() == 2
+
+
+def test_poisoned_requests():
+    q_lens, ctxs = [3, 20, 4, 2, 6], [300, 2000, 500, 64, 900]
+    for sink in (False, True):
+        w = make(18, q_lens, ctxs, 16, BF, NONE, sink)
+        w.block_table[1, 7] = w.num_pages       # a page out of range
+        w.context_lens[2] += 1                  # lengths that do not add up
+        mask = T.random_mask(np.random.default_rng(1), q_lens, 1)
+        run_both(w, mask, bad=(1, 2), status=1 | 2)
+        topk = np.zeros((w.num_rows, 2), np.int32)
+        run_both(w, mask, topk, bad=(1, 2), status=1 | 2)
+
+
+def test_more_rows_than_the_mask_or_the_bound():
+    q_lens, ctxs = [40, 3], [100, 100]
+    w = make(19, q_lens, ctxs, 4)
+    run_both(w, np.full((43, 1), 0xffffffff, np.uint32), bad=(0,), status=4)
+    c = case(w)
+    c.max_q_len = 8
+    c._args()
+    c.tree_attn()
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 4
+    check_attn(c, T.tree_attn(w, bad=(0,)))
+
+
+def test_rows_that_no_request_owns():
+    w = make(20, [3, 2], [100, 100], 4, sink=True)
+    w.cu_seqlens_q[2] = 4
+    c = case(w)
+    c.tree_attn()
+    m = torch.ones((w.num_pages, 128), device="cuda")
+    c.attn_mass(m)
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 4
+    assert (c.out.float() == 0).all() and (m == 1).all()
+    assert np.array_equal(c.lse.cpu().numpy(), np.tile(w.sinks, (5, 1)))
+
+
+def test_requests_without_rows_and_many_requests():
+    run_both(make(21, [0, 2, 0, 0, 5, 0], [10, 300, 0, 128, 40, 7], 16))
+    n = 700  # more requests than a CTA has threads
+    rng = np.random.default_rng(2)
+    q_lens = rng.integers(0, 4, n).tolist()
+    run_both(make(22, q_lens, rng.integers(0, 300, n).tolist(), 2, F8, SCALAR))
+
+
+def test_same_bits_twice_on_another_stream_and_in_a_graph():
+    q_lens, ctxs = [20, 1, 64], [6000, 20000, 3000]
+    w = make(23, q_lens, ctxs, 16, BF, NONE, True)
+    mask = T.dev(T.random_mask(np.random.default_rng(4), q_lens, 2))
+    c = case(w)
+    m0 = torch.zeros((w.num_pages, 128), device="cuda")
+    c.tree_attn(mask=mask)
+    c.attn_mass(m0, mask=mask)
+    torch.cuda.synchronize()
+    want = c.out.clone(), c.lse.clone(), m0.clone()
+
+    def again(run):
+        c.out.zero_(), c.lse.zero_(), m0.zero_()
+        torch.cuda.synchronize()
+        run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((c.out, c.lse, m0), want))
+
+    def go(stream=None):
+        c.tree_attn(mask=mask, stream=stream)
+        c.attn_mass(m0, mask=mask, stream=stream)
+
+    again(go)
+    side = torch.cuda.Stream()
+    again(lambda: go(side))
+    # garbage left in the workspace does not matter
+    for ws in c._tree_ws.values():
+        ws.fill_(0xff)
+    again(go)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        go()
+    again(g.replay)
+    again(g.replay)
+
+
+def test_offsets_past_32_bits():
+    # pools of more than 2^32 bytes: pages near their end
+    from block_sparse_paged_02_gb300 import binding as B
+    pages, hq, ctx, ql = 140000, 16, 500, 5
+    k = torch.empty((pages, 128, 1, 128), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    small = make(24, [ql], [ctx], hq)
+    at = np.array([pages - 1, 5, pages - 7, pages - 2], np.int32)
+    for i in range(4):
+        for dst, src in ((k, small.k_cache), (v, small.v_cache)):
+            page = src[small.block_table[0, i]]
+            dst[int(at[i])] = torch.from_numpy(page.view(np.int16)).view(torch.bfloat16).cuda()
+    c = case(small)
+    bt = torch.from_numpy(at[None]).cuda()
+    batch = B.make_batch(c.cu_q, c.cu_k, c.ctx, bt, pages, ql, max_q_len=ql)
+    attn = B.make_attn_args(c.q, k, v, B.MSA_KV_BF16, pages, c.out, c.lse, softmax_scale=small.softmax_scale)
+    ws = torch.empty((B.msa_tree_attn_workspace_size(1, ql, 4, hq, ql),), dtype=torch.uint8, device="cuda")
+    tree = B.make_tree()
+    B.msa_tree_attn(batch, tree, attn, ws, c.status)
+    mass = torch.zeros((pages, 128), device="cuda")
+    B.msa_attn_mass(batch, tree, attn, mass, ws, c.status)
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 0
+    check_attn(c, T.tree_attn(small))
+    want, tol = T.attn_mass(small, c.lse.cpu().numpy(), np.zeros((small.num_pages, 128), np.float32))
+    got = mass[torch.from_numpy(at).long().cuda()].double().cpu().numpy()
+    order = small.block_table[0, :4]
+    assert (np.abs(got - want[order]) <= tol[order]).all()
+
+
+def test_v_scales_over_a_wide_range():
+    # per-token scales over 2^-30 .. 2^30: the heavy ones decide, none overflows
+    w = make(25, [4], [600], 16, F8, TOKEN)
+    rng = np.random.default_rng(3)
+    w.v_scale[:] = np.exp2(rng.uniform(-30, 30, w.v_scale.shape)).astype(np.float32)
+    c = case(w)
+    c.tree_attn()
+    torch.cuda.synchronize()
+    out, lse, ot, lt = T.tree_attn(w)
+    # P times its scale is rounded relative to the largest scale met so far: 2^-24 of it each
+    vmax = float(w.v_scale.max()) * 448
+    err = np.abs(c.out.double().cpu().numpy() - out)
+    assert (err <= ot + 604 * 2.0 ** -24 * vmax).all()
