@@ -28,7 +28,7 @@ TreeWs tree_layout(int num_reqs, int bt_stride, int num_heads, int max_rows, int
     off = round_up(off + bytes, 256);
     return at;
   };
-  const size_t grid = (size_t)device_sm_count(), tile = (size_t)tree_tile_rows(max_rows, num_heads);
+  const size_t grid = (size_t)device_sm_count(), tile = (size_t)tree_part_rows(max_rows, num_heads);
   w.list_cap = w.list_words = 0;
   w.list_count = w.list_blk = w.list_rows = 0;
   if (topk > 0) {

@@ -87,51 +87,9 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
-// Items of a request: its tiles of drafted tokens times its visited blocks
-__device__ __forceinline__ long long tree_cost(const TreeLaunch& p, int q, int tok_per_tile) {
-  TreeReq r = tree_request(p, q);
-  if (r.qlen <= 0) return 0;
-  const long long n = tree_visits(p, q, r);
-  return n * ((r.qlen + tok_per_tile - 1) / tok_per_tile);
-}
-
-// A row's end: (m, l) in log2 units, the sink joined in
-struct RowEnd {
-  float f, lse;  // factor of the accumulators, natural-log lse
-};
-__device__ __forceinline__ RowEnd row_end(float m, float l, bool has_sink, float sink2, float vs) {
-  RowEnd e;
-  if (m == -INFINITY && l == 0.f) {  // nothing seen
-    e.f = 0.f;
-    e.lse = has_sink ? sink2 * kTreeLn2 : -INFINITY;
-    return e;
-  }
-  float f = 1.f;
-  if (has_sink) {
-    const float mn = fmaxf(m, sink2);
-    f = exp2f(m - mn);
-    l = l * f + exp2f(sink2 - mn);
-    m = mn;
-  }
-  e.f = f * vs / l;
-  e.lse = (m + log2f(l)) * kTreeLn2;
-  return e;
-}
-
-// every row of an unusable batch, as empty rows
-__device__ void write_all_empty(const TreeLaunch& p) {
-  const long long n = (long long)p.batch.num_rows * p.num_heads;
-  const long long step = (long long)gridDim.x * blockDim.x;
-  const long long at = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  for (long long i = at; i < n; i += step)
-    p.lse[i] = p.sinks ? __ldg(p.sinks + i % p.num_heads) : -INFINITY;
-  uint4* o = reinterpret_cast<uint4*>(p.out);
-  for (long long i = at; i < n * (kHeadDim / 8); i += step) o[i] = make_uint4(0u, 0u, 0u, 0u);
-}
-
 template <bool FP8, bool PTH, int MW>
 __global__ void __launch_bounds__(kTaThreads, 1)
-    tree_attn_kernel(const TreeLaunch p, const __grid_constant__ CUtensorMap qmap,
+    tree_attn_kernel(const __grid_constant__ TreeLaunch p, const __grid_constant__ CUtensorMap qmap,
                      const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
   using C = TaCfg<FP8, MW>;
@@ -167,7 +125,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0 && sl.begin >= sl.end) p.split[blockIdx.x].nrows = 0;
   if (!sl.tiled) {
-    write_all_empty(p);
+    tree_write_all_empty(p);
     if (tid == 0 && blockIdx.x == 0) atomicOr(p.status, MSA_DEV_MALFORMED);
     return;
   }
@@ -219,6 +177,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         rec.nrows = si.ntok * H;
         rec.row0 = si.row0;
         rec.last = (int)((e * sl.ctas - 1) / sl.total);
+        rec.q = q;
       }
       if (rq.bad) {
         const int st = acquire();
@@ -465,7 +424,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           for (int hh = 0; hh < 2; ++hh) {
             float al = 1.f;
             if (mx[hh] > m_run[hh]) {
-              al = m_run[hh] == -INFINITY ? 1.f : exp2f(m_run[hh] - mx[hh]);
+              al = m_run[hh] == -INFINITY ? 1.f : ex2_ftz(m_run[hh] - mx[hh]);
               m_run[hh] = mx[hh];
             }
             l_run[hh] *= al;
@@ -484,7 +443,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              pr[u][2 * hh + e] = exp2f(s[u][2 * hh + e] - base);
+              pr[u][2 * hh + e] = ex2_ftz(s[u][2 * hh + e] - base);
               l_run[hh] += pr[u][2 * hh + e];
             }
         }
@@ -659,7 +618,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
               const int at = nw * M + mrow[hh];
               const float2 x = ml[at];
               const float mn = fmaxf(m_run[hh], x.x), base = mn == -INFINITY ? 0.f : mn;
-              const float fa = exp2f(m_run[hh] - base), fb = exp2f(x.x - base);
+              const float fa = ex2_ftz(m_run[hh] - base), fb = ex2_ftz(x.x - base);
               // (a side that saw nothing has m = -inf and zeros)
               l_run[hh] = (m_run[hh] == -INFINITY ? l_run[hh] : l_run[hh] * fa) +
                           (x.x == -INFINITY ? x.y : x.y * fb);
@@ -683,10 +642,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           const int m = mrow[hh];
           if (m >= ntok * H) continue;
           if (fl & kWhole) {
-            RowEnd e;
+            TreeRowEnd e;
             const float sink2 = p.sinks ? __ldg(p.sinks + m % H) * kTreeLog2e : 0.f;
-            if (bad) e = row_end(-INFINITY, 0.f, p.sinks != nullptr, sink2, 1.f);
-            else e = row_end(m_run[hh], l_run[hh], p.sinks != nullptr, sink2, v_scalar);
+            if (bad) e = tree_row_end(-INFINITY, 0.f, p.sinks != nullptr, sink2, 1.f);
+            else e = tree_row_end(m_run[hh], l_run[hh], p.sinks != nullptr, sink2, v_scalar);
             const long long r = (long long)row0 * H + m;
             const bool none = bad || (m_run[hh] == -INFINITY && l_run[hh] == 0.f);
             if (c == 0) p.lse[r] = p.sinks && none ? __ldg(p.sinks + m % H) : e.lse;
@@ -744,8 +703,8 @@ constexpr int kMgFew = 8;  // up to this many partials a warp joins a row by its
 // Joins the partials of the tiles that several CTAs share.  Work units are 8
 // rows (a warp each) of a tile with few partials, or one row whose partials
 // the CTA's warps share; each CTA takes every gridDim-th unit.
-__global__ void __launch_bounds__(kMgThreads) tree_merge_kernel(const TreeLaunch p, int grid_main,
-                                                                int tile_rows) {
+__global__ void __launch_bounds__(kMgThreads) tree_merge_kernel(const __grid_constant__ TreeLaunch p,
+                                                                int grid_main, int tile_rows) {
   __shared__ float s_o[kMgWarps][kHeadDim];
   __shared__ float s_m[kMgWarps], s_l[kMgWarps];
   __shared__ int s_bad[kMgWarps];
@@ -788,12 +747,12 @@ __global__ void __launch_bounds__(kMgThreads) tree_merge_kernel(const TreeLaunch
 #pragma unroll
           for (int u = 0; u < 4; ++u) mn = fmaxf(mn, ml[u].x);
           const float ref = mn == -INFINITY ? 0.f : mn;
-          const float f0 = M == -INFINITY ? 1.f : exp2f(M - ref);
+          const float f0 = M == -INFINITY ? 1.f : ex2_ftz(M - ref);
           L *= f0;
           a.x *= f0; a.y *= f0; a.z *= f0; a.w *= f0;
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const float f = ml[u].x == -INFINITY ? 1.f : exp2f(ml[u].x - ref);
+            const float f = ml[u].x == -INFINITY ? 1.f : ex2_ftz(ml[u].x - ref);
             L += ml[u].y * f;
             a.x += v[u].x * f; a.y += v[u].y * f; a.z += v[u].z * f; a.w += v[u].w * f;
           }
@@ -818,7 +777,7 @@ __global__ void __launch_bounds__(kMgThreads) tree_merge_kernel(const TreeLaunch
           L = 0.f;
           a = make_float4(0.f, 0.f, 0.f, 0.f);
           for (int w = 0; w < kMgWarps; ++w) {
-            const float f = s_m[w] == -INFINITY ? 1.f : exp2f(s_m[w] - ref);
+            const float f = s_m[w] == -INFINITY ? 1.f : ex2_ftz(s_m[w] - ref);
             const float4 x = *reinterpret_cast<const float4*>(&s_o[w][4 * lane]);
             L += s_l[w] * f;
             a.x += x.x * f; a.y += x.y * f; a.z += x.z * f; a.w += x.w * f;
@@ -826,9 +785,14 @@ __global__ void __launch_bounds__(kMgThreads) tree_merge_kernel(const TreeLaunch
         }
       }
       if (live && (few || warp == 0)) {
+        if (bad == 2) {  // values that a row does not see could have reached it
+          const int row = rec.row0 + m / H;
+          tree_slow_row(p, rec.q, row, row - p.batch.cu_seqlens_q[rec.q], m % H);
+          continue;
+        }
         const bool none = bad || (M == -INFINITY && L == 0.f);
         const float sink = p.sinks ? __ldg(p.sinks + m % H) : 0.f;
-        const RowEnd e = row_end(M, L, p.sinks != nullptr, sink * kTreeLog2e, vs);
+        const TreeRowEnd e = tree_row_end(M, L, p.sinks != nullptr, sink * kTreeLog2e, vs);
         const long long r = (long long)rec.row0 * H + m;
         uint2 w = make_uint2(pack_bf16x2(a.x * e.f, a.y * e.f), pack_bf16x2(a.z * e.f, a.w * e.f));
         if (none) w = make_uint2(0u, 0u);
@@ -922,6 +886,19 @@ __global__ void __launch_bounds__(kPlanThreads2) tree_plan_kernel(const TreeLaun
   }
 }
 
+cudaError_t launch_merge(const TreeLaunch& p, int grid, int tile_rows, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(4 * grid);
+  cfg.blockDim = dim3(kMgThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel, p, grid, tile_rows);
+}
+
 template <bool FP8, bool PTH, int MW>
 cudaError_t launch_main(const TreeLaunch& p, cudaStream_t stream) {
   using C = TaCfg<FP8, MW>;
@@ -941,17 +918,7 @@ cudaError_t launch_main(const TreeLaunch& p, cudaStream_t stream) {
   const int grid = device_sm_count();
   kern<<<grid, kTaThreads, C::kBytes, stream>>>(p, qmap, kmap, vmap);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(4 * grid);
-  cfg.blockDim = dim3(kMgThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_merge_kernel, p, grid, (int)C::kM);
+  return e != cudaSuccess ? e : launch_merge(p, grid, C::kM, stream);
 }
 
 template <bool FP8, bool PTH>
@@ -973,6 +940,12 @@ int tree_tile_rows(int max_rows, int num_heads) {
   return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
 }
 
+// Rows of a partial: the tensor-core kernel takes pairs of 128-row tiles.
+int tree_part_rows(int max_rows, int num_heads) {
+  const int m = tree_tile_rows(max_rows, num_heads);
+  return m == 128 ? 256 : m;
+}
+
 cudaError_t launch_tree_plan(const TreeLaunch& p, cudaStream_t stream) {
   tree_plan_kernel<<<p.batch.num_reqs, kPlanThreads2, 0, stream>>>(p);
   return cudaGetLastError();
@@ -984,6 +957,11 @@ cudaError_t launch_tree_attn(const TreeLaunch& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   const bool pth = p.scale_mode == MSA_SCALE_PER_TOKEN_HEAD;
+  if (!p.kv_fp8 && !pth && tree_tile_rows(p.max_rows, p.num_heads) == 128) {
+    const int grid = device_sm_count();
+    const cudaError_t e = launch_tree_attn_tc(p, grid, stream);
+    return e != cudaSuccess ? e : launch_merge(p, grid, 256, stream);
+  }
   if (p.kv_fp8) return pth ? launch_tile<true, true>(p, stream) : launch_tile<true, false>(p, stream);
   return pth ? launch_tile<false, true>(p, stream) : launch_tile<false, false>(p, stream);
 }

@@ -1,0 +1,652 @@
+// tree_attn_tc.cu -- the draft-tree attention for wide trees (more than 64
+// rows x heads per request, bf16 pools) on the 5th-generation tensor cores.
+//
+// Same mathematics, split and partials as tree_attn.cu.  A request's rows are
+// cut into pairs of 128-row tiles; a CTA loads each visited block's K and V
+// once for both tiles, and while one tile is in its softmax the tensor cores
+// work on the other:
+//   S = Q K^T   tcgen05.mma M128 N128 K128, both operands in shared memory
+//   P = 2^(S' - m)  one thread per row (TMEM lane): two passes over its 128
+//               logits, the running reference m moves only when a block's
+//               maximum exceeds it by more than 2^8 (then that warp rescales
+//               its rows of O), P written back over S as bf16
+//   O += P V    tcgen05.mma with A = P from tensor memory, B = V (MN-major)
+// Roles: warp 0 issues the tensor copies, one thread of warps 1 and 2 issues
+// the products of tile 0 and tile 1 (an instruction takes its thread ~100
+// cycles, more than the 64 that it keeps the pipe busy, so one issuer would
+// bound the kernel), warps 4-7 and 8-11 are the tiles' softmax.  Tensor memory
+// (512 columns): S / P and O of both tiles.
+//
+// A block that not every row sees whole (the drafted tokens, the context's
+// end, selected blocks) takes a masked softmax, and its V is looked over: a
+// value that is not finite would reach rows that do not see it through 0 * V,
+// so the tile is then computed again row by row (tree_slow_row), from the
+// visible tokens alone.
+#include <string.h>
+
+#include "tcgen05.cuh"
+#include "tree_common.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kHalf = 128 * 128;  // 128 rows x 128 B: one swizzle-atom column of a tile
+constexpr int kTile = 2 * kHalf;  // 128 x 128 bf16
+constexpr int kBufs = 5;          // ring of K and V tiles, alternating
+constexpr int kInfos = 8;
+constexpr int kSmKv = 0;
+constexpr int kSmQ = kBufs * kTile;
+constexpr int kSmInfo = kSmQ + 2 * kTile;
+
+// flags of a block
+constexpr int kFirst = 1, kLast = 2, kWhole = 4, kNoData = 8, kBadPage = 16, kPoison = 32,
+              kEnd = 64, kMixed = 128, kTwo = 256;
+
+struct BlockInfo {
+  int flags;
+  int row0, ntok, j0;  // the tile pair's drafted tokens: first row in the batch, count, index
+  int ctx, qlen, seq;
+  int t0;              // position of the block's first token
+  int slot, q;
+  uint32_t bad;
+  int pad;
+  const uint32_t* rows;
+};
+
+// kv full / empty, q full / empty, info full; per tile: s_full, p_full,
+// pv_done, o_free; fill, ends
+constexpr int kNumBars = 2 * kBufs + 2 + kInfos + 8 + 2;
+constexpr int kSmBars = kSmInfo + kInfos * (int)sizeof(BlockInfo);
+constexpr int kSmMisc = kSmBars + kNumBars * 8;
+constexpr int kBytes = kSmMisc + 64;
+static_assert(kBytes <= 227 * 1024, "shared memory");
+static_assert(sizeof(BlockInfo) % 8 == 0 && kSmBars % 8 == 0, "alignment");
+
+constexpr uint32_t kTmemCols = 512;
+__device__ __forceinline__ uint32_t col_s(int t) { return 128u * t; }
+__device__ __forceinline__ uint32_t col_o(int t) { return 256u + 128u * t; }
+constexpr uint32_t kIdescS = tc::idesc_bf16(128, 128, 0);
+constexpr uint32_t kIdescO = tc::idesc_bf16(128, 128, 1);
+constexpr float kSlack = 8.f;
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// largest of 32 raw logits and acc (of their negations when NEG), those with
+// a set bit only when MASKED
+template <bool NEG, bool MASKED>
+__device__ __forceinline__ float max32(const uint32_t (&r)[32], float acc, uint32_t vis) {
+  float g[4] = {acc, acc, acc, acc};
+#pragma unroll
+  for (int t = 0; t < 32; t += 2) {
+    float a = __uint_as_float(r[t]), b = __uint_as_float(r[t + 1]);
+    if (NEG) {
+      a = -a;
+      b = -b;
+    }
+    if (MASKED) {
+      a = (vis >> t) & 1u ? a : -INFINITY;
+      b = (vis >> (t + 1)) & 1u ? b : -INFINITY;
+    }
+    g[(t >> 1) & 3] = fmax3(g[(t >> 1) & 3], a, b);
+  }
+  return fmaxf(fmax3(g[0], g[1], g[2]), g[3]);
+}
+
+template <bool NEG, bool MASKED>
+__device__ __forceinline__ float row_max(uint32_t sa, const uint32_t (&vis)[4]) {
+  uint32_t ra[32], rb[32];
+  float g = -INFINITY;
+  tc::tmem_ld32_issue(sa, ra);
+  tc::tmem_ld32_issue(sa + 32, rb);
+  tc::tmem_wait_ld(ra);
+  tc::tmem_wait_ld(rb);
+  g = max32<NEG, MASKED>(ra, g, vis[0]);
+  tc::tmem_ld32_issue(sa + 64, ra);
+  g = max32<NEG, MASKED>(rb, g, vis[1]);
+  tc::tmem_ld32_issue(sa + 96, rb);
+  tc::tmem_wait_ld(ra);
+  tc::tmem_wait_ld(rb);
+  g = max32<NEG, MASKED>(ra, g, vis[2]);
+  return max32<NEG, MASKED>(rb, g, vis[3]);
+}
+
+// two products a * b + c in one instruction
+__device__ __forceinline__ void fma2(float& x0, float& x1, float b, float c) {
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
+      "mov.b64 z, {%3, %3};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float& x0, float& x1, float a0, float a1) {
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(a0), "f"(a1));
+}
+
+// P = 2^(s * scale2 - m) of 32 columns as bf16 pairs; their fp32 sum onto l
+template <bool MASKED>
+__device__ __forceinline__ void exp32(uint32_t (&r)[32], float scale2, float neg_m, uint32_t vis,
+                                      uint32_t (&w)[16], float (&l)[4]) {
+#pragma unroll
+  for (int t = 0; t < 32; t += 2) {
+    float a = __uint_as_float(r[t]), b = __uint_as_float(r[t + 1]);
+    fma2(a, b, scale2, neg_m);
+    a = ex2_ftz(a);
+    b = ex2_ftz(b);
+    if (MASKED) {
+      a = (vis >> t) & 1u ? a : 0.f;
+      b = (vis >> (t + 1)) & 1u ? b : 0.f;
+    }
+    add2(l[t & 2], l[(t & 2) + 1], a, b);
+    w[t >> 1] = pack_bf16x2(a, b);
+  }
+}
+
+template <bool MASKED>
+__device__ __forceinline__ float row_exp(uint32_t sa, float scale2, float m,
+                                         const uint32_t (&vis)[4]) {
+  uint32_t ra[32], rb[32], w[16];
+  float l[4] = {0.f, 0.f, 0.f, 0.f};
+  tc::tmem_ld32_issue(sa, ra);
+  tc::tmem_wait_ld(ra);
+  tc::tmem_ld32_issue(sa + 32, rb);
+  exp32<MASKED>(ra, scale2, -m, vis[0], w, l);
+  tc::tmem_wait_ld(rb);
+  tc::tmem_st16(sa, w);
+  tc::tmem_ld32_issue(sa + 64, ra);
+  exp32<MASKED>(rb, scale2, -m, vis[1], w, l);
+  tc::tmem_wait_ld(ra);
+  tc::tmem_st16(sa + 16, w);
+  tc::tmem_ld32_issue(sa + 96, rb);
+  exp32<MASKED>(ra, scale2, -m, vis[2], w, l);
+  tc::tmem_wait_ld(rb);
+  tc::tmem_st16(sa + 32, w);
+  exp32<MASKED>(rb, scale2, -m, vis[3], w, l);
+  tc::tmem_st16(sa + 48, w);
+  return (l[0] + l[1]) + (l[2] + l[3]);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_attn_tc_kernel(const __grid_constant__ TreeLaunch p, const __grid_constant__ CUtensorMap qmap,
+                        const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ CUtensorMap vmap) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + kSmBars);
+  uint64_t* kv_empty = kv_full + kBufs;
+  uint64_t* q_full = kv_empty + kBufs;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* info_full = q_empty + 1;
+  uint64_t* s_full = info_full + kInfos;  // [2]
+  uint64_t* p_full = s_full + 2;
+  uint64_t* pv_done = p_full + 2;
+  uint64_t* o_free = pv_done + 2;
+  uint64_t* fill = o_free + 2;
+  uint64_t* ends = fill + 1;
+  BlockInfo* info = reinterpret_cast<BlockInfo*>(smem + kSmInfo);
+  int* misc = reinterpret_cast<int*>(smem + kSmMisc);  // [0] timeout, [4..6] odd values seen
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 8);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int H = p.num_heads;
+  const int tpt = 128 / H;  // drafted tokens per tile
+
+  if (tid == 0) {
+    for (int i = 0; i < 8; ++i) misc[i] = 0;
+    for (int s = 0; s < kBufs; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 2);  // the two issuers
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 2);
+    for (int i = 0; i < kInfos; ++i) mbar_init(&info_full[i], 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 4);
+      mbar_init(&pv_done[t], 1);
+      mbar_init(&o_free[t], 4);
+    }
+    mbar_init(fill, 1);
+    mbar_init(ends, 8);
+    fence_barrier_init();
+  }
+  if (warp == 1) tc::tmem_alloc(tmem_slot, kTmemCols);
+  const TreeSlice sl = tree_slice<kThreads>(
+      p, [&](int q) { return tree_cost(p, q, 2 * tpt); }, reinterpret_cast<long long*>(smem));
+  fence_proxy_async_smem();
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = *tmem_slot;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0 && sl.begin >= sl.end) p.split[blockIdx.x].nrows = 0;
+  if (!sl.tiled) {
+    tree_write_all_empty(p);
+    if (tid == 0 && blockIdx.x == 0) atomicOr(p.status, MSA_DEV_MALFORMED);
+  }
+
+  if (sl.begin < sl.end) {
+    if (warp == 0) {
+      // ---------------------------------------------- copies
+      long long it = sl.begin, pre = sl.pre;
+      int q = sl.q, n = 0, n_seg = 0, x = 0, fills = 0;  // blocks, segments, ring uses
+      bool ok = true;
+      TreeSplit rec;
+      rec.nrows = 0;
+      auto acquire = [&]() -> int {
+        const int b = x % kBufs;
+        if (x >= kBufs) ok = ok && warp_wait(&kv_empty[b], ((x / kBufs) - 1) & 1);
+        ++x;
+        return b;
+      };
+      auto announce = [&](const BlockInfo& bi) {
+        if (lane == 0) {
+          info[n % kInfos] = bi;
+          mbar_arrive(&info_full[n % kInfos]);
+        }
+        ++n;
+      };
+      BlockInfo bi;
+      bi.pad = 0;
+      while (ok && it < sl.end) {
+        TreeReq rq = tree_request(p, q);
+        int nv = 0, tiles = 0;
+        if (rq.qlen > 0) {
+          nv = tree_visits(p, q, rq);
+          tiles = (rq.qlen + 2 * tpt - 1) / (2 * tpt);
+        }
+        const long long cost = (long long)nv * tiles;
+        if (it >= pre + cost) {
+          pre += cost;
+          ++q;
+          continue;
+        }
+        const int tile = (int)((it - pre) / nv), b0 = (int)((it - pre) % nv);
+        const int nb = (int)min((long long)(nv - b0), sl.end - it);
+        bi.j0 = tile * 2 * tpt;
+        bi.ntok = min(2 * tpt, rq.qlen - bi.j0);
+        bi.row0 = rq.q0 + bi.j0;
+        bi.ctx = rq.ctx;
+        bi.qlen = rq.qlen;
+        bi.seq = rq.ctx + rq.qlen;
+        bi.slot = 2 * blockIdx.x + (b0 > 0 ? 0 : 1);
+        bi.q = q;
+        bi.bad = rq.bad;
+        bi.rows = nullptr;
+        const int both = (nb == nv ? kWhole : 0) | (bi.ntok > tpt ? kTwo : 0);
+        const long long s = pre + (long long)tile * nv, e = s + nv;
+        if (b0 > 0 && sl.total * (blockIdx.x - 1) / sl.ctas <= s) {
+          rec.nrows = bi.ntok * H;
+          rec.row0 = bi.row0;
+          rec.last = (int)((e * sl.ctas - 1) / sl.total);
+          rec.q = q;
+        }
+        if (n_seg > 0) ok = warp_wait(q_empty, (n_seg - 1) & 1);
+        if (!ok) break;
+        ++n_seg;
+        if (rq.bad) {
+          bi.flags = kFirst | kLast | kPoison | kNoData | kWhole | both;
+          bi.t0 = 0;
+          const int kb = acquire(), vb = acquire();
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive(q_full);
+            mbar_arrive(&kv_full[kb]);
+            mbar_arrive(&kv_full[vb]);
+          }
+          announce(bi);
+        } else if (lane == 0) {
+          mbar_arrive_expect_tx(q_full, (both & kTwo ? 2 : 1) * kTile);
+          for (int t = 0; t < (both & kTwo ? 2 : 1); ++t)
+            for (int h = 0; h < 2; ++h)
+              tma_load_2d(smem + kSmQ + t * kTile + h * kHalf, &qmap, 64 * h,
+                          (bi.row0 + t * tpt) * H, q_full);
+        }
+        for (int c0 = 0; !rq.bad && ok && c0 < nb; c0 += 32) {
+          int blk = 0, page = 0;
+          if (c0 + lane < nb) {
+            blk = b0 + c0 + lane;
+            if (p.topk_idx) blk = p.list_blk[(long long)q * p.list_cap + blk];
+            page = p.batch.block_table[(long long)q * p.batch.bt_stride + blk];
+          }
+          for (int i = 0; ok && i < min(32, nb - c0); ++i) {
+            const int b = __shfl_sync(0xffffffffu, blk, i), pg = __shfl_sync(0xffffffffu, page, i);
+            const bool bad_page = pg < 0 || pg >= p.batch.num_pages;
+            const int ntok = min(kBlock, bi.seq - kBlock * b);
+            const bool cached_all = !p.topk_idx || b >= rq.ctx / kBlock;
+            bi.rows = cached_all ? nullptr
+                                 : p.list_rows + ((long long)q * p.list_cap + b0 + c0 + i) * p.list_words;
+            bi.t0 = kBlock * b;
+            bi.flags = both | (c0 + i == 0 ? kFirst : 0) | (c0 + i == nb - 1 ? kLast : 0) |
+                       (bad_page ? kBadPage | kNoData : 0) |
+                       (bi.t0 + kBlock > rq.ctx || !cached_all ? kMixed : 0);
+            const int kb = acquire(), vb = acquire();
+            if (!ok) break;
+            uint8_t* kd = smem + kSmKv + kb * kTile;
+            uint8_t* vd = smem + kSmKv + vb * kTile;
+            if (bad_page) {
+              if (lane == 0) {
+                mbar_arrive(&kv_full[kb]);
+                mbar_arrive(&kv_full[vb]);
+                atomicOr(p.status, MSA_DEV_BAD_PAGE);
+              }
+            } else {
+              // tokens past the request's end are not data: their V rows are
+              // zeroed before the product reads them
+              uint64_t* land = ntok < kBlock ? fill : &kv_full[vb];
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&kv_full[kb], kTile);
+                mbar_arrive_expect_tx(land, kTile);
+                for (int h = 0; h < 2; ++h) {
+                  tma_load_2d(kd + h * kHalf, &kmap, 64 * h, pg * kBlock, &kv_full[kb]);
+                  tma_load_2d(vd + h * kHalf, &vmap, 64 * h, pg * kBlock, land);
+                }
+              }
+              if (ntok < kBlock) {
+                // (announced first: the other roles run meanwhile)
+                announce(bi);
+                ok = warp_wait(fill, fills & 1);
+                ++fills;
+                if (!ok) break;
+                uint4* v4 = reinterpret_cast<uint4*>(vd);
+                for (int k = ntok * 8 + lane; k < kBlock * 8; k += 32)
+                  v4[k] = v4[kHalf / 16 + k] = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&kv_full[vb]);
+                continue;
+              }
+            }
+            announce(bi);
+          }
+        }
+        it += nb;
+      }
+      if (ok) {
+        bi.flags = kEnd;
+        announce(bi);
+      } else {
+        misc[0] = 1;
+        // copies still in flight land before the CTA leaves
+        for (int i = max(0, x - kBufs); i < x; ++i) mbar_wait(&kv_full[i % kBufs], (i / kBufs) & 1);
+        if (n_seg > 0) mbar_wait(q_full, (n_seg - 1) & 1);
+      }
+      if (lane == 0) p.split[blockIdx.x] = rec;
+    } else if (warp == 1 || warp == 2) {
+      // ---------------------------------------------- products of tile t
+      const int t = warp - 1;
+      if (lane == 0) {
+        const uint64_t qd = tc::desc_kmajor_sw128(smem_u32(smem + kSmQ + t * kTile));
+        int x = 0, seg = -1, done = 0;  // done: commits to pv_done so far
+        bool ok = true;
+        for (int n = 0;; ++n) {
+          ok = mbar_wait(&info_full[n % kInfos], (n / kInfos) & 1);
+          if (!ok) break;
+          const int fl = info[n % kInfos].flags;
+          if (fl & kEnd) break;
+          const bool work = (t == 0 || (fl & kTwo)) && !(fl & kNoData);
+          const int kb = x % kBufs, kph = (x / kBufs) & 1, vb = (x + 1) % kBufs,
+                    vph = ((x + 1) / kBufs) & 1;
+          x += 2;
+          if (fl & kFirst) {
+            ++seg;
+            ok = ok && mbar_wait(q_full, seg & 1);
+          }
+          ok = ok && mbar_wait(&kv_full[kb], kph);
+          // S takes the place of the previous block's P
+          if (done > 0) ok = ok && mbar_wait(&pv_done[t], (done - 1) & 1);
+          if (!ok) break;
+          if (work) {
+            tc::fence_after();
+            const uint64_t kd = tc::desc_kmajor_sw128(smem_u32(smem + kSmKv + kb * kTile));
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+              tc::mma_ss(tmem + col_s(t), tc::desc_advance(qd, off), tc::desc_advance(kd, off),
+                         kIdescS, kk > 0 ? 1u : 0u);
+            }
+            tc::commit(&s_full[t]);
+            tc::commit(&kv_empty[kb]);
+            if (fl & kLast) tc::commit(q_empty);
+          } else {
+            mbar_arrive(&s_full[t]);
+            mbar_arrive(&kv_empty[kb]);
+            if (fl & kLast) mbar_arrive(q_empty);
+          }
+          ok = ok && mbar_wait(&p_full[t], n & 1) && mbar_wait(&kv_full[vb], vph);
+          // O of the previous segment has been read
+          if ((fl & kFirst) && seg > 0) ok = ok && mbar_wait(&o_free[t], (seg - 1) & 1);
+          if (!ok) break;
+          if (work) {
+            tc::fence_after();
+            const uint64_t vd = tc::desc_mnmajor_sw128(smem_u32(smem + kSmKv + vb * kTile), kHalf);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              tc::mma_ts(tmem + col_o(t), tmem + col_s(t) + kk * 8, tc::desc_advance(vd, kk * 2048),
+                         kIdescO, (kk > 0 || !(fl & kFirst)) ? 1u : 0u);
+            tc::commit(&pv_done[t]);
+            tc::commit(&kv_empty[vb]);
+          } else {
+            mbar_arrive(&pv_done[t]);
+            mbar_arrive(&kv_empty[vb]);
+          }
+          ++done;
+        }
+        if (!ok) misc[0] = 1;
+        // every product has completed before the tensor memory is freed
+        if (done > 0 && !mbar_wait(&pv_done[t], (done - 1) & 1)) misc[0] = 1;
+      }
+    } else if (warp >= 4) {
+      // ---------------------------------------------- softmax of tile t
+      const int t = (warp - 4) >> 2, quarter = warp & 3;
+      const int m = quarter * 32 + lane;  // row of the tile
+      const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+      const uint32_t sa = tmem + lanes + col_s(t), oa = tmem + lanes + col_o(t);
+      const int mtok = m / H, head = m % H;
+      float scale2 = p.softmax_scale * kTreeLog2e, vs = 1.f;
+      if (p.scale_mode == MSA_SCALE_SCALAR) {
+        scale2 *= __ldg(p.k_scale);
+        vs = __ldg(p.v_scale);
+      }
+      const float sink = p.sinks ? __ldg(p.sinks + head) : 0.f;
+      float m_run = -INFINITY, l_run = 0.f;
+      int x = 1, seg = -1;
+      bool bad = false, ok = true;
+      for (int n = 0;; ++n) {
+        ok = warp_wait(&info_full[n % kInfos], (n / kInfos) & 1);
+        if (!ok) break;
+        const BlockInfo& bi = info[n % kInfos];
+        const int fl = bi.flags;
+        if (fl & kEnd) break;
+        const int vb = x % kBufs, vph = (x / kBufs) & 1;
+        x += 2;
+        if (fl & kFirst) {
+          ++seg;
+          m_run = -INFINITY;
+          l_run = 0.f;
+          bad = false;
+        }
+        bad |= (fl & (kBadPage | kPoison)) != 0;
+        const int tok = t * tpt + mtok;  // drafted token of the pair
+        const bool there = (t == 0 || (fl & kTwo)) && mtok < tpt && tok < bi.ntok;
+        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+        const bool work = (t == 0 || (fl & kTwo)) && !(fl & kNoData);
+        if ((fl & kMixed) && work) {
+          const int j = bi.j0 + tok;
+          const bool sel = there && tree_row_selects(bi.rows, j);
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            vis[w] = !there ? 0u
+                            : tree_vis16(p, bi.row0 + tok, j, bi.ctx, bi.qlen, bi.t0 + 32 * w, sel) |
+                                  tree_vis16(p, bi.row0 + tok, j, bi.ctx, bi.qlen, bi.t0 + 32 * w + 16, sel) << 16;
+        }
+        ok = warp_wait(&s_full[t], n & 1);
+        if (!ok) break;
+        if (work) {
+          tc::fence_after();
+          float mx;
+          if (fl & kMixed)
+            mx = scale2 >= 0.f ? row_max<false, true>(sa, vis) * scale2 : row_max<true, true>(sa, vis) * -scale2;
+          else
+            mx = scale2 >= 0.f ? row_max<false, false>(sa, vis) * scale2 : row_max<true, false>(sa, vis) * -scale2;
+          const bool move = mx > m_run + kSlack || (m_run == -INFINITY && mx > -INFINITY);
+          if (__any_sync(0xffffffffu, move)) {
+            float al = 1.f;
+            if (mx > m_run) {
+              al = m_run == -INFINITY ? 1.f : ex2_ftz(m_run - mx);
+              m_run = mx;
+            }
+            l_run *= al;
+            // (a row without a reference has an all-zero O: nothing to rescale)
+            if (!(fl & kFirst) && __any_sync(0xffffffffu, al != 1.f)) {
+              ok = warp_wait(&pv_done[t], (n - 1) & 1);
+              if (!ok) break;
+              tc::fence_after();
+#pragma unroll 1
+              for (int c = 0; c < 128; c += 32) {
+                uint32_t r[32];
+                tc::tmem_ld32_issue(oa + c, r);
+                tc::tmem_wait_ld(r);
+                uint32_t a[16], b[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  a[i] = __float_as_uint(__uint_as_float(r[i]) * al);
+                  b[i] = __float_as_uint(__uint_as_float(r[16 + i]) * al);
+                }
+                tc::tmem_st16(oa + c, a);
+                tc::tmem_st16(oa + c + 16, b);
+              }
+            }
+          }
+          const float base = m_run == -INFINITY ? 0.f : m_run;
+          l_run += (fl & kMixed) ? row_exp<true>(sa, scale2, base, vis) : row_exp<false>(sa, scale2, base, vis);
+          tc::tmem_wait_st();
+          tc::fence_before();
+        }
+        if ((fl & kMixed) && !(fl & kNoData)) {
+          // values that are not finite among this tile's half of the block's V
+          ok = warp_wait(&kv_full[vb], vph);
+          if (!ok) break;
+          const int row = 64 * t + (m >> 1);
+          const uint8_t* src = smem + kSmKv + vb * kTile + (m & 1) * kHalf + row * 128;
+          uint32_t odd = 0;
+          if (bi.t0 + row < bi.seq) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 v = lds128(src + 16 * i);
+              odd |= (v.x & 0x7fff7fffu) + 0x00800080u;
+              odd |= (v.y & 0x7fff7fffu) + 0x00800080u;
+              odd |= (v.z & 0x7fff7fffu) + 0x00800080u;
+              odd |= (v.w & 0x7fff7fffu) + 0x00800080u;
+            }
+          }
+          if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0) && lane == 0)
+            *reinterpret_cast<volatile int*>(&misc[4 + seg % 3]) = 1;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[t]);
+        if (fl & kLast) {
+          // both tiles' warps have looked over the segment's blocks
+          if (lane == 0) mbar_arrive(ends);
+          ok = warp_wait(ends, seg & 1) && warp_wait(&pv_done[t], n & 1);
+          if (!ok) break;
+          const bool odd = *reinterpret_cast<volatile int*>(&misc[4 + seg % 3]) != 0;
+          if (warp == 4 && lane == 0) *reinterpret_cast<volatile int*>(&misc[4 + (seg + 2) % 3]) = 0;
+          tc::fence_after();
+          const bool none = bad || (m_run == -INFINITY && l_run == 0.f);
+          const TreeRowEnd e = tree_row_end(none ? -INFINITY : m_run, none ? 0.f : l_run,
+                                            p.sinks != nullptr, sink * kTreeLog2e, vs);
+          const bool have = (t == 0 || (fl & kTwo)) && !(fl & kPoison);
+          const long long r = (long long)(bi.row0 + tok) * H + head;  // row x head in the batch
+          const long long pr = (long long)bi.slot * 256 + t * tpt * H + m;
+          if (have) {
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+              uint32_t v[32];
+              tc::tmem_ld32_issue(oa + c, v);
+              tc::tmem_wait_ld(v);
+              if (there && (fl & kWhole)) {
+                uint4* dst = reinterpret_cast<uint4*>(p.out + r * kHeadDim + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    w[k] = none ? 0u
+                                : pack_bf16x2(__uint_as_float(v[8 * i + 2 * k]) * e.f,
+                                              __uint_as_float(v[8 * i + 2 * k + 1]) * e.f);
+                  dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              } else if (there) {
+                uint4* dst = reinterpret_cast<uint4*>(p.part_o + pr * kHeadDim + c);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  dst[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              }
+              __syncwarp();
+            }
+          } else if (there) {  // a poisoned request's rows
+            uint4* dst = reinterpret_cast<uint4*>(p.out + r * kHeadDim);
+            for (int i = 0; i < kHeadDim / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&o_free[t]);
+          if (there) {
+            if (fl & kWhole) p.lse[r] = none ? (p.sinks ? sink : -INFINITY) : e.lse;
+            else p.part_ml[pr] = make_float2(m_run, l_run);
+          }
+          if (t == 0 && m == 0) {
+            if (!(fl & kWhole)) p.part_bad[bi.slot] = bad ? 1 : odd ? 2 : 0;
+            if (bi.bad) atomicOr(p.status, bi.bad);
+          }
+          if ((fl & kWhole) && odd && !bad) {
+            __syncwarp();
+            // this warp's rows again, from the tokens that they see alone
+            for (int i = 0; i < 32; ++i) {
+              const int mm = quarter * 32 + i, tk = t * tpt + mm / H;
+              if (!have || mm / H >= tpt || tk >= bi.ntok) break;
+              tree_slow_row(p, bi.q, bi.row0 + tk, bi.j0 + tk, mm % H);
+            }
+          }
+        }
+      }
+      if (!ok) misc[0] = 1;
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (misc[0] && tid == 0) atomicOr(p.status, MSA_DEV_TIMEOUT);
+  if (warp == 1) {
+    tc::fence_after();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_tree_attn_tc(const TreeLaunch& p, int grid, cudaStream_t stream) {
+  CUtensorMap qmap, kmap, vmap;
+  const long long toks = max(1ll, (long long)p.batch.num_pages) * kBlock;
+  if (!encode_map_2d(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.q, kHeadDim,
+                     (long long)p.batch.num_rows * p.num_heads, kHeadDim * 2, 64, 128) ||
+      !encode_map_2d(&kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.k, kHeadDim, toks, kHeadDim * 2, 64,
+                     kBlock) ||
+      !encode_map_2d(&vmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.v, kHeadDim, toks, kHeadDim * 2, 64,
+                     kBlock))
+    return cudaErrorInvalidValue;
+  const cudaError_t e =
+      cudaFuncSetAttribute(tree_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (e != cudaSuccess) return e;
+  tree_attn_tc_kernel<<<grid, kThreads, kBytes, stream>>>(p, qmap, kmap, vmap);
+  return cudaGetLastError();
+}
+
+}  // namespace msa

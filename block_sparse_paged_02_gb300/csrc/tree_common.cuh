@@ -17,7 +17,7 @@ struct TreeSplit {
   int32_t nrows;  // 0: none
   int32_t row0;
   int32_t last;
-  int32_t pad;
+  int32_t q;
 };
 
 struct TreeLaunch {
@@ -56,7 +56,9 @@ struct TreeLaunch {
 cudaError_t launch_tree_plan(const TreeLaunch& p, cudaStream_t stream);
 cudaError_t launch_tree_attn(const TreeLaunch& p, cudaStream_t stream);
 cudaError_t launch_attn_mass(const TreeLaunch& p, cudaStream_t stream);
+cudaError_t launch_tree_attn_tc(const TreeLaunch& p, int grid, cudaStream_t stream);
 int tree_tile_rows(int max_rows, int num_heads);
+int tree_part_rows(int max_rows, int num_heads);
 
 struct EvictLaunch {
   msa_cache_view cache;
@@ -147,6 +149,128 @@ __device__ __forceinline__ uint32_t tree_vis16(const TreeLaunch& p, int row, int
 // at place `at` of its list.
 __device__ __forceinline__ bool tree_row_selects(const uint32_t* rows, int j) {
   return !rows || ((__ldg(rows + (j >> 5)) >> (j & 31)) & 1u);
+}
+
+// 2^x, results below 2^-126 as 0
+__device__ __forceinline__ float ex2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A row's end: (m, l) in log2 units, the sink joined in
+struct TreeRowEnd {
+  float f, lse;  // factor of the accumulators, natural-log lse
+};
+__device__ __forceinline__ TreeRowEnd tree_row_end(float m, float l, bool has_sink, float sink2, float vs) {
+  TreeRowEnd e;
+  if (m == -INFINITY && l == 0.f) {  // nothing seen
+    e.f = 0.f;
+    e.lse = has_sink ? sink2 * kTreeLn2 : -INFINITY;
+    return e;
+  }
+  float f = 1.f;
+  if (has_sink) {
+    const float mn = fmaxf(m, sink2);
+    f = ex2_ftz(m - mn);
+    l = l * f + ex2_ftz(sink2 - mn);
+    m = mn;
+  }
+  e.f = f * vs / l;
+  e.lse = (m + log2f(l)) * kTreeLn2;
+  return e;
+}
+
+// every row of an unusable batch, as empty rows
+__device__ __forceinline__ void tree_write_all_empty(const TreeLaunch& p) {
+  const long long n = (long long)p.batch.num_rows * p.num_heads;
+  const long long step = (long long)gridDim.x * blockDim.x;
+  const long long at = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  for (long long i = at; i < n; i += step)
+    p.lse[i] = p.sinks ? __ldg(p.sinks + i % p.num_heads) : -INFINITY;
+  uint4* o = reinterpret_cast<uint4*>(p.out);
+  for (long long i = at; i < n * (kHeadDim / 8); i += step) o[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// One row and head by one warp, from the visible tokens alone and one after
+// another: for tiles that hold a value which is not finite and which not every
+// row sees (a product over the tile would carry 0 * NaN into the others).
+static __device__ __noinline__ void tree_slow_row(const TreeLaunch& p, int q, int row, int j, int h) {
+  const int lane = threadIdx.x & 31;
+  const unsigned all = 0xffffffffu;
+  const TreeReq rq = tree_request(p, q);
+  const int seq = rq.ctx + rq.qlen;
+  const uint2 qb = *reinterpret_cast<const uint2*>(p.q + ((long long)row * p.num_heads + h) * kHeadDim + 4 * lane);
+  const float qv[4] = {bf16lo(qb.x), bf16hi(qb.x), bf16lo(qb.y), bf16hi(qb.y)};
+  float scale2 = p.softmax_scale * kTreeLog2e, vs1 = 1.f;
+  if (p.scale_mode == MSA_SCALE_SCALAR) {
+    scale2 *= __ldg(p.k_scale);
+    vs1 = __ldg(p.v_scale);
+  }
+  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int b = 0; b < rq.nb; ++b) {
+    bool sel = !p.topk_idx || b >= rq.ctx / kBlock;
+    if (!sel) {
+      for (int i = lane; i < p.topk; i += 32) sel |= p.topk_idx[(long long)row * p.topk + i] == b;
+      sel = __any_sync(all, sel) != 0;
+    }
+    const long long tok = (long long)p.batch.block_table[(long long)q * p.batch.bt_stride + b] * kBlock;
+    for (int g = 0; g < kBlock && kBlock * b + g < seq; g += 16) {
+      uint32_t vis = tree_vis16(p, row, j, rq.ctx, rq.qlen, kBlock * b + g, sel);
+      for (; vis; vis &= vis - 1) {
+        const long long at = tok + g + __ffs(vis) - 1;
+        float kk[4], vv[4];
+        if (p.kv_fp8) {
+          const uint32_t kc = *reinterpret_cast<const uint32_t*>(p.k + at * kHeadDim + 4 * lane);
+          const uint32_t vc = *reinterpret_cast<const uint32_t*>(p.v + at * kHeadDim + 4 * lane);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t k2 = e4m3x2_to_f16x2((uint16_t)(kc >> (16 * i)));
+            const uint32_t v2 = e4m3x2_to_f16x2((uint16_t)(vc >> (16 * i)));
+            const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(&k2));
+            const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(&v2));
+            kk[2 * i] = kf.x; kk[2 * i + 1] = kf.y; vv[2 * i] = vf.x; vv[2 * i + 1] = vf.y;
+          }
+        } else {
+          const uint2 kc = *reinterpret_cast<const uint2*>(p.k + (at * kHeadDim + 4 * lane) * 2);
+          const uint2 vc = *reinterpret_cast<const uint2*>(p.v + (at * kHeadDim + 4 * lane) * 2);
+          kk[0] = bf16lo(kc.x); kk[1] = bf16hi(kc.x); kk[2] = bf16lo(kc.y); kk[3] = bf16hi(kc.y);
+          vv[0] = bf16lo(vc.x); vv[1] = bf16hi(vc.x); vv[2] = bf16lo(vc.y); vv[3] = bf16hi(vc.y);
+        }
+        float s = qv[0] * kk[0] + qv[1] * kk[1] + qv[2] * kk[2] + qv[3] * kk[3];
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(all, s, x);
+        float f = scale2, vs = 1.f;
+        if (p.scale_mode == MSA_SCALE_PER_TOKEN_HEAD) {
+          f *= __ldg(p.k_scale + at);
+          vs = __ldg(p.v_scale + at);
+        }
+        s *= f;
+        const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.f : mn;
+        const float al = m == -INFINITY ? 1.f : ex2_ftz(m - base), e = ex2_ftz(s - base);
+        m = mn;
+        l = l * al + e;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = o[i] * al + e * (vs * vv[i]);
+      }
+    }
+  }
+  const bool none = m == -INFINITY && l == 0.f;
+  const float sink = p.sinks ? __ldg(p.sinks + h) : 0.f;
+  const TreeRowEnd e = tree_row_end(m, l, p.sinks != nullptr, sink * kTreeLog2e, vs1);
+  const long long r = (long long)row * p.num_heads + h;
+  uint2 w = make_uint2(pack_bf16x2(o[0] * e.f, o[1] * e.f), pack_bf16x2(o[2] * e.f, o[3] * e.f));
+  if (none) w = make_uint2(0u, 0u);
+  *reinterpret_cast<uint2*>(p.out + r * kHeadDim + 4 * lane) = w;
+  if (lane == 0) p.lse[r] = none ? (p.sinks ? sink : -INFINITY) : e.lse;
+}
+
+// Items of a request: its tiles of drafted tokens times its visited blocks
+__device__ __forceinline__ long long tree_cost(const TreeLaunch& p, int q, int tok_per_tile) {
+  TreeReq r = tree_request(p, q);
+  if (r.qlen <= 0) return 0;
+  const long long n = tree_visits(p, q, r);
+  return n * ((r.qlen + tok_per_tile - 1) / tok_per_tile);
 }
 
 // The CTA's slice of a flat item list over the requests (cost(q) items for

@@ -160,6 +160,25 @@ def test_hidden_values_do_not_leak(kv, scale, q_lens):
     assert np.isnan(m).sum() == 2
 
 
+@pytest.mark.parametrize("kv,scale", [(BF, NONE), (BF, SCALAR), (F8, TOKEN)])
+@pytest.mark.parametrize("hq,ql,ctx", [(16, 40, 20), (16, 20, 100), (4, 60, 3), (16, 9, 0)])
+def test_hidden_values_in_a_single_block(kv, scale, hq, ql, ctx):
+    # one block holds the whole request: a CTA writes its tiles without a merge
+    w = make(27, [ql, 2], [ctx, 50], hq, kv, scale, True)
+    mask = np.zeros((ql + 2, 2), np.uint32)
+    for j in range(ql + 2):
+        i = j if j < ql else j - ql
+        mask[j, i // 32] = 1 << (i % 32)  # each row sees the context and itself
+    page = w.block_table[0, 0]
+    w.v_cache[page, ctx + ql - 1, 0, 7] = 0x7f if kv == F8 else 0x7f80
+    c = case(w)
+    c.tree_attn(mask=T.dev(mask))
+    torch.cuda.synchronize()
+    keep = [r for r in range(ql + 2) if r != ql - 1]
+    check_attn(c, T.tree_attn(make(27, [ql, 2], [ctx, 50], hq, kv, scale, True), mask), keep)
+    assert not torch.isfinite(c.out[ql - 1].float()[:, 7]).any()
+
+
 def test_poisoned_requests():
     q_lens, ctxs = [3, 20, 4, 2, 6], [300, 2000, 500, 64, 900]
     for sink in (False, True):
