@@ -698,6 +698,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 // ------------------------------------------------------------------ merge
 
 constexpr int kMgThreads = 256, kMgWarps = kMgThreads / 32;
+constexpr int kMaxMainCtas = 512;  // (the main kernels run one CTA per SM)
 constexpr int kMgFew = 8;  // up to this many partials a warp joins a row by itself
 
 // Joins the partials of the tiles that several CTAs share.  Work units are 8
@@ -707,20 +708,51 @@ __global__ void __launch_bounds__(kMgThreads) tree_merge_kernel(const __grid_con
                                                                 int grid_main, int tile_rows) {
   __shared__ float s_o[kMgWarps][kHeadDim];
   __shared__ float s_m[kMgWarps], s_l[kMgWarps];
-  __shared__ int s_bad[kMgWarps];
+  __shared__ int s_bad[kMgWarps], s_sum[kMgWarps], s_base[kMaxMainCtas];
+  __shared__ TreeSplit s_rec[kMaxMainCtas];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int H = p.num_heads;
   const float vs = p.scale_mode == MSA_SCALE_SCALAR ? __ldg(p.v_scale) : 1.f;
-  long long unit = blockIdx.x, base = 0;
-  for (int c = 1; c < grid_main; ++c) {
-    const TreeSplit rec = p.split[c];
-    if (rec.nrows == 0) continue;
+  // the split tiles' work units, by a prefix sum over the records
+  long long total = 0;
+  for (int c0 = 0; c0 < grid_main; c0 += kMgThreads) {
+    const int c = c0 + threadIdx.x;
+    TreeSplit rec;
+    rec.nrows = 0;
+    if (c > 0 && c < grid_main) rec = p.split[c];
     const int n = rec.last - c + 2;  // partials: CTAs c - 1 .. last
     const bool few = n <= kMgFew;
     const int units = few ? (rec.nrows + kMgWarps - 1) / kMgWarps : rec.nrows;
-    for (; unit < base + units; unit += gridDim.x) {
-      const int at = (int)(unit - base);
+    int x = units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_sum[warp] = x;
+    __syncthreads();
+    if (c < grid_main) {
+      int before = x - units;
+      for (int w = 0; w < warp; ++w) before += s_sum[w];
+      s_base[c] = (int)total + before;
+      s_rec[c] = rec;
+    }
+    for (int w = 0; w < kMgWarps; ++w) total += s_sum[w];
+    __syncthreads();
+  }
+  for (int unit = blockIdx.x; unit < total; unit += gridDim.x) {
+    int lo = 0, hi = grid_main - 1;  // last record whose first unit is <= unit
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_base[mid] <= unit) lo = mid; else hi = mid - 1;
+    }
+    const int c = lo;
+    const TreeSplit rec = s_rec[c];
+    const int n = rec.last - c + 2;
+    const bool few = n <= kMgFew;
+    {
+      const int at = unit - s_base[c];
       const int m = few ? at * kMgWarps + warp : at;
       const bool live = m < rec.nrows;
       float M = -INFINITY, L = 0.f;
@@ -800,7 +832,6 @@ __global__ void __launch_bounds__(kMgThreads) tree_merge_kernel(const __grid_con
         if (lane == 0) p.lse[r] = none ? (p.sinks ? sink : -INFINITY) : e.lse;
       }
     }
-    base += units;
   }
 }
 
@@ -915,7 +946,7 @@ cudaError_t launch_main(const TreeLaunch& p, cudaStream_t stream) {
   auto kern = tree_attn_kernel<FP8, PTH, MW>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (e != cudaSuccess) return e;
-  const int grid = device_sm_count();
+  const int grid = min(device_sm_count(), kMaxMainCtas);
   kern<<<grid, kTaThreads, C::kBytes, stream>>>(p, qmap, kmap, vmap);
   e = cudaGetLastError();
   return e != cudaSuccess ? e : launch_merge(p, grid, C::kM, stream);
@@ -958,7 +989,7 @@ cudaError_t launch_tree_attn(const TreeLaunch& p, cudaStream_t stream) {
   }
   const bool pth = p.scale_mode == MSA_SCALE_PER_TOKEN_HEAD;
   if (!p.kv_fp8 && !pth && tree_tile_rows(p.max_rows, p.num_heads) == 128) {
-    const int grid = device_sm_count();
+    const int grid = min(device_sm_count(), kMaxMainCtas);
     const cudaError_t e = launch_tree_attn_tc(p, grid, stream);
     return e != cudaSuccess ? e : launch_merge(p, grid, 256, stream);
   }
