@@ -6,243 +6,512 @@
 // and a sum over the rows, no second pass.  A token belongs to one CTA, which
 // adds its rows in a fixed order: no atomics, the same bits every time.
 //
-// The keys are the rows of the product (S^T = K Q^T on warp MMA, m16n8k16):
-// a warp keeps its 16 tokens' keys in registers for all the rows, the sum
-// over a row's heads is a sum over accumulator columns, and only the last
-// four partial sums cross lanes.
+// The product is taken as S^T = K Q^T on the 5th-generation tensor cores
+// (tcgen05.mma M128, N = up to 256 rows, K128): the block's 128 tokens are the
+// lanes of tensor memory, so each thread adds up its own token's columns and
+// nothing crosses threads.  Per element one packed multiply-add, one 2^x, one
+// packed add.  With few rows the stream of K bounds it, with many the 2^x
+// (and, at N = 256, the products behind them).
+//
+// Blocks go in groups of two, one per epilogue warpgroup, so that one's sums
+// overlap the other's products.  A request of at most two chunks of rows
+// keeps its queries in shared memory for all its blocks; more chunks stream
+// through two buffers, each used by the group's two blocks.  e4m3 keys are
+// converted to f16 (exact) by the four loader warps.
 #include <string.h>
 
+#include "tcgen05.cuh"
 #include "tree_common.cuh"
 
 namespace msa {
 namespace {
 
-constexpr int kMaThreads = 256;
-constexpr int kQRows = 64;  // rows x heads per pass over Q
+constexpr int kThreads = 512;
+constexpr int kHalf = 128 * 128;
+constexpr int kTile = 2 * kHalf;   // 128 keys x 128 dims, 16 bits
+constexpr int kRaw = 128 * 128;    // 128 keys of e4m3
+constexpr int kInfos = 16;
+constexpr int kLoaders = 4;        // warps 12 .. 15
 
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
+struct MassInfo {
+  int flags;
+  int nblk;      // blocks of the CTA's segment (on its first block)
+  int q0, ctx, qlen;
+  int t0;        // position of the block's first token
+  int page;
+  int pad;
+  const uint32_t* rows;  // selection bits, or NULL
+};
+constexpr int kFirst = 1, kEnd = 2, kMixed = 4;
 
-template <bool FP8>
+template <bool FP8, int QR>
 struct MassCfg {
-  static constexpr int kPage = kBlock * kHeadDim * (FP8 ? 1 : 2);
-  static constexpr int kSmQ = kPage;                       // [2 halves][64 rows][128 B], swizzled
-  static constexpr int kSmLse = kSmQ + kQRows * 256;
-  static constexpr int kSmBar = kSmLse + kQRows * 4;
-  static constexpr int kSmScan = kSmBar + 16;
-  static constexpr int kBytes = kSmScan + 40 * 8 + 1024;
+  static constexpr int kTiles = FP8 ? (QR == 256 ? 2 : 3) : (QR == 256 ? 3 : QR == 64 ? 5 : 6);
+  static constexpr int kRaws = FP8 ? (QR == 256 ? 2 : QR == 64 ? 5 : 6) : 0;
+  static constexpr int kQBuf = QR * 256;
+  static constexpr int kSmK = 0;
+  static constexpr int kSmQ = kTiles * kTile;
+  static constexpr int kSmRaw = kSmQ + 2 * kQBuf;
+  static constexpr int kSmNl = kSmRaw + kRaws * kRaw;     // [2][QR] -lse (log2 units)
+  static constexpr int kSmInfo = kSmNl + 2 * QR * 4;
+  static constexpr int kSmBars = kSmInfo + kInfos * (int)sizeof(MassInfo);
+  // k full / empty, raw full / empty, q full / empty [2], d full / empty [2], info full
+  static constexpr int kNumBars = 2 * kTiles + 2 * kRaws + 8 + kInfos;
+  static constexpr int kSmMisc = kSmBars + kNumBars * 8;
+  static constexpr int kBytes = kSmMisc + 32;
+  static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ long long mass_weight(int qlen, int heads) {
-  return (qlen * heads + kQRows - 1) / kQRows;  // passes over Q per block
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
 }
 
-template <bool FP8>
-__global__ void __launch_bounds__(kMaThreads, FP8 ? 4 : 3)
-    attn_mass_kernel(const TreeLaunch p, const __grid_constant__ CUtensorMap kmap) {
-  using C = MassCfg<FP8>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
-  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::kSmBar);
-  float* s_lse = reinterpret_cast<float*>(smem + C::kSmLse);
-  long long* s_ll = reinterpret_cast<long long*>(smem + C::kSmScan);
+// Estimated cost of a block against `rows` rows x heads: the stream of its
+// keys, or its products and exponentials
+__device__ __forceinline__ long long mass_weight(int rows) { return max(20, (rows + 15) / 16); }
+
+// sum over 32 columns of 2^(s * f + nl) onto acc
+__device__ __forceinline__ void add_exp32(const uint32_t (&r)[32], float f, const float* nl,
+                                          float (&acc)[4]) {
+#pragma unroll
+  for (int t = 0; t < 32; t += 4) {
+    const float4 n = *reinterpret_cast<const float4*>(nl + t);
+    float a = __uint_as_float(r[t]), b = __uint_as_float(r[t + 1]);
+    float c = __uint_as_float(r[t + 2]), d = __uint_as_float(r[t + 3]);
+    fma2v(a, b, f, n.x, n.y);
+    fma2v(c, d, f, n.z, n.w);
+    add2(acc[0], acc[1], ex2_ftz(a), ex2_ftz(b));
+    add2(acc[2], acc[3], ex2_ftz(c), ex2_ftz(d));
+  }
+}
+
+template <bool FP8, int QR>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_mass_kernel(const __grid_constant__ TreeLaunch p, const __grid_constant__ CUtensorMap kmap) {
+  using C = MassCfg<FP8, QR>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kSmBars);
+  uint64_t* k_empty = k_full + C::kTiles;
+  uint64_t* raw_full = k_empty + C::kTiles;
+  uint64_t* raw_empty = raw_full + C::kRaws;
+  uint64_t* q_full = raw_empty + C::kRaws;  // [2]
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* d_full = q_empty + 2;
+  uint64_t* d_empty = d_full + 2;
+  uint64_t* info_full = d_empty + 2;
+  MassInfo* info = reinterpret_cast<MassInfo*>(smem + C::kSmInfo);
+  int* misc = reinterpret_cast<int*>(smem + C::kSmMisc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 4);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, c = lane & 3;
   const int H = p.num_heads;
+
   if (tid == 0) {
-    mbar_init(bar, 1);
+    misc[0] = 0;
+    for (int s = 0; s < C::kTiles; ++s) {
+      mbar_init(&k_full[s], FP8 ? kLoaders : 1);
+      // released by the products and, with bf16 keys, by the loaders: they then
+      // follow the blocks' announcements and are never lapped
+      mbar_init(&k_empty[s], FP8 ? 1 : 1 + kLoaders);
+    }
+    for (int s = 0; s < C::kRaws; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], kLoaders);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&q_full[s], kLoaders);
+      mbar_init(&q_empty[s], 9);  // the issuer and the epilogue's warps
+      mbar_init(&d_full[s], 1);
+      mbar_init(&d_empty[s], 4);
+    }
+    for (int s = 0; s < kInfos; ++s) mbar_init(&info_full[s], 1);
     fence_barrier_init();
   }
-  const TreeSlice sl = tree_slice<kMaThreads>(
+  if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
+  const TreeSlice sl = tree_slice<kThreads>(
       p,
       [&](int q) -> long long {
         TreeReq r = tree_request(p, q);
         if (r.qlen <= 0) return 0;
         const int n = tree_visits(p, q, r);
-        return r.bad ? 1 : n * mass_weight(r.qlen, H);
+        return r.bad ? 1 : n * mass_weight(r.qlen * H);
       },
-      s_ll);
+      reinterpret_cast<long long*>(smem));
+  fence_proxy_async_smem();
+  tc::fence_before();
   __syncthreads();
-  if (!sl.tiled) {
-    if (tid == 0 && blockIdx.x == 0) atomicOr(p.status, MSA_DEV_MALFORMED);
-    return;
-  }
-  if (sl.begin >= sl.end) return;
-  float scale2 = p.softmax_scale * kTreeLog2e;
-  if (p.scale_mode == MSA_SCALE_SCALAR) scale2 *= __ldg(p.k_scale);
-  const bool pth = p.scale_mode == MSA_SCALE_PER_TOKEN_HEAD;
-  long long pre = sl.pre;
-  uint32_t phase = 0;
-  const uint32_t q_s = smem_u32(smem + C::kSmQ);
+  tc::fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (!sl.tiled && tid == 0 && blockIdx.x == 0) atomicOr(p.status, MSA_DEV_MALFORMED);
 
-  for (int q = sl.q; q < p.batch.num_reqs && pre < sl.end; ++q) {
-    TreeReq rq = tree_request(p, q);
-    if (rq.qlen <= 0) continue;
-    const int nv = tree_visits(p, q, rq);  // 1 for a poisoned request
-    const long long w = rq.bad ? 1 : mass_weight(rq.qlen, H);
-    const long long first = pre;
-    pre += nv * w;
-    if (!rq.bad) {
-      // a bad page anywhere leaves the whole request as it is
-      bool bad = false;
-      for (int b = tid; b < rq.nb; b += kMaThreads) {
-        const int page = p.batch.block_table[(long long)q * p.batch.bt_stride + b];
-        bad |= page < 0 || page >= p.batch.num_pages;
-      }
-      if (__syncthreads_or(bad)) rq.bad = MSA_DEV_BAD_PAGE;
-    }
-    if (rq.bad) {
-      if (tid == 0) atomicOr(p.status, rq.bad);
-      continue;
-    }
-    // blocks whose first item lies in the slice
-    const int i0 = (int)((max(sl.begin, first) - first + w - 1) / w);
-    const int i1 = (int)min((long long)nv, (sl.end - first + w - 1) / w);
-    const int rows = rq.qlen * H, seq = rq.ctx + rq.qlen;
-    for (int i = i0; i < i1; ++i) {
-      const int b = p.topk_idx ? p.list_blk[(long long)q * p.list_cap + i] : i;
-      const int page = p.batch.block_table[(long long)q * p.batch.bt_stride + b];
-      const bool cached_all = !p.topk_idx || b >= rq.ctx / kBlock;
-      const uint32_t* sel =
-          cached_all ? nullptr : p.list_rows + ((long long)q * p.list_cap + i) * p.list_words;
-      const bool mixed = !cached_all || kBlock * b + kBlock > rq.ctx;
-      __syncthreads();  // the previous block's keys have been read
-      if (tid == 0) {
-        fence_proxy_async_smem();
-        mbar_arrive_expect_tx(bar, C::kPage);
-        tma_load_2d(smem, &kmap, 0, page * kBlock, bar);
-        if constexpr (!FP8) tma_load_2d(smem + C::kPage / 2, &kmap, 64, page * kBlock, bar);
-      }
-      const bool there = mbar_wait(bar, phase);
-      phase ^= 1;
-      if (!__syncthreads_and(there)) {
-        if (tid == 0) atomicOr(p.status, MSA_DEV_TIMEOUT);
-        return;
-      }
-      // ---- this warp's 16 tokens as the A operand
-      uint32_t ka[8][4];
-      const int t0 = kBlock * b + 16 * warp;
-      if constexpr (FP8) {
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const uint8_t* kr = smem + (16 * warp + g + 8 * hh) * kHeadDim;
-          const uint4 a = lds128(kr + (((2 * c) ^ g) << 4)), d = lds128(kr + (((2 * c + 1) ^ g) << 4));
-          const uint32_t w8[8] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            ka[kk][hh] = e4m3x2_to_f16x2((uint16_t)(w8[kk] & 0xffffu));
-            ka[kk][2 + hh] = e4m3x2_to_f16x2((uint16_t)(w8[kk] >> 16));
+  if (sl.begin < sl.end) {
+    if (warp == 0) {
+      // ---------------------------------------------- keys
+      long long pre = sl.pre;
+      int n = 0;  // blocks
+      bool ok = true;
+      for (int q = sl.q; ok && q < p.batch.num_reqs && pre < sl.end; ++q) {
+        TreeReq rq = tree_request(p, q);
+        if (rq.qlen <= 0) continue;
+        const int nv = tree_visits(p, q, rq);  // 1 for a poisoned request
+        const long long w = rq.bad ? 1 : mass_weight(rq.qlen * H);
+        const long long first = pre;
+        pre += nv * w;
+        const int32_t* bt = p.batch.block_table + (long long)q * p.batch.bt_stride;
+        if (!rq.bad) {
+          // a bad page anywhere leaves the whole request as it is
+          bool bad = false;
+#pragma unroll 4
+          for (int b = lane; b < rq.nb; b += 32) {
+            const int page = __ldg(bt + b);
+            bad |= page < 0 || page >= p.batch.num_pages;
+          }
+          if (__any_sync(0xffffffffu, bad)) rq.bad = MSA_DEV_BAD_PAGE;
+        }
+        if (rq.bad) {
+          if (lane == 0) atomicOr(p.status, rq.bad);
+          continue;
+        }
+        // blocks whose first item lies in the slice
+        const int i0 = (int)((max(sl.begin, first) - first + w - 1) / w);
+        const int i1 = (int)min((long long)nv, (sl.end - first + w - 1) / w);
+        for (int c0 = i0; ok && c0 < i1; c0 += 32) {
+          int blk = 0, page = 0;
+          if (c0 + lane < i1) {
+            blk = c0 + lane;
+            if (p.topk_idx) blk = p.list_blk[(long long)q * p.list_cap + blk];
+            page = __ldg(bt + blk);
+          }
+          for (int i = 0; i < min(32, i1 - c0); ++i) {
+            const int b = __shfl_sync(0xffffffffu, blk, i), pg = __shfl_sync(0xffffffffu, page, i);
+            if constexpr (FP8) {
+              const int s = n % C::kRaws;
+              if (n >= C::kRaws) ok = warp_wait(&raw_empty[s], ((n / C::kRaws) - 1) & 1);
+              if (!ok) break;
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&raw_full[s], kRaw);
+                bulk_g2s(smem + C::kSmRaw + s * kRaw, p.k + (long long)pg * kRaw, kRaw, &raw_full[s]);
+              }
+            } else {
+              const int s = n % C::kTiles;
+              if (n >= C::kTiles) ok = warp_wait(&k_empty[s], ((n / C::kTiles) - 1) & 1);
+              if (!ok) break;
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&k_full[s], kTile);
+                for (int h = 0; h < 2; ++h)
+                  tma_load_2d(smem + C::kSmK + s * kTile + h * kHalf, &kmap, 64 * h, pg * kBlock, &k_full[s]);
+              }
+            }
+            if (lane == 0) {
+              const bool all = !p.topk_idx || b >= rq.ctx / kBlock;
+              MassInfo mi;
+              mi.flags = (c0 + i == i0 ? kFirst : 0) | (kBlock * b + kBlock > rq.ctx || !all ? kMixed : 0);
+              mi.nblk = i1 - i0;
+              mi.q0 = rq.q0;
+              mi.ctx = rq.ctx;
+              mi.qlen = rq.qlen;
+              mi.t0 = kBlock * b;
+              mi.page = pg;
+              mi.pad = 0;
+              mi.rows = all ? nullptr : p.list_rows + ((long long)q * p.list_cap + c0 + i) * p.list_words;
+              info[n % kInfos] = mi;
+              mbar_arrive(&info_full[n % kInfos]);
+            }
+            ++n;
           }
         }
-      } else {
-        const int row = 16 * warp + (lane & 15);
+      }
+      if (ok && lane == 0) {
+        info[n % kInfos].flags = kEnd;
+        mbar_arrive(&info_full[n % kInfos]);
+      }
+      if (!ok) {
+        misc[0] = 1;
+        // copies still in flight land before the CTA leaves
+        const int ring = FP8 ? C::kRaws : C::kTiles;
+        uint64_t* bars = FP8 ? raw_full : k_full;
+        for (int i = max(0, n - ring); i < n; ++i) mbar_wait(&bars[i % ring], (i / ring) & 1);
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------- products
+      if (lane == 0) {
+        int n0 = 0, x0 = 0;     // first block, first query load of the segment
+        int steps[2] = {0, 0};  // products per epilogue warpgroup so far
+        bool ok = true;
+        for (;;) {
+          ok = mbar_wait(&info_full[n0 % kInfos], (n0 / kInfos) & 1);
+          if (!ok || (info[n0 % kInfos].flags & kEnd)) break;
+          const int nblk = info[n0 % kInfos].nblk, rows = info[n0 % kInfos].qlen * H;
+          const int chunks = (rows + QR - 1) / QR;
+          const bool resident = chunks <= 2;
+          for (int g = 0; ok && g < nblk; g += 2) {
+            const int nb = min(2, nblk - g);
+            const bool last = g + 2 >= nblk;
+            for (int c = 0; ok && c < chunks; ++c) {
+              const int x = x0 + (resident ? c : (g >> 1) * chunks + c), qb = x & 1;
+              ok = mbar_wait(&q_full[qb], (x >> 1) & 1);
+              const uint32_t idesc =
+                  tc::idesc_16(128, (min(QR, rows - c * QR) + 15) / 16 * 16, 0, FP8 ? 0 : 1);
+              const uint64_t qd = tc::desc_kmajor_sw128(smem_u32(smem + C::kSmQ + qb * C::kQBuf));
+              for (int b = 0; ok && b < nb; ++b) {
+                const int n = n0 + g + b, s = n % C::kTiles;
+                if (c == 0) ok = ok && mbar_wait(&k_full[s], (n / C::kTiles) & 1);
+                if (steps[b] > 0) ok = ok && mbar_wait(&d_empty[b], (steps[b] - 1) & 1);
+                if (!ok) break;
+                tc::fence_after();
+                const uint64_t kd = tc::desc_kmajor_sw128(smem_u32(smem + C::kSmK + s * kTile));
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const int ch = 2 * kk + (lane >> 4);
-          ldsm4(smem_u32(smem) + (ch >> 3) * (C::kPage / 2) + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
-                ka[kk]);
+                for (int kk = 0; kk < 8; ++kk)
+                  tc::mma_ss(tmem + 256 * b,
+                             tc::desc_advance(kd, (kk >> 2) * kHalf + (kk & 3) * 32),
+                             tc::desc_advance(qd, (kk >> 2) * (QR * 128) + (kk & 3) * 32), idesc,
+                             kk > 0 ? 1u : 0u);
+                tc::commit(&d_full[b]);
+                if (c == chunks - 1) tc::commit(&k_empty[s]);
+                ++steps[b];
+              }
+              if (ok && (!resident || last)) tc::commit(&q_empty[qb]);
+            }
+          }
+          if (!ok) break;
+          x0 += resident ? chunks : (nblk + 1) / 2 * chunks;
+          n0 += nblk;
         }
+        if (!ok) misc[0] = 1;
+        // every product has completed before the tensor memory is freed
+        for (int b = 0; b < 2; ++b)
+          if (steps[b] > 0 && !mbar_wait(&d_full[b], (steps[b] - 1) & 1)) misc[0] = 1;
       }
-      const long long slot = (long long)page * kBlock + 16 * warp;
-      float f[2] = {scale2, scale2};
-      if (pth) {
-        f[0] *= __ldg(p.k_scale + slot + g);
-        f[1] *= __ldg(p.k_scale + slot + g + 8);
-      }
-      float acc[2] = {0.f, 0.f};
-      for (int r0 = 0; r0 < rows; r0 += kQRows) {
-        const int n = min(kQRows, rows - r0);
-        __syncthreads();
-        for (int x = tid; x < kQRows * 16; x += kMaThreads) {  // 16-byte chunks of Q
-          const int row = x >> 4, ch = x & 15;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (row < n)
-            v = __ldg(reinterpret_cast<const uint4*>(p.q + ((long long)rq.q0 * H + r0 + row) * kHeadDim) + ch);
+    } else if (warp >= 16 - kLoaders) {
+      // ---------------------------------------------- queries; e4m3 keys to f16
+      const int lt = tid - (16 - kLoaders) * 32;
+      int n0 = 0, x0 = 0;
+      bool ok = true;
+      for (;;) {
+        ok = warp_wait(&info_full[n0 % kInfos], (n0 / kInfos) & 1);
+        if (!ok || (info[n0 % kInfos].flags & kEnd)) break;
+        const int nblk = info[n0 % kInfos].nblk, q0 = info[n0 % kInfos].q0;
+        const int rows = info[n0 % kInfos].qlen * H;
+        const int chunks = (rows + QR - 1) / QR;
+        const bool resident = chunks <= 2;
+        const uint16_t* qsrc = p.q + (long long)q0 * H * kHeadDim;
+        const float* lsrc = p.lse + (long long)q0 * H;
+        for (int g = 0; ok && g < nblk; g += 2) {
+          if constexpr (!FP8) {
+            for (int b = 0; ok && b < min(2, nblk - g); ++b) {
+              const int n = n0 + g + b;
+              ok = warp_wait(&info_full[n % kInfos], (n / kInfos) & 1);
+              if (ok && lane == 0) mbar_arrive(&k_empty[n % C::kTiles]);
+            }
+          }
           if constexpr (FP8) {
-            v.x = pack_f16x2(bf16lo(v.x), bf16hi(v.x));
-            v.y = pack_f16x2(bf16lo(v.y), bf16hi(v.y));
-            v.z = pack_f16x2(bf16lo(v.z), bf16hi(v.z));
-            v.w = pack_f16x2(bf16lo(v.w), bf16hi(v.w));
-          }
-          *reinterpret_cast<uint4*>(smem + C::kSmQ + (ch >> 3) * (kQRows * 128) + row * 128 +
-                                    (((ch & 7) ^ (row & 7)) << 4)) = v;
-        }
-        if (tid < kQRows) {
-          // a row that saw nothing (lse -inf) or lies past the end gives nothing
-          const float l = tid < n ? __ldg(p.lse + (long long)rq.q0 * H + r0 + tid) : -INFINITY;
-          s_lse[tid] = l == -INFINITY ? INFINITY : l * kTreeLog2e;
-        }
-        __syncthreads();
-        for (int u = 0; u < (n + 7) / 8; ++u) {
-          float s[4] = {0.f, 0.f, 0.f, 0.f};
-          const int row = 8 * u + (FP8 ? g : (lane & 7));
-          if constexpr (FP8) {
-            const uint8_t* qr = smem + C::kSmQ + (c >> 1) * (kQRows * 128) + row * 128;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint4 v = lds128(qr + (((4 * (c & 1) + x) ^ (row & 7)) << 4));
-              mma16816<true>(s, ka[2 * x], v.x, v.y);
-              mma16816<true>(s, ka[2 * x + 1], v.z, v.w);
-            }
-          } else {
-#pragma unroll
-            for (int kp = 0; kp < 4; ++kp) {
-              uint32_t v[4];
-              const int ch = 4 * kp + (lane >> 3);
-              ldsm4(q_s + (ch >> 3) * (kQRows * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), v);
-              mma16816<false>(s, ka[2 * kp], v[0], v[1]);
-              mma16816<false>(s, ka[2 * kp + 1], v[2], v[3]);
+            for (int b = 0; ok && b < min(2, nblk - g); ++b) {
+              const int n = n0 + g + b, s = n % C::kTiles, rs = n % C::kRaws;
+              ok = warp_wait(&raw_full[rs], (n / C::kRaws) & 1);
+              if (n >= C::kTiles) ok = ok && warp_wait(&k_empty[s], ((n / C::kTiles) - 1) & 1);
+              if (!ok) break;
+              const uint8_t* raw = smem + C::kSmRaw + rs * kRaw;
+              uint8_t* kt = smem + C::kSmK + s * kTile;
+#pragma unroll 4
+              for (int i = lt; i < kRaw / 16; i += kLoaders * 32) {
+                const int row = i >> 3, ch = 2 * (i & 7);  // 16 codes: f16 chunks ch, ch + 1
+                const uint4 v = lds128(raw + 16 * i);
+                uint8_t* dst = kt + (ch >> 3) * kHalf + row * 128;
+                *reinterpret_cast<uint4*>(dst + (((ch & 7) ^ (row & 7)) << 4)) =
+                    make_uint4(e4m3x2_to_f16x2((uint16_t)v.x), e4m3x2_to_f16x2((uint16_t)(v.x >> 16)),
+                               e4m3x2_to_f16x2((uint16_t)v.y), e4m3x2_to_f16x2((uint16_t)(v.y >> 16)));
+                *reinterpret_cast<uint4*>(dst + ((((ch & 7) + 1) ^ (row & 7)) << 4)) =
+                    make_uint4(e4m3x2_to_f16x2((uint16_t)v.z), e4m3x2_to_f16x2((uint16_t)(v.z >> 16)),
+                               e4m3x2_to_f16x2((uint16_t)v.w), e4m3x2_to_f16x2((uint16_t)(v.w >> 16)));
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive(&k_full[s]);
+                mbar_arrive(&raw_empty[rs]);
+              }
             }
           }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int m = 8 * u + 2 * c + e;
-            const float l = s_lse[m];
-            uint32_t vis = 0xffffu;
-            if (l == INFINITY) {
-              vis = 0;
-            } else if (mixed) {
-              const int j = (r0 + m) / H;
-              vis = tree_vis16(p, rq.q0 + j, j, rq.ctx, rq.qlen, t0, tree_row_selects(sel, j));
+          for (int c = 0; ok && c < chunks && (g == 0 || !resident); ++c) {
+            const int x = x0 + (resident ? c : (g >> 1) * chunks + c), qb = x & 1;
+            if (x >= 2) ok = ok && warp_wait(&q_empty[qb], ((x >> 1) - 1) & 1);
+            if (!ok) break;
+            const int r0 = c * QR, nr = min(QR, rows - r0), n16 = (nr + 15) / 16 * 16;
+            uint8_t* qd = smem + C::kSmQ + qb * C::kQBuf;
+#pragma unroll 4
+            for (int i = lt; i < n16 * 16; i += kLoaders * 32) {
+              const int row = i >> 4, ch = i & 15;
+              uint4 v = make_uint4(0u, 0u, 0u, 0u);  // rows past the end give S = 0
+              if (row < nr) v = __ldg(reinterpret_cast<const uint4*>(qsrc + (long long)(r0 + row) * kHeadDim) + ch);
+              if constexpr (FP8) {
+                v.x = pack_f16x2(bf16lo(v.x), bf16hi(v.x));
+                v.y = pack_f16x2(bf16lo(v.y), bf16hi(v.y));
+                v.z = pack_f16x2(bf16lo(v.z), bf16hi(v.z));
+                v.w = pack_f16x2(bf16lo(v.w), bf16hi(v.w));
+              }
+              *reinterpret_cast<uint4*>(qd + (ch >> 3) * (QR * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = v;
             }
-            const float p0 = exp2f(fmaf(s[e], f[0], -l)), p1 = exp2f(fmaf(s[2 + e], f[1], -l));
-            acc[0] += (vis >> g) & 1u ? p0 : 0.f;
-            acc[1] += (vis >> (g + 8)) & 1u ? p1 : 0.f;
+            float* nl = reinterpret_cast<float*>(smem + C::kSmNl) + qb * QR;
+            for (int i = lt; i < min(QR, (nr + 31) / 32 * 32); i += kLoaders * 32) {
+              // a row that saw nothing (lse -inf) or lies past the end gives 2^-inf = 0
+              const float l = i < nr ? __ldg(lsrc + r0 + i) : -INFINITY;
+              nl[i] = l == -INFINITY ? -INFINITY : -l * kTreeLog2e;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[qb]);
           }
         }
+        if (!ok) break;
+        x0 += resident ? chunks : (nblk + 1) / 2 * chunks;
+        n0 += nblk;
       }
+      if (!ok) misc[0] = 1;
+    } else if (warp >= 4) {
+      // ---------------------------------------------- sums
+      const int w = (warp - 4) >> 2, quarter = warp & 3;
+      const int tok = quarter * 32 + lane;  // token of the block = tensor-memory lane
+      const uint32_t da = tmem + ((uint32_t)(quarter * 32) << 16) + 256 * w;
+      float scale2 = p.softmax_scale * kTreeLog2e;
+      if (p.scale_mode == MSA_SCALE_SCALAR) scale2 *= __ldg(p.k_scale);
+      int n0 = 0, x0 = 0, step = 0;
+      bool ok = true;
+      for (;;) {
+        ok = warp_wait(&info_full[n0 % kInfos], (n0 / kInfos) & 1);
+        if (!ok || (info[n0 % kInfos].flags & kEnd)) break;
+        const int nblk = info[n0 % kInfos].nblk, qlen = info[n0 % kInfos].qlen;
+        const int q0 = info[n0 % kInfos].q0, ctx = info[n0 % kInfos].ctx;
+        const int rows = qlen * H, chunks = (rows + QR - 1) / QR;
+        const bool resident = chunks <= 2;
+        for (int g = 0; ok && g < nblk; g += 2) {
+          const bool have = g + w < nblk, last = g + 2 >= nblk;
+          int fl = 0, t = 0;
+          const uint32_t* sel = nullptr;
+          float* slot = nullptr;
+          float f = scale2, old = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+          if (have) {
+            const int n = n0 + g + w;
+            ok = warp_wait(&info_full[n % kInfos], (n / kInfos) & 1);
+            if (!ok) break;
+            const MassInfo& mi = info[n % kInfos];
+            fl = mi.flags;
+            t = mi.t0 + tok;
+            sel = mi.rows;
+            const long long at = (long long)mi.page * kBlock + tok;
+            slot = p.mass + at;
+            if (p.scale_mode == MSA_SCALE_PER_TOKEN_HEAD) f *= __ldg(p.k_scale + at);
+            if (t < ctx) old = *slot;
+          }
+          for (int c = 0; ok && c < chunks; ++c) {
+            const int x = x0 + (resident ? c : (g >> 1) * chunks + c), qb = x & 1;
+            ok = warp_wait(&q_full[qb], (x >> 1) & 1);
+            if (have) {
+              ok = ok && warp_wait(&d_full[w], step & 1);
+              if (!ok) break;
+              ++step;
+              tc::fence_after();
+              const int nr = min(QR, rows - c * QR);
+              const float* nl = reinterpret_cast<const float*>(smem + C::kSmNl) + qb * QR;
+              if (!(fl & kMixed)) {
+                // columns past the end: S = 0 (or, behind the last 16, what an
+                // earlier product left) and nl = -inf; full pairs of loads
+                // while they last
+                int k = 0;
+                if constexpr (QR >= 64) {
+                  for (; k + 64 <= nr; k += 64) {
+                    uint32_t ra[32], rb[32];
+                    tc::tmem_ld32_issue(da + k, ra);
+                    tc::tmem_ld32_issue(da + k + 32, rb);
+                    tc::tmem_wait_ld(ra);
+                    tc::tmem_wait_ld(rb);
+                    add_exp32(ra, f, nl + k, acc);
+                    add_exp32(rb, f, nl + k + 32, acc);
+                  }
+                }
+                for (; k < nr; k += 16) {
+                  uint32_t r[16];
+                  tc::tmem_ld16(da + k, r);
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        acc[hh] += __shfl_xor_sync(0xffffffffu, acc[hh], 1);
-        acc[hh] += __shfl_xor_sync(0xffffffffu, acc[hh], 2);
-        const int t = t0 + g + 8 * hh;
-        if (c == 0 && t < seq) {
-          float* m = p.mass + slot + g + 8 * hh;
-          *m = t < rq.ctx ? *m + acc[hh] : acc[hh];
+                  for (int i = 0; i < 16; i += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(nl + k + i);
+                    float a = __uint_as_float(r[i]), b = __uint_as_float(r[i + 1]);
+                    float d = __uint_as_float(r[i + 2]), e = __uint_as_float(r[i + 3]);
+                    fma2v(a, b, f, v.x, v.y);
+                    fma2v(d, e, f, v.z, v.w);
+                    add2(acc[0], acc[1], ex2_ftz(a), ex2_ftz(b));
+                    add2(acc[2], acc[3], ex2_ftz(d), ex2_ftz(e));
+                  }
+                }
+              } else {
+                for (int k = 0; k < nr; k += 16) {
+                  uint32_t r[16];
+                  tc::tmem_ld16(da + k, r);
+                  int j = (c * QR + k) / H, h = (c * QR + k) % H;
+                  bool vis = tree_vis_token(p, q0 + j, j, ctx, qlen, t, sel);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) {
+                    const float e = ex2_ftz(fmaf(__uint_as_float(r[i]), f, nl[k + i]));
+                    if (k + i < nr && vis && nl[k + i] != -INFINITY) acc[i & 3] += e;
+                    if (++h == H) {
+                      h = 0;
+                      ++j;
+                      vis = j < qlen && tree_vis_token(p, q0 + j, j, ctx, qlen, t, sel);
+                    }
+                  }
+                  __syncwarp();
+                }
+              }
+              tc::fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&d_empty[w]);
+            }
+            if (!ok) break;
+            __syncwarp();
+            if (lane == 0 && (!resident || last)) mbar_arrive(&q_empty[qb]);
+          }
+          // (a masked token of the block's rows that no row sees adds nothing)
+          if (ok && have && t < ctx + qlen) {
+            const float s = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+            *slot = t < ctx ? old + s : s;
+          }
         }
+        if (!ok) break;
+        x0 += resident ? chunks : (nblk + 1) / 2 * chunks;
+        n0 += nblk;
       }
+      if (!ok) misc[0] = 1;
     }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (misc[0] && tid == 0) atomicOr(p.status, MSA_DEV_TIMEOUT);
+  if (warp == 1) {
+    tc::fence_after();
+    tc::tmem_dealloc(tmem, 512);
   }
 }
 
-template <bool FP8>
+template <bool FP8, int QR>
 cudaError_t launch_mass(const TreeLaunch& p, cudaStream_t stream) {
-  using C = MassCfg<FP8>;
+  using C = MassCfg<FP8, QR>;
   CUtensorMap kmap;
-  const CUtensorMapDataType t = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  if (!encode_map_2d(&kmap, t, p.k, kHeadDim, max(1ll, (long long)p.batch.num_pages) * kBlock,
-                     kHeadDim * (FP8 ? 1 : 2), FP8 ? 128 : 64, kBlock))
+  memset(&kmap, 0, sizeof(kmap));
+  if (!FP8 && !encode_map_2d(&kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.k, kHeadDim,
+                             max(1ll, (long long)p.batch.num_pages) * kBlock, kHeadDim * 2, 64, kBlock))
     return cudaErrorInvalidValue;
-  auto kern = attn_mass_kernel<FP8>;
+  auto kern = attn_mass_kernel<FP8, QR>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (e != cudaSuccess) return e;
-  kern<<<device_sm_count() * (FP8 ? 4 : 3), kMaThreads, C::kBytes, stream>>>(p, kmap);
+  kern<<<device_sm_count(), kThreads, C::kBytes, stream>>>(p, kmap);
   return cudaGetLastError();
+}
+
+template <bool FP8>
+cudaError_t launch_rows(const TreeLaunch& p, cudaStream_t stream) {
+  // rows of a chunk: few rows leave the shared memory to the stream of keys
+  const int rows = p.max_rows * p.num_heads;
+  if (rows <= 16) return launch_mass<FP8, 16>(p, stream);
+  if (rows <= 128) return launch_mass<FP8, 64>(p, stream);
+  return launch_mass<FP8, 256>(p, stream);
 }
 
 }  // namespace
@@ -252,7 +521,7 @@ cudaError_t launch_attn_mass(const TreeLaunch& p, cudaStream_t stream) {
     const cudaError_t e = launch_tree_plan(p, stream);
     if (e != cudaSuccess) return e;
   }
-  return p.kv_fp8 ? launch_mass<true>(p, stream) : launch_mass<false>(p, stream);
+  return p.kv_fp8 ? launch_rows<true>(p, stream) : launch_rows<false>(p, stream);
 }
 
 }  // namespace msa

@@ -118,20 +118,6 @@ __device__ __forceinline__ float row_max(uint32_t sa, const uint32_t (&vis)[4]) 
   return max32<NEG, MASKED>(rb, g, vis[3]);
 }
 
-// two products a * b + c in one instruction
-__device__ __forceinline__ void fma2(float& x0, float& x1, float b, float c) {
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
-      "mov.b64 z, {%3, %3};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "+f"(x0), "+f"(x1)
-      : "f"(b), "f"(c));
-}
-__device__ __forceinline__ void add2(float& x0, float& x1, float a0, float a1) {
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
-      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "+f"(x0), "+f"(x1)
-      : "f"(a0), "f"(a1));
-}
-
 // P = 2^(s * scale2 - m) of 32 columns as bf16 pairs; their fp32 sum onto l
 template <bool MASKED>
 __device__ __forceinline__ void exp32(uint32_t (&r)[32], float scale2, float neg_m, uint32_t vis,

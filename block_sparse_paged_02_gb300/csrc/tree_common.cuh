@@ -158,6 +158,28 @@ __device__ __forceinline__ float ex2_ftz(float x) {
   return y;
 }
 
+// two products a * b + c in one instruction
+__device__ __forceinline__ void fma2(float& x0, float& x1, float b, float c) {
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
+      "mov.b64 z, {%3, %3};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float& x0, float& x1, float a0, float a1) {
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(a0), "f"(a1));
+}
+
+// the same with an addend for each
+__device__ __forceinline__ void fma2v(float& x0, float& x1, float b, float c0, float c1) {
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
+      "mov.b64 z, {%3, %4};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(b), "f"(c0), "f"(c1));
+}
+
 // A row's end: (m, l) in log2 units, the sink joined in
 struct TreeRowEnd {
   float f, lse;  // factor of the accumulators, natural-log lse
@@ -263,6 +285,17 @@ static __device__ __noinline__ void tree_slow_row(const TreeLaunch& p, int q, in
   if (none) w = make_uint2(0u, 0u);
   *reinterpret_cast<uint2*>(p.out + r * kHeadDim + 4 * lane) = w;
   if (lane == 0) p.lse[r] = none ? (p.sinks ? sink : -INFINITY) : e.lse;
+}
+
+// The visibility of one token at position t to row j (sel: the block's
+// selection bits, NULL when every row reads its cached tokens)
+__device__ __forceinline__ bool tree_vis_token(const TreeLaunch& p, int row, int j, int ctx, int qlen,
+                                               int t, const uint32_t* sel) {
+  if (t < ctx) return tree_row_selects(sel, j);
+  const int i = t - ctx;
+  if (i >= qlen) return false;
+  if (!p.mask) return i <= j;
+  return (__ldg(p.mask + (long long)row * p.mask_words + (i >> 5)) >> (i & 31)) & 1u;
 }
 
 // Items of a request: its tiles of drafted tokens times its visited blocks

@@ -261,6 +261,59 @@ def test_same_bits_twice_on_another_stream_and_in_a_graph():
     again(g.replay)
 
 
+@pytest.mark.parametrize("kv", [BF, F8])
+@pytest.mark.parametrize("hq,q_lens", [(16, [1, 1, 1]), (8, [12, 5, 1]), (16, [40, 1, 24]), (16, [20, 70, 3])])
+def test_long_slices(kv, hq, q_lens):
+    # dozens of blocks per CTA, so that every ring goes round many times (reference in 64 bits
+    # on the GPU; bounds as in tree_ref, with its terms bounded over all tokens)
+    from block_sparse_paged_02_gb300 import binding as B
+    ctxs = [250001, 300000, 170100]
+    g = torch.Generator("cuda").manual_seed(5)
+    seqs = [x + y for x, y in zip(ctxs, q_lens)]
+    nb = [(n + 127) // 128 for n in seqs]
+    pages, n = sum(nb), sum(q_lens)
+    perm = torch.randperm(pages, generator=g, device="cuda").int()
+    bt = torch.full((3, max(nb)), -1, dtype=torch.int32, device="cuda")
+    for r in range(3):
+        bt[r, :nb[r]] = perm[sum(nb[:r]):sum(nb[:r + 1])]
+    k, v = (torch.randn((pages, 128, 1, 128), generator=g, device="cuda") for _ in range(2))
+    k, v = (x.to(torch.float8_e4m3fn if kv == F8 else torch.bfloat16) for x in (k, v))
+    q = (2 * torch.randn((n, hq, 128), generator=g, device="cuda")).to(torch.bfloat16)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    cu = np.concatenate([[0], np.cumsum(q_lens)])
+    batch = B.make_batch(i32(cu.tolist()), i32(np.concatenate([[0], np.cumsum(seqs)]).tolist()), i32(ctxs), bt, pages, n,
+                         max_q_len=max(q_lens))
+    out, lse = torch.zeros((n, hq, 128), dtype=torch.bfloat16, device="cuda"), torch.zeros((n, hq), device="cuda")
+    raw = (lambda x: x.view(torch.uint8)) if kv == F8 else (lambda x: x)
+    attn = B.make_attn_args(q, raw(k), raw(v), kv, pages, out, lse, softmax_scale=0.0883)
+    ws = torch.empty((B.msa_tree_attn_workspace_size(3, n, bt.shape[1], hq, max(q_lens)),), dtype=torch.uint8, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tree = B.make_tree()
+    mass = torch.ones((pages, 128), device="cuda")
+    B.msa_tree_attn(batch, tree, attn, ws, st)
+    B.msa_attn_mass(batch, tree, attn, mass, ws, st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    for r in range(3):
+        at = bt[r, :nb[r]].long()
+        kk, vv = (x[at].view(-1, 128)[:seqs[r]].double() for x in (k, v))
+        got = torch.zeros(seqs[r], dtype=torch.float64, device="cuda")
+        for j in range(q_lens[r]):
+            row, end = int(cu[r]) + j, ctxs[r] + j + 1
+            z = 0.0883 * q[row].double() @ kk[:end].T
+            ref = torch.logsumexp(z, 1)
+            p = torch.exp(z - ref[:, None])
+            o, a = p @ vv[:end], p @ vv[:end].abs()
+            d = 130 * 2.0 ** -23 * 0.0883 * float((q[row].double().abs() @ kk[:4096].abs().T).max()) * 1.5
+            assert ((out[row].double() - o).abs() <= (2.0 ** -8 + 2 * d + 1e-4) * a + 2.0 ** -8 * o.abs()).all()
+            assert ((lse[row].double() - ref).abs() <= d + 1e-4).all()
+            got[:end] += torch.exp(z - lse[row].double()[:, None]).sum(0)
+        m = mass[at].view(-1)[:seqs[r]].double()
+        want = got + (torch.arange(seqs[r], device="cuda") < ctxs[r])
+        # near 1 the stored sum rounds by 2^-24; the weights themselves by 2 d and 2^-21 |s|
+        assert ((m - want).abs() <= (2 * d + 2.0 ** -21 * 60 + q_lens[r] * hq * 2.0 ** -24) * got + 2.0 ** -23 * want).all()
+
+
 def test_offsets_past_32_bits():
     # pools of more than 2^32 bytes: pages near their end
     from block_sparse_paged_02_gb300 import binding as B
