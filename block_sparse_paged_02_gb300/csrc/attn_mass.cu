@@ -70,11 +70,11 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
 // keys, or its products and exponentials
 __device__ __forceinline__ long long mass_weight(int rows) { return max(20, (rows + 15) / 16); }
 
-// sum over 32 columns of 2^(s * f + nl) onto acc
-__device__ __forceinline__ void add_exp32(const uint32_t (&r)[32], float f, const float* nl,
+// sum over 64 columns of 2^(s * f + nl) onto acc
+__device__ __forceinline__ void add_exp64(const uint32_t (&r)[64], float f, const float* nl,
                                           float (&acc)[4]) {
 #pragma unroll
-  for (int t = 0; t < 32; t += 4) {
+  for (int t = 0; t < 64; t += 4) {
     const float4 n = *reinterpret_cast<const float4*>(nl + t);
     float a = __uint_as_float(r[t]), b = __uint_as_float(r[t + 1]);
     float c = __uint_as_float(r[t + 2]), d = __uint_as_float(r[t + 3]);
@@ -418,13 +418,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int k = 0;
                 if constexpr (QR >= 64) {
                   for (; k + 64 <= nr; k += 64) {
-                    uint32_t ra[32], rb[32];
-                    tc::tmem_ld32_issue(da + k, ra);
-                    tc::tmem_ld32_issue(da + k + 32, rb);
-                    tc::tmem_wait_ld(ra);
-                    tc::tmem_wait_ld(rb);
-                    add_exp32(ra, f, nl + k, acc);
-                    add_exp32(rb, f, nl + k + 32, acc);
+                    uint32_t r[64];
+                    tc::tmem_ld64(da + k, r);
+                    add_exp64(r, f, nl + k, acc);
                   }
                 }
                 for (; k < nr; k += 16) {

@@ -988,7 +988,7 @@ cudaError_t launch_tree_attn(const TreeLaunch& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   const bool pth = p.scale_mode == MSA_SCALE_PER_TOKEN_HEAD;
-  if (!p.kv_fp8 && !pth && tree_tile_rows(p.max_rows, p.num_heads) == 128) {
+  if ((p.kv_fp8 || !pth) && tree_tile_rows(p.max_rows, p.num_heads) == 128) {
     const int grid = min(device_sm_count(), kMaxMainCtas);
     const cudaError_t e = launch_tree_attn_tc(p, grid, stream);
     return e != cudaSuccess ? e : launch_merge(p, grid, 256, stream);

@@ -1,5 +1,5 @@
 // tree_attn_tc.cu -- the draft-tree attention for wide trees (more than 64
-// rows x heads per request, bf16 pools) on the 5th-generation tensor cores.
+// rows x heads per request) on the 5th-generation tensor cores.
 //
 // Same mathematics, split and partials as tree_attn.cu.  A request's rows are
 // cut into pairs of 128-row tiles; a CTA loads each visited block's K and V
@@ -15,7 +15,10 @@
 // the products of tile 0 and tile 1 (an instruction takes its thread ~100
 // cycles, more than the 64 that it keeps the pipe busy, so one issuer would
 // bound the kernel), warps 4-7 and 8-11 are the tiles' softmax.  Tensor memory
-// (512 columns): S / P and O of both tiles.
+// (512 columns): S / P and O of both tiles.  With e4m3 pools warps 12-15 turn the
+// tiles into f16 (exact) and the products run in f16; a scale per token joins the
+// logits and P in the softmax.  (bf16 pools with a scale per token stay on
+// tree_attn.cu.)
 //
 // A block that not every row sees whole (the drafted tokens, the context's
 // end, selected blocks) takes a masked softmax, and its V is looked over: a
@@ -30,15 +33,10 @@
 namespace msa {
 namespace {
 
-constexpr int kThreads = 384;
 constexpr int kHalf = 128 * 128;  // 128 rows x 128 B: one swizzle-atom column of a tile
 constexpr int kTile = 2 * kHalf;  // 128 x 128 bf16
-constexpr int kBufs = 5;          // ring of K and V tiles, alternating
+constexpr int kRaw = 128 * 128;   // 128 x 128 e4m3
 constexpr int kInfos = 8;
-constexpr int kSmKv = 0;
-constexpr int kSmQ = kBufs * kTile;
-constexpr int kSmInfo = kSmQ + 2 * kTile;
-
 // flags of a block
 constexpr int kFirst = 1, kLast = 2, kWhole = 4, kNoData = 8, kBadPage = 16, kPoison = 32,
               kEnd = 64, kMixed = 128, kTwo = 256;
@@ -50,24 +48,37 @@ struct BlockInfo {
   int t0;              // position of the block's first token
   int slot, q;
   uint32_t bad;
-  int pad;
+  int page;
   const uint32_t* rows;
 };
 
-// kv full / empty, q full / empty, info full; per tile: s_full, p_full,
-// pv_done, o_free; fill, ends
-constexpr int kNumBars = 2 * kBufs + 2 + kInfos + 8 + 2;
-constexpr int kSmBars = kSmInfo + kInfos * (int)sizeof(BlockInfo);
-constexpr int kSmMisc = kSmBars + kNumBars * 8;
-constexpr int kBytes = kSmMisc + 64;
-static_assert(kBytes <= 227 * 1024, "shared memory");
-static_assert(sizeof(BlockInfo) % 8 == 0 && kSmBars % 8 == 0, "alignment");
+constexpr int kScales = 4;  // blocks whose scales are held
+constexpr int kConv = 4;    // converting warps (e4m3 pools)
+
+template <bool FP8, bool PTH>
+struct TcCfg {
+  // (e4m3: 512 threads, 128 registers each; else 384, 168)
+  static constexpr int kThreads = FP8 ? 512 : 384;
+  static constexpr int kBufs = FP8 ? 3 : 5;  // ring of 16-bit K and V tiles, alternating
+  static constexpr int kRaws = FP8 ? 3 : 0;  // ring of e4m3 tiles
+  static constexpr int kSmKv = 0;
+  static constexpr int kSmQ = kBufs * kTile;
+  static constexpr int kSmRaw = kSmQ + 2 * kTile;
+  static constexpr int kSmScale = kSmRaw + kRaws * kRaw;  // [kScales][2][128], then maxima [4]
+  static constexpr int kSmInfo = kSmScale + (PTH ? kScales * (2 * 128 + 4) * 4 : 0);
+  static constexpr int kSmBars = kSmInfo + kInfos * (int)sizeof(BlockInfo);
+  // kv full / empty, raw full / empty, q full / empty, info full, scales full;
+  // per tile: s_full, p_full, pv_done, o_free; fill, ends
+  static constexpr int kNumBars = 2 * kBufs + 2 * kRaws + 2 + kInfos + kScales + 8 + 2;
+  static constexpr int kSmMisc = kSmBars + kNumBars * 8;
+  static constexpr int kBytes = kSmMisc + 64;
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+  static_assert(sizeof(BlockInfo) % 8 == 0 && kSmBars % 8 == 0, "alignment");
+};
 
 constexpr uint32_t kTmemCols = 512;
 __device__ __forceinline__ uint32_t col_s(int t) { return 128u * t; }
 __device__ __forceinline__ uint32_t col_o(int t) { return 256u + 128u * t; }
-constexpr uint32_t kIdescS = tc::idesc_bf16(128, 128, 0);
-constexpr uint32_t kIdescO = tc::idesc_bf16(128, 128, 1);
 constexpr float kSlack = 8.f;
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
@@ -79,106 +90,118 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
-// largest of 32 raw logits and acc (of their negations when NEG), those with
-// a set bit only when MASKED
-template <bool NEG, bool MASKED>
-__device__ __forceinline__ float max32(const uint32_t (&r)[32], float acc, uint32_t vis) {
+// largest of 64 logits and acc (of their negations when NEG), those with a set
+// bit only when MASKED, each times its token's factor ks when PTH
+template <bool NEG, bool MASKED, bool PTH>
+__device__ __forceinline__ float max64(const uint32_t (&r)[64], float acc, uint32_t vis0,
+                                       uint32_t vis1, const float* ks) {
   float g[4] = {acc, acc, acc, acc};
 #pragma unroll
-  for (int t = 0; t < 32; t += 2) {
+  for (int t = 0; t < 64; t += 2) {
     float a = __uint_as_float(r[t]), b = __uint_as_float(r[t + 1]);
+    if (PTH) {
+      const float2 k = *reinterpret_cast<const float2*>(ks + t);
+      mul2v(a, b, k.x, k.y);
+    }
     if (NEG) {
       a = -a;
       b = -b;
     }
     if (MASKED) {
-      a = (vis >> t) & 1u ? a : -INFINITY;
-      b = (vis >> (t + 1)) & 1u ? b : -INFINITY;
+      const uint32_t vis = t < 32 ? vis0 : vis1;
+      a = (vis >> (t & 31)) & 1u ? a : -INFINITY;
+      b = (vis >> ((t + 1) & 31)) & 1u ? b : -INFINITY;
     }
     g[(t >> 1) & 3] = fmax3(g[(t >> 1) & 3], a, b);
   }
   return fmaxf(fmax3(g[0], g[1], g[2]), g[3]);
 }
 
-template <bool NEG, bool MASKED>
-__device__ __forceinline__ float row_max(uint32_t sa, const uint32_t (&vis)[4]) {
-  uint32_t ra[32], rb[32];
-  float g = -INFINITY;
-  tc::tmem_ld32_issue(sa, ra);
-  tc::tmem_ld32_issue(sa + 32, rb);
-  tc::tmem_wait_ld(ra);
-  tc::tmem_wait_ld(rb);
-  g = max32<NEG, MASKED>(ra, g, vis[0]);
-  tc::tmem_ld32_issue(sa + 64, ra);
-  g = max32<NEG, MASKED>(rb, g, vis[1]);
-  tc::tmem_ld32_issue(sa + 96, rb);
-  tc::tmem_wait_ld(ra);
-  tc::tmem_wait_ld(rb);
-  g = max32<NEG, MASKED>(ra, g, vis[2]);
-  return max32<NEG, MASKED>(rb, g, vis[3]);
+template <bool NEG, bool MASKED, bool PTH>
+__device__ __forceinline__ float row_max(uint32_t sa, const uint32_t (&vis)[4], const float* ks) {
+  uint32_t r[64];
+  tc::tmem_ld64(sa, r);
+  const float g = max64<NEG, MASKED, PTH>(r, -INFINITY, vis[0], vis[1], ks);
+  tc::tmem_ld64(sa + 64, r);
+  return max64<NEG, MASKED, PTH>(r, g, vis[2], vis[3], ks + 64);
 }
 
-// P = 2^(s * scale2 - m) of 32 columns as bf16 pairs; their fp32 sum onto l
-template <bool MASKED>
-__device__ __forceinline__ void exp32(uint32_t (&r)[32], float scale2, float neg_m, uint32_t vis,
-                                      uint32_t (&w)[16], float (&l)[4]) {
-#pragma unroll
-  for (int t = 0; t < 32; t += 2) {
-    float a = __uint_as_float(r[t]), b = __uint_as_float(r[t + 1]);
-    fma2(a, b, scale2, neg_m);
-    a = ex2_ftz(a);
-    b = ex2_ftz(b);
-    if (MASKED) {
-      a = (vis >> t) & 1u ? a : 0.f;
-      b = (vis >> (t + 1)) & 1u ? b : 0.f;
-    }
-    add2(l[t & 2], l[(t & 2) + 1], a, b);
-    w[t >> 1] = pack_bf16x2(a, b);
-  }
-}
-
-template <bool MASKED>
+// P = 2^(s * scale2 - m) of the 128 columns at sa as 16-bit pairs over the first
+// 64 of them (with PTH the token's ks in the place of scale2, and P times its
+// vs); returns the fp32 sum of the 2^...
+template <bool MASKED, bool FP8, bool PTH>
 __device__ __forceinline__ float row_exp(uint32_t sa, float scale2, float m,
-                                         const uint32_t (&vis)[4]) {
-  uint32_t ra[32], rb[32], w[16];
+                                         const uint32_t (&vis)[4], const float* ks,
+                                         const float* vs) {
   float l[4] = {0.f, 0.f, 0.f, 0.f};
-  tc::tmem_ld32_issue(sa, ra);
-  tc::tmem_wait_ld(ra);
-  tc::tmem_ld32_issue(sa + 32, rb);
-  exp32<MASKED>(ra, scale2, -m, vis[0], w, l);
-  tc::tmem_wait_ld(rb);
-  tc::tmem_st16(sa, w);
-  tc::tmem_ld32_issue(sa + 64, ra);
-  exp32<MASKED>(rb, scale2, -m, vis[1], w, l);
-  tc::tmem_wait_ld(ra);
-  tc::tmem_st16(sa + 16, w);
-  tc::tmem_ld32_issue(sa + 96, rb);
-  exp32<MASKED>(ra, scale2, -m, vis[2], w, l);
-  tc::tmem_wait_ld(rb);
-  tc::tmem_st16(sa + 32, w);
-  exp32<MASKED>(rb, scale2, -m, vis[3], w, l);
-  tc::tmem_st16(sa + 48, w);
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t r[64];
+    tc::tmem_ld64(sa + 64 * half, r);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const int t = 64 * half + 32 * q + i;
+        float a = __uint_as_float(r[32 * q + i]), b = __uint_as_float(r[32 * q + i + 1]);
+        if (PTH) {
+          const float2 k = *reinterpret_cast<const float2*>(ks + t);
+          fma2p(a, b, k.x, k.y, -m);
+        } else {
+          fma2(a, b, scale2, -m);
+        }
+        a = ex2_ftz(a);
+        b = ex2_ftz(b);
+        const uint32_t v = MASKED ? vis[2 * half + q] : 0u;
+        if (MASKED) {
+          a = (v >> i) & 1u ? a : 0.f;
+          b = (v >> (i + 1)) & 1u ? b : 0.f;
+        }
+        add2(l[i & 2], l[(i & 2) + 1], a, b);
+        if (PTH) {
+          const float2 x = *reinterpret_cast<const float2*>(vs + t);
+          mul2v(a, b, x.x, x.y);
+          if (MASKED) {  // (the scale of a token that the row does not see may be anything)
+            a = (v >> i) & 1u ? a : 0.f;
+            b = (v >> (i + 1)) & 1u ? b : 0.f;
+          }
+        }
+        w[i >> 1] = FP8 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+      }
+      tc::tmem_st16(sa + 32 * half + 16 * q, w);
+    }
+  }
   return (l[0] + l[1]) + (l[2] + l[3]);
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool FP8, bool PTH>
+__global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
     tree_attn_tc_kernel(const __grid_constant__ TreeLaunch p, const __grid_constant__ CUtensorMap qmap,
                         const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap) {
+  using C = TcCfg<FP8, PTH>;
+  constexpr int kBufs = C::kBufs, kRaws = C::kRaws, kThreads = C::kThreads;
+  constexpr int kSmKv = C::kSmKv, kSmQ = C::kSmQ;
+  constexpr uint32_t kIdescS = tc::idesc_16(128, 128, 0, FP8 ? 0 : 1);
+  constexpr uint32_t kIdescO = tc::idesc_16(128, 128, 1, FP8 ? 0 : 1);
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + kSmBars);
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::kSmBars);
   uint64_t* kv_empty = kv_full + kBufs;
-  uint64_t* q_full = kv_empty + kBufs;
+  uint64_t* raw_full = kv_empty + kBufs;
+  uint64_t* raw_empty = raw_full + kRaws;
+  uint64_t* q_full = raw_empty + kRaws;
   uint64_t* q_empty = q_full + 1;
   uint64_t* info_full = q_empty + 1;
-  uint64_t* s_full = info_full + kInfos;  // [2]
+  uint64_t* sc_full = info_full + kInfos;
+  uint64_t* s_full = sc_full + kScales;  // [2]
   uint64_t* p_full = s_full + 2;
   uint64_t* pv_done = p_full + 2;
   uint64_t* o_free = pv_done + 2;
   uint64_t* fill = o_free + 2;
   uint64_t* ends = fill + 1;
-  BlockInfo* info = reinterpret_cast<BlockInfo*>(smem + kSmInfo);
-  int* misc = reinterpret_cast<int*>(smem + kSmMisc);  // [0] timeout, [4..6] odd values seen
+  BlockInfo* info = reinterpret_cast<BlockInfo*>(smem + C::kSmInfo);
+  int* misc = reinterpret_cast<int*>(smem + C::kSmMisc);  // [0] timeout, [4..6] odd values seen
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 8);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int H = p.num_heads;
@@ -187,10 +210,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 8; ++i) misc[i] = 0;
     for (int s = 0; s < kBufs; ++s) {
-      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_full[s], FP8 ? kConv : 1);
       mbar_init(&kv_empty[s], 2);  // the two issuers
     }
-    mbar_init(q_full, 1);
+    for (int s = 0; s < kRaws; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], kConv);
+    }
+    for (int s = 0; s < kScales; ++s) mbar_init(&sc_full[s], kConv);
+    mbar_init(q_full, FP8 ? kConv : 1);
     mbar_init(q_empty, 2);
     for (int i = 0; i < kInfos; ++i) mbar_init(&info_full[i], 1);
     for (int t = 0; t < 2; ++t) {
@@ -227,8 +255,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       TreeSplit rec;
       rec.nrows = 0;
       auto acquire = [&]() -> int {
-        const int b = x % kBufs;
-        if (x >= kBufs) ok = ok && warp_wait(&kv_empty[b], ((x / kBufs) - 1) & 1);
+        constexpr int ring = FP8 ? kRaws : kBufs;
+        uint64_t* freed = FP8 ? raw_empty : kv_empty;
+        const int b = x % ring;
+        if (x >= ring) ok = ok && warp_wait(&freed[b], ((x / ring) - 1) & 1);
         ++x;
         return b;
       };
@@ -240,7 +270,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++n;
       };
       BlockInfo bi;
-      bi.pad = 0;
+      bi.page = 0;
+      // e4m3: a block's two tiles (none for pg < 0, which still takes its places in
+      // the ring, so that no block is announced far ahead of the other roles);
+      // announced with the first, as the second may have to wait for a place that
+      // the announced block's conversion frees
+      auto push = [&](BlockInfo& b, int pg) {
+        const uint8_t* src[2] = {p.k, p.v};
+        b.page = pg;
+        for (int kv = 0; kv < 2; ++kv) {
+          const int rb = acquire();
+          if (!ok) return;
+          if (lane == 0) {
+            if (pg < 0) {
+              mbar_arrive(&raw_full[rb]);
+            } else {
+              mbar_arrive_expect_tx(&raw_full[rb], kRaw);
+              bulk_g2s(smem + C::kSmRaw + rb * kRaw, src[kv] + (long long)pg * kRaw, kRaw, &raw_full[rb]);
+            }
+          }
+          if (kv == 0) announce(b);
+        }
+      };
       while (ok && it < sl.end) {
         TreeReq rq = tree_request(p, q);
         int nv = 0, tiles = 0;
@@ -274,10 +325,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           rec.last = (int)((e * sl.ctas - 1) / sl.total);
           rec.q = q;
         }
-        if (n_seg > 0) ok = warp_wait(q_empty, (n_seg - 1) & 1);
+        // (e4m3: the converting warps bring the queries, and pass over empty blocks)
+        if (!FP8 && n_seg > 0) ok = warp_wait(q_empty, (n_seg - 1) & 1);
         if (!ok) break;
         ++n_seg;
-        if (rq.bad) {
+        if (rq.bad && FP8) {
+          bi.flags = kFirst | kLast | kPoison | kNoData | kWhole | both;
+          bi.t0 = 0;
+          push(bi, -1);
+          if (!ok) break;
+        } else if (rq.bad) {
           bi.flags = kFirst | kLast | kPoison | kNoData | kWhole | both;
           bi.t0 = 0;
           const int kb = acquire(), vb = acquire();
@@ -288,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&kv_full[vb]);
           }
           announce(bi);
-        } else if (lane == 0) {
+        } else if (!FP8 && lane == 0) {
           mbar_arrive_expect_tx(q_full, (both & kTwo ? 2 : 1) * kTile);
           for (int t = 0; t < (both & kTwo ? 2 : 1); ++t)
             for (int h = 0; h < 2; ++h)
@@ -313,6 +370,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             bi.flags = both | (c0 + i == 0 ? kFirst : 0) | (c0 + i == nb - 1 ? kLast : 0) |
                        (bad_page ? kBadPage | kNoData : 0) |
                        (bi.t0 + kBlock > rq.ctx || !cached_all ? kMixed : 0);
+            if constexpr (FP8) {
+              if (bad_page && lane == 0) atomicOr(p.status, MSA_DEV_BAD_PAGE);
+              push(bi, bad_page ? -1 : pg);
+              continue;
+            }
             const int kb = acquire(), vb = acquire();
             if (!ok) break;
             uint8_t* kd = smem + kSmKv + kb * kTile;
@@ -361,8 +423,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         misc[0] = 1;
         // copies still in flight land before the CTA leaves
-        for (int i = max(0, x - kBufs); i < x; ++i) mbar_wait(&kv_full[i % kBufs], (i / kBufs) & 1);
-        if (n_seg > 0) mbar_wait(q_full, (n_seg - 1) & 1);
+        const int ring = FP8 ? kRaws : kBufs;
+        uint64_t* bars = FP8 ? raw_full : kv_full;
+        for (int i = max(0, x - ring); i < x; ++i) mbar_wait(&bars[i % ring], (i / ring) & 1);
+        if (!FP8 && n_seg > 0) mbar_wait(q_full, (n_seg - 1) & 1);
       }
       if (lane == 0) p.split[blockIdx.x] = rec;
     } else if (warp == 1 || warp == 2) {
@@ -429,7 +493,98 @@ __global__ void __launch_bounds__(kThreads, 1)
         // every product has completed before the tensor memory is freed
         if (done > 0 && !mbar_wait(&pv_done[t], (done - 1) & 1)) misc[0] = 1;
       }
-    } else if (warp >= 4) {
+    } else if (FP8 && warp >= 12) {
+      // ---------------------------------------------- e4m3 tiles to f16, queries
+      const int ct = tid - 12 * 32;
+      int x = 0, rx = 0, seg = -1;  // 16-bit tiles, e4m3 tiles, segments
+      bool ok = true;
+      for (int n = 0;; ++n) {
+        ok = warp_wait(&info_full[n % kInfos], (n / kInfos) & 1);
+        if (!ok) break;
+        const BlockInfo& bi = info[n % kInfos];
+        const int fl = bi.flags;
+        if (fl & kEnd) break;
+        if (fl & kFirst) {
+          ++seg;
+          if (seg > 0) ok = warp_wait(q_empty, (seg - 1) & 1);
+          if (!ok) break;
+          if (!(fl & kPoison)) {
+            const uint16_t* src = p.q + (long long)bi.row0 * H * kHeadDim;
+            const int rows = bi.ntok * H, per = tpt * H;
+#pragma unroll 4
+            for (int i = ct; i < 2 * 128 * 16; i += kConv * 32) {
+              const int t = i >> 11, m = (i >> 4) & 127, ch = i & 15, row = t * per + m;
+              uint4 v = make_uint4(0u, 0u, 0u, 0u);
+              if (m < per && row < rows)
+                v = __ldg(reinterpret_cast<const uint4*>(src + (long long)row * kHeadDim) + ch);
+              v.x = pack_f16x2(bf16lo(v.x), bf16hi(v.x));
+              v.y = pack_f16x2(bf16lo(v.y), bf16hi(v.y));
+              v.z = pack_f16x2(bf16lo(v.z), bf16hi(v.z));
+              v.w = pack_f16x2(bf16lo(v.w), bf16hi(v.w));
+              *reinterpret_cast<uint4*>(smem + kSmQ + t * kTile + (ch >> 3) * kHalf + m * 128 +
+                                        (((ch & 7) ^ (m & 7)) << 4)) = v;
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_full);
+        }
+        if constexpr (PTH) {
+          // the block's scales (a thread per token), k's with the softmax's own
+          float ks = 0.f, vs = 0.f;
+          if (!(fl & kNoData) && bi.t0 + ct < bi.seq) {
+            const long long at = (long long)bi.page * kBlock + ct;
+            ks = __ldg(p.k_scale + at) * (p.softmax_scale * kTreeLog2e);
+            vs = __ldg(p.v_scale + at);
+          }
+          float* sc = reinterpret_cast<float*>(smem + C::kSmScale) + (n % kScales) * (2 * 128 + 4);
+          sc[ct] = ks;
+          sc[128 + ct] = vs;
+          float mx = fabsf(vs);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          if (lane == 0) sc[256 + warp - 12] = mx;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sc_full[n % kScales]);
+        }
+        for (int kv = 0; ok && kv < 2; ++kv, ++x) {
+          const int b = x % kBufs;
+          if (x >= kBufs) ok = warp_wait(&kv_empty[b], ((x / kBufs) - 1) & 1);
+          if (!ok) break;
+          const int rb = rx % kRaws;
+          ok = warp_wait(&raw_full[rb], (rx / kRaws) & 1);
+          if (!ok) break;
+          ++rx;
+          if (!(fl & kNoData)) {
+            const uint8_t* raw = smem + C::kSmRaw + rb * kRaw;
+            uint8_t* tile = smem + kSmKv + b * kTile;
+            // tokens past the request's end are not data: zeros
+            const int there = min(kBlock, bi.seq - bi.t0);
+#pragma unroll 4
+            for (int i = ct; i < kRaw / 16; i += kConv * 32) {
+              const int row = i >> 3, ch = 2 * (i & 7);  // 16 codes: f16 chunks ch, ch + 1
+              uint4 v = lds128(raw + 16 * i);
+              if (row >= there) v = make_uint4(0u, 0u, 0u, 0u);
+              uint8_t* dst = tile + (ch >> 3) * kHalf + row * 128;
+              *reinterpret_cast<uint4*>(dst + (((ch & 7) ^ (row & 7)) << 4)) =
+                  make_uint4(e4m3x2_to_f16x2((uint16_t)v.x), e4m3x2_to_f16x2((uint16_t)(v.x >> 16)),
+                             e4m3x2_to_f16x2((uint16_t)v.y), e4m3x2_to_f16x2((uint16_t)(v.y >> 16)));
+              *reinterpret_cast<uint4*>(dst + ((((ch & 7) + 1) ^ (row & 7)) << 4)) =
+                  make_uint4(e4m3x2_to_f16x2((uint16_t)v.z), e4m3x2_to_f16x2((uint16_t)(v.z >> 16)),
+                             e4m3x2_to_f16x2((uint16_t)v.w), e4m3x2_to_f16x2((uint16_t)(v.w >> 16)));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (lane == 0) {
+            mbar_arrive(&raw_empty[rb]);
+            mbar_arrive(&kv_full[b]);
+          }
+        }
+        if (!ok) break;
+      }
+      if (!ok) misc[0] = 1;
+    } else if (warp >= 4 && warp < 12) {
       // ---------------------------------------------- softmax of tile t
       const int t = (warp - 4) >> 2, quarter = warp & 3;
       const int m = quarter * 32 + lane;  // row of the tile
@@ -443,6 +598,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float sink = p.sinks ? __ldg(p.sinks + head) : 0.f;
       float m_run = -INFINITY, l_run = 0.f;
+      // PTH: P carries its token's v scale over a power of two that only grows,
+      // so that it keeps its range in 16 bits whatever the scales
+      float vref = 0.f;
       int x = 1, seg = -1;
       bool bad = false, ok = true;
       for (int n = 0;; ++n) {
@@ -457,6 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++seg;
           m_run = -INFINITY;
           l_run = 0.f;
+          vref = 0.f;
           bad = false;
         }
         bad |= (fl & (kBadPage | kPoison)) != 0;
@@ -477,42 +636,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (work) {
           tc::fence_after();
+          const float* ks = nullptr;
+          float grow = 1.f;  // what O is scaled by for a larger vref
+          if constexpr (PTH) {
+            ok = warp_wait(&sc_full[n % kScales], (n / kScales) & 1);
+            if (!ok) break;
+            ks = reinterpret_cast<const float*>(smem + C::kSmScale) + (n % kScales) * (2 * 128 + 4);
+            const float vm = fmaxf(fmaxf(ks[256], ks[257]), fmaxf(ks[258], ks[259]));
+            if (vm > vref) {
+              // the next power of two above vm (its exponent field, plus one)
+              const float nr = __uint_as_float(min((__float_as_uint(vm) & 0x7f800000u) + 0x00800000u, 0x7e800000u));
+              grow = vref > 0.f ? vref / nr : 1.f;
+              vref = nr;
+            }
+          }
+          // (with PTH the tokens' factors carry the softmax scale and its sign)
+          const float sg = PTH ? 1.f : scale2;
           float mx;
           if (fl & kMixed)
-            mx = scale2 >= 0.f ? row_max<false, true>(sa, vis) * scale2 : row_max<true, true>(sa, vis) * -scale2;
+            mx = sg >= 0.f ? row_max<false, true, PTH>(sa, vis, ks) * sg : row_max<true, true, PTH>(sa, vis, ks) * -sg;
           else
-            mx = scale2 >= 0.f ? row_max<false, false>(sa, vis) * scale2 : row_max<true, false>(sa, vis) * -scale2;
+            mx = sg >= 0.f ? row_max<false, false, PTH>(sa, vis, ks) * sg : row_max<true, false, PTH>(sa, vis, ks) * -sg;
           const bool move = mx > m_run + kSlack || (m_run == -INFINITY && mx > -INFINITY);
-          if (__any_sync(0xffffffffu, move)) {
+          if (__any_sync(0xffffffffu, move) || grow != 1.f) {
             float al = 1.f;
             if (mx > m_run) {
               al = m_run == -INFINITY ? 1.f : ex2_ftz(m_run - mx);
               m_run = mx;
             }
             l_run *= al;
+            al *= grow;
             // (a row without a reference has an all-zero O: nothing to rescale)
             if (!(fl & kFirst) && __any_sync(0xffffffffu, al != 1.f)) {
               ok = warp_wait(&pv_done[t], (n - 1) & 1);
               if (!ok) break;
               tc::fence_after();
 #pragma unroll 1
-              for (int c = 0; c < 128; c += 32) {
-                uint32_t r[32];
-                tc::tmem_ld32_issue(oa + c, r);
-                tc::tmem_wait_ld(r);
-                uint32_t a[16], b[16];
+              for (int c = 0; c < 128; c += 16) {
+                uint32_t r[16];
+                tc::tmem_ld16(oa + c, r);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  a[i] = __float_as_uint(__uint_as_float(r[i]) * al);
-                  b[i] = __float_as_uint(__uint_as_float(r[16 + i]) * al);
-                }
-                tc::tmem_st16(oa + c, a);
-                tc::tmem_st16(oa + c + 16, b);
+                for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * al);
+                tc::tmem_st16(oa + c, r);
               }
             }
           }
-          const float base = m_run == -INFINITY ? 0.f : m_run;
-          l_run += (fl & kMixed) ? row_exp<true>(sa, scale2, base, vis) : row_exp<false>(sa, scale2, base, vis);
+          float base = m_run == -INFINITY ? 0.f : m_run, unit = 1.f;
+          if constexpr (PTH) {
+            // 2^(x - log2 vref): the sum is taken back by the same power of two
+            unit = vref > 0.f ? vref : 1.f;
+            base += (float)((int)(__float_as_uint(unit) >> 23) - 127);
+          }
+          l_run += unit * ((fl & kMixed) ? row_exp<true, FP8, PTH>(sa, scale2, base, vis, ks, ks + 128)
+                                         : row_exp<false, FP8, PTH>(sa, scale2, base, vis, ks, ks + 128));
           tc::tmem_wait_st();
           tc::fence_before();
         }
@@ -527,10 +703,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const uint4 v = lds128(src + 16 * i);
-              odd |= (v.x & 0x7fff7fffu) + 0x00800080u;
-              odd |= (v.y & 0x7fff7fffu) + 0x00800080u;
-              odd |= (v.z & 0x7fff7fffu) + 0x00800080u;
-              odd |= (v.w & 0x7fff7fffu) + 0x00800080u;
+              constexpr uint32_t one = FP8 ? 0x04000400u : 0x00800080u;  // an exponent's last bit
+              odd |= (v.x & 0x7fff7fffu) + one;
+              odd |= (v.y & 0x7fff7fffu) + one;
+              odd |= (v.z & 0x7fff7fffu) + one;
+              odd |= (v.w & 0x7fff7fffu) + one;
             }
           }
           if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0) && lane == 0)
@@ -547,21 +724,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (warp == 4 && lane == 0) *reinterpret_cast<volatile int*>(&misc[4 + (seg + 2) % 3]) = 0;
           tc::fence_after();
           const bool none = bad || (m_run == -INFINITY && l_run == 0.f);
+          const float back = PTH ? vref : 1.f;
           const TreeRowEnd e = tree_row_end(none ? -INFINITY : m_run, none ? 0.f : l_run,
-                                            p.sinks != nullptr, sink * kTreeLog2e, vs);
+                                            p.sinks != nullptr, sink * kTreeLog2e, PTH ? back : vs);
           const bool have = (t == 0 || (fl & kTwo)) && !(fl & kPoison);
           const long long r = (long long)(bi.row0 + tok) * H + head;  // row x head in the batch
           const long long pr = (long long)bi.slot * 256 + t * tpt * H + m;
           if (have) {
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-              uint32_t v[32];
-              tc::tmem_ld32_issue(oa + c, v);
-              tc::tmem_wait_ld(v);
+            for (int c = 0; c < 128; c += 16) {
+              uint32_t v[16];
+              tc::tmem_ld16(oa + c, v);
               if (there && (fl & kWhole)) {
                 uint4* dst = reinterpret_cast<uint4*>(p.out + r * kHeadDim + c);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2; ++i) {
                   uint32_t w[4];
 #pragma unroll
                   for (int k = 0; k < 4; ++k)
@@ -573,8 +750,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               } else if (there) {
                 uint4* dst = reinterpret_cast<uint4*>(p.part_o + pr * kHeadDim + c);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  dst[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                for (int i = 0; i < 4; ++i)
+                  dst[i] = make_uint4(__float_as_uint(__uint_as_float(v[4 * i]) * back),
+                                      __float_as_uint(__uint_as_float(v[4 * i + 1]) * back),
+                                      __float_as_uint(__uint_as_float(v[4 * i + 2]) * back),
+                                      __float_as_uint(__uint_as_float(v[4 * i + 3]) * back));
               }
               __syncwarp();
             }
@@ -616,23 +796,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+template <bool FP8, bool PTH>
+cudaError_t launch_tc(const TreeLaunch& p, int grid, cudaStream_t stream) {
+  using C = TcCfg<FP8, PTH>;
+  CUtensorMap qmap, kmap, vmap;
+  memset(&qmap, 0, sizeof(qmap));
+  memset(&kmap, 0, sizeof(kmap));
+  memset(&vmap, 0, sizeof(vmap));
+  const long long toks = max(1ll, (long long)p.batch.num_pages) * kBlock;
+  if (!FP8 &&
+      (!encode_map_2d(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.q, kHeadDim,
+                      (long long)p.batch.num_rows * p.num_heads, kHeadDim * 2, 64, 128) ||
+       !encode_map_2d(&kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.k, kHeadDim, toks, kHeadDim * 2, 64,
+                      kBlock) ||
+       !encode_map_2d(&vmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.v, kHeadDim, toks, kHeadDim * 2, 64,
+                      kBlock)))
+    return cudaErrorInvalidValue;
+  auto kern = tree_attn_tc_kernel<FP8, PTH>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, C::kThreads, C::kBytes, stream>>>(p, qmap, kmap, vmap);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_tree_attn_tc(const TreeLaunch& p, int grid, cudaStream_t stream) {
-  CUtensorMap qmap, kmap, vmap;
-  const long long toks = max(1ll, (long long)p.batch.num_pages) * kBlock;
-  if (!encode_map_2d(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.q, kHeadDim,
-                     (long long)p.batch.num_rows * p.num_heads, kHeadDim * 2, 64, 128) ||
-      !encode_map_2d(&kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.k, kHeadDim, toks, kHeadDim * 2, 64,
-                     kBlock) ||
-      !encode_map_2d(&vmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.v, kHeadDim, toks, kHeadDim * 2, 64,
-                     kBlock))
-    return cudaErrorInvalidValue;
-  const cudaError_t e =
-      cudaFuncSetAttribute(tree_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
-  if (e != cudaSuccess) return e;
-  tree_attn_tc_kernel<<<grid, kThreads, kBytes, stream>>>(p, qmap, kmap, vmap);
-  return cudaGetLastError();
+  if (!p.kv_fp8) return launch_tc<false, false>(p, grid, stream);
+  return p.scale_mode == MSA_SCALE_PER_TOKEN_HEAD ? launch_tc<true, true>(p, grid, stream)
+                                                  : launch_tc<true, false>(p, grid, stream);
 }
 
 }  // namespace msa

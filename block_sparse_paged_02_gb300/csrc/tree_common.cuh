@@ -172,6 +172,19 @@ __device__ __forceinline__ void add2(float& x0, float& x1, float a0, float a1) {
       : "f"(a0), "f"(a1));
 }
 
+// the same with a factor for each
+__device__ __forceinline__ void fma2p(float& x0, float& x1, float b0, float b1, float c) {
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "mov.b64 z, {%4, %4};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(b0), "f"(b1), "f"(c));
+}
+__device__ __forceinline__ void mul2v(float& x0, float& x1, float b0, float b1) {
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(b0), "f"(b1));
+}
 // the same with an addend for each
 __device__ __forceinline__ void fma2v(float& x0, float& x1, float b, float c0, float c1) {
   asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"

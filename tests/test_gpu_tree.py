@@ -191,6 +191,27 @@ def test_poisoned_requests():
         run_both(w, mask, topk, bad=(1, 2), status=1 | 2)
 
 
+@pytest.mark.parametrize("kv,scale", [(BF, NONE), (F8, SCALAR), (F8, TOKEN)])
+@pytest.mark.parametrize("ql,hq", [(1, 4), (20, 16)])
+def test_many_poisoned_requests_and_bad_pages(kv, scale, ql, hq):
+    # far more empty blocks than any ring holds
+    n = 400
+    q_lens, ctxs = [ql] * n, [130] * n
+    w = make(26, q_lens, ctxs, hq, kv, scale, True)
+    w.context_lens[1::2] += 1
+    w.block_table[4::8, 1] = -1
+    bad = tuple(range(1, n, 2)) + tuple(range(4, n, 8))
+    c = case(w)
+    c.tree_attn()
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 3
+    check_attn(c, T.tree_attn(w, None, None, bad))
+    # one request, every page bad
+    w = make(26, [ql], [128 * 300], hq, kv, scale, True)
+    w.block_table[:] = -1
+    run_both(w, bad=(0,), status=1)
+
+
 def test_more_rows_than_the_mask_or_the_bound():
     q_lens, ctxs = [40, 3], [100, 100]
     w = make(19, q_lens, ctxs, 4)

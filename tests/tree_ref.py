@@ -49,7 +49,10 @@ def tree_attn(w, mask=None, topk_idx=None, bad=()):
     absolute values (truncating accumulation: a whole step per term); 2^x by 2^-22 and P's
     rounding by 2^-8 (bf16; f16 is finer) of each term, so of a = sum p |v|; sums of n terms in
     fp32 by at most n / 32 * 2^-24 per lane chain plus the joins (taken as 2e-5); the bf16 result
-    by 2^-8 of itself."""
+    by 2^-8 of itself.  With e4m3 values P is f16, whose steps below 2^-14 are 2^-24: P holds
+    2^(x - m) times the token's scale over a power of two r that is at most twice the largest
+    scale (1, with one scale or none), and 2^m / den <= 1, so that a weight is off by at most
+    2^-25 r, and the result by that times the sum of the visible tokens' |codes|."""
     n, h, _ = w.q.shape
     out, lse = np.zeros((n, h, 128)), np.full((n, h), -np.inf)
     out_tol, lse_tol = np.zeros((n, h, 128)), np.zeros((n, h))
@@ -84,6 +87,14 @@ def tree_attn(w, mask=None, topk_idx=None, bad=()):
             lse[q0 + j] = (m + np.log(den))[:, 0]
             d = dz.max(1, keepdims=True)
             out_tol[q0 + j] = (2.0 ** -8 + 2 * d + 3e-5) * (p @ np.abs(v[see])) + 2.0 ** -8 * np.abs(out[q0 + j]) + 1e-30
+            if w.kv_dtype == W.KV_FP8:
+                codes = np.abs(values(w.v_cache[pages]).reshape(-1, 128)[:tot][see]).sum(0)
+                r16 = 1.0
+                if w.scale_mode == W.SCALE_SCALAR:
+                    r16 = abs(float(w.v_scale[0]))
+                elif w.scale_mode == W.SCALE_PER_TOKEN_HEAD:
+                    r16 = 2 * float(np.abs(w.v_scale[pages].reshape(-1)[:tot]).max())
+                out_tol[q0 + j] += 2.0 ** -25 * r16 * codes
             lse_tol[q0 + j] = d[:, 0] + 2e-5 + 2.0 ** -22 * np.abs(lse[q0 + j])
     return out, lse, out_tol, lse_tol
 
