@@ -438,22 +438,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                   }
                 }
               } else {
+                // a lane holds the visibility of the warp's 32 tokens to one of
+                // 32 rows, fetched for 32 rows at a time
+                const int tw = t - lane;
+                int j = c * QR / H, h = c * QR % H, j0 = -64;
+                uint32_t win = 0, row = 0;
                 for (int k = 0; k < nr; k += 16) {
                   uint32_t r[16];
                   tc::tmem_ld16(da + k, r);
-                  int j = (c * QR + k) / H, h = (c * QR + k) % H;
-                  bool vis = tree_vis_token(p, q0 + j, j, ctx, qlen, t, sel);
 #pragma unroll
                   for (int i = 0; i < 16; ++i) {
-                    const float e = ex2_ftz(fmaf(__uint_as_float(r[i]), f, nl[k + i]));
-                    if (k + i < nr && vis && nl[k + i] != -INFINITY) acc[i & 3] += e;
+                    if (j >= j0 + 32) {  // (the same for all lanes)
+                      j0 = j;
+                      win = 0;
+                      if (j0 + lane < qlen) {
+                        const bool rs = tree_row_selects(sel, j0 + lane);
+                        win = tree_vis16(p, q0 + j0 + lane, j0 + lane, ctx, qlen, tw, rs) |
+                              tree_vis16(p, q0 + j0 + lane, j0 + lane, ctx, qlen, tw + 16, rs) << 16;
+                      }
+                      row = __shfl_sync(0xffffffffu, win, 0);
+                    }
+                    const float n = nl[k + i], e = ex2_ftz(fmaf(__uint_as_float(r[i]), f, n));
+                    acc[i & 3] += ((row >> lane) & 1u) && n != -INFINITY ? e : 0.f;
                     if (++h == H) {
                       h = 0;
                       ++j;
-                      vis = j < qlen && tree_vis_token(p, q0 + j, j, ctx, qlen, t, sel);
+                      row = __shfl_sync(0xffffffffu, win, (j - j0) & 31);
                     }
                   }
-                  __syncwarp();
                 }
               }
               tc::fence_before();

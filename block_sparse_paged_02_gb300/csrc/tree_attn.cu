@@ -670,19 +670,20 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           } else {
             if (m == 0 && c == 0) p.part_bad[slot] = bad ? 1 : 0;
             if (c == 0) p.part_ml[(long long)slot * M + m] = make_float2(m_run[hh], l_run[hh]);
-            float* dst = p.part_o + ((long long)slot * M + m) * kHeadDim;
+            // [4-dim group][row][4 dims]: rows of a group are contiguous
+            float* dst = p.part_o + ((long long)slot * (kHeadDim / 4) * M + m) * 4;
             if constexpr (FP8) {
 #pragma unroll
               for (int e2 = 0; e2 < 2; ++e2)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                  *reinterpret_cast<float4*>(dst + 32 * c + 16 * e2 + 4 * j) =
+                  *reinterpret_cast<float4*>(dst + (8 * c + 4 * e2 + j) * M * 4) =
                       make_float4(o[4 * j][2 * hh + e2], o[4 * j + 1][2 * hh + e2],
                                   o[4 * j + 2][2 * hh + e2], o[4 * j + 3][2 * hh + e2]);
             } else {
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                *reinterpret_cast<float2*>(dst + 8 * j + 2 * c) =
+                *reinterpret_cast<float2*>(dst + (2 * j + (c >> 1)) * M * 4 + 2 * (c & 1)) =
                     make_float2(o[j][2 * hh], o[j][2 * hh + 1]);
             }
           }
@@ -752,8 +753,11 @@ __global__ void __launch_bounds__(kMgThreads) tree_merge_kernel(const __grid_con
     const int n = rec.last - c + 2;
     const bool few = n <= kMgFew;
     {
+      // few: a thread per (row, 4 dims), 8 rows; else a warp per partial, a lane
+      // per 4 dims of the one row
       const int at = unit - s_base[c];
-      const int m = few ? at * kMgWarps + warp : at;
+      const int m = few ? at * kMgWarps + (threadIdx.x & 7) : at;
+      const int g = few ? threadIdx.x >> 3 : lane;
       const bool live = m < rec.nrows;
       float M = -INFINITY, L = 0.f;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -772,7 +776,7 @@ __global__ void __launch_bounds__(kMgThreads) tree_merge_kernel(const __grid_con
               const long long slot = 2ll * (c - 1 + i) + (i == 0 ? 1 : 0);
               bad |= p.part_bad[slot];
               ml[u] = p.part_ml[slot * tile_rows + m];
-              v[u] = *reinterpret_cast<const float4*>(p.part_o + (slot * tile_rows + m) * kHeadDim + 4 * lane);
+              v[u] = reinterpret_cast<const float4*>(p.part_o)[(slot * (kHeadDim / 4) + g) * tile_rows + m];
             }
           }
           float mn = M;
@@ -816,20 +820,25 @@ __global__ void __launch_bounds__(kMgThreads) tree_merge_kernel(const __grid_con
           }
         }
       }
-      if (live && (few || warp == 0)) {
-        if (bad == 2) {  // values that a row does not see could have reached it
-          const int row = rec.row0 + m / H;
-          tree_slow_row(p, rec.q, row, row - p.batch.cu_seqlens_q[rec.q], m % H);
-          continue;
+      // values that a row does not see could have reached the tile (the whole
+      // tile's partials say so alike): its rows again, a warp each
+      if (__syncthreads_or(live && (few || warp == 0) && bad == 2)) {
+        const int mm = few ? at * kMgWarps + warp : at;
+        if (mm < rec.nrows && (few || warp == 0)) {
+          const int row = rec.row0 + mm / H;
+          tree_slow_row(p, rec.q, row, row - p.batch.cu_seqlens_q[rec.q], mm % H);
         }
+        continue;
+      }
+      if (live && (few || warp == 0)) {
         const bool none = bad || (M == -INFINITY && L == 0.f);
         const float sink = p.sinks ? __ldg(p.sinks + m % H) : 0.f;
         const TreeRowEnd e = tree_row_end(M, L, p.sinks != nullptr, sink * kTreeLog2e, vs);
         const long long r = (long long)rec.row0 * H + m;
         uint2 w = make_uint2(pack_bf16x2(a.x * e.f, a.y * e.f), pack_bf16x2(a.z * e.f, a.w * e.f));
         if (none) w = make_uint2(0u, 0u);
-        *reinterpret_cast<uint2*>(p.out + r * kHeadDim + 4 * lane) = w;
-        if (lane == 0) p.lse[r] = none ? (p.sinks ? sink : -INFINITY) : e.lse;
+        *reinterpret_cast<uint2*>(p.out + r * kHeadDim + 4 * g) = w;
+        if (g == 0) p.lse[r] = none ? (p.sinks ? sink : -INFINITY) : e.lse;
       }
     }
   }

@@ -5,17 +5,18 @@
 // cut into pairs of 128-row tiles; a CTA loads each visited block's K and V
 // once for both tiles, and while one tile is in its softmax the tensor cores
 // work on the other:
-//   S = Q K^T   tcgen05.mma M128 N128 K128, both operands in shared memory
-//   P = 2^(S' - m)  one thread per row (TMEM lane): two passes over its 128
-//               logits, the running reference m moves only when a block's
+//   S = Q K^T   tcgen05.mma M128 N64 K128, both operands in shared memory
+//   P = 2^(S' - m)  one thread per row (TMEM lane), 64 logits at a time in
+//               registers; the running reference m moves only when a step's
 //               maximum exceeds it by more than 2^8 (then that warp rescales
-//               its rows of O), P written back over S as bf16
+//               its rows of O); P written back over S in 16 bits
 //   O += P V    tcgen05.mma with A = P from tensor memory, B = V (MN-major)
 // Roles: warp 0 issues the tensor copies, one thread of warps 1 and 2 issues
 // the products of tile 0 and tile 1 (an instruction takes its thread ~100
 // cycles, more than the 64 that it keeps the pipe busy, so one issuer would
 // bound the kernel), warps 4-7 and 8-11 are the tiles' softmax.  Tensor memory
-// (512 columns): S / P and O of both tiles.  With e4m3 pools warps 12-15 turn the
+// (512 columns): two S / P buffers of 64 tokens and O for each tile, so that the
+// next step's S is computed during a step's softmax.  With e4m3 pools warps 12-15 turn the
 // tiles into f16 (exact) and the products run in f16; a scale per token joins the
 // logits and P in the softmax.  (bf16 pools with a scale per token stay on
 // tree_attn.cu.)
@@ -39,7 +40,7 @@ constexpr int kRaw = 128 * 128;   // 128 x 128 e4m3
 constexpr int kInfos = 8;
 // flags of a block
 constexpr int kFirst = 1, kLast = 2, kWhole = 4, kNoData = 8, kBadPage = 16, kPoison = 32,
-              kEnd = 64, kMixed = 128, kTwo = 256;
+              kEnd = 64, kMixed = 128, kTwo = 256, kHalves = 512;
 
 struct BlockInfo {
   int flags;
@@ -68,8 +69,9 @@ struct TcCfg {
   static constexpr int kSmInfo = kSmScale + (PTH ? kScales * (2 * 128 + 4) * 4 : 0);
   static constexpr int kSmBars = kSmInfo + kInfos * (int)sizeof(BlockInfo);
   // kv full / empty, raw full / empty, q full / empty, info full, scales full;
-  // per tile: s_full, p_full, pv_done, o_free; fill, ends
-  static constexpr int kNumBars = 2 * kBufs + 2 * kRaws + 2 + kInfos + kScales + 8 + 2;
+  // per tile: s_full, p_full, pv_done [2 each], o_free; fill, ends.  (A role may be
+  // two steps ahead of another, which one barrier's parity would not tell apart.)
+  static constexpr int kNumBars = 2 * kBufs + 2 * kRaws + 2 + kInfos + kScales + 14 + 2;
   static constexpr int kSmMisc = kSmBars + kNumBars * 8;
   static constexpr int kBytes = kSmMisc + 64;
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -77,7 +79,7 @@ struct TcCfg {
 };
 
 constexpr uint32_t kTmemCols = 512;
-__device__ __forceinline__ uint32_t col_s(int t) { return 128u * t; }
+__device__ __forceinline__ uint32_t col_s(int t, int step) { return 128u * t + 64u * (step & 1); }
 __device__ __forceinline__ uint32_t col_o(int t) { return 256u + 128u * t; }
 constexpr float kSlack = 8.f;
 
@@ -117,60 +119,46 @@ __device__ __forceinline__ float max64(const uint32_t (&r)[64], float acc, uint3
   return fmaxf(fmax3(g[0], g[1], g[2]), g[3]);
 }
 
-template <bool NEG, bool MASKED, bool PTH>
-__device__ __forceinline__ float row_max(uint32_t sa, const uint32_t (&vis)[4], const float* ks) {
-  uint32_t r[64];
-  tc::tmem_ld64(sa, r);
-  const float g = max64<NEG, MASKED, PTH>(r, -INFINITY, vis[0], vis[1], ks);
-  tc::tmem_ld64(sa + 64, r);
-  return max64<NEG, MASKED, PTH>(r, g, vis[2], vis[3], ks + 64);
-}
-
-// P = 2^(s * scale2 - m) of the 128 columns at sa as 16-bit pairs over the first
-// 64 of them (with PTH the token's ks in the place of scale2, and P times its
-// vs); returns the fp32 sum of the 2^...
+// P = 2^(s * scale2 - m) of 64 logits as 16-bit pairs into the 32 columns at pa
+// (with PTH the token's ks in the place of scale2, and P times its vs); returns
+// the fp32 sum of the 2^...
 template <bool MASKED, bool FP8, bool PTH>
-__device__ __forceinline__ float row_exp(uint32_t sa, float scale2, float m,
-                                         const uint32_t (&vis)[4], const float* ks,
-                                         const float* vs) {
+__device__ __forceinline__ float exp64(const uint32_t (&r)[64], uint32_t pa, float scale2, float m,
+                                       uint32_t vis0, uint32_t vis1, const float* ks,
+                                       const float* vs) {
   float l[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    uint32_t r[64];
-    tc::tmem_ld64(sa + 64 * half, r);
+  for (int q = 0; q < 2; ++q) {
+    uint32_t w[16];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint32_t w[16];
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const int t = 64 * half + 32 * q + i;
-        float a = __uint_as_float(r[32 * q + i]), b = __uint_as_float(r[32 * q + i + 1]);
-        if (PTH) {
-          const float2 k = *reinterpret_cast<const float2*>(ks + t);
-          fma2p(a, b, k.x, k.y, -m);
-        } else {
-          fma2(a, b, scale2, -m);
-        }
-        a = ex2_ftz(a);
-        b = ex2_ftz(b);
-        const uint32_t v = MASKED ? vis[2 * half + q] : 0u;
-        if (MASKED) {
+    for (int i = 0; i < 32; i += 2) {
+      const int t = 32 * q + i;
+      float a = __uint_as_float(r[t]), b = __uint_as_float(r[t + 1]);
+      if (PTH) {
+        const float2 k = *reinterpret_cast<const float2*>(ks + t);
+        fma2p(a, b, k.x, k.y, -m);
+      } else {
+        fma2(a, b, scale2, -m);
+      }
+      a = ex2_ftz(a);
+      b = ex2_ftz(b);
+      const uint32_t v = q ? vis1 : vis0;
+      if (MASKED) {
+        a = (v >> i) & 1u ? a : 0.f;
+        b = (v >> (i + 1)) & 1u ? b : 0.f;
+      }
+      add2(l[i & 2], l[(i & 2) + 1], a, b);
+      if (PTH) {
+        const float2 x = *reinterpret_cast<const float2*>(vs + t);
+        mul2v(a, b, x.x, x.y);
+        if (MASKED) {  // (the scale of a token that the row does not see may be anything)
           a = (v >> i) & 1u ? a : 0.f;
           b = (v >> (i + 1)) & 1u ? b : 0.f;
         }
-        add2(l[i & 2], l[(i & 2) + 1], a, b);
-        if (PTH) {
-          const float2 x = *reinterpret_cast<const float2*>(vs + t);
-          mul2v(a, b, x.x, x.y);
-          if (MASKED) {  // (the scale of a token that the row does not see may be anything)
-            a = (v >> i) & 1u ? a : 0.f;
-            b = (v >> (i + 1)) & 1u ? b : 0.f;
-          }
-        }
-        w[i >> 1] = FP8 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
       }
-      tc::tmem_st16(sa + 32 * half + 16 * q, w);
+      w[i >> 1] = FP8 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
     }
+    tc::tmem_st16(pa + 16 * q, w);
   }
   return (l[0] + l[1]) + (l[2] + l[3]);
 }
@@ -183,7 +171,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
   using C = TcCfg<FP8, PTH>;
   constexpr int kBufs = C::kBufs, kRaws = C::kRaws, kThreads = C::kThreads;
   constexpr int kSmKv = C::kSmKv, kSmQ = C::kSmQ;
-  constexpr uint32_t kIdescS = tc::idesc_16(128, 128, 0, FP8 ? 0 : 1);
+  constexpr uint32_t kIdescS = tc::idesc_16(128, 64, 0, FP8 ? 0 : 1);
   constexpr uint32_t kIdescO = tc::idesc_16(128, 128, 1, FP8 ? 0 : 1);
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::kSmBars);
@@ -194,10 +182,10 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
   uint64_t* q_empty = q_full + 1;
   uint64_t* info_full = q_empty + 1;
   uint64_t* sc_full = info_full + kInfos;
-  uint64_t* s_full = sc_full + kScales;  // [2]
-  uint64_t* p_full = s_full + 2;
-  uint64_t* pv_done = p_full + 2;
-  uint64_t* o_free = pv_done + 2;
+  uint64_t* s_full = sc_full + kScales;  // [tile][buffer]
+  uint64_t* p_full = s_full + 4;
+  uint64_t* pv_done = p_full + 4;
+  uint64_t* o_free = pv_done + 4;  // [tile]
   uint64_t* fill = o_free + 2;
   uint64_t* ends = fill + 1;
   BlockInfo* info = reinterpret_cast<BlockInfo*>(smem + C::kSmInfo);
@@ -222,9 +210,11 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
     mbar_init(q_empty, 2);
     for (int i = 0; i < kInfos; ++i) mbar_init(&info_full[i], 1);
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);
-      mbar_init(&pv_done[t], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&s_full[2 * t + b], 1);
+        mbar_init(&p_full[2 * t + b], 4);
+        mbar_init(&pv_done[2 * t + b], 1);
+      }
       mbar_init(&o_free[t], 4);
     }
     mbar_init(fill, 1);
@@ -369,7 +359,8 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
             bi.t0 = kBlock * b;
             bi.flags = both | (c0 + i == 0 ? kFirst : 0) | (c0 + i == nb - 1 ? kLast : 0) |
                        (bad_page ? kBadPage | kNoData : 0) |
-                       (bi.t0 + kBlock > rq.ctx || !cached_all ? kMixed : 0);
+                       (bi.t0 + kBlock > rq.ctx || !cached_all ? kMixed : 0) |
+                       (!bad_page && ntok > 64 ? kHalves : 0);
             if constexpr (FP8) {
               if (bad_page && lane == 0) atomicOr(p.status, MSA_DEV_BAD_PAGE);
               push(bi, bad_page ? -1 : pg);
@@ -431,67 +422,100 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
       if (lane == 0) p.split[blockIdx.x] = rec;
     } else if (warp == 1 || warp == 2) {
       // ---------------------------------------------- products of tile t
+      // in steps of 64 tokens.  S of the next step is issued before P V of this
+      // one, into the tile's other buffer, so that the softmax finds it ready;
+      // a buffer is free again when P V of the step before last is done.
       const int t = warp - 1;
       if (lane == 0) {
         const uint64_t qd = tc::desc_kmajor_sw128(smem_u32(smem + kSmQ + t * kTile));
-        int x = 0, seg = -1, done = 0;  // done: commits to pv_done so far
         bool ok = true;
-        for (int n = 0;; ++n) {
-          ok = mbar_wait(&info_full[n % kInfos], (n / kInfos) & 1);
-          if (!ok) break;
-          const int fl = info[n % kInfos].flags;
-          if (fl & kEnd) break;
-          const bool work = (t == 0 || (fl & kTwo)) && !(fl & kNoData);
-          const int kb = x % kBufs, kph = (x / kBufs) & 1, vb = (x + 1) % kBufs,
-                    vph = ((x + 1) / kBufs) & 1;
-          x += 2;
-          if (fl & kFirst) {
-            ++seg;
-            ok = ok && mbar_wait(q_full, seg & 1);
+        int seg = -1, n = -1, half = 0, fl = 0;  // S's place in the steps
+        // the next step, if any: advances (n, half, fl)
+        auto advance = [&]() -> bool {
+          if (n >= 0 && half == 0 && (fl & kHalves)) {
+            half = 1;
+            return true;
           }
-          ok = ok && mbar_wait(&kv_full[kb], kph);
-          // S takes the place of the previous block's P
-          if (done > 0) ok = ok && mbar_wait(&pv_done[t], (done - 1) & 1);
-          if (!ok) break;
+          ++n;
+          half = 0;
+          ok = ok && mbar_wait(&info_full[n % kInfos], (n / kInfos) & 1);
+          if (!ok) return false;
+          fl = info[n % kInfos].flags;
+          return !(fl & kEnd);
+        };
+        auto issue_s = [&](int step) {
+          const int kb = (2 * n) % kBufs;
+          const bool work = (t == 0 || (fl & kTwo)) && !(fl & kNoData);
+          const bool ends_block = half == 1 || !(fl & kHalves);
+          if (half == 0) {
+            if (fl & kFirst) {
+              ++seg;
+              ok = ok && mbar_wait(q_full, seg & 1);
+            }
+            ok = ok && mbar_wait(&kv_full[kb], ((2 * n) / kBufs) & 1);
+          }
+          if (step >= 2) ok = ok && mbar_wait(&pv_done[2 * t + (step & 1)], ((step >> 1) - 1) & 1);
+          if (!ok) return;
+          uint64_t* full = &s_full[2 * t + (step & 1)];
           if (work) {
             tc::fence_after();
-            const uint64_t kd = tc::desc_kmajor_sw128(smem_u32(smem + kSmKv + kb * kTile));
+            const uint64_t kd = tc::desc_kmajor_sw128(smem_u32(smem + kSmKv + kb * kTile + half * 64 * 128));
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
               const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-              tc::mma_ss(tmem + col_s(t), tc::desc_advance(qd, off), tc::desc_advance(kd, off),
+              tc::mma_ss(tmem + col_s(t, step), tc::desc_advance(qd, off), tc::desc_advance(kd, off),
                          kIdescS, kk > 0 ? 1u : 0u);
             }
-            tc::commit(&s_full[t]);
-            tc::commit(&kv_empty[kb]);
-            if (fl & kLast) tc::commit(q_empty);
+            tc::commit(full);
+            if (ends_block) tc::commit(&kv_empty[kb]);
+            if (ends_block && (fl & kLast)) tc::commit(q_empty);
           } else {
-            mbar_arrive(&s_full[t]);
-            mbar_arrive(&kv_empty[kb]);
-            if (fl & kLast) mbar_arrive(q_empty);
+            mbar_arrive(full);
+            if (ends_block) mbar_arrive(&kv_empty[kb]);
+            if (ends_block && (fl & kLast)) mbar_arrive(q_empty);
           }
-          ok = ok && mbar_wait(&p_full[t], n & 1) && mbar_wait(&kv_full[vb], vph);
+        };
+        auto issue_pv = [&](int step, int pn, int phalf, int pfl, int pseg) {
+          const int vb = (2 * pn + 1) % kBufs;
+          const bool work = (t == 0 || (pfl & kTwo)) && !(pfl & kNoData);
+          const bool ends_block = phalf == 1 || !(pfl & kHalves);
+          const bool first = (pfl & kFirst) && phalf == 0;
+          ok = ok && mbar_wait(&p_full[2 * t + (step & 1)], (step >> 1) & 1);
+          if (phalf == 0) ok = ok && mbar_wait(&kv_full[vb], ((2 * pn + 1) / kBufs) & 1);
           // O of the previous segment has been read
-          if ((fl & kFirst) && seg > 0) ok = ok && mbar_wait(&o_free[t], (seg - 1) & 1);
-          if (!ok) break;
+          if (first && pseg > 0) ok = ok && mbar_wait(&o_free[t], (pseg - 1) & 1);
+          if (!ok) return;
           if (work) {
             tc::fence_after();
-            const uint64_t vd = tc::desc_mnmajor_sw128(smem_u32(smem + kSmKv + vb * kTile), kHalf);
+            const uint64_t vd = tc::desc_mnmajor_sw128(
+                smem_u32(smem + kSmKv + vb * kTile + phalf * 64 * 128), kHalf);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              tc::mma_ts(tmem + col_o(t), tmem + col_s(t) + kk * 8, tc::desc_advance(vd, kk * 2048),
-                         kIdescO, (kk > 0 || !(fl & kFirst)) ? 1u : 0u);
-            tc::commit(&pv_done[t]);
-            tc::commit(&kv_empty[vb]);
+            for (int kk = 0; kk < 4; ++kk)
+              tc::mma_ts(tmem + col_o(t), tmem + col_s(t, step) + kk * 8, tc::desc_advance(vd, kk * 2048),
+                         kIdescO, (kk > 0 || !first) ? 1u : 0u);
+            tc::commit(&pv_done[2 * t + (step & 1)]);
+            if (ends_block) tc::commit(&kv_empty[vb]);
           } else {
-            mbar_arrive(&pv_done[t]);
-            mbar_arrive(&kv_empty[vb]);
+            mbar_arrive(&pv_done[2 * t + (step & 1)]);
+            if (ends_block) mbar_arrive(&kv_empty[vb]);
           }
-          ++done;
+        };
+        int step = 0;
+        bool more = advance();
+        if (more) issue_s(0);
+        while (ok && more) {
+          const int pn = n, phalf = half, pfl = fl, pseg = seg;
+          more = advance();
+          // (a new segment's queries arrive after this one's last S: P V first)
+          const bool late = more && (fl & kFirst) && half == 0;
+          if (ok && more && !late) issue_s(step + 1);
+          if (ok) issue_pv(step, pn, phalf, pfl, pseg);
+          if (ok && late) issue_s(step + 1);
+          ++step;
         }
         if (!ok) misc[0] = 1;
         // every product has completed before the tensor memory is freed
-        if (done > 0 && !mbar_wait(&pv_done[t], (done - 1) & 1)) misc[0] = 1;
+        if (step > 0 && !mbar_wait(&pv_done[2 * t + ((step - 1) & 1)], ((step - 1) >> 1) & 1)) misc[0] = 1;
       }
     } else if (FP8 && warp >= 12) {
       // ---------------------------------------------- e4m3 tiles to f16, queries
@@ -589,7 +613,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
       const int t = (warp - 4) >> 2, quarter = warp & 3;
       const int m = quarter * 32 + lane;  // row of the tile
       const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-      const uint32_t sa = tmem + lanes + col_s(t), oa = tmem + lanes + col_o(t);
+      const uint32_t oa = tmem + lanes + col_o(t);
       const int mtok = m / H, head = m % H;
       float scale2 = p.softmax_scale * kTreeLog2e, vs = 1.f;
       if (p.scale_mode == MSA_SCALE_SCALAR) {
@@ -601,7 +625,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
       // PTH: P carries its token's v scale over a power of two that only grows,
       // so that it keeps its range in 16 bits whatever the scales
       float vref = 0.f;
-      int x = 1, seg = -1;
+      int x = 1, seg = -1, step = 0;
       bool bad = false, ok = true;
       for (int n = 0;; ++n) {
         ok = warp_wait(&info_full[n % kInfos], (n / kInfos) & 1);
@@ -621,104 +645,125 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
         bad |= (fl & (kBadPage | kPoison)) != 0;
         const int tok = t * tpt + mtok;  // drafted token of the pair
         const bool there = (t == 0 || (fl & kTwo)) && mtok < tpt && tok < bi.ntok;
-        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
         const bool work = (t == 0 || (fl & kTwo)) && !(fl & kNoData);
-        if ((fl & kMixed) && work) {
+        bool masked = (fl & kMixed) != 0;
+        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+        if (masked && work) {
           const int j = bi.j0 + tok;
           const bool sel = there && tree_row_selects(bi.rows, j);
+          if (bi.t0 + kBlock <= bi.ctx) {  // cached tokens alone: all or none
+            vis[0] = vis[1] = vis[2] = vis[3] = sel ? ~0u : 0u;
+            masked = !__all_sync(0xffffffffu, sel || !there);
+          } else {
 #pragma unroll
-          for (int w = 0; w < 4; ++w)
-            vis[w] = !there ? 0u
-                            : tree_vis16(p, bi.row0 + tok, j, bi.ctx, bi.qlen, bi.t0 + 32 * w, sel) |
-                                  tree_vis16(p, bi.row0 + tok, j, bi.ctx, bi.qlen, bi.t0 + 32 * w + 16, sel) << 16;
-        }
-        ok = warp_wait(&s_full[t], n & 1);
-        if (!ok) break;
-        if (work) {
-          tc::fence_after();
-          const float* ks = nullptr;
-          float grow = 1.f;  // what O is scaled by for a larger vref
-          if constexpr (PTH) {
-            ok = warp_wait(&sc_full[n % kScales], (n / kScales) & 1);
-            if (!ok) break;
-            ks = reinterpret_cast<const float*>(smem + C::kSmScale) + (n % kScales) * (2 * 128 + 4);
-            const float vm = fmaxf(fmaxf(ks[256], ks[257]), fmaxf(ks[258], ks[259]));
-            if (vm > vref) {
-              // the next power of two above vm (its exponent field, plus one)
-              const float nr = __uint_as_float(min((__float_as_uint(vm) & 0x7f800000u) + 0x00800000u, 0x7e800000u));
-              grow = vref > 0.f ? vref / nr : 1.f;
-              vref = nr;
-            }
+            for (int w = 0; w < 4; ++w)
+              vis[w] = !there ? 0u
+                              : tree_vis16(p, bi.row0 + tok, j, bi.ctx, bi.qlen, bi.t0 + 32 * w, sel) |
+                                    tree_vis16(p, bi.row0 + tok, j, bi.ctx, bi.qlen, bi.t0 + 32 * w + 16, sel) << 16;
           }
-          // (with PTH the tokens' factors carry the softmax scale and its sign)
-          const float sg = PTH ? 1.f : scale2;
-          float mx;
-          if (fl & kMixed)
-            mx = sg >= 0.f ? row_max<false, true, PTH>(sa, vis, ks) * sg : row_max<true, true, PTH>(sa, vis, ks) * -sg;
-          else
-            mx = sg >= 0.f ? row_max<false, false, PTH>(sa, vis, ks) * sg : row_max<true, false, PTH>(sa, vis, ks) * -sg;
-          const bool move = mx > m_run + kSlack || (m_run == -INFINITY && mx > -INFINITY);
-          if (__any_sync(0xffffffffu, move) || grow != 1.f) {
-            float al = 1.f;
-            if (mx > m_run) {
-              al = m_run == -INFINITY ? 1.f : ex2_ftz(m_run - mx);
-              m_run = mx;
-            }
-            l_run *= al;
-            al *= grow;
-            // (a row without a reference has an all-zero O: nothing to rescale)
-            if (!(fl & kFirst) && __any_sync(0xffffffffu, al != 1.f)) {
-              ok = warp_wait(&pv_done[t], (n - 1) & 1);
-              if (!ok) break;
-              tc::fence_after();
+        }
+        const float* ks = nullptr;
+        float grow = 1.f;  // what O is scaled by for a larger vref
+        if (PTH && work) {
+          ok = warp_wait(&sc_full[n % kScales], (n / kScales) & 1);
+          if (!ok) break;
+          ks = reinterpret_cast<const float*>(smem + C::kSmScale) + (n % kScales) * (2 * 128 + 4);
+          const float vm = fmaxf(fmaxf(ks[256], ks[257]), fmaxf(ks[258], ks[259]));
+          if (vm > vref) {
+            // the next power of two above vm (its exponent field, plus one)
+            const float nr = __uint_as_float(min((__float_as_uint(vm) & 0x7f800000u) + 0x00800000u, 0x7e800000u));
+            grow = vref > 0.f ? vref / nr : 1.f;
+            vref = nr;
+          }
+        }
+        const int halves = (fl & kHalves) ? 2 : 1;
 #pragma unroll 1
-              for (int c = 0; c < 128; c += 16) {
-                uint32_t r[16];
-                tc::tmem_ld16(oa + c, r);
+        for (int half = 0; half < halves; ++half, ++step) {
+          ok = warp_wait(&s_full[2 * t + (step & 1)], (step >> 1) & 1);
+          if (!ok) break;
+          if (work) {
+            tc::fence_after();
+            const uint32_t sa = tmem + lanes + col_s(t, step);
+            const uint32_t v0 = half ? vis[2] : vis[0], v1 = half ? vis[3] : vis[1];
+            const float* kh = PTH ? ks + 64 * half : nullptr;
+            uint32_t r[64];
+            tc::tmem_ld64(sa, r);
+            // (with PTH the tokens' factors carry the softmax scale and its sign)
+            const float sg = PTH ? 1.f : scale2;
+            float mx;
+            if (masked)
+              mx = sg >= 0.f ? max64<false, true, PTH>(r, -INFINITY, v0, v1, kh) * sg
+                             : max64<true, true, PTH>(r, -INFINITY, v0, v1, kh) * -sg;
+            else
+              mx = sg >= 0.f ? max64<false, false, PTH>(r, -INFINITY, v0, v1, kh) * sg
+                             : max64<true, false, PTH>(r, -INFINITY, v0, v1, kh) * -sg;
+            const bool move = mx > m_run + kSlack || (m_run == -INFINITY && mx > -INFINITY);
+            if (__any_sync(0xffffffffu, move) || grow != 1.f) {
+              float al = 1.f;
+              if (mx > m_run) {
+                al = m_run == -INFINITY ? 1.f : ex2_ftz(m_run - mx);
+                m_run = mx;
+              }
+              l_run *= al;
+              al *= grow;
+              grow = 1.f;
+              // (a row without a reference has an all-zero O: nothing to rescale)
+              if (!((fl & kFirst) && half == 0) && __any_sync(0xffffffffu, al != 1.f)) {
+                ok = warp_wait(&pv_done[2 * t + ((step - 1) & 1)], ((step - 1) >> 1) & 1);
+                if (!ok) break;
+                tc::fence_after();
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 16) {
+                  uint32_t x[16];
+                  tc::tmem_ld16(oa + c, x);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * al);
-                tc::tmem_st16(oa + c, r);
+                  for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * al);
+                  tc::tmem_st16(oa + c, x);
+                }
               }
             }
-          }
-          float base = m_run == -INFINITY ? 0.f : m_run, unit = 1.f;
-          if constexpr (PTH) {
-            // 2^(x - log2 vref): the sum is taken back by the same power of two
-            unit = vref > 0.f ? vref : 1.f;
-            base += (float)((int)(__float_as_uint(unit) >> 23) - 127);
-          }
-          l_run += unit * ((fl & kMixed) ? row_exp<true, FP8, PTH>(sa, scale2, base, vis, ks, ks + 128)
-                                         : row_exp<false, FP8, PTH>(sa, scale2, base, vis, ks, ks + 128));
-          tc::tmem_wait_st();
-          tc::fence_before();
-        }
-        if ((fl & kMixed) && !(fl & kNoData)) {
-          // values that are not finite among this tile's half of the block's V
-          ok = warp_wait(&kv_full[vb], vph);
-          if (!ok) break;
-          const int row = 64 * t + (m >> 1);
-          const uint8_t* src = smem + kSmKv + vb * kTile + (m & 1) * kHalf + row * 128;
-          uint32_t odd = 0;
-          if (bi.t0 + row < bi.seq) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint4 v = lds128(src + 16 * i);
-              constexpr uint32_t one = FP8 ? 0x04000400u : 0x00800080u;  // an exponent's last bit
-              odd |= (v.x & 0x7fff7fffu) + one;
-              odd |= (v.y & 0x7fff7fffu) + one;
-              odd |= (v.z & 0x7fff7fffu) + one;
-              odd |= (v.w & 0x7fff7fffu) + one;
+            float base = m_run == -INFINITY ? 0.f : m_run, unit = 1.f;
+            if constexpr (PTH) {
+              // 2^(x - log2 vref): the sum is taken back by the same power of two
+              unit = vref > 0.f ? vref : 1.f;
+              base += (float)((int)(__float_as_uint(unit) >> 23) - 127);
             }
+            const float* vh = PTH ? kh + 128 : nullptr;
+            l_run += unit * (masked ? exp64<true, FP8, PTH>(r, sa, scale2, base, v0, v1, kh, vh)
+                                    : exp64<false, FP8, PTH>(r, sa, scale2, base, v0, v1, kh, vh));
+            tc::tmem_wait_st();
+            tc::fence_before();
           }
-          if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0) && lane == 0)
-            *reinterpret_cast<volatile int*>(&misc[4 + seg % 3]) = 1;
+          if (half == 0 && (fl & kMixed) && !(fl & kNoData)) {
+            // values that are not finite among this tile's half of the block's V
+            ok = warp_wait(&kv_full[vb], vph);
+            if (!ok) break;
+            const int row = 64 * t + (m >> 1);
+            const uint8_t* src = smem + kSmKv + vb * kTile + (m & 1) * kHalf + row * 128;
+            uint32_t odd = 0;
+            if (bi.t0 + row < bi.seq) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint4 v = lds128(src + 16 * i);
+                constexpr uint32_t one = FP8 ? 0x04000400u : 0x00800080u;  // an exponent's last bit
+                odd |= (v.x & 0x7fff7fffu) + one;
+                odd |= (v.y & 0x7fff7fffu) + one;
+                odd |= (v.z & 0x7fff7fffu) + one;
+                odd |= (v.w & 0x7fff7fffu) + one;
+              }
+            }
+            if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0) && lane == 0)
+              *reinterpret_cast<volatile int*>(&misc[4 + seg % 3]) = 1;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * t + (step & 1)]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[t]);
+        if (!ok) break;
         if (fl & kLast) {
           // both tiles' warps have looked over the segment's blocks
           if (lane == 0) mbar_arrive(ends);
-          ok = warp_wait(ends, seg & 1) && warp_wait(&pv_done[t], n & 1);
+          ok = warp_wait(ends, seg & 1) &&
+               warp_wait(&pv_done[2 * t + ((step - 1) & 1)], ((step - 1) >> 1) & 1);
           if (!ok) break;
           const bool odd = *reinterpret_cast<volatile int*>(&misc[4 + seg % 3]) != 0;
           if (warp == 4 && lane == 0) *reinterpret_cast<volatile int*>(&misc[4 + (seg + 2) % 3]) = 0;
@@ -729,7 +774,8 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
                                             p.sinks != nullptr, sink * kTreeLog2e, PTH ? back : vs);
           const bool have = (t == 0 || (fl & kTwo)) && !(fl & kPoison);
           const long long r = (long long)(bi.row0 + tok) * H + head;  // row x head in the batch
-          const long long pr = (long long)bi.slot * 256 + t * tpt * H + m;
+          const int pm = t * tpt * H + m;  // row of the pair
+          const long long pr = (long long)bi.slot * 256 + pm;
           if (have) {
 #pragma unroll 1
             for (int c = 0; c < 128; c += 16) {
@@ -748,10 +794,11 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
                   dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
               } else if (there) {
-                uint4* dst = reinterpret_cast<uint4*>(p.part_o + pr * kHeadDim + c);
+                // [4-dim group][row][4 dims]: the warp's rows are contiguous
+                uint4* dst = reinterpret_cast<uint4*>(p.part_o) + ((long long)bi.slot * 32 + c / 4) * 256 + pm;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                  dst[i] = make_uint4(__float_as_uint(__uint_as_float(v[4 * i]) * back),
+                  dst[256 * i] = make_uint4(__float_as_uint(__uint_as_float(v[4 * i]) * back),
                                       __float_as_uint(__uint_as_float(v[4 * i + 1]) * back),
                                       __float_as_uint(__uint_as_float(v[4 * i + 2]) * back),
                                       __float_as_uint(__uint_as_float(v[4 * i + 3]) * back));
