@@ -48,6 +48,7 @@ template <bool FP8, int QR>
 struct MassCfg {
   static constexpr int kTiles = FP8 ? (QR == 256 ? 2 : 3) : (QR == 256 ? 3 : QR == 64 ? 5 : 6);
   static constexpr int kRaws = FP8 ? (QR == 256 ? 2 : QR == 64 ? 5 : 6) : 0;
+  static constexpr int kCols = QR < 64 ? 16 : 64;  // columns summed at a time
   static constexpr int kQBuf = QR * 256;
   static constexpr int kSmK = 0;
   static constexpr int kSmQ = kTiles * kTile;
@@ -70,18 +71,27 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
 // keys, or its products and exponentials
 __device__ __forceinline__ long long mass_weight(int rows) { return max(20, (rows + 15) / 16); }
 
-// sum over 64 columns of 2^(s * f + nl) onto acc
-__device__ __forceinline__ void add_exp64(const uint32_t (&r)[64], float f, const float* nl,
-                                          float (&acc)[4]) {
+// sum over W columns of 2^(s * f + nl) onto acc; MASKED: of those with a set bit
+template <int W, bool MASKED>
+__device__ __forceinline__ void add_exp(uint32_t da, float f, const float* nl, uint32_t bits0,
+                                        uint32_t bits1, float (&acc)[4]) {
+  uint32_t r[W];
+  if constexpr (W == 64) tc::tmem_ld64(da, r);
+  else tc::tmem_ld16(da, r);
 #pragma unroll
-  for (int t = 0; t < 64; t += 4) {
+  for (int t = 0; t < W; t += 4) {
     const float4 n = *reinterpret_cast<const float4*>(nl + t);
-    float a = __uint_as_float(r[t]), b = __uint_as_float(r[t + 1]);
-    float c = __uint_as_float(r[t + 2]), d = __uint_as_float(r[t + 3]);
-    fma2v(a, b, f, n.x, n.y);
-    fma2v(c, d, f, n.z, n.w);
-    add2(acc[0], acc[1], ex2_ftz(a), ex2_ftz(b));
-    add2(acc[2], acc[3], ex2_ftz(c), ex2_ftz(d));
+    float x[4] = {__uint_as_float(r[t]), __uint_as_float(r[t + 1]), __uint_as_float(r[t + 2]),
+                  __uint_as_float(r[t + 3])};
+    fma2v(x[0], x[1], f, n.x, n.y);
+    fma2v(x[2], x[3], f, n.z, n.w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = ex2_ftz(x[i]);
+      if (MASKED) x[i] = ((t < 32 ? bits0 : bits1) >> ((t + i) & 31)) & 1u ? x[i] : 0.f;
+    }
+    add2(acc[0], acc[1], x[0], x[1]);
+    add2(acc[2], acc[3], x[2], x[3]);
   }
 }
 
@@ -89,6 +99,7 @@ template <bool FP8, int QR>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_mass_kernel(const __grid_constant__ TreeLaunch p, const __grid_constant__ CUtensorMap kmap) {
   using C = MassCfg<FP8, QR>;
+  constexpr int W = C::kCols;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kSmBars);
   uint64_t* k_empty = k_full + C::kTiles;
@@ -240,7 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (;;) {
           ok = mbar_wait(&info_full[n0 % kInfos], (n0 / kInfos) & 1);
           if (!ok || (info[n0 % kInfos].flags & kEnd)) break;
-          const int nblk = info[n0 % kInfos].nblk, rows = info[n0 % kInfos].qlen * H;
+          const int nblk = info[n0 % kInfos].nblk;
+          const int rows = info[n0 % kInfos].qlen * H;
           const int chunks = (rows + QR - 1) / QR;
           const bool resident = chunks <= 2;
           for (int g = 0; ok && g < nblk; g += 2) {
@@ -351,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint4*>(qd + (ch >> 3) * (QR * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = v;
             }
             float* nl = reinterpret_cast<float*>(smem + C::kSmNl) + qb * QR;
-            for (int i = lt; i < min(QR, (nr + 31) / 32 * 32); i += kLoaders * 32) {
+            for (int i = lt; i < min(QR, (nr + W - 1) / W * W); i += kLoaders * 32) {
               // a row that saw nothing (lse -inf) or lies past the end gives 2^-inf = 0
               const float l = i < nr ? __ldg(lsrc + r0 + i) : -INFINITY;
               nl[i] = l == -INFINITY ? -INFINITY : -l * kTreeLog2e;
@@ -411,62 +423,46 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc::fence_after();
               const int nr = min(QR, rows - c * QR);
               const float* nl = reinterpret_cast<const float*>(smem + C::kSmNl) + qb * QR;
+              // W columns at a time; in a block that not every row sees whole, and
+              // behind the last row, those that count are picked by a bit each
+              int k = 0;
               if (!(fl & kMixed)) {
-                // columns past the end: S = 0 (or, behind the last 16, what an
-                // earlier product left) and nl = -inf; full pairs of loads
-                // while they last
-                int k = 0;
-                if constexpr (QR >= 64) {
-                  for (; k + 64 <= nr; k += 64) {
-                    uint32_t r[64];
-                    tc::tmem_ld64(da + k, r);
-                    add_exp64(r, f, nl + k, acc);
-                  }
-                }
-                for (; k < nr; k += 16) {
-                  uint32_t r[16];
-                  tc::tmem_ld16(da + k, r);
-#pragma unroll
-                  for (int i = 0; i < 16; i += 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(nl + k + i);
-                    float a = __uint_as_float(r[i]), b = __uint_as_float(r[i + 1]);
-                    float d = __uint_as_float(r[i + 2]), e = __uint_as_float(r[i + 3]);
-                    fma2v(a, b, f, v.x, v.y);
-                    fma2v(d, e, f, v.z, v.w);
-                    add2(acc[0], acc[1], ex2_ftz(a), ex2_ftz(b));
-                    add2(acc[2], acc[3], ex2_ftz(d), ex2_ftz(e));
-                  }
-                }
-              } else {
-                // a lane holds the visibility of the warp's 32 tokens to one of
-                // 32 rows, fetched for 32 rows at a time
-                const int tw = t - lane;
-                int j = c * QR / H, h = c * QR % H, j0 = -64;
-                uint32_t win = 0, row = 0;
-                for (int k = 0; k < nr; k += 16) {
-                  uint32_t r[16];
-                  tc::tmem_ld16(da + k, r);
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) {
-                    if (j >= j0 + 32) {  // (the same for all lanes)
+                for (; k + W <= nr; k += W) add_exp<W, false>(da + k, f, nl + k, 0u, 0u, acc);
+              }
+              int j0 = -64;  // a lane holds the sight of row j0 + lane on the warp's tokens
+              uint32_t win = 0;
+              for (; k < nr; k += W) {
+                uint32_t bits[2] = {0u, 0u};
+                if (fl & kMixed) {
+                  // the rows that the columns belong to, in turn
+                  const int first = c * QR + k, end = min(first + W, rows);
+                  for (int at = first; at < end;) {
+                    const int j = at / H, upto = min(end, (j + 1) * H) - first;
+                    if (j >= j0 + 32) {
                       j0 = j;
                       win = 0;
                       if (j0 + lane < qlen) {
-                        const bool rs = tree_row_selects(sel, j0 + lane);
-                        win = tree_vis16(p, q0 + j0 + lane, j0 + lane, ctx, qlen, tw, rs) |
-                              tree_vis16(p, q0 + j0 + lane, j0 + lane, ctx, qlen, tw + 16, rs) << 16;
+                        const int r = j0 + lane, tw = t - lane;
+                        const bool rs = tree_row_selects(sel, r);
+                        win = tree_vis16(p, q0 + r, r, ctx, qlen, tw, rs) |
+                              tree_vis16(p, q0 + r, r, ctx, qlen, tw + 16, rs) << 16;
                       }
-                      row = __shfl_sync(0xffffffffu, win, 0);
                     }
-                    const float n = nl[k + i], e = ex2_ftz(fmaf(__uint_as_float(r[i]), f, n));
-                    acc[i & 3] += ((row >> lane) & 1u) && n != -INFINITY ? e : 0.f;
-                    if (++h == H) {
-                      h = 0;
-                      ++j;
-                      row = __shfl_sync(0xffffffffu, win, (j - j0) & 31);
+                    const uint32_t row = __shfl_sync(0xffffffffu, win, j - j0);
+                    if ((row >> lane) & 1u) {
+                      const uint64_t m = ((upto == 64 ? 0ull : 1ull << upto) - 1ull) & ~((1ull << (at - first)) - 1ull);
+                      bits[0] |= (uint32_t)m;
+                      bits[1] |= (uint32_t)(m >> 32);
                     }
+                    at = first + upto;
                   }
+                } else {
+                  const uint64_t m = (1ull << (nr - k)) - 1ull;
+                  bits[0] = (uint32_t)m;
+                  bits[1] = (uint32_t)(m >> 32);
                 }
+                __syncwarp();
+                add_exp<W, true>(da + k, f, nl + k, bits[0], bits[1], acc);
               }
               tc::fence_before();
               __syncwarp();

@@ -5,18 +5,15 @@
 // cut into pairs of 128-row tiles; a CTA loads each visited block's K and V
 // once for both tiles, and while one tile is in its softmax the tensor cores
 // work on the other:
-//   S = Q K^T   tcgen05.mma M128 N64 K128, both operands in shared memory
+//   S = Q K^T   tcgen05.mma M128 N128 K128, both operands in shared memory
 //   P = 2^(S' - m)  one thread per row (TMEM lane), 64 logits at a time in
 //               registers; the running reference m moves only when a step's
 //               maximum exceeds it by more than 2^8 (then that warp rescales
 //               its rows of O); P written back over S in 16 bits
 //   O += P V    tcgen05.mma with A = P from tensor memory, B = V (MN-major)
-// Roles: warp 0 issues the tensor copies, one thread of warps 1 and 2 issues
-// the products of tile 0 and tile 1 (an instruction takes its thread ~100
-// cycles, more than the 64 that it keeps the pipe busy, so one issuer would
-// bound the kernel), warps 4-7 and 8-11 are the tiles' softmax.  Tensor memory
-// (512 columns): two S / P buffers of 64 tokens and O for each tile, so that the
-// next step's S is computed during a step's softmax.  With e4m3 pools warps 12-15 turn the
+// Roles: warp 0 issues the tensor copies, one thread of warps 1 and 2 issues the
+// products of tile 0 and tile 1, warps 4-7 and 8-11 are the tiles' softmax.  Tensor memory
+// (512 columns): S / P and O of both tiles.  With e4m3 pools warps 12-15 turn the
 // tiles into f16 (exact) and the products run in f16; a scale per token joins the
 // logits and P in the softmax.  (bf16 pools with a scale per token stay on
 // tree_attn.cu.)
@@ -69,9 +66,8 @@ struct TcCfg {
   static constexpr int kSmInfo = kSmScale + (PTH ? kScales * (2 * 128 + 4) * 4 : 0);
   static constexpr int kSmBars = kSmInfo + kInfos * (int)sizeof(BlockInfo);
   // kv full / empty, raw full / empty, q full / empty, info full, scales full;
-  // per tile: s_full, p_full, pv_done [2 each], o_free; fill, ends.  (A role may be
-  // two steps ahead of another, which one barrier's parity would not tell apart.)
-  static constexpr int kNumBars = 2 * kBufs + 2 * kRaws + 2 + kInfos + kScales + 14 + 2;
+  // per tile: s_full, p_full and pv_done of the two halves, o_free; go, fill, ends
+  static constexpr int kNumBars = 2 * kBufs + 2 * kRaws + 2 + kInfos + kScales + 12 + 3;
   static constexpr int kSmMisc = kSmBars + kNumBars * 8;
   static constexpr int kBytes = kSmMisc + 64;
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -79,7 +75,7 @@ struct TcCfg {
 };
 
 constexpr uint32_t kTmemCols = 512;
-__device__ __forceinline__ uint32_t col_s(int t, int step) { return 128u * t + 64u * (step & 1); }
+__device__ __forceinline__ uint32_t col_s(int t) { return 128u * t; }
 __device__ __forceinline__ uint32_t col_o(int t) { return 256u + 128u * t; }
 constexpr float kSlack = 8.f;
 
@@ -171,7 +167,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
   using C = TcCfg<FP8, PTH>;
   constexpr int kBufs = C::kBufs, kRaws = C::kRaws, kThreads = C::kThreads;
   constexpr int kSmKv = C::kSmKv, kSmQ = C::kSmQ;
-  constexpr uint32_t kIdescS = tc::idesc_16(128, 64, 0, FP8 ? 0 : 1);
+  constexpr uint32_t kIdescS = tc::idesc_16(128, 128, 0, FP8 ? 0 : 1);
   constexpr uint32_t kIdescO = tc::idesc_16(128, 128, 1, FP8 ? 0 : 1);
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::kSmBars);
@@ -182,11 +178,12 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
   uint64_t* q_empty = q_full + 1;
   uint64_t* info_full = q_empty + 1;
   uint64_t* sc_full = info_full + kInfos;
-  uint64_t* s_full = sc_full + kScales;  // [tile][buffer]
-  uint64_t* p_full = s_full + 4;
-  uint64_t* pv_done = p_full + 4;
-  uint64_t* o_free = pv_done + 4;  // [tile]
-  uint64_t* fill = o_free + 2;
+  uint64_t* s_full = sc_full + kScales;  // [tile]
+  uint64_t* p_full = s_full + 2;         // [tile][half]
+  uint64_t* pv_done = p_full + 4;        // [tile][half]
+  uint64_t* o_free = pv_done + 4;        // [tile]
+  uint64_t* go = o_free + 2;
+  uint64_t* fill = go + 1;
   uint64_t* ends = fill + 1;
   BlockInfo* info = reinterpret_cast<BlockInfo*>(smem + C::kSmInfo);
   int* misc = reinterpret_cast<int*>(smem + C::kSmMisc);  // [0] timeout, [4..6] odd values seen
@@ -210,13 +207,14 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
     mbar_init(q_empty, 2);
     for (int i = 0; i < kInfos; ++i) mbar_init(&info_full[i], 1);
     for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
       for (int b = 0; b < 2; ++b) {
-        mbar_init(&s_full[2 * t + b], 1);
         mbar_init(&p_full[2 * t + b], 4);
         mbar_init(&pv_done[2 * t + b], 1);
       }
       mbar_init(&o_free[t], 4);
     }
+    mbar_init(go, 4);
     mbar_init(fill, 1);
     mbar_init(ends, 8);
     fence_barrier_init();
@@ -422,100 +420,78 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
       if (lane == 0) p.split[blockIdx.x] = rec;
     } else if (warp == 1 || warp == 2) {
       // ---------------------------------------------- products of tile t
-      // in steps of 64 tokens.  S of the next step is issued before P V of this
-      // one, into the tile's other buffer, so that the softmax finds it ready;
-      // a buffer is free again when P V of the step before last is done.
+      // S of a block, then P V of its two halves as their softmax is done.  Tile 1
+      // starts a segment half a step behind tile 0 (`go`): in step with each other
+      // both tiles would use the tensor cores, and then both wait for a softmax.
       const int t = warp - 1;
       if (lane == 0) {
         const uint64_t qd = tc::desc_kmajor_sw128(smem_u32(smem + kSmQ + t * kTile));
+        uint64_t *pf = p_full + 2 * t, *pv = pv_done + 2 * t;
         bool ok = true;
-        int seg = -1, n = -1, half = 0, fl = 0;  // S's place in the steps
-        // the next step, if any: advances (n, half, fl)
-        auto advance = [&]() -> bool {
-          if (n >= 0 && half == 0 && (fl & kHalves)) {
-            half = 1;
-            return true;
-          }
-          ++n;
-          half = 0;
-          ok = ok && mbar_wait(&info_full[n % kInfos], (n / kInfos) & 1);
-          if (!ok) return false;
-          fl = info[n % kInfos].flags;
-          return !(fl & kEnd);
-        };
-        auto issue_s = [&](int step) {
-          const int kb = (2 * n) % kBufs;
+        int seg = -1, n = 0;
+        for (;; ++n) {
+          ok = mbar_wait(&info_full[n % kInfos], (n / kInfos) & 1);
+          if (!ok) break;
+          const int fl = info[n % kInfos].flags;
+          if (fl & kEnd) break;
           const bool work = (t == 0 || (fl & kTwo)) && !(fl & kNoData);
-          const bool ends_block = half == 1 || !(fl & kHalves);
-          if (half == 0) {
-            if (fl & kFirst) {
-              ++seg;
-              ok = ok && mbar_wait(q_full, seg & 1);
-            }
-            ok = ok && mbar_wait(&kv_full[kb], ((2 * n) / kBufs) & 1);
+          const int kb = (2 * n) % kBufs, vb = (2 * n + 1) % kBufs;
+          if (fl & kFirst) {
+            ++seg;
+            ok = mbar_wait(q_full, seg & 1);
+            if (t == 1 && work) ok = ok && mbar_wait(go, seg & 1);
           }
-          if (step >= 2) ok = ok && mbar_wait(&pv_done[2 * t + (step & 1)], ((step >> 1) - 1) & 1);
-          if (!ok) return;
-          uint64_t* full = &s_full[2 * t + (step & 1)];
+          ok = ok && mbar_wait(&kv_full[kb], ((2 * n) / kBufs) & 1);
+          // S takes the place of the previous block's P
+          if (n > 0) ok = ok && mbar_wait(&pv[1], (n - 1) & 1);
+          if (!ok) break;
           if (work) {
             tc::fence_after();
-            const uint64_t kd = tc::desc_kmajor_sw128(smem_u32(smem + kSmKv + kb * kTile + half * 64 * 128));
+            const uint64_t kd = tc::desc_kmajor_sw128(smem_u32(smem + kSmKv + kb * kTile));
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
               const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-              tc::mma_ss(tmem + col_s(t, step), tc::desc_advance(qd, off), tc::desc_advance(kd, off),
-                         kIdescS, kk > 0 ? 1u : 0u);
+              tc::mma_ss(tmem + col_s(t), tc::desc_advance(qd, off), tc::desc_advance(kd, off), kIdescS,
+                         kk > 0 ? 1u : 0u);
             }
-            tc::commit(full);
-            if (ends_block) tc::commit(&kv_empty[kb]);
-            if (ends_block && (fl & kLast)) tc::commit(q_empty);
+            tc::commit(&s_full[t]);
+            tc::commit(&kv_empty[kb]);
+            if (fl & kLast) tc::commit(q_empty);
           } else {
-            mbar_arrive(full);
-            if (ends_block) mbar_arrive(&kv_empty[kb]);
-            if (ends_block && (fl & kLast)) mbar_arrive(q_empty);
+            mbar_arrive(&s_full[t]);
+            mbar_arrive(&kv_empty[kb]);
+            if (fl & kLast) mbar_arrive(q_empty);
           }
-        };
-        auto issue_pv = [&](int step, int pn, int phalf, int pfl, int pseg) {
-          const int vb = (2 * pn + 1) % kBufs;
-          const bool work = (t == 0 || (pfl & kTwo)) && !(pfl & kNoData);
-          const bool ends_block = phalf == 1 || !(pfl & kHalves);
-          const bool first = (pfl & kFirst) && phalf == 0;
-          ok = ok && mbar_wait(&p_full[2 * t + (step & 1)], (step >> 1) & 1);
-          if (phalf == 0) ok = ok && mbar_wait(&kv_full[vb], ((2 * pn + 1) / kBufs) & 1);
-          // O of the previous segment has been read
-          if (first && pseg > 0) ok = ok && mbar_wait(&o_free[t], (pseg - 1) & 1);
-          if (!ok) return;
-          if (work) {
-            tc::fence_after();
-            const uint64_t vd = tc::desc_mnmajor_sw128(
-                smem_u32(smem + kSmKv + vb * kTile + phalf * 64 * 128), kHalf);
+          const uint64_t vd = tc::desc_mnmajor_sw128(smem_u32(smem + kSmKv + vb * kTile), kHalf);
+          for (int half = 0; ok && half < 2; ++half) {
+            ok = mbar_wait(&pf[half], n & 1);
+            if (half == 0) {
+              ok = ok && mbar_wait(&kv_full[vb], ((2 * n + 1) / kBufs) & 1);
+              // O of the previous segment has been read
+              if ((fl & kFirst) && seg > 0) ok = ok && mbar_wait(&o_free[t], (seg - 1) & 1);
+            }
+            if (!ok) break;
+            if (work && (half == 0 || (fl & kHalves))) {
+              tc::fence_after();
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc::mma_ts(tmem + col_o(t), tmem + col_s(t, step) + kk * 8, tc::desc_advance(vd, kk * 2048),
-                         kIdescO, (kk > 0 || !first) ? 1u : 0u);
-            tc::commit(&pv_done[2 * t + (step & 1)]);
-            if (ends_block) tc::commit(&kv_empty[vb]);
-          } else {
-            mbar_arrive(&pv_done[2 * t + (step & 1)]);
-            if (ends_block) mbar_arrive(&kv_empty[vb]);
+              for (int kk = 0; kk < 4; ++kk)
+                tc::mma_ts(tmem + col_o(t), tmem + col_s(t) + half * 32 + kk * 8,
+                           tc::desc_advance(vd, (half * 4 + kk) * 2048), kIdescO,
+                           (kk > 0 || half > 0 || !(fl & kFirst)) ? 1u : 0u);
+              tc::commit(&pv[half]);
+            } else if (work) {
+              tc::commit(&pv[half]);  // (after the first half's products)
+            } else {
+              mbar_arrive(&pv[half]);
+            }
           }
-        };
-        int step = 0;
-        bool more = advance();
-        if (more) issue_s(0);
-        while (ok && more) {
-          const int pn = n, phalf = half, pfl = fl, pseg = seg;
-          more = advance();
-          // (a new segment's queries arrive after this one's last S: P V first)
-          const bool late = more && (fl & kFirst) && half == 0;
-          if (ok && more && !late) issue_s(step + 1);
-          if (ok) issue_pv(step, pn, phalf, pfl, pseg);
-          if (ok && late) issue_s(step + 1);
-          ++step;
+          if (!ok) break;
+          if (work) tc::commit(&kv_empty[vb]);
+          else mbar_arrive(&kv_empty[vb]);
         }
         if (!ok) misc[0] = 1;
         // every product has completed before the tensor memory is freed
-        if (step > 0 && !mbar_wait(&pv_done[2 * t + ((step - 1) & 1)], ((step - 1) >> 1) & 1)) misc[0] = 1;
+        if (n > 0 && !mbar_wait(&pv[1], (n - 1) & 1)) misc[0] = 1;
       }
     } else if (FP8 && warp >= 12) {
       // ---------------------------------------------- e4m3 tiles to f16, queries
@@ -625,7 +601,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
       // PTH: P carries its token's v scale over a power of two that only grows,
       // so that it keeps its range in 16 bits whatever the scales
       float vref = 0.f;
-      int x = 1, seg = -1, step = 0;
+      int x = 1, seg = -1;
       bool bad = false, ok = true;
       for (int n = 0;; ++n) {
         ok = warp_wait(&info_full[n % kInfos], (n / kInfos) & 1);
@@ -676,14 +652,13 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
             vref = nr;
           }
         }
-        const int halves = (fl & kHalves) ? 2 : 1;
+        ok = warp_wait(&s_full[t], n & 1);
+        if (!ok) break;
 #pragma unroll 1
-        for (int half = 0; half < halves; ++half, ++step) {
-          ok = warp_wait(&s_full[2 * t + (step & 1)], (step >> 1) & 1);
-          if (!ok) break;
-          if (work) {
+        for (int half = 0; half < 2; ++half) {
+          if (work && (half == 0 || (fl & kHalves))) {
             tc::fence_after();
-            const uint32_t sa = tmem + lanes + col_s(t, step);
+            const uint32_t sa = tmem + lanes + col_s(t) + 64 * half;
             const uint32_t v0 = half ? vis[2] : vis[0], v1 = half ? vis[3] : vis[1];
             const float* kh = PTH ? ks + 64 * half : nullptr;
             uint32_t r[64];
@@ -709,7 +684,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
               grow = 1.f;
               // (a row without a reference has an all-zero O: nothing to rescale)
               if (!((fl & kFirst) && half == 0) && __any_sync(0xffffffffu, al != 1.f)) {
-                ok = warp_wait(&pv_done[2 * t + ((step - 1) & 1)], ((step - 1) >> 1) & 1);
+                ok = half ? warp_wait(&pv_done[2 * t], n & 1) : warp_wait(&pv_done[2 * t + 1], (n - 1) & 1);
                 if (!ok) break;
                 tc::fence_after();
 #pragma unroll 1
@@ -729,8 +704,10 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
               base += (float)((int)(__float_as_uint(unit) >> 23) - 127);
             }
             const float* vh = PTH ? kh + 128 : nullptr;
-            l_run += unit * (masked ? exp64<true, FP8, PTH>(r, sa, scale2, base, v0, v1, kh, vh)
-                                    : exp64<false, FP8, PTH>(r, sa, scale2, base, v0, v1, kh, vh));
+            // P of the halves side by side, over logits that have been read
+            const uint32_t pa = tmem + lanes + col_s(t) + 32 * half;
+            l_run += unit * (masked ? exp64<true, FP8, PTH>(r, pa, scale2, base, v0, v1, kh, vh)
+                                    : exp64<false, FP8, PTH>(r, pa, scale2, base, v0, v1, kh, vh));
             tc::tmem_wait_st();
             tc::fence_before();
           }
@@ -756,14 +733,16 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
               *reinterpret_cast<volatile int*>(&misc[4 + seg % 3]) = 1;
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[2 * t + (step & 1)]);
+          if (lane == 0) {
+            mbar_arrive(&p_full[2 * t + half]);
+            if (t == 0 && half == 0 && (fl & kFirst)) mbar_arrive(go);
+          }
         }
         if (!ok) break;
         if (fl & kLast) {
           // both tiles' warps have looked over the segment's blocks
           if (lane == 0) mbar_arrive(ends);
-          ok = warp_wait(ends, seg & 1) &&
-               warp_wait(&pv_done[2 * t + ((step - 1) & 1)], ((step - 1) >> 1) & 1);
+          ok = warp_wait(ends, seg & 1) && warp_wait(&pv_done[2 * t + 1], n & 1);
           if (!ok) break;
           const bool odd = *reinterpret_cast<volatile int*>(&misc[4 + seg % 3]) != 0;
           if (warp == 4 && lane == 0) *reinterpret_cast<volatile int*>(&misc[4 + (seg + 2) % 3]) = 0;
