@@ -5,20 +5,22 @@
 // Selection.  Orderable 32-bit keys of the masses (NaN lowest, -0 = +0), a
 // radix selection of the need-th largest by digits of 11, 11 and 10 bits, then
 // an ordered pass that keeps keys above it and the first of those equal to it.
-// One thread-block cluster per request: each CTA reads its share of the tokens
-// once, keeps the keys in shared memory for the later passes, and the cluster
-// adds up its histograms through distributed shared memory.  The masses are
-// 4 bytes a token, so the pass over memory is short and the time is the chain
-// of cluster barriers and histogram scans, not bandwidth.
+// One thread-block cluster per request; each CTA reads its share of the tokens
+// once, into registers (large shares into shared memory), a warp a contiguous run of them.  The masses are 4
+// bytes a token, so the time is not bandwidth but the chain of histograms and
+// cluster barriers: each pass counts in shared memory, adds its counts that are
+// not zero to every CTA of the cluster, and needs one barrier; tokens of weight
+// zero, often a large part, are counted by ballot instead of 32 adds to one bin.
 #include "tree_common.cuh"
 
 namespace msa {
 namespace {
 
-constexpr int kEvThreads = 1024;
+constexpr int kEvThreads = 512;
+constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvBins = 2048;
-constexpr int kEvKeys = 52 * 1024;  // keys that a CTA's shared memory holds
 constexpr int kEvMaxCluster = 16;
+constexpr uint32_t kZeroKey = 0x80000000u;  // of a weight of 0
 
 __device__ __forceinline__ bool bad_pages(const msa_cache_view& c, int r, int nb, int nt) {
   bool bad = false;
@@ -29,181 +31,224 @@ __device__ __forceinline__ bool bad_pages(const msa_cache_view& c, int r, int nb
   return __syncthreads_or(bad) != 0;
 }
 
-// inclusive sum over the CTA's threads; *total: the sum over all.  scratch: 33 ints
-__device__ __forceinline__ int cta_scan(int v, int* scratch, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int n = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += n;
-  }
-  if (lane == 31) scratch[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    int x = scratch[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += n;
-    }
-    scratch[lane] = x;
-  }
-  __syncthreads();
-  *total = scratch[31];
-  const int before = warp ? scratch[warp - 1] : 0;
-  __syncthreads();
-  return before + v;
+__device__ __forceinline__ void red_dsmem_add(uint32_t addr, int v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// grid: (cluster, requests), one cluster per request
-__global__ void __launch_bounds__(kEvThreads, 1) evict_select_kernel(const EvictLaunch p, int cap) {
-  extern __shared__ uint32_t s_key[];  // [cap]
-  __shared__ int hist[kEvBins];
-  __shared__ int s_scan[33];
-  __shared__ int s_digit, s_left, s_above, s_eq;
-  __shared__ int s_wa[32], s_we[32];
+// grid: (cluster, requests), one cluster per request.  KEYS: keys a thread
+// holds in registers (a CTA's share has at most kEvThreads * KEYS tokens);
+// kInShared: in shared memory; 0: none, they are read again in every pass.
+constexpr int kInShared = -1;
+constexpr int kSharedKeys = 44 * 1024;
+template <int KEYS>
+__global__ void __launch_bounds__(kEvThreads, KEYS > 0 ? 2 : 1)
+    evict_select_kernel(const EvictLaunch p) {
+  extern __shared__ uint32_t s_key[];  // KEYS == kInShared
+  // counts of this CTA, and of the cluster, for each digit
+  __shared__ int hist[2][kEvBins];
+  __shared__ int total[3][kEvBins];
+  __shared__ int s_scan[kEvWarps], s_digit, s_left, s_bad, s_count[2];
+  __shared__ int s_wa[kEvWarps], s_we[kEvWarps];
   const int r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x, C = gridDim.x;
+  const unsigned all = 0xffffffffu;
   const msa_cache_view& cv = p.cache;
   int32_t* keep = p.keep + (long long)r * p.budget;
   const int L = cv.lens[r];
-  uint32_t bad = 0;
-  if (L < 0 || (long long)L > (long long)kBlock * cv.bt_stride) bad = MSA_DEV_MALFORMED;
-  else if (bad_pages(cv, r, (L + kBlock - 1) / kBlock, kEvThreads)) bad = MSA_DEV_BAD_PAGE;
-  const int kl = bad ? 0 : min(L, p.budget);
-  const int all = C * kEvThreads, me = rank * kEvThreads + tid;
-  if (me == 0) {
-    p.keep_len[r] = bad ? -1 : kl;
-    if (bad) atomicOr(p.status, bad);
+  const bool malformed = L < 0 || (long long)L > (long long)kBlock * cv.bt_stride;
+  for (int i = tid; i < 3 * kEvBins; i += kEvThreads) {
+    (&total[0][0])[i] = 0;
+    if (i < 2 * kEvBins) (&hist[0][0])[i] = 0;
   }
-  for (int i = kl + me; i < p.budget; i += all) keep[i] = -1;
-  if (bad) return;
-  if (L <= p.budget) {
-    for (int i = me; i < L; i += all) keep[i] = i;
-    return;
-  }
-  // this CTA's tokens: whole blocks, [t0, t1)
-  const int nb = (L + kBlock - 1) / kBlock;
-  const int per = (nb + C - 1) / C * kBlock;
-  const int t0 = min(L, rank * per), t1 = min(L, t0 + per);
+  if (tid == 0) s_bad = 0;
+  // every CTA of the cluster runs and is cleared before another adds to it
+  if (C > 1) cluster_sync();
+  else __syncthreads();
+
+  // ---- this warp's run of tokens, [w0, w1): whole groups of 32
+  const int per = malformed ? 0 : (L + C - 1) / C;
+  const int sub = (per + kEvWarps * 32 - 1) / (kEvWarps * 32) * 32;
+  const long long first = ((long long)rank * kEvWarps + warp) * sub;
+  const int w0 = malformed ? 0 : (int)min((long long)L, first), w1 = malformed ? 0 : min(L, w0 + sub);
   const int lo = p.first, hi = L - p.recent;  // those that are ranked: [lo, hi)
   const int need = p.budget - p.first - p.recent;
   const int32_t* bt = cv.block_table + (long long)r * cv.bt_stride;
-  const bool held = per <= cap;
-  auto load_key = [&](int t) {
-    return score_key(__ldg(p.mass + (long long)__ldg(bt + t / kBlock) * kBlock + t % kBlock));
+  bool bad = false;
+  auto load_key = [&](int t) -> uint32_t {
+    const int page = __ldg(bt + t / kBlock);
+    if (page < 0 || page >= cv.num_pages) {
+      bad = true;
+      return 0u;
+    }
+    return score_key(__ldg(p.mass + (long long)page * kBlock + t % kBlock));
   };
-  auto key_at = [&](int t) { return held ? s_key[t - t0] : load_key(t); };
-  if (held && need > 0) {
-#pragma unroll 4
-    for (int t = t0 + tid; t < t1; t += kEvThreads) s_key[t - t0] = load_key(t);
+  uint32_t keys[KEYS > 0 ? KEYS : 1];
+  uint32_t* run = s_key + warp * sub + lane;  // this lane's column of the warp's run
+  if constexpr (KEYS > 0) {
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i) {
+      const int t = w0 + 32 * i + lane;
+      keys[i] = t < w1 ? load_key(t) : 0u;
+    }
+  } else if constexpr (KEYS == kInShared) {
+#pragma unroll 8
+    for (int t = w0; t < w1; t += 32) run[t - w0] = t + lane < w1 ? load_key(t + lane) : 0u;
+  } else {
+    for (int t = w0 + lane; t < w1; t += 32) load_key(t);
   }
-  const int a = max(lo, t0), b = min(hi, t1);
+  // f(t, key) for each of this thread's tokens, whole warps at a time
+  auto each = [&](auto f) {
+    if constexpr (KEYS > 0) {
+#pragma unroll
+      for (int i = 0; i < KEYS; ++i) {
+        if (w0 + 32 * i >= w1) break;
+        f(w0 + 32 * i + lane, keys[i]);
+      }
+    } else if constexpr (KEYS == kInShared) {
+#pragma unroll 4
+      for (int t = w0; t < w1; t += 32) f(t + lane, run[t - w0]);
+    } else {
+      for (int t = w0; t < w1; t += 32) f(t + lane, t + lane < w1 ? load_key(t + lane) : 0u);
+    }
+  };
+  if (__any_sync(all, bad) && lane == 0) {
+    for (int c = 0; c < C; ++c) st_dsmem_s32(mapa_shared(smem_u32(&s_bad), c), 1);
+  }
+
   uint32_t prefix = 0;
   int left = need;  // how many of the keys that match the prefix are kept
-  if (need > 0) {
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const uint32_t mask = pass == 2 ? 1023u : 2047u;
-      for (int i = tid; i < kEvBins; i += kEvThreads) hist[i] = 0;
-      __syncthreads();
-      for (int t = a + tid; t < b; t += kEvThreads) {
-        const uint32_t k = key_at(t);
-        const int up = pass == 1 ? 21 : 10;  // the digits already fixed lie above
-        if (pass == 0 || (k >> up) == (prefix >> up)) atomicAdd(&hist[(k >> shift) & mask], 1);
+  const bool rank_them = !malformed && need > 0 && L > p.budget;
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, up = pass == 1 ? 21 : 10;
+    const uint32_t mask = pass == 2 ? 1023u : 2047u;
+    if (rank_them) {
+      if (pass == 2) {  // the first digit's counts again
+        for (int i = tid; i < kEvBins; i += kEvThreads) hist[0][i] = 0;
+        __syncthreads();
       }
-      if (C > 1) cluster_sync();
-      else __syncthreads();
-      // the cluster's counts of two bins per thread, largest digit first
-      int n[2] = {0, 0};
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int bin = kEvBins - 1 - (2 * tid + k);
-        if (C > 1) {
-          const uint32_t at = smem_u32(&hist[bin]);
-          for (int c = 0; c < C; ++c) n[k] += ld_dsmem_s32(mapa_shared(at, c));
-        } else {
-          n[k] = hist[bin];
+      int zeros = 0;
+      each([&](int t, uint32_t k) {
+        const bool in = t >= lo && t < hi && t < w1 && (pass == 0 || (k >> up) == (prefix >> up));
+        const bool zero = in && k == kZeroKey;
+        zeros += __popc(__ballot_sync(all, zero));
+        if (in && !zero) atomicAdd(&hist[pass & 1][(k >> shift) & mask], 1);
+      });
+      if (zeros && lane == 0) atomicAdd(&hist[pass & 1][(kZeroKey >> shift) & mask], zeros);
+      __syncthreads();
+      for (int i = tid; i < kEvBins; i += kEvThreads) {
+        const int n = hist[pass & 1][i];
+        if (n) {
+          const uint32_t at = smem_u32(&total[pass][i]);
+          for (int c = 0; c < C; ++c) red_dsmem_add(mapa_shared(at, c), n);
         }
       }
-      int total;
-      const int upto = cta_scan(n[0] + n[1], s_scan, &total);
-      const int before = upto - n[0] - n[1];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int x = k ? before + n[0] : before;
-        if (x < left && x + n[k] >= left) {
-          s_digit = kEvBins - 1 - (2 * tid + k);
-          s_left = left - x;
-        }
-      }
-      __syncthreads();
-      prefix |= (uint32_t)s_digit << shift;
-      left = s_left;
-      // no CTA clears its counts while another still reads them
-      if (C > 1) cluster_sync();
-      else __syncthreads();
     }
+    if (C > 1) cluster_sync();
+    else __syncthreads();
+    if (pass == 0) {
+      // (every CTA's pages have been looked at)
+      const uint32_t why = malformed ? MSA_DEV_MALFORMED : s_bad ? MSA_DEV_BAD_PAGE : 0u;
+      const int kl = why ? 0 : min(L, p.budget);
+      const int everyone = C * kEvThreads, me = rank * kEvThreads + tid;
+      if (me == 0) {
+        p.keep_len[r] = why ? -1 : kl;
+        if (why) atomicOr(p.status, why);
+      }
+      for (int i = kl + me; i < p.budget; i += everyone) keep[i] = -1;
+      if (!why && L <= p.budget)
+        for (int i = me; i < L; i += everyone) keep[i] = i;
+      if (why || L <= p.budget) {
+        // no CTA leaves while another may still add to it
+        if (C > 1) cluster_sync();
+        return;
+      }
+    }
+    if (!rank_them) continue;
+    // the digit, from the largest down: 4 bins a thread
+    int n[4], sum = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      n[k] = total[pass][kEvBins - 1 - (4 * tid + k)];
+      sum += n[k];
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(all, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) s_scan[warp] = inc;
+    __syncthreads();
+    int at = inc - sum;
+    for (int w = 0; w < warp; ++w) at += s_scan[w];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (at < left && at + n[k] >= left) {
+        s_digit = kEvBins - 1 - (4 * tid + k);
+        s_left = left - at;
+      }
+      at += n[k];
+    }
+    __syncthreads();
+    prefix |= (uint32_t)s_digit << shift;
+    left = s_left;
   }
-  // ordered pass: a warp takes a contiguous part of the CTA's tokens, counts
-  // what it keeps and what equals the border, then writes behind the others
-  const int sub = (per / 32 + 31) / 32 * 32;
-  const int w0 = min(t1, t0 + warp * sub), w1 = min(t1, w0 + sub);
-  auto classify = [&](int t, bool& above, bool& eq) {
-    above = eq = false;
-    if (t < w1) {
-      if (t < lo || t >= hi) above = true;
-      else if (need > 0) {
-        const uint32_t k = key_at(t);
-        above = k > prefix;
-        eq = k == prefix;
-      }
-    }
+
+  // ---- ordered pass: count what each warp keeps and what equals the border,
+  // then write behind the others
+  auto classify = [&](int t, uint32_t k, unsigned& ba, unsigned& be) {
+    const bool forced = t < lo || t >= hi;
+    ba = __ballot_sync(all, t < w1 && (forced || (need > 0 && k > prefix)));
+    be = __ballot_sync(all, t < w1 && !forced && need > 0 && k == prefix);
   };
   int n_above = 0, n_eq = 0;
-  for (int t = w0; t < w1; t += 32) {
-    bool above, eq;
-    classify(t + lane, above, eq);
-    n_above += __popc(__ballot_sync(0xffffffffu, above));
-    n_eq += __popc(__ballot_sync(0xffffffffu, eq));
-  }
+  each([&](int t, uint32_t k) {
+    unsigned ba, be;
+    classify(t, k, ba, be);
+    n_above += __popc(ba);
+    n_eq += __popc(be);
+  });
   if (lane == 0) {
     s_wa[warp] = n_above;
     s_we[warp] = n_eq;
   }
   __syncthreads();
-  int above_before = 0, eq_before = 0, above_cta = 0, eq_cta = 0;
-  for (int w = 0; w < 32; ++w) {
+  int above = 0, eq = 0, above_cta = 0, eq_cta = 0;
+#pragma unroll
+  for (int w = 0; w < kEvWarps; ++w) {
     if (w < warp) {
-      above_before += s_wa[w];
-      eq_before += s_we[w];
+      above += s_wa[w];
+      eq += s_we[w];
     }
     above_cta += s_wa[w];
     eq_cta += s_we[w];
   }
   if (C > 1) {
     if (tid == 0) {
-      s_above = above_cta;
-      s_eq = eq_cta;
+      s_count[0] = above_cta;
+      s_count[1] = eq_cta;
     }
     cluster_sync();
-    for (int c = 0; c < rank; ++c) {
-      above_before += ld_dsmem_s32(mapa_shared(smem_u32(&s_above), c));
-      eq_before += ld_dsmem_s32(mapa_shared(smem_u32(&s_eq), c));
+    // lane c reads CTA c's counts (C <= 16)
+    int a = 0, e = 0;
+    if (lane < rank) {
+      a = ld_dsmem_s32(mapa_shared(smem_u32(&s_count[0]), lane));
+      e = ld_dsmem_s32(mapa_shared(smem_u32(&s_count[1]), lane));
     }
+    above += __reduce_add_sync(all, a);
+    eq += __reduce_add_sync(all, e);
   }
-  for (int t = w0; t < w1; t += 32) {
-    bool above, eq;
-    classify(t + lane, above, eq);
-    const unsigned be = __ballot_sync(0xffffffffu, eq), ba = __ballot_sync(0xffffffffu, above);
+  each([&](int t, uint32_t k) {
+    unsigned ba, be;
+    classify(t, k, ba, be);
     const unsigned below = (1u << lane) - 1u;
-    const int eq_at = eq_before + __popc(be & below);
+    const int eq_at = eq + __popc(be & below);
     // kept before this token: those above the border, and the first `left` equal to it
-    if (above || (eq && eq_at < left))
-      keep[above_before + __popc(ba & below) + min(eq_at, left)] = t + lane;
-    above_before += __popc(ba);
-    eq_before += __popc(be);
-  }
+    if ((ba >> lane & 1u) || ((be >> lane & 1u) && eq_at < left))
+      keep[above + __popc(ba & below) + min(eq_at, left)] = t;
+    above += __popc(ba);
+    eq += __popc(be);
+  });
   // no CTA leaves while another reads its counts
   if (C > 1) cluster_sync();
 }
@@ -327,45 +372,59 @@ __global__ void __launch_bounds__(kCpThreads) kv_compact_kernel(const CompactLau
 
 }  // namespace
 
-// CTAs per request: enough that one holds about 4096 tokens, while the grid
-// fits the GPU about twice; 16 (beyond the portable 8) where the device can
-// place such a cluster.
+// CTAs per request: as many as leave each 2048 tokens or more while the grid
+// fits the GPU at once; 16 (beyond the portable 8) where the device can place
+// such a cluster.  Then the fewest registers that hold the share.
+template <int KEYS>
+cudaError_t launch_evict(const EvictLaunch& p, int C, long long share, cudaStream_t stream,
+                         bool* placed) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(C, p.cache.num_reqs);
+  cfg.blockDim = dim3(kEvThreads);
+  cfg.stream = stream;
+  if (KEYS == kInShared) {
+    // (a share, rounded up to 32 tokens a warp)
+    cfg.dynamicSmemBytes = ((size_t)((share + kEvThreads - 1) / kEvThreads) * kEvThreads) * 4;
+    const cudaError_t e = cudaFuncSetAttribute(
+        evict_select_kernel<KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedKeys * 4);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  *placed = true;
+  if (C > 8) {
+    const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<KEYS>,
+                                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    int fit = 0;
+    if (cudaOccupancyMaxActiveClusters(&fit, evict_select_kernel<KEYS>, &cfg) != cudaSuccess || fit < 1) {
+      cudaGetLastError();
+      *placed = false;
+      return cudaSuccess;
+    }
+  }
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<KEYS>, p);
+}
+
 cudaError_t launch_evict_select(const EvictLaunch& p, cudaStream_t stream) {
   const long long most = (long long)p.cache.bt_stride * kBlock;
-  const int sms = device_sm_count();
   int C = 1;
-  while (C < kEvMaxCluster && most > 4096ll * C && (long long)p.cache.num_reqs * C * 2 <= 2ll * sms) C *= 2;
+  while (C < kEvMaxCluster && most >= 4096ll * C && (long long)p.cache.num_reqs * C <= device_sm_count())
+    C *= 2;
   for (;; C /= 2) {
-    const long long per = (most / kBlock + C - 1) / C * kBlock;
-    const int cap = (int)min(per, (long long)kEvKeys);
-    const size_t bytes = (size_t)cap * 4;
-    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kEvKeys * 4);
-    if (e != cudaSuccess) return e;
-    if (C > 8) {
-      e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-      if (e != cudaSuccess) return e;
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(C, p.cache.num_reqs);
-    cfg.blockDim = dim3(kEvThreads);
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = C;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (C > 8) {
-      int fit = 0;
-      if (cudaOccupancyMaxActiveClusters(&fit, evict_select_kernel, &cfg) != cudaSuccess || fit < 1) {
-        cudaGetLastError();
-        continue;
-      }
-    }
-    return cudaLaunchKernelEx(&cfg, evict_select_kernel, p, cap);
+    const long long share = (most + C - 1) / C;
+    bool placed;
+    cudaError_t e;
+    if (share <= 4 * kEvThreads) e = launch_evict<4>(p, C, share, stream, &placed);
+    else if (share <= 16 * kEvThreads) e = launch_evict<16>(p, C, share, stream, &placed);
+    else if (share <= kSharedKeys) e = launch_evict<kInShared>(p, C, share, stream, &placed);
+    else e = launch_evict<0>(p, C, share, stream, &placed);
+    if (placed) return e;
   }
 }
 
