@@ -16,11 +16,10 @@
 namespace msa {
 namespace {
 
-constexpr int kEvThreads = 512;
-constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvBins = 2048;
 constexpr int kEvMaxCluster = 16;
-constexpr uint32_t kZeroKey = 0x80000000u;  // of a weight of 0
+constexpr uint32_t kZeroKey = 0x80000000u;    // of a weight of 0
+constexpr uint32_t kForcedKey = 0xffffffffu;  // above every weight's: always kept
 
 __device__ __forceinline__ bool bad_pages(const msa_cache_view& c, int r, int nb, int nt) {
   bool bad = false;
@@ -36,13 +35,20 @@ __device__ __forceinline__ void red_dsmem_add(uint32_t addr, int v) {
 }
 
 // grid: (cluster, requests), one cluster per request.  KEYS: keys a thread
-// holds in registers (a CTA's share has at most kEvThreads * KEYS tokens);
+// holds in registers (a CTA's share has at most its threads * KEYS tokens);
 // kInShared: in shared memory; 0: none, they are read again in every pass.
 constexpr int kInShared = -1;
 constexpr int kSharedKeys = 44 * 1024;
 template <int KEYS>
-__global__ void __launch_bounds__(kEvThreads, KEYS > 0 ? 2 : 1)
+struct EvCfg {
+  static constexpr int kThreads = KEYS > 0 ? 512 : 1024;
+};
+
+template <int KEYS>
+__global__ void __launch_bounds__(EvCfg<KEYS>::kThreads, KEYS > 0 ? 2 : 1)
     evict_select_kernel(const EvictLaunch p) {
+  constexpr int kEvThreads = EvCfg<KEYS>::kThreads, kEvWarps = kEvThreads / 32;
+  constexpr int kBinsPer = kEvBins / kEvThreads;
   extern __shared__ uint32_t s_key[];  // KEYS == kInShared
   // counts of this CTA, and of the cluster, for each digit
   __shared__ int hist[2][kEvBins];
@@ -74,27 +80,36 @@ __global__ void __launch_bounds__(kEvThreads, KEYS > 0 ? 2 : 1)
   const int need = p.budget - p.first - p.recent;
   const int32_t* bt = cv.block_table + (long long)r * cv.bt_stride;
   bool bad = false;
-  auto load_key = [&](int t) -> uint32_t {
-    const int page = __ldg(bt + t / kBlock);
-    if (page < 0 || page >= cv.num_pages) {
-      bad = true;
-      return 0u;
+  // The keys of tokens [t, t + 32 n) of the warp's run, n <= 16: the pages of
+  // all of them at once, a lane each, then the weights at once (a bad page
+  // reads page 0's, and is noted; there is none without pages).
+  auto load = [&](int t, int n, auto put) {
+    int page = 0;
+    if (lane < n && t + 32 * lane < w1) {
+      page = __ldg(bt + (t + 32 * lane) / kBlock);
+      if (page < 0 || page >= cv.num_pages) {
+        bad = true;
+        page = 0;
+      }
     }
-    return score_key(__ldg(p.mass + (long long)page * kBlock + t % kBlock));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (i >= n) break;
+      const int pg = __shfl_sync(all, page, i), at = t + 32 * i + lane;
+      const bool there = at < w1 && cv.num_pages > 0;
+      const float m = there ? __ldg(p.mass + (long long)pg * kBlock + at % kBlock) : 0.f;
+      put(i, at < lo || at >= hi ? kForcedKey : score_key(m));
+    }
   };
   uint32_t keys[KEYS > 0 ? KEYS : 1];
   uint32_t* run = s_key + warp * sub + lane;  // this lane's column of the warp's run
   if constexpr (KEYS > 0) {
-#pragma unroll
-    for (int i = 0; i < KEYS; ++i) {
-      const int t = w0 + 32 * i + lane;
-      keys[i] = t < w1 ? load_key(t) : 0u;
-    }
-  } else if constexpr (KEYS == kInShared) {
-#pragma unroll 8
-    for (int t = w0; t < w1; t += 32) run[t - w0] = t + lane < w1 ? load_key(t + lane) : 0u;
+    load(w0, KEYS, [&](int i, uint32_t k) { keys[i] = k; });
   } else {
-    for (int t = w0 + lane; t < w1; t += 32) load_key(t);
+    for (int t = w0; t < w1; t += 512)
+      load(t, min(16, (w1 - t + 31) / 32), [&](int i, uint32_t k) {
+        if (KEYS == kInShared) run[t - w0 + 32 * i] = k;
+      });
   }
   // f(t, key) for each of this thread's tokens, whole warps at a time
   auto each = [&](auto f) {
@@ -108,7 +123,8 @@ __global__ void __launch_bounds__(kEvThreads, KEYS > 0 ? 2 : 1)
 #pragma unroll 4
       for (int t = w0; t < w1; t += 32) f(t + lane, run[t - w0]);
     } else {
-      for (int t = w0; t < w1; t += 32) f(t + lane, t + lane < w1 ? load_key(t + lane) : 0u);
+      for (int t = w0; t < w1; t += 32)
+        load(t, 1, [&](int, uint32_t k) { f(t + lane, k); });
     }
   };
   if (__any_sync(all, bad) && lane == 0) {
@@ -128,7 +144,7 @@ __global__ void __launch_bounds__(kEvThreads, KEYS > 0 ? 2 : 1)
       }
       int zeros = 0;
       each([&](int t, uint32_t k) {
-        const bool in = t >= lo && t < hi && t < w1 && (pass == 0 || (k >> up) == (prefix >> up));
+        const bool in = t < w1 && (pass == 0 ? k != kForcedKey : (k >> up) == (prefix >> up));
         const bool zero = in && k == kZeroKey;
         zeros += __popc(__ballot_sync(all, zero));
         if (in && !zero) atomicAdd(&hist[pass & 1][(k >> shift) & mask], 1);
@@ -164,11 +180,11 @@ __global__ void __launch_bounds__(kEvThreads, KEYS > 0 ? 2 : 1)
       }
     }
     if (!rank_them) continue;
-    // the digit, from the largest down: 4 bins a thread
-    int n[4], sum = 0;
+    // the digit, from the largest down
+    int n[kBinsPer], sum = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      n[k] = total[pass][kEvBins - 1 - (4 * tid + k)];
+    for (int k = 0; k < kBinsPer; ++k) {
+      n[k] = total[pass][kEvBins - 1 - (kBinsPer * tid + k)];
       sum += n[k];
     }
     int inc = sum;
@@ -182,9 +198,9 @@ __global__ void __launch_bounds__(kEvThreads, KEYS > 0 ? 2 : 1)
     int at = inc - sum;
     for (int w = 0; w < warp; ++w) at += s_scan[w];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kBinsPer; ++k) {
       if (at < left && at + n[k] >= left) {
-        s_digit = kEvBins - 1 - (4 * tid + k);
+        s_digit = kEvBins - 1 - (kBinsPer * tid + k);
         s_left = left - at;
       }
       at += n[k];
@@ -196,10 +212,10 @@ __global__ void __launch_bounds__(kEvThreads, KEYS > 0 ? 2 : 1)
 
   // ---- ordered pass: count what each warp keeps and what equals the border,
   // then write behind the others
+  const uint32_t border = need > 0 ? prefix : kForcedKey - 1;
   auto classify = [&](int t, uint32_t k, unsigned& ba, unsigned& be) {
-    const bool forced = t < lo || t >= hi;
-    ba = __ballot_sync(all, t < w1 && (forced || (need > 0 && k > prefix)));
-    be = __ballot_sync(all, t < w1 && !forced && need > 0 && k == prefix);
+    ba = __ballot_sync(all, t < w1 && k > border);
+    be = __ballot_sync(all, t < w1 && k == border && need > 0);
   };
   int n_above = 0, n_eq = 0;
   each([&](int t, uint32_t k) {
@@ -380,6 +396,7 @@ cudaError_t launch_evict(const EvictLaunch& p, int C, long long share, cudaStrea
                          bool* placed) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(C, p.cache.num_reqs);
+  constexpr int kEvThreads = EvCfg<KEYS>::kThreads;
   cfg.blockDim = dim3(kEvThreads);
   cfg.stream = stream;
   if (KEYS == kInShared) {
@@ -420,8 +437,8 @@ cudaError_t launch_evict_select(const EvictLaunch& p, cudaStream_t stream) {
     const long long share = (most + C - 1) / C;
     bool placed;
     cudaError_t e;
-    if (share <= 4 * kEvThreads) e = launch_evict<4>(p, C, share, stream, &placed);
-    else if (share <= 16 * kEvThreads) e = launch_evict<16>(p, C, share, stream, &placed);
+    if (share <= 4 * EvCfg<4>::kThreads) e = launch_evict<4>(p, C, share, stream, &placed);
+    else if (share <= 16 * EvCfg<16>::kThreads) e = launch_evict<16>(p, C, share, stream, &placed);
     else if (share <= kSharedKeys) e = launch_evict<kInShared>(p, C, share, stream, &placed);
     else e = launch_evict<0>(p, C, share, stream, &placed);
     if (placed) return e;
