@@ -140,12 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
   const TreeSlice sl = tree_slice<kThreads>(
       p,
-      [&](int q) -> long long {
-        TreeReq r = tree_request(p, q);
-        if (r.qlen <= 0) return 0;
-        const int n = tree_visits(p, q, r);
-        return r.bad ? 1 : n * mass_weight(r.qlen * H);
-      },
+      [&](const TreeReq& r, int nv) -> long long { return r.bad ? 1 : nv * mass_weight(r.qlen * H); },
       reinterpret_cast<long long*>(smem));
   fence_proxy_async_smem();
   tc::fence_before();
@@ -161,9 +156,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       int n = 0;  // blocks
       bool ok = true;
       for (int q = sl.q; ok && q < p.batch.num_reqs && pre < sl.end; ++q) {
-        TreeReq rq = tree_request(p, q);
-        if (rq.qlen <= 0) continue;
-        const int nv = tree_visits(p, q, rq);  // 1 for a poisoned request
+        TreeReq rq = sl.first;
+        int nv = sl.visits;
+        if (q != sl.q) {
+          rq = tree_request(p, q);
+          if (rq.qlen <= 0) continue;
+          nv = tree_visits(p, q, rq);  // 1 for a poisoned request
+        }
         const long long w = rq.bad ? 1 : mass_weight(rq.qlen * H);
         const long long first = pre;
         pre += nv * w;

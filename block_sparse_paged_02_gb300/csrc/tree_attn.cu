@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     fence_barrier_init();
   }
   const TreeSlice sl = tree_slice<kTaThreads>(
-      p, [&](int q) { return tree_cost(p, q, tpt); }, s_ll);
+      p, [&](const TreeReq& r, int nv) { return (long long)nv * ((r.qlen + tpt - 1) / tpt); }, s_ll);
   fence_proxy_async_smem();
   __syncthreads();  // scratch is free, barriers are initialised
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -146,12 +146,13 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       return st;
     };
     while (ok && it < sl.end) {
-      TreeReq rq = tree_request(p, q);
-      int nv = 0, tiles = 0;
-      if (rq.qlen > 0) {
-        nv = tree_visits(p, q, rq);
-        tiles = (rq.qlen + tpt - 1) / tpt;
+      TreeReq rq = sl.first;
+      int nv = sl.visits;
+      if (q != sl.q) {
+        rq = tree_request(p, q);
+        nv = rq.qlen > 0 ? tree_visits(p, q, rq) : 0;
       }
+      const int tiles = (rq.qlen + tpt - 1) / tpt;
       const long long cost = (long long)nv * tiles;
       if (it >= pre + cost) {
         pre += cost;
@@ -363,24 +364,41 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             kw[u][0] = a.x; kw[u][1] = a.y; kw[u][2] = a.z; kw[u][3] = a.w;
             kw[u][4] = b.x; kw[u][5] = b.y; kw[u][6] = b.z; kw[u][7] = b.w;
           }
+          // (two chains per n-tile: the even and the odd k-steps)
+          float s2[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
-              mma16816<true>(s[u], qa[kk], e4m3x2_to_f16x2((uint16_t)(kw[u][kk] & 0xffffu)),
+              mma16816<true>(kk & 1 ? s2[u] : s[u], qa[kk], e4m3x2_to_f16x2((uint16_t)(kw[u][kk] & 0xffffu)),
                              e4m3x2_to_f16x2((uint16_t)(kw[u][kk] >> 16)));
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[u][e] += s2[u][e];
         } else {
           const uint32_t kb = smem_u32(ks);
+          uint32_t kf[4][2][4];
 #pragma unroll
           for (int kp = 0; kp < 4; ++kp)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              uint32_t b[4];
               const int row = 16 * slab + 8 * u + (lane & 7), ch = 4 * kp + (lane >> 3);
-              ldsm4(kb + (ch >> 3) * (C::kTile / 2) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), b);
-              mma16816<false>(s[u], qa[2 * kp], b[0], b[1]);
-              mma16816<false>(s[u], qa[2 * kp + 1], b[2], b[3]);
+              ldsm4(kb + (ch >> 3) * (C::kTile / 2) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), kf[kp][u]);
             }
+          // (two chains per n-tile: the even and the odd k-steps)
+          float s2[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+          for (int kp = 0; kp < 4; ++kp)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              mma16816<false>(s[u], qa[2 * kp], kf[kp][u][0], kf[kp][u][1]);
+              mma16816<false>(s2[u], qa[2 * kp + 1], kf[kp][u][2], kf[kp][u][3]);
+            }
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[u][e] += s2[u][e];
         }
         // ---- scale and mask
         uint32_t vis[2] = {0xffffu, 0xffffu};
@@ -530,24 +548,30 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           }
         } else {
           const uint32_t vb = smem_u32(vs);
+          uint32_t vf[8][4];
 #pragma unroll
           for (int jp = 0; jp < 8; ++jp) {
-            uint32_t b[4];
             const int row = 16 * slab + (lane & 15), ch = 2 * jp + (lane >> 4);
-            ldsm4t(vb + (ch >> 3) * (C::kTile / 2) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), b);
-            if (fl & kMixed) {
+            ldsm4t(vb + (ch >> 3) * (C::kTile / 2) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), vf[jp]);
+          }
+          if (fl & kMixed) {
+#pragma unroll
+            for (int jp = 0; jp < 8; ++jp)
 #pragma unroll
               for (int w = 0; w < 4; ++w) {
-                const bool o0 = (b[w] & 0x7f80u) == 0x7f80u, o1 = (b[w] & 0x7f800000u) == 0x7f800000u;
+                uint32_t& b = vf[jp][w];
+                const bool o0 = (b & 0x7f80u) == 0x7f80u, o1 = (b & 0x7f800000u) == 0x7f800000u;
                 odd |= o0 | o1;
-                b[w] &= (o0 ? 0xffff0000u : 0xffffffffu) & (o1 ? 0x0000ffffu : 0xffffffffu);
+                b &= (o0 ? 0xffff0000u : 0xffffffffu) & (o1 ? 0x0000ffffu : 0xffffffffu);
               }
-            }
-            mma16816<false>(o[2 * jp], pa, b[0], b[1]);
-            mma16816<false>(o[2 * jp + 1], pa, b[2], b[3]);
+          }
+#pragma unroll
+          for (int jp = 0; jp < 8; ++jp) {
+            mma16816<false>(o[2 * jp], pa, vf[jp][0], vf[jp][1]);
+            mma16816<false>(o[2 * jp + 1], pa, vf[jp][2], vf[jp][3]);
           }
         }
-        if (__any_sync(full_mask, odd)) {
+        if ((fl & kMixed) && __any_sync(full_mask, odd)) {
 #pragma unroll 1
           for (int t = 0; t < 16; ++t) {
             const int src = (lane & ~3) | ((t & 7) >> 1);
@@ -596,46 +620,95 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         }
       }
       if constexpr (NW > 1) {
+        // The upper half of the token groups hands its sums to the lower half
+        // (lane by lane: who reads a place writes the joined sums back to it);
+        // then all threads join the 64 / M groups left and write the rows.
         float* acc = reinterpret_cast<float*>(smem + C::kSmAcc);
         float2* ml = reinterpret_cast<float2*>(smem + C::kSmMl);
+        // place of accumulator (j, e) in its row: its dim (e4m3: spread over the banks)
+        auto place = [&](int j, int e) {
+          return FP8 ? 33 * c + 16 * e + j : 8 * j + 2 * c + e;
+        };
+        if (nw >= NW / 2) {
 #pragma unroll
-        for (int step = NW / 2; step >= 1; step >>= 1) {
-          if (nw >= step && nw < 2 * step) {
+          for (int hh = 0; hh < 2; ++hh) {
+            const int at = (nw - NW / 2) * M + mrow[hh];
+            if (c == 0) ml[at] = make_float2(m_run[hh], l_run[hh]);
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const int at = (nw - step) * M + mrow[hh];
-              if (c == 0) ml[at] = make_float2(m_run[hh], l_run[hh]);
+            for (int j = 0; j < 16; ++j)
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                *reinterpret_cast<float2*>(acc + at * kAccPad + 8 * j + 2 * c) =
-                    make_float2(o[j][2 * hh], o[j][2 * hh + 1]);
-            }
+              for (int e = 0; e < 2; ++e) acc[at * kAccPad + place(j, e)] = o[j][2 * hh + e];
           }
-          csync();
-          if (nw < step) {
+        }
+        csync();
+        if (nw < NW / 2) {
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const int at = nw * M + mrow[hh];
-              const float2 x = ml[at];
-              const float mn = fmaxf(m_run[hh], x.x), base = mn == -INFINITY ? 0.f : mn;
-              const float fa = ex2_ftz(m_run[hh] - base), fb = ex2_ftz(x.x - base);
-              // (a side that saw nothing has m = -inf and zeros)
-              l_run[hh] = (m_run[hh] == -INFINITY ? l_run[hh] : l_run[hh] * fa) +
-                          (x.x == -INFINITY ? x.y : x.y * fb);
-              const float ga = m_run[hh] == -INFINITY ? 1.f : fa, gb = x.x == -INFINITY ? 1.f : fb;
-              m_run[hh] = mn;
+          for (int hh = 0; hh < 2; ++hh) {
+            const int at = nw * M + mrow[hh];
+            const float2 x = ml[at];
+            const float mn = fmaxf(m_run[hh], x.x), base = mn == -INFINITY ? 0.f : mn;
+            // (a side that saw nothing has m = -inf and zeros)
+            const float ga = m_run[hh] == -INFINITY ? 1.f : ex2_ftz(m_run[hh] - base);
+            const float gb = x.x == -INFINITY ? 1.f : ex2_ftz(x.x - base);
+            __syncwarp();
+            if (c == 0) ml[at] = make_float2(mn, l_run[hh] * ga + x.y * gb);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float2 y = *reinterpret_cast<const float2*>(acc + at * kAccPad + 8 * j + 2 * c);
-                o[j][2 * hh] = o[j][2 * hh] * ga + y.x * gb;
-                o[j][2 * hh + 1] = o[j][2 * hh + 1] * ga + y.y * gb;
+            for (int j = 0; j < 16; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float* y = acc + at * kAccPad + place(j, e);
+                *y = o[j][2 * hh + e] * ga + *y * gb;
+              }
+          }
+        }
+        csync();
+        if (!dead) {
+          constexpr int G = 64 / M, kPer = M / 2;  // groups left; dims of a thread
+          const int m = tid * kPer / kHeadDim, d0 = tid * kPer % kHeadDim;
+          float mg[G], lt = 0.f, mt = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < G; ++i) mt = fmaxf(mt, ml[i * M + m].x);
+          const float base = mt == -INFINITY ? 0.f : mt;
+#pragma unroll
+          for (int i = 0; i < G; ++i) {
+            const float2 x = ml[i * M + m];
+            mg[i] = x.x == -INFINITY ? 1.f : ex2_ftz(x.x - base);
+            lt += x.y * mg[i];
+          }
+          if (m < ntok * H) {
+            const bool whole = (fl & kWhole) != 0, none = bad || (mt == -INFINITY && lt == 0.f);
+            const float sink = p.sinks ? __ldg(p.sinks + m % H) : 0.f;
+            const TreeRowEnd e = tree_row_end(none ? -INFINITY : mt, none ? 0.f : lt, p.sinks != nullptr,
+                                              sink * kTreeLog2e, v_scalar);
+            const long long r = (long long)row0 * H + m;
+            if (whole) {
+              if (d0 == 0) p.lse[r] = none ? (p.sinks ? sink : -INFINITY) : e.lse;
+            } else if (d0 == 0) {
+              p.part_ml[(long long)slot * M + m] = make_float2(mt, lt);
+              if (m == 0) p.part_bad[slot] = bad ? 1 : 0;
+            }
+#pragma unroll
+            for (int d = d0; d < d0 + kPer; d += 4) {
+              float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int i = 0; i < G; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  v[k] += mg[i] * acc[(i * M + m) * kAccPad + (FP8 ? d + k + (d >> 5) : d + k)];
+              if (whole) {
+                const uint2 w = make_uint2(pack_bf16x2(v[0] * e.f, v[1] * e.f), pack_bf16x2(v[2] * e.f, v[3] * e.f));
+                *reinterpret_cast<uint2*>(p.out + r * kHeadDim + d) = none ? make_uint2(0u, 0u) : w;
+              } else {
+                // [4-dim group][row][4 dims]
+                reinterpret_cast<float4*>(p.part_o)[((long long)slot * (kHeadDim / 4) + d / 4) * M + m] =
+                    make_float4(v[0], v[1], v[2], v[3]);
               }
             }
           }
-          csync();
+          if (bad && why && tid == 0) atomicOr(p.status, why);
         }
-      }
-      if (nw == 0 && !dead) {
+        csync();  // read before the next tile's sums overwrite it
+      } else if (!dead) {
         if (bad && why && warp == 0 && lane == 0) atomicOr(p.status, why);
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {

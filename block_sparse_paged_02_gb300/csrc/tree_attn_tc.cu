@@ -221,7 +221,8 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
   }
   if (warp == 1) tc::tmem_alloc(tmem_slot, kTmemCols);
   const TreeSlice sl = tree_slice<kThreads>(
-      p, [&](int q) { return tree_cost(p, q, 2 * tpt); }, reinterpret_cast<long long*>(smem));
+      p, [&](const TreeReq& r, int nv) { return (long long)nv * ((r.qlen + 2 * tpt - 1) / (2 * tpt)); },
+      reinterpret_cast<long long*>(smem));
   fence_proxy_async_smem();
   tc::fence_before();
   __syncthreads();
@@ -281,12 +282,13 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
         }
       };
       while (ok && it < sl.end) {
-        TreeReq rq = tree_request(p, q);
-        int nv = 0, tiles = 0;
-        if (rq.qlen > 0) {
-          nv = tree_visits(p, q, rq);
-          tiles = (rq.qlen + 2 * tpt - 1) / (2 * tpt);
+        TreeReq rq = sl.first;
+        int nv = sl.visits;
+        if (q != sl.q) {
+          rq = tree_request(p, q);
+          nv = rq.qlen > 0 ? tree_visits(p, q, rq) : 0;
         }
+        const int tiles = (rq.qlen + 2 * tpt - 1) / (2 * tpt);
         const long long cost = (long long)nv * tiles;
         if (it >= pre + cost) {
           pre += cost;

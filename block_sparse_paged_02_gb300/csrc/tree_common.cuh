@@ -311,22 +311,15 @@ __device__ __forceinline__ bool tree_vis_token(const TreeLaunch& p, int row, int
   return (__ldg(p.mask + (long long)row * p.mask_words + (i >> 5)) >> (i & 31)) & 1u;
 }
 
-// Items of a request: its tiles of drafted tokens times its visited blocks
-__device__ __forceinline__ long long tree_cost(const TreeLaunch& p, int q, int tok_per_tile) {
-  TreeReq r = tree_request(p, q);
-  if (r.qlen <= 0) return 0;
-  const long long n = tree_visits(p, q, r);
-  return n * ((r.qlen + tok_per_tile - 1) / tok_per_tile);
-}
-
-// The CTA's slice of a flat item list over the requests (cost(q) items for
-// request q): items [begin, end) of total, cut into `ctas` equal parts, none
+// The CTA's slice of a flat item list over the requests (cost(request, its
+// visits) items each): items [begin, end) of total, cut into `ctas` equal parts, none
 // empty (later CTAs idle).  Every thread of the CTA takes part; s_ll: 40 long
 // longs of shared scratch, free again after a barrier.
 struct TreeSlice {
   long long total, begin, end, pre;  // pre: first item of request q
-  int q, ctas;
-  bool tiled;  // cu_seqlens_q tiles [0, num_rows); otherwise the rest is 0
+  int q, ctas, visits;
+  TreeReq first;  // request q, which visits `visits` blocks
+  bool tiled;     // cu_seqlens_q tiles [0, num_rows); otherwise the rest is 0
 };
 
 template <int NT, typename Cost>
@@ -334,60 +327,84 @@ __device__ __forceinline__ TreeSlice tree_slice(const TreeLaunch& p, Cost cost, 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int R = p.batch.num_reqs;
   TreeSlice s;
-  bool ok = p.batch.cu_seqlens_q[0] == 0 && p.batch.cu_seqlens_q[R] == p.batch.num_rows;
-  for (int q = tid; q < R; q += NT) ok &= p.batch.cu_seqlens_q[q + 1] >= p.batch.cu_seqlens_q[q];
-  s.tiled = __syncthreads_and(ok) != 0;
   s.total = s.begin = s.end = s.pre = 0;
   s.q = 0;
   s.ctas = 1;
-  if (!s.tiled) return s;
-  long long mine = 0, keep = 0;
-  for (int q = tid; q < R; q += NT) {
-    keep = cost(q);
-    mine += keep;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) s_ll[warp] = mine;
-  __syncthreads();
-  for (int w = 0; w < NT / 32; ++w) s.total += s_ll[w];
-  s.ctas = (int)max(1ll, min((long long)gridDim.x, s.total));
-  if ((int)blockIdx.x < s.ctas) {
-    s.begin = s.total * blockIdx.x / s.ctas;
-    s.end = s.total * (blockIdx.x + 1) / s.ctas;
-  }
-  __syncthreads();
-  if (s.begin >= s.end) return s;
-  // the request that holds item s.begin
-  long long base = 0;
-  for (int q0 = 0; q0 < R; q0 += NT) {
-    const int q = q0 + tid;
-    long long c = 0;
-    if (q < R) c = R <= NT ? keep : cost(q);
-    long long inc = c;
+  s.visits = 0;
+  // costs and checks of NT requests at a time, their sum by a scan; with few
+  // requests one round gives both the total and the place of the slice
+  bool ok = true;
+  long long inc = 0, c = 0;
+  TreeReq rq;
+  int nv = 0;
+  auto round = [&](int q) {
+    c = 0;
+    if (q < R) {
+      rq = tree_request(p, q);
+      ok &= rq.qlen >= 0 && (q > 0 || rq.q0 == 0) && (q < R - 1 || rq.q0 + rq.qlen == p.batch.num_rows);
+      if (ok && rq.qlen > 0) {
+        nv = tree_visits(p, q, rq);
+        c = cost(rq, nv);
+      }
+    }
+    inc = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long n = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += n;
     }
     if (lane == 31) s_ll[warp] = inc;
-    __syncthreads();
-    long long before = base, sum = 0;
+  };
+  for (int q0 = 0; q0 < R; q0 += NT) {
+    round(q0 + tid);
+    s.tiled = __syncthreads_and(ok) != 0;
+    if (!s.tiled) return s;
+    for (int w = 0; w < NT / 32; ++w) s.total += s_ll[w];
+    if (q0 + NT < R) __syncthreads();
+  }
+  s.ctas = (int)max(1ll, min((long long)gridDim.x, s.total));
+  if ((int)blockIdx.x < s.ctas) {
+    s.begin = s.total * blockIdx.x / s.ctas;
+    s.end = s.total * (blockIdx.x + 1) / s.ctas;
+  }
+  if (s.begin >= s.end) return s;
+  long long base = 0;
+  for (int q0 = 0; q0 < R; q0 += NT) {
+    if (R > NT) {
+      __syncthreads();
+      round(q0 + tid);
+      __syncthreads();
+    }
+    long long before = base;
     for (int w = 0; w < NT / 32; ++w) {
       if (w < warp) before += s_ll[w];
-      sum += s_ll[w];
+      base += s_ll[w];
     }
     const long long pre = before + inc - c;
     if (c > 0 && pre <= s.begin && s.begin < pre + c) {
-      s_ll[32] = q;
+      // the request that holds the slice's first item, for all threads
+      s_ll[32] = q0 + tid;
       s_ll[33] = pre;
+      s_ll[34] = nv;
+      int* g = reinterpret_cast<int*>(s_ll + 35);
+      g[0] = rq.q0;
+      g[1] = rq.qlen;
+      g[2] = rq.ctx;
+      g[3] = rq.nb;
+      g[4] = (int)rq.bad;
     }
-    base += sum;
     __syncthreads();
     if (base > s.begin) break;
   }
+  const int* g = reinterpret_cast<const int*>(s_ll + 35);
   s.q = (int)s_ll[32];
   s.pre = s_ll[33];
+  s.visits = (int)s_ll[34];
+  s.first.q0 = g[0];
+  s.first.qlen = g[1];
+  s.first.ctx = g[2];
+  s.first.nb = g[3];
+  s.first.bad = (uint32_t)g[4];
   return s;
 }
 
