@@ -108,6 +108,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   const unsigned full_mask = 0xffffffffu;
   const int H = p.num_heads;
   const int tpt = M / H;  // drafted tokens per tile
+  __shared__ float s_sink[kMaxHeads];
+  if (tid < H) s_sink[tid] = p.sinks ? __ldg(p.sinks + tid) : 0.f;
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -119,7 +121,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     fence_barrier_init();
   }
   const TreeSlice sl = tree_slice<kTaThreads>(
-      p, [&](const TreeReq& r, int nv) { return (long long)nv * ((r.qlen + tpt - 1) / tpt); }, s_ll);
+      p, [&](const TreeReq& r, int nv) { return tree_items(nv, (r.qlen + tpt - 1) / tpt); }, s_ll);
   fence_proxy_async_smem();
   __syncthreads();  // scratch is free, barriers are initialised
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -153,14 +155,16 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         nv = rq.qlen > 0 ? tree_visits(p, q, rq) : 0;
       }
       const int tiles = (rq.qlen + tpt - 1) / tpt;
-      const long long cost = (long long)nv * tiles;
+      const long long cost = nv > 0 ? tree_items(nv, tiles) : 0;
       if (it >= pre + cost) {
         pre += cost;
         ++q;
         continue;
       }
-      const int tile = (int)((it - pre) / nv), b0 = (int)((it - pre) % nv);
-      const int nb = (int)min((long long)(nv - b0), sl.end - it);
+      const TreeSeg sg = tree_segment(it, sl.end, pre, nv);
+      const int tile = sg.tile, b0 = sg.b0, nb = sg.nb;
+      it = sg.next;
+      if (nb == 0) continue;
       const bool whole = nb == nv;
       StageInfo si;
       si.j0 = tile * tpt;
@@ -172,12 +176,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       si.slot = 2 * blockIdx.x + (b0 > 0 ? 0 : 1);
       si.bad = rq.bad;
       si.rows = nullptr;
-      const long long s = pre + (long long)tile * nv, e = s + nv;
-      if (b0 > 0 && sl.total * (blockIdx.x - 1) / sl.ctas <= s) {
+      if (b0 > 0 && sl.total * (blockIdx.x - 1) / sl.ctas <= sg.first) {
         // second of the CTAs that share this tile: it names them to the merge
         rec.nrows = si.ntok * H;
         rec.row0 = si.row0;
-        rec.last = (int)((e * sl.ctas - 1) / sl.total);
+        rec.last = (int)((sg.end * sl.ctas - 1) / sl.total);
         rec.q = q;
       }
       if (rq.bad) {
@@ -250,7 +253,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         }
       }
       if (!rq.bad) ++n_seg;
-      it += nb;
     }
     if (ok) {
       const int st = acquire();
@@ -646,6 +648,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           for (int hh = 0; hh < 2; ++hh) {
             const int at = nw * M + mrow[hh];
             const float2 x = ml[at];
+            float y[16][2];
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) y[j][e] = acc[at * kAccPad + place(j, e)];
             const float mn = fmaxf(m_run[hh], x.x), base = mn == -INFINITY ? 0.f : mn;
             // (a side that saw nothing has m = -inf and zeros)
             const float ga = m_run[hh] == -INFINITY ? 1.f : ex2_ftz(m_run[hh] - base);
@@ -655,16 +662,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float* y = acc + at * kAccPad + place(j, e);
-                *y = o[j][2 * hh + e] * ga + *y * gb;
-              }
+              for (int e = 0; e < 2; ++e)
+                acc[at * kAccPad + place(j, e)] = o[j][2 * hh + e] * ga + y[j][e] * gb;
           }
         }
         csync();
         if (!dead) {
-          constexpr int G = 64 / M, kPer = M / 2;  // groups left; dims of a thread
-          const int m = tid * kPer / kHeadDim, d0 = tid * kPer % kHeadDim;
+          constexpr int G = 64 / M, T = 256 / M;  // groups left; threads of a row
+          const int m = tid / T, d0 = 4 * (tid % T);
           float mg[G], lt = 0.f, mt = -INFINITY;
 #pragma unroll
           for (int i = 0; i < G; ++i) mt = fmaxf(mt, ml[i * M + m].x);
@@ -677,7 +682,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           }
           if (m < ntok * H) {
             const bool whole = (fl & kWhole) != 0, none = bad || (mt == -INFINITY && lt == 0.f);
-            const float sink = p.sinks ? __ldg(p.sinks + m % H) : 0.f;
+            const float sink = s_sink[m % H];
             const TreeRowEnd e = tree_row_end(none ? -INFINITY : mt, none ? 0.f : lt, p.sinks != nullptr,
                                               sink * kTreeLog2e, v_scalar);
             const long long r = (long long)row0 * H + m;
@@ -688,7 +693,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
               if (m == 0) p.part_bad[slot] = bad ? 1 : 0;
             }
 #pragma unroll
-            for (int d = d0; d < d0 + kPer; d += 4) {
+            for (int d = d0; d < kHeadDim; d += 4 * T) {
               float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
               for (int i = 0; i < G; ++i)

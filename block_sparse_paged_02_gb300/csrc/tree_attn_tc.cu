@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
   }
   if (warp == 1) tc::tmem_alloc(tmem_slot, kTmemCols);
   const TreeSlice sl = tree_slice<kThreads>(
-      p, [&](const TreeReq& r, int nv) { return (long long)nv * ((r.qlen + 2 * tpt - 1) / (2 * tpt)); },
+      p, [&](const TreeReq& r, int nv) { return tree_items(nv, (r.qlen + 2 * tpt - 1) / (2 * tpt)); },
       reinterpret_cast<long long*>(smem));
   fence_proxy_async_smem();
   tc::fence_before();
@@ -289,14 +289,16 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
           nv = rq.qlen > 0 ? tree_visits(p, q, rq) : 0;
         }
         const int tiles = (rq.qlen + 2 * tpt - 1) / (2 * tpt);
-        const long long cost = (long long)nv * tiles;
+        const long long cost = nv > 0 ? tree_items(nv, tiles) : 0;
         if (it >= pre + cost) {
           pre += cost;
           ++q;
           continue;
         }
-        const int tile = (int)((it - pre) / nv), b0 = (int)((it - pre) % nv);
-        const int nb = (int)min((long long)(nv - b0), sl.end - it);
+        const TreeSeg sg = tree_segment(it, sl.end, pre, nv);
+        const int tile = sg.tile, b0 = sg.b0, nb = sg.nb;
+        it = sg.next;
+        if (nb == 0) continue;
         bi.j0 = tile * 2 * tpt;
         bi.ntok = min(2 * tpt, rq.qlen - bi.j0);
         bi.row0 = rq.q0 + bi.j0;
@@ -308,11 +310,10 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
         bi.bad = rq.bad;
         bi.rows = nullptr;
         const int both = (nb == nv ? kWhole : 0) | (bi.ntok > tpt ? kTwo : 0);
-        const long long s = pre + (long long)tile * nv, e = s + nv;
-        if (b0 > 0 && sl.total * (blockIdx.x - 1) / sl.ctas <= s) {
+        if (b0 > 0 && sl.total * (blockIdx.x - 1) / sl.ctas <= sg.first) {
           rec.nrows = bi.ntok * H;
           rec.row0 = bi.row0;
-          rec.last = (int)((e * sl.ctas - 1) / sl.total);
+          rec.last = (int)((sg.end * sl.ctas - 1) / sl.total);
           rec.q = q;
         }
         // (e4m3: the converting warps bring the queries, and pass over empty blocks)
@@ -406,7 +407,6 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
             announce(bi);
           }
         }
-        it += nb;
       }
       if (ok) {
         bi.flags = kEnd;
