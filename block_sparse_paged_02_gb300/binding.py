@@ -328,16 +328,43 @@ def _typed(name: str, t: Optional[torch.Tensor], dtypes, shape=None):
         return
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if shape is not None and (t.ndim != len(shape) or
-                              any(w is not None and w != n for w, n in zip(shape, t.shape))):
+    if shape is not None and t.shape != shape and (
+            t.ndim != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape))):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _here(*tensors: Optional[torch.Tensor]):
-    """The tensors live on the current device, on which the call is enqueued."""
+# The calls of this part are made once per layer and step: pointers go through
+# ctypes as plain integers, and the stream is the current one's raw handle.
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("libmsa takes device tensors")
+    if not t.is_contiguous():
+        raise ValueError("libmsa takes contiguous tensors")
+    return t.data_ptr()
+
+
+def _on(stream, *tensors: Optional[torch.Tensor]) -> int:
+    """The raw stream of a call on the current device, on which its tensors have to live."""
+    device = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
-            raise ValueError(f"tensor on {t.device}, but cuda:{torch.cuda.current_device()} is current")
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensor on {t.device}, but cuda:{device} is current")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _first(struct) -> Optional[torch.Tensor]:
+    """The first tensor behind an argument structure that this module made."""
+    keep = getattr(struct, "_keep", None)
+    return keep[0] if keep else None
+
+
+def _calls() -> ctypes.CDLL:
+    return _lib if _lib is not None else lib()
 
 
 def make_tree(mask: Optional[torch.Tensor] = None,
@@ -354,9 +381,11 @@ def make_tree(mask: Optional[torch.Tensor] = None,
 
 
 def _tree_rows(batch: msa_batch, tree: msa_tree):
-    for name, t in zip(("mask", "topk_idx"), tree._keep):
-        if t is not None and int(t.shape[0]) != batch.num_rows:
-            raise ValueError(f"{name} has {t.shape[0]} rows, the batch {batch.num_rows}")
+    mask, topk_idx = tree._keep
+    if mask is not None and mask.shape[0] != batch.num_rows:
+        raise ValueError(f"mask has {mask.shape[0]} rows, the batch {batch.num_rows}")
+    if topk_idx is not None and topk_idx.shape[0] != batch.num_rows:
+        raise ValueError(f"topk_idx has {topk_idx.shape[0]} rows, the batch {batch.num_rows}")
 
 
 def msa_tree_attn_workspace_size(num_reqs, num_rows, bt_stride, num_heads, max_q_len=0,
@@ -366,17 +395,17 @@ def msa_tree_attn_workspace_size(num_reqs, num_rows, bt_stride, num_heads, max_q
 
 
 def _bytes(t: Optional[torch.Tensor]) -> int:
-    return int(t.numel() * t.element_size()) if t is not None else 0
+    return t.nbytes if t is not None else 0
 
 
 def msa_tree_attn(batch: msa_batch, tree: msa_tree, attn: msa_attn_args, workspace, dev_status,
                   stream=None):
     """Attention of every drafted row over its request's cache (see msa_cache.h)."""
     _tree_rows(batch, tree)
-    _here(dev_status, workspace)
-    _check("msa_tree_attn", lib().msa_tree_attn(
-        ctypes.byref(batch), ctypes.byref(tree), ctypes.byref(attn), _p(workspace),
-        _bytes(workspace), _p(dev_status), _stream(stream)))
+    ws, st = _ptr(workspace), _ptr(dev_status)
+    _check("msa_tree_attn", _calls().msa_tree_attn(
+        ctypes.byref(batch), ctypes.byref(tree), ctypes.byref(attn), ws, _bytes(workspace), st,
+        _on(stream, dev_status, workspace, _first(batch), _first(attn))))
 
 
 def msa_attn_mass(batch: msa_batch, tree: msa_tree, attn: msa_attn_args, mass, workspace,
@@ -385,10 +414,10 @@ def msa_attn_mass(batch: msa_batch, tree: msa_tree, attn: msa_attn_args, mass, w
     log-sum-exps are read from the attention arguments' lse."""
     _tree_rows(batch, tree)
     _typed("mass", mass, (torch.float32,), (batch.num_pages, 128))
-    _here(dev_status, workspace, mass)
-    _check("msa_attn_mass", lib().msa_attn_mass(
-        ctypes.byref(batch), ctypes.byref(tree), ctypes.byref(attn), _p(mass), _p(workspace),
-        _bytes(workspace), _p(dev_status), _stream(stream)))
+    m, ws, st = _ptr(mass), _ptr(workspace), _ptr(dev_status)
+    _check("msa_attn_mass", _calls().msa_attn_mass(
+        ctypes.byref(batch), ctypes.byref(tree), ctypes.byref(attn), m, ws, _bytes(workspace), st,
+        _on(stream, dev_status, workspace, mass, _first(batch), _first(attn))))
 
 
 def make_cache_view(lens, block_table, num_pages: int) -> msa_cache_view:
@@ -408,10 +437,10 @@ def msa_evict_select(cache: msa_cache_view, mass, budget: int, keep_first: int, 
     _typed("mass", mass, (torch.float32,), (cache.num_pages, 128))
     _typed("keep", keep, (torch.int32,), (cache.num_reqs, int(budget)))
     _typed("keep_len", keep_len, (torch.int32,), (cache.num_reqs,))
-    _here(dev_status, mass, keep, keep_len)
-    _check("msa_evict_select", lib().msa_evict_select(
-        ctypes.byref(cache), _p(mass), int(budget), int(keep_first), int(keep_recent), _p(keep),
-        _p(keep_len), _p(dev_status), _stream(stream)))
+    m, k, n, st = _ptr(mass), _ptr(keep), _ptr(keep_len), _ptr(dev_status)
+    _check("msa_evict_select", _calls().msa_evict_select(
+        ctypes.byref(cache), m, int(budget), int(keep_first), int(keep_recent), k, n, st,
+        _on(stream, dev_status, mass, keep, keep_len, _first(cache))))
 
 
 def make_kv_pools(k_cache, v_cache, kv_dtype: int, *, scale_mode: int = MSA_SCALE_NONE,
@@ -447,10 +476,10 @@ def msa_kv_compact(cache: msa_cache_view, base, keep, keep_len, pools: msa_kv_po
     _typed("keep_len", keep_len, (torch.int32,), (cache.num_reqs,))
     if pools._pages != cache.num_pages:
         raise ValueError(f"the pools have {pools._pages} pages, the cache view {cache.num_pages}")
-    _here(dev_status, base, keep, keep_len, pools._keep[0])
-    _check("msa_kv_compact", lib().msa_kv_compact(
-        ctypes.byref(cache), _p(base), _p(keep), int(keep.shape[1]), _p(keep_len),
-        ctypes.byref(pools), _p(dev_status), _stream(stream)))
+    b, k, n, st = _ptr(base), _ptr(keep), _ptr(keep_len), _ptr(dev_status)
+    _check("msa_kv_compact", _calls().msa_kv_compact(
+        ctypes.byref(cache), b, k, keep.shape[1], n, ctypes.byref(pools), st,
+        _on(stream, dev_status, base, keep, keep_len, _first(cache), _first(pools))))
 
 
 def make_trace(after_score=None, after_topk=None, after_attn=None) -> msa_trace:

@@ -23,8 +23,9 @@ constexpr uint32_t kForcedKey = 0xffffffffu;  // above every weight's: always ke
 
 __device__ __forceinline__ bool bad_pages(const msa_cache_view& c, int r, int nb, int nt) {
   bool bad = false;
+#pragma unroll 4
   for (int b = threadIdx.x; b < nb; b += nt) {
-    const int page = c.block_table[(long long)r * c.bt_stride + b];
+    const int page = __ldg(c.block_table + (long long)r * c.bt_stride + b);
     bad |= page < 0 || page >= c.num_pages;
   }
   return __syncthreads_or(bad) != 0;
@@ -356,9 +357,10 @@ __global__ void __launch_bounds__(kCpThreads) kv_compact_kernel(const CompactLau
   if (!bad) {
     const int32_t* keep = p.keep + (long long)r * p.keep_stride;
     bool list_bad = false;
+#pragma unroll 8
     for (int i = tid; i < n; i += kCpThreads) {
-      const int k = keep[i], before = i > 0 ? keep[i - 1] : -1;
-      list_bad |= k <= before || k < 0 || k >= L - base;
+      const int k = __ldg(keep + i), before = __ldg(keep + max(i - 1, 0));
+      list_bad |= (i > 0 && k <= before) || k < 0 || k >= L - base;
     }
     if (__syncthreads_or(list_bad)) bad = MSA_DEV_BAD_TABLE;
   }
