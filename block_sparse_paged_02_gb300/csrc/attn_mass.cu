@@ -74,7 +74,7 @@ __device__ __forceinline__ long long mass_weight(int rows) { return max(20, (row
 // sum over W columns of 2^(s * f + nl) onto acc; MASKED: of those with a set bit
 template <int W, bool MASKED>
 __device__ __forceinline__ void add_exp(uint32_t da, float f, const float* nl, uint32_t bits0,
-                                        uint32_t bits1, float (&acc)[4]) {
+                                        uint32_t bits1, float (&acc)[8]) {
   uint32_t r[W];
   if constexpr (W == 64) tc::tmem_ld64(da, r);
   else tc::tmem_ld16(da, r);
@@ -90,8 +90,9 @@ __device__ __forceinline__ void add_exp(uint32_t da, float f, const float* nl, u
       x[i] = ex2_ftz(x[i]);
       if (MASKED) x[i] = ((t < 32 ? bits0 : bits1) >> ((t + i) & 31)) & 1u ? x[i] : 0.f;
     }
-    add2(acc[0], acc[1], x[0], x[1]);
-    add2(acc[2], acc[3], x[2], x[3]);
+    // (eight sums: with four, the packed adds' latency would bound the loop)
+    add2(acc[t & 4], acc[(t & 4) + 1], x[0], x[1]);
+    add2(acc[(t & 4) + 2], acc[(t & 4) + 3], x[2], x[3]);
   }
 }
 
@@ -398,7 +399,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           int fl = 0, t = 0;
           const uint32_t* sel = nullptr;
           float* slot = nullptr;
-          float f = scale2, old = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+          float f = scale2, old = 0.f;
+          float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
           if (have) {
             const int n = n0 + g + w;
             ok = warp_wait(&info_full[n % kInfos], (n / kInfos) & 1);
@@ -473,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // (a masked token of the block's rows that no row sees adds nothing)
           if (ok && have && t < ctx + qlen) {
-            const float s = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+            const float s = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
             *slot = t < ctx ? old + s : s;
           }
         }

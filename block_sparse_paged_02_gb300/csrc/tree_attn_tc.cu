@@ -93,7 +93,7 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 template <bool NEG, bool MASKED, bool PTH>
 __device__ __forceinline__ float max64(const uint32_t (&r)[64], float acc, uint32_t vis0,
                                        uint32_t vis1, const float* ks) {
-  float g[4] = {acc, acc, acc, acc};
+  float g[8] = {acc, acc, acc, acc, acc, acc, acc, acc};
 #pragma unroll
   for (int t = 0; t < 64; t += 2) {
     float a = __uint_as_float(r[t]), b = __uint_as_float(r[t + 1]);
@@ -110,9 +110,9 @@ __device__ __forceinline__ float max64(const uint32_t (&r)[64], float acc, uint3
       a = (vis >> (t & 31)) & 1u ? a : -INFINITY;
       b = (vis >> ((t + 1) & 31)) & 1u ? b : -INFINITY;
     }
-    g[(t >> 1) & 3] = fmax3(g[(t >> 1) & 3], a, b);
+    g[(t >> 1) & 7] = fmax3(g[(t >> 1) & 7], a, b);
   }
-  return fmaxf(fmax3(g[0], g[1], g[2]), g[3]);
+  return fmax3(fmax3(g[0], g[1], g[2]), fmax3(g[3], g[4], g[5]), fmaxf(g[6], g[7]));
 }
 
 // P = 2^(s * scale2 - m) of 64 logits as 16-bit pairs into the 32 columns at pa
@@ -122,7 +122,9 @@ template <bool MASKED, bool FP8, bool PTH>
 __device__ __forceinline__ float exp64(const uint32_t (&r)[64], uint32_t pa, float scale2, float m,
                                        uint32_t vis0, uint32_t vis1, const float* ks,
                                        const float* vs) {
-  float l[4] = {0.f, 0.f, 0.f, 0.f};
+  // (eight sums: with four, the packed adds' latency bound the softmax, 900
+  // cycles for a warp's 64 columns against 390)
+  float l[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     uint32_t w[16];
@@ -143,7 +145,7 @@ __device__ __forceinline__ float exp64(const uint32_t (&r)[64], uint32_t pa, flo
         a = (v >> i) & 1u ? a : 0.f;
         b = (v >> (i + 1)) & 1u ? b : 0.f;
       }
-      add2(l[i & 2], l[(i & 2) + 1], a, b);
+      add2(l[i & 6], l[(i & 6) + 1], a, b);
       if (PTH) {
         const float2 x = *reinterpret_cast<const float2*>(vs + t);
         mul2v(a, b, x.x, x.y);
@@ -156,7 +158,7 @@ __device__ __forceinline__ float exp64(const uint32_t (&r)[64], uint32_t pa, flo
     }
     tc::tmem_st16(pa + 16 * q, w);
   }
-  return (l[0] + l[1]) + (l[2] + l[3]);
+  return ((l[0] + l[1]) + (l[2] + l[3])) + ((l[4] + l[5]) + (l[6] + l[7]));
 }
 
 template <bool FP8, bool PTH>
