@@ -84,7 +84,13 @@ __global__ void __launch_bounds__(EvCfg<KEYS>::kThreads, KEYS > 0 ? 2 : 1)
   // The keys of tokens [t, t + 32 n) of the warp's run, n <= 16: the pages of
   // all of them at once, a lane each, then the weights at once (a bad page
   // reads page 0's, and is noted; there is none without pages).
+  constexpr int most = KEYS > 0 ? (KEYS < 16 ? KEYS : 16) : KEYS == kInShared ? 16 : 1;
   auto load = [&](int t, int n, auto put) {
+    if (cv.num_pages == 0) {  // no page: every token's is bad
+      bad |= t < w1;
+      for (int i = 0; i < n; ++i) put(i, 0u);
+      return;
+    }
     int page = 0;
     if (lane < n && t + 32 * lane < w1) {
       page = __ldg(bt + (t + 32 * lane) / kBlock);
@@ -93,13 +99,17 @@ __global__ void __launch_bounds__(EvCfg<KEYS>::kThreads, KEYS > 0 ? 2 : 1)
         page = 0;
       }
     }
+    // (all loads unconditional and before the first use, so that they are in
+    // flight together; beyond the run they read a slot of a page that is there)
+    float m[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < most)
+        m[i] = __ldg(p.mass + (long long)__shfl_sync(all, page, i) * kBlock + (t + 32 * i + lane) % kBlock);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      if (i >= n) break;
-      const int pg = __shfl_sync(all, page, i), at = t + 32 * i + lane;
-      const bool there = at < w1 && cv.num_pages > 0;
-      const float m = there ? __ldg(p.mass + (long long)pg * kBlock + at % kBlock) : 0.f;
-      put(i, at < lo || at >= hi ? kForcedKey : score_key(m));
+      const int at = t + 32 * i + lane;
+      if (i < most && i < n) put(i, at < lo || at >= hi ? kForcedKey : score_key(m[i]));
     }
   };
   uint32_t keys[KEYS > 0 ? KEYS : 1];
@@ -107,8 +117,8 @@ __global__ void __launch_bounds__(EvCfg<KEYS>::kThreads, KEYS > 0 ? 2 : 1)
   if constexpr (KEYS > 0) {
     load(w0, KEYS, [&](int i, uint32_t k) { keys[i] = k; });
   } else {
-    for (int t = w0; t < w1; t += 512)
-      load(t, min(16, (w1 - t + 31) / 32), [&](int i, uint32_t k) {
+    for (int t = w0; t < w1; t += 32 * most)
+      load(t, min(most, (w1 - t + 31) / 32), [&](int i, uint32_t k) {
         if (KEYS == kInShared) run[t - w0 + 32 * i] = k;
       });
   }
@@ -135,6 +145,10 @@ __global__ void __launch_bounds__(EvCfg<KEYS>::kThreads, KEYS > 0 ? 2 : 1)
   uint32_t prefix = 0;
   int left = need;  // how many of the keys that match the prefix are kept
   const bool rank_them = !malformed && need > 0 && L > p.budget;
+  // The cluster's counts are added up in every CTA, or, in a large cluster, in
+  // the first alone, which tells the others the digit (16 adds for each of up
+  // to 2048 counts took 10 K cycles in the second pass).
+  const int holders = C <= 4 ? C : 1;
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, up = pass == 1 ? 21 : 10;
     const uint32_t mask = pass == 2 ? 1023u : 2047u;
@@ -146,6 +160,7 @@ __global__ void __launch_bounds__(EvCfg<KEYS>::kThreads, KEYS > 0 ? 2 : 1)
       int zeros = 0;
       each([&](int t, uint32_t k) {
         const bool in = t < w1 && (pass == 0 ? k != kForcedKey : (k >> up) == (prefix >> up));
+        if (pass > 0 && !__any_sync(all, in)) return;
         const bool zero = in && k == kZeroKey;
         zeros += __popc(__ballot_sync(all, zero));
         if (in && !zero) atomicAdd(&hist[pass & 1][(k >> shift) & mask], 1);
@@ -156,7 +171,7 @@ __global__ void __launch_bounds__(EvCfg<KEYS>::kThreads, KEYS > 0 ? 2 : 1)
         const int n = hist[pass & 1][i];
         if (n) {
           const uint32_t at = smem_u32(&total[pass][i]);
-          for (int c = 0; c < C; ++c) red_dsmem_add(mapa_shared(at, c), n);
+          for (int c = 0; c < holders; ++c) red_dsmem_add(mapa_shared(at, c), n);
         }
       }
     }
@@ -182,6 +197,7 @@ __global__ void __launch_bounds__(EvCfg<KEYS>::kThreads, KEYS > 0 ? 2 : 1)
     }
     if (!rank_them) continue;
     // the digit, from the largest down
+    if (rank < holders) {
     int n[kBinsPer], sum = 0;
 #pragma unroll
     for (int k = 0; k < kBinsPer; ++k) {
@@ -206,7 +222,19 @@ __global__ void __launch_bounds__(EvCfg<KEYS>::kThreads, KEYS > 0 ? 2 : 1)
       }
       at += n[k];
     }
-    __syncthreads();
+    }
+    if (holders < C) {
+      if (rank == 0) {
+        __syncthreads();
+        if (tid < C) {
+          st_dsmem_s32(mapa_shared(smem_u32(&s_digit), tid), s_digit);
+          st_dsmem_s32(mapa_shared(smem_u32(&s_left), tid), s_left);
+        }
+      }
+      cluster_sync();
+    } else {
+      __syncthreads();
+    }
     prefix |= (uint32_t)s_digit << shift;
     left = s_left;
   }
