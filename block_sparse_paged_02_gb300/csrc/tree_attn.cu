@@ -778,16 +778,26 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 
 constexpr int kMgThreads = 256, kMgWarps = kMgThreads / 32;
 constexpr int kMaxMainCtas = 512;  // (the main kernels run one CTA per SM)
-constexpr int kMgFew = 8;  // up to this many partials a warp joins a row by itself
+constexpr int kMgSets = kMgThreads / 32;  // sets of 32 threads, 4 dims a thread
+constexpr int kMgLoads = 4;               // partials that a thread has in flight
 
-// Joins the partials of the tiles that several CTAs share.  Work units are 8
-// rows (a warp each) of a tile with few partials, or one row whose partials
-// the CTA's warps share; each CTA takes every gridDim-th unit.
-__global__ void __launch_bounds__(kMgThreads) tree_merge_kernel(const __grid_constant__ TreeLaunch p,
+// Sets that share a row's partials.  Two rows or more to a unit fill the 32-byte
+// sectors of a partial (a row to a unit: 119 us against 113 for 2 requests of 33 rows
+// x 12 heads over 131K tokens, 39 partials to a row); a row alone is for tiles that
+// most of the GPU shared.  Eight loads in flight took 100 registers and as many us
+// more as the fewer resident CTAs cost (wide trees 84 -> 88).
+__device__ __forceinline__ int merge_parts(int n) {
+  return n <= 8 ? 1 : n <= 16 ? 2 : n <= 64 ? 4 : 8;
+}
+
+// Joins the partials of the tiles that several CTAs share.  A work unit is
+// kMgSets / parts rows of a tile, each row's partials shared by `parts` sets;
+// each CTA takes every gridDim-th unit.
+__global__ void __launch_bounds__(kMgThreads, 3) tree_merge_kernel(const __grid_constant__ TreeLaunch p,
                                                                 int grid_main, int tile_rows) {
-  __shared__ float s_o[kMgWarps][kHeadDim];
-  __shared__ float s_m[kMgWarps], s_l[kMgWarps];
-  __shared__ int s_bad[kMgWarps], s_sum[kMgWarps], s_base[kMaxMainCtas];
+  __shared__ float4 s_o[kMgThreads];
+  __shared__ float s_m[kMgSets], s_l[kMgSets];
+  __shared__ int s_bad[kMgSets], s_sum[kMgWarps], s_base[kMaxMainCtas];
   __shared__ TreeSplit s_rec[kMaxMainCtas];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -801,8 +811,8 @@ __global__ void __launch_bounds__(kMgThreads) tree_merge_kernel(const __grid_con
     rec.nrows = 0;
     if (c > 0 && c < grid_main) rec = p.split[c];
     const int n = rec.last - c + 2;  // partials: CTAs c - 1 .. last
-    const bool few = n <= kMgFew;
-    const int units = few ? (rec.nrows + kMgWarps - 1) / kMgWarps : rec.nrows;
+    const int per = kMgSets / merge_parts(n);
+    const int units = (rec.nrows + per - 1) / per;
     int x = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -829,95 +839,90 @@ __global__ void __launch_bounds__(kMgThreads) tree_merge_kernel(const __grid_con
     const int c = lo;
     const TreeSplit rec = s_rec[c];
     const int n = rec.last - c + 2;
-    const bool few = n <= kMgFew;
-    {
-      // few: a thread per (row, 4 dims), 8 rows; else a warp per partial, a lane
-      // per 4 dims of the one row
-      const int at = unit - s_base[c];
-      const int m = few ? at * kMgWarps + (threadIdx.x & 7) : at;
-      const int g = few ? threadIdx.x >> 3 : lane;
-      const bool live = m < rec.nrows;
-      float M = -INFINITY, L = 0.f;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      int bad = 0;
-      if (live) {
-        const int first = few ? 0 : warp, step = few ? 1 : kMgWarps;
-        for (int i0 = first; i0 < n; i0 += 4 * step) {
-          float2 ml[4];
-          float4 v[4];
+    const int parts = merge_parts(n), per = kMgSets / parts;
+    // neighbouring threads take the unit's rows, then the 4-dim groups, then the parts
+    const int row = threadIdx.x & (per - 1), x = threadIdx.x / per;
+    const int g = x & 31, part = x >> 5;
+    const int m0 = (unit - s_base[c]) * per, m = m0 + row;
+    const bool live = m < rec.nrows;
+    float M = -INFINITY, L = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    int bad = 0;
+    if (live) {
+      for (int i0 = part; i0 < n; i0 += kMgLoads * parts) {
+        float2 ml[kMgLoads];
+        float4 v[kMgLoads];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int i = i0 + u * step;
-            ml[u] = make_float2(-INFINITY, 0.f);
-            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i < n) {
-              const long long slot = 2ll * (c - 1 + i) + (i == 0 ? 1 : 0);
-              bad |= p.part_bad[slot];
-              ml[u] = p.part_ml[slot * tile_rows + m];
-              v[u] = reinterpret_cast<const float4*>(p.part_o)[(slot * (kHeadDim / 4) + g) * tile_rows + m];
-            }
+        for (int u = 0; u < kMgLoads; ++u) {
+          const int i = i0 + u * parts;
+          ml[u] = make_float2(-INFINITY, 0.f);
+          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < n) {
+            const long long slot = 2ll * (c - 1 + i) + (i == 0 ? 1 : 0);
+            bad |= p.part_bad[slot];
+            ml[u] = p.part_ml[slot * tile_rows + m];
+            v[u] = reinterpret_cast<const float4*>(p.part_o)[(slot * (kHeadDim / 4) + g) * tile_rows + m];
           }
-          float mn = M;
+        }
+        float mn = M;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) mn = fmaxf(mn, ml[u].x);
-          const float ref = mn == -INFINITY ? 0.f : mn;
-          const float f0 = M == -INFINITY ? 1.f : ex2_ftz(M - ref);
-          L *= f0;
-          a.x *= f0; a.y *= f0; a.z *= f0; a.w *= f0;
+        for (int u = 0; u < kMgLoads; ++u) mn = fmaxf(mn, ml[u].x);
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        const float f0 = M == -INFINITY ? 1.f : ex2_ftz(M - ref);
+        L *= f0;
+        a.x *= f0; a.y *= f0; a.z *= f0; a.w *= f0;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float f = ml[u].x == -INFINITY ? 1.f : ex2_ftz(ml[u].x - ref);
-            L += ml[u].y * f;
-            a.x += v[u].x * f; a.y += v[u].y * f; a.z += v[u].z * f; a.w += v[u].w * f;
-          }
-          M = mn;
+        for (int u = 0; u < kMgLoads; ++u) {
+          const float f = ml[u].x == -INFINITY ? 1.f : ex2_ftz(ml[u].x - ref);
+          L += ml[u].y * f;
+          a.x += v[u].x * f; a.y += v[u].y * f; a.z += v[u].z * f; a.w += v[u].w * f;
+        }
+        M = mn;
+      }
+    }
+    if (parts > 1) {
+      __syncthreads();  // the previous unit's sums have been read
+      s_o[threadIdx.x] = a;
+      if (g == 0) {
+        s_m[part * per + row] = M;
+        s_l[part * per + row] = L;
+        s_bad[part * per + row] = bad;
+      }
+      __syncthreads();
+      if (part == 0) {
+        for (int k = 1; k < parts; ++k) {
+          bad |= s_bad[k * per + row];
+          M = fmaxf(M, s_m[k * per + row]);
+        }
+        const float ref = M == -INFINITY ? 0.f : M;
+        L = 0.f;
+        a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < parts; ++k) {
+          const float mk = s_m[k * per + row], f = mk == -INFINITY ? 1.f : ex2_ftz(mk - ref);
+          const float4 o = s_o[k * 32 * per + threadIdx.x];
+          L += s_l[k * per + row] * f;
+          a.x += o.x * f; a.y += o.y * f; a.z += o.z * f; a.w += o.w * f;
         }
       }
-      if (!few) {
-        __syncthreads();  // the previous unit's sums have been read
-        *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = a;
-        if (lane == 0) {
-          s_m[warp] = M;
-          s_l[warp] = L;
-          s_bad[warp] = bad;
-        }
-        __syncthreads();
-        if (warp == 0) {
-          for (int w = 0; w < kMgWarps; ++w) {
-            bad |= s_bad[w];
-            M = fmaxf(M, s_m[w]);
-          }
-          const float ref = M == -INFINITY ? 0.f : M;
-          L = 0.f;
-          a = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int w = 0; w < kMgWarps; ++w) {
-            const float f = s_m[w] == -INFINITY ? 1.f : ex2_ftz(s_m[w] - ref);
-            const float4 x = *reinterpret_cast<const float4*>(&s_o[w][4 * lane]);
-            L += s_l[w] * f;
-            a.x += x.x * f; a.y += x.y * f; a.z += x.z * f; a.w += x.w * f;
-          }
-        }
+    }
+    // values that a row does not see could have reached the tile (the whole
+    // tile's partials say so alike): its rows again, a warp each
+    if (__syncthreads_or(live && part == 0 && bad == 2)) {
+      if (warp < per && m0 + warp < rec.nrows) {
+        const int mm = m0 + warp, r = rec.row0 + mm / H;
+        tree_slow_row(p, rec.q, r, r - p.batch.cu_seqlens_q[rec.q], mm % H);
       }
-      // values that a row does not see could have reached the tile (the whole
-      // tile's partials say so alike): its rows again, a warp each
-      if (__syncthreads_or(live && (few || warp == 0) && bad == 2)) {
-        const int mm = few ? at * kMgWarps + warp : at;
-        if (mm < rec.nrows && (few || warp == 0)) {
-          const int row = rec.row0 + mm / H;
-          tree_slow_row(p, rec.q, row, row - p.batch.cu_seqlens_q[rec.q], mm % H);
-        }
-        continue;
-      }
-      if (live && (few || warp == 0)) {
-        const bool none = bad || (M == -INFINITY && L == 0.f);
-        const float sink = p.sinks ? __ldg(p.sinks + m % H) : 0.f;
-        const TreeRowEnd e = tree_row_end(M, L, p.sinks != nullptr, sink * kTreeLog2e, vs);
-        const long long r = (long long)rec.row0 * H + m;
-        uint2 w = make_uint2(pack_bf16x2(a.x * e.f, a.y * e.f), pack_bf16x2(a.z * e.f, a.w * e.f));
-        if (none) w = make_uint2(0u, 0u);
-        *reinterpret_cast<uint2*>(p.out + r * kHeadDim + 4 * g) = w;
-        if (g == 0) p.lse[r] = none ? (p.sinks ? sink : -INFINITY) : e.lse;
-      }
+      continue;
+    }
+    if (live && part == 0) {
+      const bool none = bad || (M == -INFINITY && L == 0.f);
+      const float sink = p.sinks ? __ldg(p.sinks + m % H) : 0.f;
+      const TreeRowEnd e = tree_row_end(M, L, p.sinks != nullptr, sink * kTreeLog2e, vs);
+      const long long r = (long long)rec.row0 * H + m;
+      uint2 w = make_uint2(pack_bf16x2(a.x * e.f, a.y * e.f), pack_bf16x2(a.z * e.f, a.w * e.f));
+      if (none) w = make_uint2(0u, 0u);
+      *reinterpret_cast<uint2*>(p.out + r * kHeadDim + 4 * g) = w;
+      if (g == 0) p.lse[r] = none ? (p.sinks ? sink : -INFINITY) : e.lse;
     }
   }
 }
@@ -1006,7 +1011,8 @@ __global__ void __launch_bounds__(kPlanThreads2) tree_plan_kernel(const TreeLaun
 
 cudaError_t launch_merge(const TreeLaunch& p, int grid, int tile_rows, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(4 * grid);
+  // (a unit holds a row x head at least)
+  cfg.gridDim = dim3((unsigned)max(1ll, min(6ll * grid, (long long)p.batch.num_rows * p.num_heads)));
   cfg.blockDim = dim3(kMgThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
