@@ -409,9 +409,10 @@ __device__ __forceinline__ TreeSlice tree_slice(const TreeLaunch& p, Cost cost, 
 }
 
 // A tile counts its blocks and kTreeTileCost items more, for what its start and
-// end cost (queries in, sums joined and written): without them the CTAs that
-// got many short requests ended 20 us behind on a 50 us batch.
-constexpr int kTreeTileCost = 1;
+// end cost (queries in, sums joined and written).  64 requests of one row took 70 us
+// without it, 56 with one item, 53 with three or four, 54.5 with seven; wide trees
+// (8 requests of 48..64 rows x 16 heads) 85 with one, 82 with four, 83 with seven.
+constexpr int kTreeTileCost = 4;
 
 // The part of a tile that the slice holds from item `it` on, in request items
 // [pre, pre + tiles * (nv + kTreeTileCost)).
