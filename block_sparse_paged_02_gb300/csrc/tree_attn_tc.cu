@@ -434,9 +434,9 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
       // kAhead (bf16): S in two products of 64 tokens.  The first goes over the
       // second half's logits as soon as they are in registers, so that the softmax
       // goes on while P V runs; the second goes over P.  In one product, behind P V,
-      // 8 requests of 48..64 rows x 16 heads took 101 us against 84.  e4m3: 118 us in
-      // one product, 136 in two (the queries read twice as often from the shared
-      // memory that the converting warps write to).
+      // 8 requests of 48..64 rows x 16 heads took 101 us against 84.  e4m3 (2 requests
+      // of 33 rows x 12 heads over 131K tokens): 106 us in one product, 118 in two (105
+      // with a fourth 16-bit tile and more registers for the softmax besides).
       const int t = warp - 1;
       if (lane == 0) {
         const uint64_t qd = tc::desc_kmajor_sw128(smem_u32(smem + kSmQ + t * kTile));
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
           if (!(fl & kPoison)) {
             const uint16_t* src = p.q + (long long)bi.row0 * H * kHeadDim;
             const int rows = bi.ntok * H, per = tpt * H;
-#pragma unroll 4
+#pragma unroll 8
             for (int i = ct; i < 2 * 128 * 16; i += kConv * 32) {
               const int t = i >> 11, m = (i >> 4) & 127, ch = i & 15, row = t * per + m;
               uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -601,7 +601,9 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
             uint8_t* tile = smem + kSmKv + b * kTile;
             // tokens past the request's end are not data: zeros
             const int there = min(kBlock, bi.seq - bi.t0);
-#pragma unroll 4
+            // (two at a time: eight took 114 us where two took 105, the softmax's
+            // instructions wait behind them)
+#pragma unroll 2
             for (int i = ct; i < kRaw / 16; i += kConv * 32) {
               const int row = i >> 3, ch = 2 * (i & 7);  // 16 codes: f16 chunks ch, ch + 1
               uint4 v = lds128(raw + 16 * i);
