@@ -32,6 +32,7 @@ constexpr int kTile = 2 * kHalf;   // 128 keys x 128 dims, 16 bits
 constexpr int kRaw = 128 * 128;    // 128 keys of e4m3
 constexpr int kInfos = 16;
 constexpr int kLoaders = 4;        // warps 12 .. 15
+constexpr int kPiece = 128;        // rows x heads of a product; four of them in tensor memory
 
 struct MassInfo {
   int flags;
@@ -56,8 +57,8 @@ struct MassCfg {
   static constexpr int kSmNl = kSmRaw + kRaws * kRaw;     // [2][QR] -lse (log2 units)
   static constexpr int kSmInfo = kSmNl + 2 * QR * 4;
   static constexpr int kSmBars = kSmInfo + kInfos * (int)sizeof(MassInfo);
-  // k full / empty, raw full / empty, q full / empty [2], d full / empty [2], info full
-  static constexpr int kNumBars = 2 * kTiles + 2 * kRaws + 8 + kInfos;
+  // k full / empty, raw full / empty, q full / empty [2], d full / empty [2][2], drained, info full
+  static constexpr int kNumBars = 2 * kTiles + 2 * kRaws + 13 + kInfos;
   static constexpr int kSmMisc = kSmBars + kNumBars * 8;
   static constexpr int kBytes = kSmMisc + 32;
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -108,9 +109,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* raw_empty = raw_full + C::kRaws;
   uint64_t* q_full = raw_empty + C::kRaws;  // [2]
   uint64_t* q_empty = q_full + 2;
-  uint64_t* d_full = q_empty + 2;
-  uint64_t* d_empty = d_full + 2;
-  uint64_t* info_full = d_empty + 2;
+  uint64_t* d_full = q_empty + 2;  // [warpgroup][buffer]
+  uint64_t* d_empty = d_full + 4;
+  uint64_t* drained = d_empty + 4;
+  uint64_t* info_full = drained + 1;
   MassInfo* info = reinterpret_cast<MassInfo*>(smem + C::kSmInfo);
   int* misc = reinterpret_cast<int*>(smem + C::kSmMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 4);
@@ -132,9 +134,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&q_full[s], kLoaders);
       mbar_init(&q_empty[s], 9);  // the issuer and the epilogue's warps
-      mbar_init(&d_full[s], 1);
-      mbar_init(&d_empty[s], 4);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&d_full[2 * s + b], 1);
+        mbar_init(&d_empty[2 * s + b], 4);
+      }
     }
+    mbar_init(drained, 1);
     for (int s = 0; s < kInfos; ++s) mbar_init(&info_full[s], 1);
     fence_barrier_init();
   }
@@ -246,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------- products
       if (lane == 0) {
         int n0 = 0, x0 = 0;     // first block, first query load of the segment
-        int steps[2] = {0, 0};  // products per epilogue warpgroup so far
+        int steps[2] = {0, 0};  // pieces per epilogue warpgroup so far
         bool ok = true;
         for (;;) {
           ok = mbar_wait(&info_full[n0 % kInfos], (n0 / kInfos) & 1);
@@ -261,25 +266,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; ok && c < chunks; ++c) {
               const int x = x0 + (resident ? c : (g >> 1) * chunks + c), qb = x & 1;
               ok = mbar_wait(&q_full[qb], (x >> 1) & 1);
-              const uint32_t idesc =
-                  tc::idesc_16(128, (min(QR, rows - c * QR) + 15) / 16 * 16, 0, FP8 ? 0 : 1);
+              const int n16 = (min(QR, rows - c * QR) + 15) / 16 * 16;
               const uint64_t qd = tc::desc_kmajor_sw128(smem_u32(smem + C::kSmQ + qb * C::kQBuf));
-              for (int b = 0; ok && b < nb; ++b) {
-                const int n = n0 + g + b, s = n % C::kTiles;
-                if (c == 0) ok = ok && mbar_wait(&k_full[s], (n / C::kTiles) & 1);
-                if (steps[b] > 0) ok = ok && mbar_wait(&d_empty[b], (steps[b] - 1) & 1);
-                if (!ok) break;
-                tc::fence_after();
-                const uint64_t kd = tc::desc_kmajor_sw128(smem_u32(smem + C::kSmK + s * kTile));
+              for (int k0 = 0; ok && k0 < n16; k0 += kPiece) {
+                const uint32_t idesc = tc::idesc_16(128, min(kPiece, n16 - k0), 0, FP8 ? 0 : 1);
+                for (int b = 0; ok && b < nb; ++b) {
+                  const int n = n0 + g + b, s = n % C::kTiles, buf = 2 * b + (steps[b] & 1);
+                  if (c == 0 && k0 == 0) ok = ok && mbar_wait(&k_full[s], (n / C::kTiles) & 1);
+                  if (steps[b] >= 2) ok = ok && mbar_wait(&d_empty[buf], ((steps[b] >> 1) - 1) & 1);
+                  if (!ok) break;
+                  tc::fence_after();
+                  const uint64_t kd = tc::desc_kmajor_sw128(smem_u32(smem + C::kSmK + s * kTile));
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                  tc::mma_ss(tmem + 256 * b,
-                             tc::desc_advance(kd, (kk >> 2) * kHalf + (kk & 3) * 32),
-                             tc::desc_advance(qd, (kk >> 2) * (QR * 128) + (kk & 3) * 32), idesc,
-                             kk > 0 ? 1u : 0u);
-                tc::commit(&d_full[b]);
-                if (c == chunks - 1) tc::commit(&k_empty[s]);
-                ++steps[b];
+                  for (int kk = 0; kk < 8; ++kk)
+                    tc::mma_ss(tmem + kPiece * buf,
+                               tc::desc_advance(kd, (kk >> 2) * kHalf + (kk & 3) * 32),
+                               tc::desc_advance(qd, k0 * 128 + (kk >> 2) * (QR * 128) + (kk & 3) * 32),
+                               idesc, kk > 0 ? 1u : 0u);
+                  tc::commit(&d_full[buf]);
+                  if (c == chunks - 1 && k0 + kPiece >= n16) tc::commit(&k_empty[s]);
+                  ++steps[b];
+                }
               }
               if (ok && (!resident || last)) tc::commit(&q_empty[qb]);
             }
@@ -290,8 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) misc[0] = 1;
         // every product has completed before the tensor memory is freed
-        for (int b = 0; b < 2; ++b)
-          if (steps[b] > 0 && !mbar_wait(&d_full[b], (steps[b] - 1) & 1)) misc[0] = 1;
+        tc::commit(drained);
+        if (!mbar_wait(drained, 0)) misc[0] = 1;
       }
     } else if (warp >= 16 - kLoaders) {
       // ---------------------------------------------- queries; e4m3 keys to f16
@@ -323,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!ok) break;
               const uint8_t* raw = smem + C::kSmRaw + rs * kRaw;
               uint8_t* kt = smem + C::kSmK + s * kTile;
-#pragma unroll 4
+#pragma unroll 2
               for (int i = lt; i < kRaw / 16; i += kLoaders * 32) {
                 const int row = i >> 3, ch = 2 * (i & 7);  // 16 codes: f16 chunks ch, ch + 1
                 const uint4 v = lds128(raw + 16 * i);
@@ -349,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             const int r0 = c * QR, nr = min(QR, rows - r0), n16 = (nr + 15) / 16 * 16;
             uint8_t* qd = smem + C::kSmQ + qb * C::kQBuf;
-#pragma unroll 4
+#pragma unroll 8
             for (int i = lt; i < n16 * 16; i += kLoaders * 32) {
               const int row = i >> 4, ch = i & 15;
               uint4 v = make_uint4(0u, 0u, 0u, 0u);  // rows past the end give S = 0
@@ -382,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------- sums
       const int w = (warp - 4) >> 2, quarter = warp & 3;
       const int tok = quarter * 32 + lane;  // token of the block = tensor-memory lane
-      const uint32_t da = tmem + ((uint32_t)(quarter * 32) << 16) + 256 * w;
+      const uint32_t d0 = tmem + ((uint32_t)(quarter * 32) << 16) + 2 * kPiece * w;
       float scale2 = p.softmax_scale * kTreeLog2e;
       if (p.scale_mode == MSA_SCALE_SCALAR) scale2 *= __ldg(p.k_scale);
       int n0 = 0, x0 = 0, step = 0;
@@ -417,22 +424,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; ok && c < chunks; ++c) {
             const int x = x0 + (resident ? c : (g >> 1) * chunks + c), qb = x & 1;
             ok = warp_wait(&q_full[qb], (x >> 1) & 1);
-            if (have) {
-              ok = ok && warp_wait(&d_full[w], step & 1);
+            const int nr = min(QR, rows - c * QR);
+            const float* nl = reinterpret_cast<const float*>(smem + C::kSmNl) + qb * QR;
+            int j0 = -64;  // a lane holds the sight of row j0 + lane on the warp's tokens
+            uint32_t win = 0;
+            for (int k0 = 0; ok && have && k0 < nr; k0 += kPiece, ++step) {
+              const int buf = step & 1, k1 = min(nr, k0 + kPiece);
+              ok = warp_wait(&d_full[2 * w + buf], (step >> 1) & 1);
               if (!ok) break;
-              ++step;
               tc::fence_after();
-              const int nr = min(QR, rows - c * QR);
-              const float* nl = reinterpret_cast<const float*>(smem + C::kSmNl) + qb * QR;
+              const uint32_t da = d0 + kPiece * buf - k0;
               // W columns at a time; in a block that not every row sees whole, and
               // behind the last row, those that count are picked by a bit each
-              int k = 0;
+              int k = k0;
               if (!(fl & kMixed)) {
-                for (; k + W <= nr; k += W) add_exp<W, false>(da + k, f, nl + k, 0u, 0u, acc);
+                for (; k + W <= k1; k += W) add_exp<W, false>(da + k, f, nl + k, 0u, 0u, acc);
               }
-              int j0 = -64;  // a lane holds the sight of row j0 + lane on the warp's tokens
-              uint32_t win = 0;
-              for (; k < nr; k += W) {
+              for (; k < k1; k += W) {
                 uint32_t bits[2] = {0u, 0u};
                 if (fl & kMixed) {
                   // the rows that the columns belong to, in turn
@@ -467,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               tc::fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&d_empty[w]);
+              if (lane == 0) mbar_arrive(&d_empty[2 * w + buf]);
             }
             if (!ok) break;
             __syncwarp();
