@@ -32,6 +32,7 @@ constexpr int kTile = 2 * kHalf;   // 128 keys x 128 dims, 16 bits
 constexpr int kRaw = 128 * 128;    // 128 keys of e4m3
 constexpr int kInfos = 16;
 constexpr int kLoaders = 4;        // warps 12 .. 15
+constexpr int kStart = 4;          // blocks that a request's start and end count as
 constexpr int kPiece = 128;        // rows x heads of a product; four of them in tensor memory
 
 struct MassInfo {
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
   const TreeSlice sl = tree_slice<kThreads>(
       p,
-      [&](const TreeReq& r, int nv) -> long long { return r.bad ? 1 : nv * mass_weight(r.qlen * H); },
+      [&](const TreeReq& r, int nv) -> long long { return r.bad ? 1 : (nv + kStart) * mass_weight(r.qlen * H); },
       reinterpret_cast<long long*>(smem));
   fence_proxy_async_smem();
   tc::fence_before();
@@ -170,8 +171,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           nv = tree_visits(p, q, rq);  // 1 for a poisoned request
         }
         const long long w = rq.bad ? 1 : mass_weight(rq.qlen * H);
-        const long long first = pre;
-        pre += nv * w;
+        const long long first = pre + (rq.bad ? 0 : kStart * w);  // the first block's first item
+        pre = first + nv * w;
         const int32_t* bt = p.batch.block_table + (long long)q * p.batch.bt_stride;
         if (!rq.bad) {
           // a bad page anywhere leaves the whole request as it is
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // blocks whose first item lies in the slice
         const int i0 = (int)((max(sl.begin, first) - first + w - 1) / w);
-        const int i1 = (int)min((long long)nv, (sl.end - first + w - 1) / w);
+        const int i1 = (int)min((long long)nv, (max(sl.end, first) - first + w - 1) / w);
         for (int c0 = i0; ok && c0 < i1; c0 += 32) {
           int blk = 0, page = 0;
           if (c0 + lane < i1) {
@@ -401,25 +402,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q0 = info[n0 % kInfos].q0, ctx = info[n0 % kInfos].ctx;
         const int rows = qlen * H, chunks = (rows + QR - 1) / QR;
         const bool resident = chunks <= 2;
+        float f_next = 0.f, old_next = 0.f;  // of the warpgroup's next block, loaded ahead
+        const auto ahead = [&](int n) {
+          if (!warp_wait(&info_full[n % kInfos], (n / kInfos) & 1)) return false;
+          const long long at = (long long)info[n % kInfos].page * kBlock + tok;
+          f_next = scale2;
+          if (p.scale_mode == MSA_SCALE_PER_TOKEN_HEAD) f_next *= __ldg(p.k_scale + at);
+          if (info[n % kInfos].t0 + tok < ctx) old_next = p.mass[at];
+          return true;
+        };
+        if (w < nblk) ok = ahead(n0 + w);
         for (int g = 0; ok && g < nblk; g += 2) {
           const bool have = g + w < nblk, last = g + 2 >= nblk;
           int fl = 0, t = 0;
           const uint32_t* sel = nullptr;
           float* slot = nullptr;
-          float f = scale2, old = 0.f;
+          const float f = f_next, old = old_next;
           float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
           if (have) {
-            const int n = n0 + g + w;
-            ok = warp_wait(&info_full[n % kInfos], (n / kInfos) & 1);
-            if (!ok) break;
-            const MassInfo& mi = info[n % kInfos];
+            const MassInfo& mi = info[(n0 + g + w) % kInfos];
             fl = mi.flags;
             t = mi.t0 + tok;
             sel = mi.rows;
-            const long long at = (long long)mi.page * kBlock + tok;
-            slot = p.mass + at;
-            if (p.scale_mode == MSA_SCALE_PER_TOKEN_HEAD) f *= __ldg(p.k_scale + at);
-            if (t < ctx) old = *slot;
+            slot = p.mass + (long long)mi.page * kBlock + tok;
           }
           for (int c = 0; ok && c < chunks; ++c) {
             const int x = x0 + (resident ? c : (g >> 1) * chunks + c), qb = x & 1;
@@ -480,6 +485,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             __syncwarp();
             if (lane == 0 && (!resident || last)) mbar_arrive(&q_empty[qb]);
+            // (streamed queries: the next block's place may wait for the other warpgroup,
+            // which waits for this one's chunks; so behind the last of them)
+            if (c == (resident ? 0 : chunks - 1) && g + 2 + w < nblk) ok = ahead(n0 + g + 2 + w);
           }
           // (a masked token of the block's rows that no row sees adds nothing)
           if (ok && have && t < ctx + qlen) {
