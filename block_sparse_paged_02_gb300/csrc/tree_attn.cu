@@ -1045,29 +1045,36 @@ cudaError_t launch_main(const TreeLaunch& p, cudaStream_t stream) {
   return e != cudaSuccess ? e : launch_merge(p, grid, C::kM, stream);
 }
 
+// Up to 32 rows x heads per request (one token of up to 16 heads, two of 16) the
+// stream of K and V bounds both kernels and warp MMA starts sooner; above, the
+// 5th-generation tensor cores, whose tiles of 128 rows cost the same however few
+// are used.  16 requests of 16384 tokens, us, this kernel / tree_attn_tc.cu:
+//   rows x heads         32          64          128
+//   bf16              39.6 / 40.7  61.7 / 41.0  86.9 / 44.8
+//   e4m3, scales      46.4 / 58.9  71.4 / 60.9   121 / 66.7
+// bf16 pools with a scale per token, which the latter does not take, stay here.
+// The tile is the smallest that holds a request's rows, so that short trees do not
+// carry empty rows through the products (one token of 16 heads: tile 16).
 template <bool FP8, bool PTH>
 cudaError_t launch_tile(const TreeLaunch& p, cudaStream_t stream) {
-  switch (tree_tile_rows(p.max_rows, p.num_heads)) {
-    case 16: return launch_main<FP8, PTH, 1>(p, stream);
-    case 32: return launch_main<FP8, PTH, 2>(p, stream);
-    case 64: return launch_main<FP8, PTH, 4>(p, stream);
-    default: return launch_main<FP8, PTH, 8>(p, stream);
+  const int m = p.max_rows * p.num_heads;
+  if (m <= 16) return launch_main<FP8, PTH, 1>(p, stream);
+  if (m <= 32) return launch_main<FP8, PTH, 2>(p, stream);
+  if constexpr (!FP8 && PTH) {
+    return m <= 64 ? launch_main<FP8, PTH, 4>(p, stream) : launch_main<FP8, PTH, 8>(p, stream);
+  } else {
+    const int grid = min(device_sm_count(), kMaxMainCtas);
+    const cudaError_t e = launch_tree_attn_tc(p, grid, stream);
+    return e != cudaSuccess ? e : launch_merge(p, grid, 256, stream);
   }
 }
 
 }  // namespace
 
-// Rows of a tile: the smallest that holds all of a request's rows, at most
-// 128, so that short trees do not carry empty rows through the products.
-int tree_tile_rows(int max_rows, int num_heads) {
-  const int m = max_rows * num_heads;
-  return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
-}
-
-// Rows of a partial: the tensor-core kernel takes pairs of 128-row tiles.
+// Rows of a partial, at most: the tensor-core kernel takes pairs of 128-row tiles.
 int tree_part_rows(int max_rows, int num_heads) {
-  const int m = tree_tile_rows(max_rows, num_heads);
-  return m == 128 ? 256 : m;
+  const int m = max_rows * num_heads;
+  return m <= 16 ? 16 : m <= 32 ? 32 : 256;
 }
 
 cudaError_t launch_tree_plan(const TreeLaunch& p, cudaStream_t stream) {
@@ -1081,11 +1088,6 @@ cudaError_t launch_tree_attn(const TreeLaunch& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   const bool pth = p.scale_mode == MSA_SCALE_PER_TOKEN_HEAD;
-  if ((p.kv_fp8 || !pth) && tree_tile_rows(p.max_rows, p.num_heads) == 128) {
-    const int grid = min(device_sm_count(), kMaxMainCtas);
-    const cudaError_t e = launch_tree_attn_tc(p, grid, stream);
-    return e != cudaSuccess ? e : launch_merge(p, grid, 256, stream);
-  }
   if (p.kv_fp8) return pth ? launch_tile<true, true>(p, stream) : launch_tile<true, false>(p, stream);
   return pth ? launch_tile<false, true>(p, stream) : launch_tile<false, false>(p, stream);
 }

@@ -57,7 +57,6 @@ cudaError_t launch_tree_plan(const TreeLaunch& p, cudaStream_t stream);
 cudaError_t launch_tree_attn(const TreeLaunch& p, cudaStream_t stream);
 cudaError_t launch_attn_mass(const TreeLaunch& p, cudaStream_t stream);
 cudaError_t launch_tree_attn_tc(const TreeLaunch& p, int grid, cudaStream_t stream);
-int tree_tile_rows(int max_rows, int num_heads);
 int tree_part_rows(int max_rows, int num_heads);
 
 struct EvictLaunch {
