@@ -7,14 +7,18 @@
 // adds its rows in a fixed order: no atomics, the same bits every time.
 //
 // The product is taken as S^T = K Q^T on the 5th-generation tensor cores
-// (tcgen05.mma M128, N = up to 256 rows, K128): the block's 128 tokens are the
+// (tcgen05.mma M128, N = up to 128 rows, K128): the block's 128 tokens are the
 // lanes of tensor memory, so each thread adds up its own token's columns and
 // nothing crosses threads.  Per element one packed multiply-add, one 2^x, one
-// packed add.  With few rows the stream of K bounds it, with many the 2^x
-// (and, at N = 256, the products behind them).
+// packed add.  With few rows the stream of K bounds it (64 requests of one row x 16
+// heads, 134 MB, in 31 us: 4.3 TB/s), with many the issue of the sums, two warps to
+// a scheduler (8 windows of 32 rows x 16 heads over 8191..65000 e4m3 tokens in 43 us,
+// 693 TFLOP/s; 39 without the 2^x or with an eighth of the products).  A quarter of
+// the 2^x as a polynomial took 54 us where 49 were; 16 columns at a time 47 against 43.
 //
 // Blocks go in groups of two, one per epilogue warpgroup, so that one's sums
-// overlap the other's products.  A request of at most two chunks of rows
+// overlap the other's products, and each has two buffers of 128 columns, so that
+// its own next product runs meanwhile (49.5 us before, 46 then).  A request of at most two chunks of rows
 // keeps its queries in shared memory for all its blocks; more chunks stream
 // through two buffers, each used by the group's two blocks.  e4m3 keys are
 // converted to f16 (exact) by the four loader warps.
@@ -32,7 +36,10 @@ constexpr int kTile = 2 * kHalf;   // 128 keys x 128 dims, 16 bits
 constexpr int kRaw = 128 * 128;    // 128 keys of e4m3
 constexpr int kInfos = 16;
 constexpr int kLoaders = 4;        // warps 12 .. 15
-constexpr int kStart = 4;          // blocks that a request's start and end count as
+// Blocks that a request's start and end count as when the work is split: its queries
+// come in, its last blocks are masked by row (window 53 us with 0, 50.5 with 2, 47.4
+// with 4 and with 6 before the loads ahead; decode 32.6, 31.1, 31.2, 31.6)
+constexpr int kStart = 4;
 constexpr int kPiece = 128;        // rows x heads of a product; four of them in tensor memory
 
 struct MassInfo {
@@ -48,9 +55,9 @@ constexpr int kFirst = 1, kEnd = 2, kMixed = 4;
 
 template <bool FP8, int QR>
 struct MassCfg {
-  static constexpr int kTiles = FP8 ? (QR == 256 ? 2 : 3) : (QR == 256 ? 3 : QR == 64 ? 5 : 6);
-  static constexpr int kRaws = FP8 ? (QR == 256 ? 2 : QR == 64 ? 5 : 6) : 0;
-  static constexpr int kCols = QR < 64 ? 16 : 64;  // columns summed at a time
+  static constexpr int kTiles = FP8 ? (QR == 256 ? 2 : 3) : (QR == 256 ? 3 : 6);
+  static constexpr int kRaws = FP8 ? (QR == 256 ? 2 : 6) : 0;
+  static constexpr int kCols = QR == 256 ? 64 : 16;  // columns summed at a time
   static constexpr int kQBuf = QR * 256;
   static constexpr int kSmK = 0;
   static constexpr int kSmQ = kTiles * kTile;
@@ -69,8 +76,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
 }
 
-// Estimated cost of a block against `rows` rows x heads: the stream of its
-// keys, or its products and exponentials
+// Estimated cost of a block against `rows` rows x heads: the stream of its keys, or
+// its products and exponentials (half and twice the 20 measure the same to 0.1 us)
 __device__ __forceinline__ long long mass_weight(int rows) { return max(20, (rows + 15) / 16); }
 
 // sum over W columns of 2^(s * f + nl) onto acc; MASKED: of those with a set bit
@@ -528,11 +535,12 @@ cudaError_t launch_mass(const TreeLaunch& p, cudaStream_t stream) {
 
 template <bool FP8>
 cudaError_t launch_rows(const TreeLaunch& p, cudaStream_t stream) {
-  // rows of a chunk: few rows leave the shared memory to the stream of keys
+  // rows of a chunk: one token's leave the shared memory to the stream of keys.  16
+  // requests of 16384 tokens, us, chunks of 16 / 64 / 256: 16 rows x heads bf16
+  // 20.5 / 23.9 / 21.7, e4m3 18.6 / 24.6 / 22.4; 64: bf16 - / 22.9 / 21.0; 128: bf16
+  // - / 28.1 / 24.8
   const int rows = p.max_rows * p.num_heads;
-  if (rows <= 16) return launch_mass<FP8, 16>(p, stream);
-  if (rows <= 128) return launch_mass<FP8, 64>(p, stream);
-  return launch_mass<FP8, 256>(p, stream);
+  return rows <= 16 ? launch_mass<FP8, 16>(p, stream) : launch_mass<FP8, 256>(p, stream);
 }
 
 }  // namespace

@@ -94,8 +94,9 @@ msa_status msa_tree_attn(const msa_batch* batch, const msa_tree* tree, const msa
  *   attn      q, k_cache, k_scale and lse are read; v_cache, v_scale, sinks
  *             and out are not used and may be NULL
  *   mass      fp32 [num_pages, 128]
- * Requests of one call must not share pages (a shared slot would be updated
- * by several requests at once).  Poisoned requests leave mass as it is. */
+ * Requests of one call must not share pages, nor may one name a page twice (a
+ * shared slot would be updated by several blocks at once).  Poisoned requests
+ * leave mass as it is. */
 msa_status msa_attn_mass(const msa_batch* batch, const msa_tree* tree, const msa_attn_args* attn,
                          float* mass, void* workspace, size_t workspace_bytes,
                          uint32_t* dev_status, cudaStream_t stream);
@@ -166,7 +167,8 @@ typedef struct msa_kv_pools {
  * (keep_len > keep_stride, base + keep >= lens, base < 0) is left as it is
  * and sets MSA_DEV_BAD_TABLE; a length out of range sets MSA_DEV_MALFORMED,
  * a bad page id among the request's blocks MSA_DEV_BAD_PAGE, likewise.
- * Pages of a request must not be shared with another request of the call.
+ * Pages of a request must not be shared with another request of the call, nor
+ * named twice.
  * Supported: head_dim 128, 1 <= num_kv_heads <= 64, keep_stride >= 1, the
  * index shapes of msa_index_cache, num_reqs <= 4096, bt_stride <= 16384. */
 msa_status msa_kv_compact(const msa_cache_view* cache, const int32_t* base, const int32_t* keep,
