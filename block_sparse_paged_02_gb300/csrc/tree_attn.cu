@@ -183,7 +183,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         rec.nrows = si.ntok * H;
         rec.row0 = si.row0;
         rec.last = (int)((sg.end * sl.ctas - 1) / sl.total);
-        rec.q = q;
       }
       if (rq.bad) {
         const int st = acquire();
@@ -906,15 +905,7 @@ __global__ void __launch_bounds__(kMgThreads, 3) tree_merge_kernel(const __grid_
           a.x += o.x * f; a.y += o.y * f; a.z += o.z * f; a.w += o.w * f;
         }
       }
-    }
-    // values that a row does not see could have reached the tile (the whole
-    // tile's partials say so alike): its rows again, a warp each
-    if (__syncthreads_or(live && part == 0 && bad == 2)) {
-      if (warp < per && m0 + warp < rec.nrows) {
-        const int mm = m0 + warp, r = rec.row0 + mm / H;
-        tree_slow_row(p, rec.q, r, r - p.batch.cu_seqlens_q[rec.q], mm % H);
-      }
-      continue;
+      __syncthreads();  // read before the next unit overwrites them
     }
     if (live && part == 0) {
       const bool none = bad || (M == -INFINITY && L == 0.f);

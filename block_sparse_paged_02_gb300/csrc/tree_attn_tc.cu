@@ -12,7 +12,7 @@
 //               its rows of O); P written back over S in 16 bits
 //   O += P V    tcgen05.mma with A = P from tensor memory, B = V (MN-major)
 // Roles: warp 0 issues the tensor copies, one thread of warps 1 and 2 issues the
-// products of tile 0 and tile 1, warps 4-7 and 8-11 are the tiles' softmax.  Tensor memory
+// products of tile 0 and tile 1, warp 3 looks bf16 V over (below), warps 4-7 and 8-11 are the tiles' softmax.  Tensor memory
 // (512 columns): S / P and O of both tiles.  With e4m3 pools warps 12-15 turn the
 // tiles into f16 (exact) and the products run in f16; a scale per token joins the
 // logits and P in the softmax.  (bf16 pools with a scale per token stay on
@@ -28,8 +28,8 @@
 // A block that not every row sees whole (the drafted tokens, the context's
 // end, selected blocks) takes a masked softmax, and its V is looked over: a
 // value that is not finite would reach rows that do not see it through 0 * V,
-// so the tile is then computed again row by row (tree_slow_row), from the
-// visible tokens alone.
+// so that block's P V is then added to O row by row, from the visible tokens
+// alone (pv_by_hand).
 #include <string.h>
 
 #include "tcgen05.cuh"
@@ -51,12 +51,15 @@ struct BlockInfo {
   int row0, ntok, j0;  // the tile pair's drafted tokens: first row in the batch, count, index
   int ctx, qlen, seq;
   int t0;              // position of the block's first token
-  int slot, q;
+  int slot;
   uint32_t bad;
   int page;
   const uint32_t* rows;
 };
 
+// blocks that the warp looking V over may be ahead of the softmax, and one more (both
+// rings of tiles hold it to two)
+constexpr int kLooks = 4;
 constexpr int kScales = 4;  // blocks whose scales are held
 constexpr int kConv = 4;    // converting warps (e4m3 pools)
 
@@ -75,8 +78,8 @@ struct TcCfg {
   static constexpr int kSmBars = kSmInfo + kInfos * (int)sizeof(BlockInfo);
   // kv full / empty, raw full / empty, q full / empty, info full, scales full;
   // per tile: s_full, p_full and pv_done of the two halves, s_read, o_free, drained;
-  // fill, ends
-  static constexpr int kNumBars = 2 * kBufs + 2 * kRaws + 2 + kInfos + kScales + 18 + 2;
+  // fill, looked
+  static constexpr int kNumBars = 2 * kBufs + 2 * kRaws + 2 + kInfos + kScales + 18 + 1 + kLooks;
   static constexpr int kSmMisc = kSmBars + kNumBars * 8;
   static constexpr int kBytes = kSmMisc + 64;
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -170,6 +173,62 @@ __device__ __forceinline__ float exp64(const uint32_t (&r)[64], uint32_t pa, flo
   return ((l[0] + l[1]) + (l[2] + l[3])) + ((l[4] + l[5]) + (l[6] + l[7]));
 }
 
+// O += P V of a block for the row of this thread, the tokens with a set bit of vis
+// alone; P (that of the first 64 tokens times f0) at pa and O at oa in tensor memory,
+// V at v, `words` x 32 tokens; O starts with it when fresh
+template <bool FP8>
+__device__ __noinline__ void pv_by_hand(uint32_t oa, uint32_t pa, const uint8_t* v, uint4 vis4,
+                                        int words, float f0, bool fresh) {
+  tc::tmem_wait_st();
+#pragma unroll 1
+  for (int c = 0; c < 128; c += 16) {
+    uint32_t o[16];
+    if (!fresh) tc::tmem_ld16(oa + c, o);
+    float acc[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = fresh ? 0.f : __uint_as_float(o[i]);
+#pragma unroll 1
+    for (int w = 0; w < words; ++w) {
+      uint32_t pr[16];
+      tc::tmem_ld16(pa + 16 * w, pr);
+      const uint32_t vis = w == 0 ? vis4.x : w == 1 ? vis4.y : w == 2 ? vis4.z : vis4.w;
+      const float f = w < 2 ? f0 : 1.f;
+#pragma unroll
+      for (int t = 0; t < 32; ++t) {
+        if ((vis >> t) & 1u) {
+          const int tok = 32 * w + t;
+          const uint8_t* row = v + (c >> 6) * kHalf + tok * 128;
+          float x;
+          if (FP8) {
+            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&pr[t >> 1]));
+            x = t & 1 ? h.y : h.x;
+          } else {
+            x = t & 1 ? bf16hi(pr[t >> 1]) : bf16lo(pr[t >> 1]);
+          }
+          x *= f;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint4 q = lds128(row + (((((c >> 3) & 7) + k) ^ (tok & 7)) << 4));
+            const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float2 y;
+              if (FP8) y = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+              else y = make_float2(bf16lo(u[i]), bf16hi(u[i]));
+              acc[8 * k + 2 * i] += x * y.x;
+              acc[8 * k + 2 * i + 1] += x * y.y;
+            }
+          }
+        }
+      }
+      __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(acc[i]);
+    tc::tmem_st16(oa + c, o);
+  }
+}
+
 template <bool FP8, bool PTH>
 __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
     tree_attn_tc_kernel(const __grid_constant__ TreeLaunch p, const __grid_constant__ CUtensorMap qmap,
@@ -197,10 +256,10 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
   uint64_t* s_read = pv_done + 4;        // [tile]: the second half's logits are in registers
   uint64_t* o_free = s_read + 2;         // [tile]
   uint64_t* fill = o_free + 2;
-  uint64_t* ends = fill + 1;
-  uint64_t* drained = ends + 1;          // [tile]
+  uint64_t* drained = fill + 1;          // [tile]
+  uint64_t* looked = drained + 2;        // [kLooks]
   BlockInfo* info = reinterpret_cast<BlockInfo*>(smem + C::kSmInfo);
-  int* misc = reinterpret_cast<int*>(smem + C::kSmMisc);  // [0] timeout, [4..6] odd values seen
+  int* misc = reinterpret_cast<int*>(smem + C::kSmMisc);  // [0] timeout, [4 + n % kLooks] n + 1: odd values in block n's V
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 8);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int H = p.num_heads;
@@ -210,7 +269,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
     for (int i = 0; i < 8; ++i) misc[i] = 0;
     for (int s = 0; s < kBufs; ++s) {
       mbar_init(&kv_full[s], FP8 ? kConv : 1);
-      mbar_init(&kv_empty[s], 2);  // the two issuers
+      mbar_init(&kv_empty[s], FP8 ? 2 : 3);  // the two issuers, the warp that looks V over
     }
     for (int s = 0; s < kRaws; ++s) {
       mbar_init(&raw_full[s], 1);
@@ -231,7 +290,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
       mbar_init(&drained[t], 1);
     }
     mbar_init(fill, 1);
-    mbar_init(ends, 8);
+    for (int i = 0; i < kLooks; ++i) mbar_init(&looked[i], 1);
     fence_barrier_init();
   }
   if (warp == 1) tc::tmem_alloc(tmem_slot, kTmemCols);
@@ -321,7 +380,6 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
         bi.qlen = rq.qlen;
         bi.seq = rq.ctx + rq.qlen;
         bi.slot = 2 * blockIdx.x + (b0 > 0 ? 0 : 1);
-        bi.q = q;
         bi.bad = rq.bad;
         bi.rows = nullptr;
         const int both = (nb == nv ? kWhole : 0) | (bi.ntok > tpt ? kTwo : 0);
@@ -329,7 +387,6 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
           rec.nrows = bi.ntok * H;
           rec.row0 = bi.row0;
           rec.last = (int)((sg.end * sl.ctas - 1) / sl.total);
-          rec.q = q;
         }
         // (e4m3: the converting warps bring the queries, and pass over empty blocks)
         if (!FP8 && n_seg > 0) ok = warp_wait(q_empty, (n_seg - 1) & 1);
@@ -498,8 +555,9 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
             if (fl & kLast) mbar_arrive(q_empty);
           }
           const uint64_t vd = tc::desc_mnmajor_sw128(smem_u32(smem + kSmKv + vb * kTile), kHalf);
+          bool hand = false;  // the softmax adds the block's P V itself
           const auto pv_half = [&](int half) {
-            if (work && (half == 0 || (fl & kHalves))) {
+            if (work && !hand && (half == 0 || (fl & kHalves))) {
               tc::fence_after();
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
@@ -515,6 +573,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
           if ((fl & kFirst) && seg > 0) ok = ok && mbar_wait(&o_free[t], (seg - 1) & 1);
           ok = ok && mbar_wait(&pf[0], n & 1);
           if (!ok) break;
+          hand = (fl & kMixed) && *reinterpret_cast<volatile int*>(&misc[4 + n % kLooks]) == n + 1;
           pv_half(0);
           int next = kFirst;
           const auto follow = [&]() {
@@ -541,6 +600,46 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
         tc::commit(&drained[t]);
         if (!mbar_wait(&drained[t], 0)) misc[0] = 1;
       }
+    } else if (!FP8 && warp == 3) {
+      // ---------------------------------------------- values that are not finite
+      // in the V of blocks that not every row sees (e4m3: the converting warps look)
+      bool ok = true;
+      for (int n = 0;; ++n) {
+        ok = warp_wait(&info_full[n % kInfos], (n / kInfos) & 1);
+        if (!ok) break;
+        const BlockInfo& bi = info[n % kInfos];
+        const int fl = bi.flags;
+        if (fl & kEnd) break;
+        // (every use of a place is followed, so that the ring never laps this warp)
+        const int kb = (2 * n) % kBufs, vb = (2 * n + 1) % kBufs;
+        ok = warp_wait(&kv_full[kb], ((2 * n) / kBufs) & 1);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(&kv_empty[kb]);
+        ok = warp_wait(&kv_full[vb], ((2 * n + 1) / kBufs) & 1);
+        if (!ok) break;
+        if ((fl & kMixed) && !(fl & kNoData)) {
+          // (tokens past the request's end are zeros)
+          const uint8_t* src = smem + kSmKv + vb * kTile + lane * 16;
+          uint32_t odd = 0;
+#pragma unroll 8
+          for (int i = 0; i < kTile; i += 512) {
+            const uint4 v = lds128(src + i);
+            constexpr uint32_t one = 0x00800080u;  // an exponent's last bit
+            odd |= (v.x & 0x7fff7fffu) + one;
+            odd |= (v.y & 0x7fff7fffu) + one;
+            odd |= (v.z & 0x7fff7fffu) + one;
+            odd |= (v.w & 0x7fff7fffu) + one;
+          }
+          const bool any = __any_sync(0xffffffffu, (odd & 0x80008000u) != 0);
+          if (lane == 0 && any) *reinterpret_cast<volatile int*>(&misc[4 + n % kLooks]) = n + 1;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&looked[n % kLooks]);
+          mbar_arrive(&kv_empty[vb]);
+        }
+      }
+      if (!ok) misc[0] = 1;
     } else if (FP8 && warp >= 12) {
       // ---------------------------------------------- e4m3 tiles to f16, queries
       const int ct = tid - 12 * 32;
@@ -624,6 +723,18 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
                              e4m3x2_to_f16x2((uint16_t)v.w), e4m3x2_to_f16x2((uint16_t)(v.w >> 16)));
             }
             fence_proxy_async_smem();
+            if (kv == 1 && (fl & kMixed)) {
+              // a code of NaN among the thread's: 0x7f without its sign
+              uint32_t odd = 0;
+#pragma unroll 2
+              for (int i = ct; i < kRaw / 16; i += kConv * 32) {
+                const uint4 v = lds128(raw + 16 * i);
+                if ((i >> 3) < there)
+                  odd |= ((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u) |
+                         ((v.z & 0x7f7f7f7fu) + 0x01010101u) | ((v.w & 0x7f7f7f7fu) + 0x01010101u);
+              }
+              if (odd & 0x80808080u) *reinterpret_cast<volatile int*>(&misc[4 + n % kLooks]) = n + 1;
+            }
             __syncwarp();
           }
           if (lane == 0) {
@@ -651,7 +762,6 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
       // PTH: P carries its token's v scale over a power of two that only grows,
       // so that it keeps its range in 16 bits whatever the scales
       float vref = 0.f;
-      int x = 1, seg = -1;
       bool bad = false, ok = true;
       for (int n = 0;; ++n) {
         ok = warp_wait(&info_full[n % kInfos], (n / kInfos) & 1);
@@ -659,10 +769,8 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
         const BlockInfo& bi = info[n % kInfos];
         const int fl = bi.flags;
         if (fl & kEnd) break;
-        const int vb = x % kBufs, vph = (x / kBufs) & 1;
-        x += 2;
+        const int vb = (2 * n + 1) % kBufs;
         if (fl & kFirst) {
-          ++seg;
           m_run = -INFINITY;
           l_run = 0.f;
           vref = 0.f;
@@ -688,6 +796,8 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
                                     tree_vis16(p, bi.row0 + tok, j, bi.ctx, bi.qlen, bi.t0 + 32 * w + 16, sel) << 16;
           }
         }
+        bool hand = false;
+        float moved = 1.f;  // what the second half scaled the first one's P by
         const float* ks = nullptr;
         float grow = 1.f;  // what O is scaled by for a larger vref
         if (PTH && work) {
@@ -737,6 +847,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
                 m_run = mx;
               }
               l_run *= al;
+              if (half) moved = al;
               al *= grow;
               grow = 1.f;
               // (a row without a reference has an all-zero O: nothing to rescale)
@@ -771,39 +882,32 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
             mbar_arrive(&s_read[t]);
           }
           if (half == 0 && (fl & kMixed) && !(fl & kNoData)) {
-            // values that are not finite among this tile's half of the block's V
-            ok = warp_wait(&kv_full[vb], vph);
+            ok = FP8 ? warp_wait(&kv_full[vb], ((2 * n + 1) / kBufs) & 1)
+                     : warp_wait(&looked[n % kLooks], (n / kLooks) & 1);
             if (!ok) break;
-            const int row = 64 * t + (m >> 1);
-            const uint8_t* src = smem + kSmKv + vb * kTile + (m & 1) * kHalf + row * 128;
-            uint32_t odd = 0;
-            if (bi.t0 + row < bi.seq) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint4 v = lds128(src + 16 * i);
-                constexpr uint32_t one = FP8 ? 0x04000400u : 0x00800080u;  // an exponent's last bit
-                odd |= (v.x & 0x7fff7fffu) + one;
-                odd |= (v.y & 0x7fff7fffu) + one;
-                odd |= (v.z & 0x7fff7fffu) + one;
-                odd |= (v.w & 0x7fff7fffu) + one;
-              }
-            }
-            if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0) && lane == 0)
-              *reinterpret_cast<volatile int*>(&misc[4 + seg % 3]) = 1;
+            hand = *reinterpret_cast<volatile int*>(&misc[4 + n % kLooks]) == n + 1;
           }
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&p_full[2 * t + half]);
+          if (lane == 0 && !(hand && half)) mbar_arrive(&p_full[2 * t + half]);
+        }
+        if (!ok) break;
+        if (hand) {
+          if (work) {
+            // (P V of the blocks before is complete: this block's S waited for it)
+            tc::fence_after();
+            pv_by_hand<FP8>(oa, tmem + lanes + col_s(t) + (kAhead ? 64 * (n & 1) : 0),
+                            smem + kSmKv + vb * kTile, make_uint4(vis[0], vis[1], vis[2], vis[3]),
+                            fl & kHalves ? 4 : 2, moved, (fl & kFirst) != 0);
+            tc::tmem_wait_st();
+            tc::fence_before();
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * t + 1]);
         }
         if (!ok) break;
         if (fl & kLast) {
-          // both tiles' warps have looked over the segment's blocks
-          if (lane == 0) mbar_arrive(ends);
-          ok = warp_wait(ends, seg & 1) && warp_wait(&pv_done[2 * t + 1], n & 1);
+          ok = warp_wait(&pv_done[2 * t + 1], n & 1);
           if (!ok) break;
-          const bool odd = *reinterpret_cast<volatile int*>(&misc[4 + seg % 3]) != 0;
-          if (warp == 4 && lane == 0) *reinterpret_cast<volatile int*>(&misc[4 + (seg + 2) % 3]) = 0;
           tc::fence_after();
           const bool none = bad || (m_run == -INFINITY && l_run == 0.f);
           const float back = PTH ? vref : 1.f;
@@ -854,17 +958,8 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
             else p.part_ml[pr] = make_float2(m_run, l_run);
           }
           if (t == 0 && m == 0) {
-            if (!(fl & kWhole)) p.part_bad[bi.slot] = bad ? 1 : odd ? 2 : 0;
+            if (!(fl & kWhole)) p.part_bad[bi.slot] = bad ? 1 : 0;
             if (bi.bad) atomicOr(p.status, bi.bad);
-          }
-          if ((fl & kWhole) && odd && !bad) {
-            __syncwarp();
-            // this warp's rows again, from the tokens that they see alone
-            for (int i = 0; i < 32; ++i) {
-              const int mm = quarter * 32 + i, tk = t * tpt + mm / H;
-              if (!have || mm / H >= tpt || tk >= bi.ntok) break;
-              tree_slow_row(p, bi.q, bi.row0 + tk, bi.j0 + tk, mm % H);
-            }
           }
         }
       }

@@ -17,7 +17,6 @@ struct TreeSplit {
   int32_t nrows;  // 0: none
   int32_t row0;
   int32_t last;
-  int32_t q;
 };
 
 struct TreeLaunch {
@@ -224,79 +223,6 @@ __device__ __forceinline__ void tree_write_all_empty(const TreeLaunch& p) {
     p.lse[i] = p.sinks ? __ldg(p.sinks + i % p.num_heads) : -INFINITY;
   uint4* o = reinterpret_cast<uint4*>(p.out);
   for (long long i = at; i < n * (kHeadDim / 8); i += step) o[i] = make_uint4(0u, 0u, 0u, 0u);
-}
-
-// One row and head by one warp, from the visible tokens alone and one after
-// another: for tiles that hold a value which is not finite and which not every
-// row sees (a product over the tile would carry 0 * NaN into the others).
-static __device__ __noinline__ void tree_slow_row(const TreeLaunch& p, int q, int row, int j, int h) {
-  const int lane = threadIdx.x & 31;
-  const unsigned all = 0xffffffffu;
-  const TreeReq rq = tree_request(p, q);
-  const int seq = rq.ctx + rq.qlen;
-  const uint2 qb = *reinterpret_cast<const uint2*>(p.q + ((long long)row * p.num_heads + h) * kHeadDim + 4 * lane);
-  const float qv[4] = {bf16lo(qb.x), bf16hi(qb.x), bf16lo(qb.y), bf16hi(qb.y)};
-  float scale2 = p.softmax_scale * kTreeLog2e, vs1 = 1.f;
-  if (p.scale_mode == MSA_SCALE_SCALAR) {
-    scale2 *= __ldg(p.k_scale);
-    vs1 = __ldg(p.v_scale);
-  }
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int b = 0; b < rq.nb; ++b) {
-    bool sel = !p.topk_idx || b >= rq.ctx / kBlock;
-    if (!sel) {
-      for (int i = lane; i < p.topk; i += 32) sel |= p.topk_idx[(long long)row * p.topk + i] == b;
-      sel = __any_sync(all, sel) != 0;
-    }
-    const long long tok = (long long)p.batch.block_table[(long long)q * p.batch.bt_stride + b] * kBlock;
-    for (int g = 0; g < kBlock && kBlock * b + g < seq; g += 16) {
-      uint32_t vis = tree_vis16(p, row, j, rq.ctx, rq.qlen, kBlock * b + g, sel);
-      for (; vis; vis &= vis - 1) {
-        const long long at = tok + g + __ffs(vis) - 1;
-        float kk[4], vv[4];
-        if (p.kv_fp8) {
-          const uint32_t kc = *reinterpret_cast<const uint32_t*>(p.k + at * kHeadDim + 4 * lane);
-          const uint32_t vc = *reinterpret_cast<const uint32_t*>(p.v + at * kHeadDim + 4 * lane);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t k2 = e4m3x2_to_f16x2((uint16_t)(kc >> (16 * i)));
-            const uint32_t v2 = e4m3x2_to_f16x2((uint16_t)(vc >> (16 * i)));
-            const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(&k2));
-            const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(&v2));
-            kk[2 * i] = kf.x; kk[2 * i + 1] = kf.y; vv[2 * i] = vf.x; vv[2 * i + 1] = vf.y;
-          }
-        } else {
-          const uint2 kc = *reinterpret_cast<const uint2*>(p.k + (at * kHeadDim + 4 * lane) * 2);
-          const uint2 vc = *reinterpret_cast<const uint2*>(p.v + (at * kHeadDim + 4 * lane) * 2);
-          kk[0] = bf16lo(kc.x); kk[1] = bf16hi(kc.x); kk[2] = bf16lo(kc.y); kk[3] = bf16hi(kc.y);
-          vv[0] = bf16lo(vc.x); vv[1] = bf16hi(vc.x); vv[2] = bf16lo(vc.y); vv[3] = bf16hi(vc.y);
-        }
-        float s = qv[0] * kk[0] + qv[1] * kk[1] + qv[2] * kk[2] + qv[3] * kk[3];
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(all, s, x);
-        float f = scale2, vs = 1.f;
-        if (p.scale_mode == MSA_SCALE_PER_TOKEN_HEAD) {
-          f *= __ldg(p.k_scale + at);
-          vs = __ldg(p.v_scale + at);
-        }
-        s *= f;
-        const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.f : mn;
-        const float al = m == -INFINITY ? 1.f : ex2_ftz(m - base), e = ex2_ftz(s - base);
-        m = mn;
-        l = l * al + e;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = o[i] * al + e * (vs * vv[i]);
-      }
-    }
-  }
-  const bool none = m == -INFINITY && l == 0.f;
-  const float sink = p.sinks ? __ldg(p.sinks + h) : 0.f;
-  const TreeRowEnd e = tree_row_end(m, l, p.sinks != nullptr, sink * kTreeLog2e, vs1);
-  const long long r = (long long)row * p.num_heads + h;
-  uint2 w = make_uint2(pack_bf16x2(o[0] * e.f, o[1] * e.f), pack_bf16x2(o[2] * e.f, o[3] * e.f));
-  if (none) w = make_uint2(0u, 0u);
-  *reinterpret_cast<uint2*>(p.out + r * kHeadDim + 4 * lane) = w;
-  if (lane == 0) p.lse[r] = none ? (p.sinks ? sink : -INFINITY) : e.lse;
 }
 
 // The visibility of one token at position t to row j (sel: the block's

@@ -160,6 +160,33 @@ def test_hidden_values_do_not_leak(kv, scale, q_lens):
     assert np.isnan(m).sum() == 2
 
 
+@pytest.mark.parametrize("kv,scale", [(BF, NONE), (BF, TOKEN), (F8, TOKEN)])
+def test_hidden_values_in_many_requests(kv, scale):
+    # more requests than CTAs: tiles of several blocks that one CTA holds whole, every
+    # third with a token that only its own row sees and that holds NaN
+    rng = np.random.default_rng(29)
+    q_lens = [int(x) for x in rng.integers(3, 7, 200)]
+    ctxs = [int(x) for x in rng.integers(0, 400, 200)]
+    w = make(31, q_lens, ctxs, 16, kv, scale)
+    clean = W.custom(31, q_lens, [x + y for x, y in zip(ctxs, q_lens)], hq=16, kv_dtype=kv, scale_mode=scale)
+    mask = T.random_mask(rng, q_lens, 1, "tree")
+    hidden = []
+    for r in range(0, 200, 3):
+        q1 = int(w.cu_seqlens_q[r + 1])
+        pos = ctxs[r] + q_lens[r] - 1
+        w.v_cache[w.block_table[r, pos // 128], pos % 128, 0, ::5] = 0x7f if kv == F8 else 0x7fc0
+        mask[q1 - q_lens[r]:q1, 0] &= ~np.uint32(1 << (q_lens[r] - 1)).view(mask.dtype)
+        mask[q1 - 1, 0] |= 1 << (q_lens[r] - 1)
+        hidden.append(q1 - 1)
+    c = case(w)
+    c.tree_attn(mask=T.dev(mask))
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 0
+    check_attn(c, T.tree_attn(clean, mask), [r for r in range(w.num_rows) if r not in set(hidden)])
+    got = c.out.float().cpu().numpy()
+    assert all(np.isnan(got[r, :, ::5]).all() for r in hidden)
+
+
 @pytest.mark.parametrize("kv,scale", [(BF, NONE), (BF, SCALAR), (F8, TOKEN)])
 @pytest.mark.parametrize("hq,ql,ctx", [(16, 40, 20), (16, 20, 100), (4, 60, 3), (16, 9, 0)])
 def test_hidden_values_in_a_single_block(kv, scale, hq, ql, ctx):
