@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   if (p.scale_mode == MSA_SCALE_SCALAR) scale2 *= __ldg(p.k_scale);
   const float v_scalar = p.scale_mode == MSA_SCALE_SCALAR ? __ldg(p.v_scale) : 1.f;
   const uint32_t q_s = smem_u32(smem + C::kSmQ);
-  float o[16][4], m_run[2], l_run[2], vref = 0.f;
+  float o[16][4], m_run[2], l_run[2], vref[2] = {0.f, 0.f};
   uint32_t qa[8][4];
   bool bad = false;
   uint32_t cph = 0;
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     if (fl & kFirst) {
       m_run[0] = m_run[1] = -INFINITY;
       l_run[0] = l_run[1] = 0.f;
-      vref = 0.f;
+      vref[0] = vref[1] = 0.f;
       bad = (fl & kPoison) != 0;
       stage_of_tile = 0;
 #pragma unroll
@@ -471,35 +471,36 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if constexpr (PTH) {
           // v scales folded into P, relative to a power of two that only
           // grows, so that P keeps its range in 16 bits whatever the scales
-          float vm = 0.f;
+          // (of the tokens that the row sees: another's scale must not cost it its range)
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+          for (int hh = 0; hh < 2; ++hh) {
+            float vm = 0.f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (t0 + 8 * u + 2 * c + e < si.seq) vm = fmaxf(vm, fabsf(vsc[u][e]));
-          vm = fmaxf(vm, __shfl_xor_sync(full_mask, vm, 1));
-          vm = fmaxf(vm, __shfl_xor_sync(full_mask, vm, 2));
-          if (vm > vref) {
-            // the next power of two above vm (its exponent field, plus one)
-            const float nr = __uint_as_float(min((__float_as_uint(vm) & 0x7f800000u) + 0x00800000u,
-                                                 0x7e800000u));
-            const float f = vref / nr;
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              o[j][0] *= f; o[j][1] *= f; o[j][2] *= f; o[j][3] *= f;
+              for (int e = 0; e < 2; ++e)
+                if ((vis[hh] >> (8 * u + 2 * c + e)) & 1u) vm = fmaxf(vm, fabsf(vsc[u][e]));
+            vm = fmaxf(vm, __shfl_xor_sync(full_mask, vm, 1));
+            vm = fmaxf(vm, __shfl_xor_sync(full_mask, vm, 2));
+            if (vm > vref[hh]) {
+              // the next power of two above vm (its exponent field, plus one)
+              const float nr = __uint_as_float(min((__float_as_uint(vm) & 0x7f800000u) + 0x00800000u,
+                                                   0x7e800000u));
+              const float f = vref[hh] / nr;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                o[j][2 * hh] *= f;
+                o[j][2 * hh + 1] *= f;
+              }
+              vref[hh] = nr;
             }
-            vref = nr;
+            const float iv = vref[hh] > 0.f ? 1.f / vref[hh] : 0.f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                pr[u][2 * hh + e] = (vis[hh] >> (8 * u + 2 * c + e)) & 1u ? pr[u][2 * hh + e] * (vsc[u][e] * iv) : 0.f;
           }
-          const float iv = vref > 0.f ? 1.f / vref : 0.f;
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int t = 8 * u + 2 * c + e;
-              const float f = vsc[u][e] * iv;
-              pr[u][e] = (vis[0] >> t) & 1u ? pr[u][e] * f : 0.f;
-              pr[u][2 + e] = (vis[1] >> t) & 1u ? pr[u][2 + e] * f : 0.f;
-            }
         }
         uint32_t pa[4];
         if constexpr (FP8) {
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       if constexpr (PTH) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          o[j][0] *= vref; o[j][1] *= vref; o[j][2] *= vref; o[j][3] *= vref;
+          o[j][0] *= vref[0]; o[j][1] *= vref[0]; o[j][2] *= vref[1]; o[j][3] *= vref[1];
         }
       }
       if constexpr (NW > 1) {

@@ -804,7 +804,16 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
           ok = warp_wait(&sc_full[n % kScales], (n / kScales) & 1);
           if (!ok) break;
           ks = reinterpret_cast<const float*>(smem + C::kSmScale) + (n % kScales) * (2 * 128 + 4);
-          const float vm = fmaxf(fmaxf(ks[256], ks[257]), fmaxf(ks[258], ks[259]));
+          float vm = fmaxf(fmaxf(ks[256], ks[257]), fmaxf(ks[258], ks[259]));
+          if (masked && __any_sync(0xffffffffu, vm > vref)) {
+            // of the tokens that this row sees: another's scale must not cost it its range
+            vm = 0.f;
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w)
+              for (uint32_t left = vis[w]; left; left &= left - 1)
+                vm = fmaxf(vm, fabsf(ks[128 + 32 * w + __ffs(left) - 1]));
+            __syncwarp();
+          }
           if (vm > vref) {
             // the next power of two above vm (its exponent field, plus one)
             const float nr = __uint_as_float(min((__float_as_uint(vm) & 0x7f800000u) + 0x00800000u, 0x7e800000u));
@@ -840,7 +849,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
               mx = sg >= 0.f ? max64<false, false, PTH>(r, -INFINITY, v0, v1, kh) * sg
                              : max64<true, false, PTH>(r, -INFINITY, v0, v1, kh) * -sg;
             const bool move = mx > m_run + kSlack || (m_run == -INFINITY && mx > -INFINITY);
-            if (__any_sync(0xffffffffu, move) || grow != 1.f) {
+            if (__any_sync(0xffffffffu, move || grow != 1.f)) {
               float al = 1.f;
               if (mx > m_run) {
                 al = m_run == -INFINITY ? 1.f : ex2_ftz(m_run - mx);

@@ -405,3 +405,21 @@ def test_v_scales_over_a_wide_range():
     vmax = float(w.v_scale.max()) * 448
     err = np.abs(c.out.double().cpu().numpy() - out)
     assert (err <= ot + 604 * 2.0 ** -24 * vmax).all()
+
+
+@pytest.mark.parametrize("kv", [BF, F8])
+@pytest.mark.parametrize("scale", [2.0 ** 60, np.inf, np.nan])
+@pytest.mark.parametrize("ql,ctx", [(2, 300), (7, 300), (7, 0), (20, 1000)])
+def test_hidden_scales_do_not_leak(kv, scale, ql, ctx):
+    # the last drafted token, which its own row alone sees, has a v scale beside which every
+    # other one's P would round to nothing
+    w = make(33, [ql], [ctx], 16, kv, TOKEN)
+    clean = W.custom(33, [ql], [ctx + ql], hq=16, kv_dtype=kv, scale_mode=TOKEN)
+    mask = T.random_mask(np.random.default_rng(2), [ql], 1, "tree")
+    pos = ctx + ql - 1
+    w.v_scale[w.block_table[0, pos // 128], pos % 128] = scale
+    c = case(w)
+    c.tree_attn(mask=T.dev(mask))
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 0
+    check_attn(c, T.tree_attn(clean, mask), slice(0, ql - 1))
