@@ -18,9 +18,9 @@
 // logits and P in the softmax.  (bf16 pools with a scale per token stay on
 // tree_attn.cu.)
 //
-// Measured: 8 requests of 48..64 rows x 16 heads over 8192..32768 bf16 tokens 82 us,
-// 65 GFLOP (789 TFLOP/s; 34 us at cuBLAS's rate); 2 of 33 rows x 12 heads over 131K
-// e4m3 tokens with scales 106 us; 16 of 16..32 rows that select 16 blocks each 43 us.
+// Measured: 8 requests of 48..64 rows x 16 heads over 8192..32768 bf16 tokens 83 us,
+// 65 GFLOP (780 TFLOP/s; 34 us at cuBLAS's rate); 2 of 33 rows x 12 heads over 131K
+// e4m3 tokens with scales 102 us; 16 of 16..32 rows that select 16 blocks each 42 us.
 // Bound by the chain of a block through S, softmax and P V at two tiles a CTA: the
 // wide trees take 79 us without the 2^x, 81 with a quarter of the products, 64
 // without both, of which 5 go by before the first product and 11 in the merge.
@@ -62,6 +62,20 @@ struct BlockInfo {
 constexpr int kLooks = 4;
 constexpr int kScales = 4;  // blocks whose scales are held
 constexpr int kConv = 4;    // converting warps (e4m3 pools)
+
+// e4m3: 512 threads are launched with 128 registers each; the softmax warpgroups take
+// 24 more from the two others (104 + 152 + 152 + 104 = 4 * 128), which ends their
+// spills: 120 us without, 103 with it for 2 requests of 33 rows x 12 heads over 131K
+// tokens with scales; 160 and 96 are the same to 0.1 us
+constexpr int kRegsFew = 104, kRegsMore = 152;
+template <int N>
+__device__ __forceinline__ void regs_fewer() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 template <bool FP8, bool PTH>
 struct TcCfg {
@@ -171,6 +185,17 @@ __device__ __forceinline__ float exp64(const uint32_t (&r)[64], uint32_t pa, flo
     tc::tmem_st16(pa + 16 * q, w);
   }
   return ((l[0] + l[1]) + (l[2] + l[3])) + ((l[4] + l[5]) + (l[6] + l[7]));
+}
+
+// largest |v scale| of the tokens with a set bit
+__device__ __noinline__ float seen_max(const float* vs, uint4 vis) {
+  float m = 0.f;
+#pragma unroll 1
+  for (int w = 0; w < 4; ++w)
+    for (uint32_t left = w == 0 ? vis.x : w == 1 ? vis.y : w == 2 ? vis.z : vis.w; left; left &= left - 1)
+      m = fmaxf(m, fabsf(vs[32 * w + __ffs(left) - 1]));
+  __syncwarp();
+  return m;
 }
 
 // O += P V of a block for the row of this thread, the tokens with a set bit of vis
@@ -310,7 +335,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
   }
 
   if (sl.begin < sl.end) {
-    if (warp == 0) {
+    const auto copies = [&]() {
       // ---------------------------------------------- copies
       long long it = sl.begin, pre = sl.pre;
       int q = sl.q, n = 0, n_seg = 0, x = 0, fills = 0;  // blocks, segments, ring uses
@@ -492,15 +517,16 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
         if (!FP8 && n_seg > 0) mbar_wait(q_full, (n_seg - 1) & 1);
       }
       if (lane == 0) p.split[blockIdx.x] = rec;
-    } else if (warp == 1 || warp == 2) {
+    };
+    const auto products = [&]() {
       // ---------------------------------------------- products of tile t
       // P V of a block's two halves as their softmax is done, and S of the next.
       // kAhead (bf16): S in two products of 64 tokens.  The first goes over the
       // second half's logits as soon as they are in registers, so that the softmax
       // goes on while P V runs; the second goes over P.  In one product, behind P V,
       // 8 requests of 48..64 rows x 16 heads took 101 us against 84.  e4m3 (2 requests
-      // of 33 rows x 12 heads over 131K tokens): 106 us in one product, 118 in two (105
-      // with a fourth 16-bit tile and more registers for the softmax besides).
+      // of 33 rows x 12 heads over 131K tokens): 106 us in one product, 118 in two
+      // (before registers were moved to the softmax).
       const int t = warp - 1;
       if (lane == 0) {
         const uint64_t qd = tc::desc_kmajor_sw128(smem_u32(smem + kSmQ + t * kTile));
@@ -600,7 +626,8 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
         tc::commit(&drained[t]);
         if (!mbar_wait(&drained[t], 0)) misc[0] = 1;
       }
-    } else if (!FP8 && warp == 3) {
+    };
+    const auto look = [&]() {
       // ---------------------------------------------- values that are not finite
       // in the V of blocks that not every row sees (e4m3: the converting warps look)
       bool ok = true;
@@ -640,7 +667,8 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
         }
       }
       if (!ok) misc[0] = 1;
-    } else if (FP8 && warp >= 12) {
+    };
+    const auto convert = [&]() {
       // ---------------------------------------------- e4m3 tiles to f16, queries
       const int ct = tid - 12 * 32;
       int x = 0, rx = 0, seg = -1;  // 16-bit tiles, e4m3 tiles, segments
@@ -745,7 +773,8 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
         if (!ok) break;
       }
       if (!ok) misc[0] = 1;
-    } else if (warp >= 4 && warp < 12) {
+    };
+    const auto softmax = [&]() {
       // ---------------------------------------------- softmax of tile t
       const int t = (warp - 4) >> 2, quarter = warp & 3;
       const int m = quarter * 32 + lane;  // row of the tile
@@ -807,12 +836,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
           float vm = fmaxf(fmaxf(ks[256], ks[257]), fmaxf(ks[258], ks[259]));
           if (masked && __any_sync(0xffffffffu, vm > vref)) {
             // of the tokens that this row sees: another's scale must not cost it its range
-            vm = 0.f;
-#pragma unroll 1
-            for (int w = 0; w < 4; ++w)
-              for (uint32_t left = vis[w]; left; left &= left - 1)
-                vm = fmaxf(vm, fabsf(ks[128 + 32 * w + __ffs(left) - 1]));
-            __syncwarp();
+            vm = seen_max(ks + 128, make_uint4(vis[0], vis[1], vis[2], vis[3]));
           }
           if (vm > vref) {
             // the next power of two above vm (its exponent field, plus one)
@@ -973,6 +997,29 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
         }
       }
       if (!ok) misc[0] = 1;
+    };
+    if constexpr (FP8) {
+      // (a warpgroup's warps give and take registers together; bf16 dispatched like this
+      // measured 91 us where the plain order below measures 83)
+      if (warp < 4) {
+        regs_fewer<kRegsFew>();
+        if (warp == 0) copies();
+        else if (warp < 3) products();
+      } else if (warp >= 12) {
+        regs_fewer<kRegsFew>();
+        convert();
+      } else {
+        regs_more<kRegsMore>();
+        softmax();
+      }
+    } else if (warp == 0) {
+      copies();
+    } else if (warp < 3) {
+      products();
+    } else if (warp == 3) {
+      look();
+    } else {
+      softmax();
     }
   }
   tc::fence_before();
