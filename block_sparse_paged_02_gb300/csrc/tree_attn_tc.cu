@@ -12,11 +12,11 @@
 //               its rows of O); P written back over S in 16 bits
 //   O += P V    tcgen05.mma with A = P from tensor memory, B = V (MN-major)
 // Roles: warp 0 issues the tensor copies, one thread of warps 1 and 2 issues the
-// products of tile 0 and tile 1, warp 3 looks bf16 V over (below), warps 4-7 and 8-11 are the tiles' softmax.  Tensor memory
-// (512 columns): S / P and O of both tiles.  With e4m3 pools warps 12-15 turn the
-// tiles into f16 (exact) and the products run in f16; a scale per token joins the
-// logits and P in the softmax.  (bf16 pools with a scale per token stay on
-// tree_attn.cu.)
+// products of tile 0 and tile 1, warp 3 looks bf16 V over (below), warps 4-7 and
+// 8-11 are the tiles' softmax.  Tensor memory (512 columns): S / P and O of both
+// tiles.  With e4m3 pools warps 12-15 turn the tiles into f16 (exact) and the
+// products run in f16; a scale per token joins the logits and P in the softmax.
+// (bf16 pools with a scale per token stay on tree_attn.cu.)
 //
 // Measured: 8 requests of 48..64 rows x 16 heads over 8192..32768 bf16 tokens 83 us,
 // 65 GFLOP (780 TFLOP/s; 34 us at cuBLAS's rate); 2 of 33 rows x 12 heads over 131K

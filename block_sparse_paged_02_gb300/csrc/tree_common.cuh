@@ -225,17 +225,6 @@ __device__ __forceinline__ void tree_write_all_empty(const TreeLaunch& p) {
   for (long long i = at; i < n * (kHeadDim / 8); i += step) o[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// The visibility of one token at position t to row j (sel: the block's
-// selection bits, NULL when every row reads its cached tokens)
-__device__ __forceinline__ bool tree_vis_token(const TreeLaunch& p, int row, int j, int ctx, int qlen,
-                                               int t, const uint32_t* sel) {
-  if (t < ctx) return tree_row_selects(sel, j);
-  const int i = t - ctx;
-  if (i >= qlen) return false;
-  if (!p.mask) return i <= j;
-  return (__ldg(p.mask + (long long)row * p.mask_words + (i >> 5)) >> (i & 31)) & 1u;
-}
-
 // The CTA's slice of a flat item list over the requests (cost(request, its
 // visits) items each): items [begin, end) of total, cut into `ctas` equal parts, none
 // empty (later CTAs idle).  Every thread of the CTA takes part; s_ll: 40 long
