@@ -423,3 +423,30 @@ def test_hidden_scales_do_not_leak(kv, scale, ql, ctx):
     torch.cuda.synchronize()
     assert int(c.status.item()) == 0
     check_attn(c, T.tree_attn(clean, mask), slice(0, ql - 1))
+
+
+def test_two_calls_at_once():
+    # two batches on two streams, each with its workspace: the bits of the calls one by one
+    ws = [make(41, [20, 64], [3000, 700], 16, BF, NONE), make(42, [5, 1], [9000, 2000], 8, F8, TOKEN),
+          make(43, [1] * 9, [500 + 900 * i for i in range(9)], 16, BF, TOKEN)]
+    cases = [case(w) for w in ws]
+    masses = [torch.zeros((w.num_pages, 128), device="cuda") for w in ws]
+    alone = []
+    for c, m in zip(cases, masses):
+        c.tree_attn()
+        c.attn_mass(m)
+        torch.cuda.synchronize()
+        alone.append((c.out.clone(), c.lse.clone(), m.clone()))
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(20):
+        for m in masses:
+            m.zero_()
+        torch.cuda.synchronize()
+        for c, m, s in zip(cases, masses, streams):
+            c.tree_attn(stream=s)
+            c.attn_mass(m, stream=s)
+        torch.cuda.synchronize()
+        for c, m, (o, l, want) in zip(cases, masses, alone):
+            assert int(c.status.item()) == 0
+            assert torch.equal(c.out.view(torch.int16), o.view(torch.int16))
+            assert torch.equal(c.lse, l) and torch.equal(m, want)
