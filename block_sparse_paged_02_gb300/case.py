@@ -2,6 +2,7 @@
 the output buffers and workspace the C ABI needs.  Marshalling only."""
 from __future__ import annotations
 
+import contextlib
 from typing import Optional
 
 import numpy as np
@@ -19,6 +20,16 @@ def _dev(a: np.ndarray, device, dtype=None) -> torch.Tensor:
     if dtype is not None:
         t = t.to(dtype)
     return t.to(device)
+
+
+def _allocating_on(stream):
+    """Where a call on `stream` allocates what its kernels write: on that stream, so that the
+    block's earlier and later users are ordered with the call."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):  # a raw handle
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 class DeviceCase:
@@ -164,22 +175,30 @@ class DeviceCase:
         """msa_tree_attn of the batch's rows over the whole context (or the blocks of topk_idx,
         device int32 [num_rows, k]) and each other (mask: device int32 [num_rows, words])."""
         tree = B.make_tree(mask, topk_idx)
-        B.msa_tree_attn(self.batch, tree, self.attn, self._tree_workspace(tree), self.status, stream)
+        B.msa_tree_attn(self.batch, tree, self.attn, self._tree_workspace(tree, stream), self.status,
+                        stream)
 
     def attn_mass(self, mass, mask=None, topk_idx=None, stream=None):
         """msa_attn_mass of the rows whose lse a call of tree_attn wrote."""
         tree = B.make_tree(mask, topk_idx)
-        B.msa_attn_mass(self.batch, tree, self.attn, mass, self._tree_workspace(tree), self.status,
-                        stream)
+        B.msa_attn_mass(self.batch, tree, self.attn, mass, self._tree_workspace(tree, stream),
+                        self.status, stream)
 
-    def _tree_workspace(self, tree):
-        # one per selection width, kept for the life of the case
-        if tree.topk not in self._tree_ws:
+    def _tree_workspace(self, tree, stream):
+        # One per stream and selection width, kept for the life of the case: calls on two
+        # streams may overlap.  A captured call takes its own from its graph's pool, as graphs
+        # may be replayed beside each other and beside eager calls.
+        with _allocating_on(stream):
+            captured = torch.cuda.is_current_stream_capturing()
+            key = (torch.cuda.current_stream().cuda_stream, tree.topk)
+            if not captured and key in self._tree_ws:
+                return self._tree_ws[key]
             need = B.msa_tree_attn_workspace_size(self.w.num_reqs, self.num_rows, self.w.bt_stride,
                                                   self.w.hq, self.max_q_len, tree.topk)
-            self._tree_ws[tree.topk] = torch.empty((max(need, 16),), dtype=torch.uint8,
-                                                   device=self.device)
-        return self._tree_ws[tree.topk]
+            ws = torch.empty((max(need, 16),), dtype=torch.uint8, device=self.device)
+            if not captured:
+                self._tree_ws[key] = ws
+            return ws
 
     def kv_pools(self, mass=None):
         """The pools whose tokens msa_kv_compact moves together."""
@@ -189,9 +208,11 @@ class DeviceCase:
 
     def evict_select(self, lens, mass, budget: int, keep_first: int = 0, keep_recent: int = 0,
                      stream=None):
-        """The kept positions [R, budget] and their counts [R] of requests holding `lens` tokens."""
-        keep = torch.empty((self.w.num_reqs, budget), dtype=torch.int32, device=self.device)
-        keep_len = torch.empty((self.w.num_reqs,), dtype=torch.int32, device=self.device)
+        """The kept positions [R, budget] and their counts [R] of requests holding `lens` tokens,
+        as tensors of the call's stream."""
+        with _allocating_on(stream):
+            keep = torch.empty((self.w.num_reqs, budget), dtype=torch.int32, device=self.device)
+            keep_len = torch.empty((self.w.num_reqs,), dtype=torch.int32, device=self.device)
         B.msa_evict_select(B.make_cache_view(lens, self.bt, self.w.num_pages), mass, budget,
                            keep_first, keep_recent, keep, keep_len, self.status, stream)
         return keep, keep_len
