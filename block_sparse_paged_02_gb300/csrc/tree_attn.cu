@@ -34,7 +34,6 @@ constexpr int kConsWarps = 8;
 constexpr int kTaThreads = (kConsWarps + 1) * 32;
 constexpr int kStageTok = 64;
 constexpr int kAccPad = 132;
-constexpr float kSlack = 8.f;  // log2 units: the reference maximum moves only past this
 
 // stage flags
 constexpr int kFirst = 1, kLast = 2, kWhole = 4, kNoData = 8, kBadPage = 16, kPoison = 32,
@@ -279,7 +278,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   if (p.scale_mode == MSA_SCALE_SCALAR) scale2 *= __ldg(p.k_scale);
   const float v_scalar = p.scale_mode == MSA_SCALE_SCALAR ? __ldg(p.v_scale) : 1.f;
   const uint32_t q_s = smem_u32(smem + C::kSmQ);
-  float o[16][4], m_run[2], l_run[2], vref[2] = {0.f, 0.f};
+  constexpr float kHead = FP8 ? kHalfHead : 0.f;
+  float o[16][4], m_run[2], l_run[2];
   uint32_t qa[8][4];
   bool bad = false;
   uint32_t cph = 0;
@@ -309,7 +309,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     if (fl & kFirst) {
       m_run[0] = m_run[1] = -INFINITY;
       l_run[0] = l_run[1] = 0.f;
-      vref[0] = vref[1] = 0.f;
       bad = (fl & kPoison) != 0;
       stage_of_tile = 0;
 #pragma unroll
@@ -416,28 +415,31 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             }
           }
         }
-        float vsc[2][2];
+        float vsc[2][2], z[2][4];  // a token's v scale, and the exponents of P (times it)
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int t = 8 * u + 2 * c + e;
-            float f = scale2;
+            float f = scale2, lv = 0.f;
             if constexpr (PTH) {
               f *= scl[16 * slab + t];
               vsc[u][e] = scl[kStageTok + 16 * slab + t];
+              lv = log2_scale(vsc[u][e]);
             }
             s[u][e] = (vis[0] >> t) & 1u ? s[u][e] * f : -INFINITY;
             s[u][2 + e] = (vis[1] >> t) & 1u ? s[u][2 + e] * f : -INFINITY;
+            z[u][e] = PTH ? s[u][e] + lv : s[u][e];
+            z[u][2 + e] = PTH ? s[u][2 + e] + lv : s[u][2 + e];
           }
-        // ---- running maximum, moved only when it grows by more than the slack
+        // ---- the reference of P, moved only when an exponent exceeds it by more than the slack
         float mx[2];
         bool move = false;
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          mx[hh] = fmaxf(fmaxf(s[0][2 * hh], s[0][2 * hh + 1]), fmaxf(s[1][2 * hh], s[1][2 * hh + 1]));
+          mx[hh] = fmaxf(fmaxf(z[0][2 * hh], z[0][2 * hh + 1]), fmaxf(z[1][2 * hh], z[1][2 * hh + 1]));
           mx[hh] = fmaxf(mx[hh], __shfl_xor_sync(full_mask, mx[hh], 1));
-          mx[hh] = fmaxf(mx[hh], __shfl_xor_sync(full_mask, mx[hh], 2));
+          mx[hh] = fmaxf(mx[hh], __shfl_xor_sync(full_mask, mx[hh], 2)) - kHead;
           move |= mx[hh] > m_run[hh] + kSlack || (m_run[hh] == -INFINITY && mx[hh] > -INFINITY);
         }
         if (__any_sync(full_mask, move)) {
@@ -469,38 +471,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             }
         }
         if constexpr (PTH) {
-          // v scales folded into P, relative to a power of two that only
-          // grows, so that P keeps its range in 16 bits whatever the scales
-          // (of the tokens that the row sees: another's scale must not cost it its range)
+          // (the scale of a token that the row does not see may be anything)
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            float vm = 0.f;
+          for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-                if ((vis[hh] >> (8 * u + 2 * c + e)) & 1u) vm = fmaxf(vm, fabsf(vsc[u][e]));
-            vm = fmaxf(vm, __shfl_xor_sync(full_mask, vm, 1));
-            vm = fmaxf(vm, __shfl_xor_sync(full_mask, vm, 2));
-            if (vm > vref[hh]) {
-              // the next power of two above vm (its exponent field, plus one)
-              const float nr = __uint_as_float(min((__float_as_uint(vm) & 0x7f800000u) + 0x00800000u,
-                                                   0x7e800000u));
-              const float f = vref[hh] / nr;
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                o[j][2 * hh] *= f;
-                o[j][2 * hh + 1] *= f;
-              }
-              vref[hh] = nr;
-            }
-            const float iv = vref[hh] > 0.f ? 1.f / vref[hh] : 0.f;
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                pr[u][2 * hh + e] = (vis[hh] >> (8 * u + 2 * c + e)) & 1u ? pr[u][2 * hh + e] * (vsc[u][e] * iv) : 0.f;
-          }
+                pr[u][2 * hh + e] = (vis[hh] >> (8 * u + 2 * c + e)) & 1u ? pr[u][2 * hh + e] * vsc[u][e] : 0.f;
         }
         uint32_t pa[4];
         if constexpr (FP8) {
@@ -616,12 +594,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       for (int hh = 0; hh < 2; ++hh) {
         l_run[hh] += __shfl_xor_sync(full_mask, l_run[hh], 1);
         l_run[hh] += __shfl_xor_sync(full_mask, l_run[hh], 2);
-      }
-      if constexpr (PTH) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          o[j][0] *= vref[0]; o[j][1] *= vref[0]; o[j][2] *= vref[1]; o[j][3] *= vref[1];
-        }
       }
       if constexpr (NW > 1) {
         // The upper half of the token groups hands its sums to the lower half

@@ -60,7 +60,15 @@ struct BlockInfo {
 // blocks that the warp looking V over may be ahead of the softmax, and one more (both
 // rings of tiles hold it to two)
 constexpr int kLooks = 4;
-constexpr int kScales = 4;  // blocks whose scales are held
+// blocks whose scales are held: the factors of the logits, the v scales, log2 of their
+// magnitudes; then the largest and the smallest of these of each 32 tokens
+constexpr int kScales = 4;
+constexpr int kSoV = 128, kSoLog = 2 * 128, kSoRange = 3 * 128, kScaleWords = 3 * 128 + 8;
+// With a scale per token P is kept relative to max(s + log2 |v scale|).  Where the 64
+// tokens' scales lie within 2^kNear, max(s) + max(log2 |v scale|) stands for it, at most that
+// much above: the exact maximum needs a second word per token from shared memory for every
+// row (2 requests of 33 rows x 12 heads over 131K tokens: 109 us with it everywhere, 105 so).
+constexpr float kNear = 4.f;
 constexpr int kConv = 4;    // converting warps (e4m3 pools)
 
 // e4m3: 512 threads are launched with 128 registers each; the softmax warpgroups take
@@ -87,8 +95,8 @@ struct TcCfg {
   static constexpr int kSmKv = 0;
   static constexpr int kSmQ = kBufs * kTile;
   static constexpr int kSmRaw = kSmQ + 2 * kTile;
-  static constexpr int kSmScale = kSmRaw + kRaws * kRaw;  // [kScales][2][128], then maxima [4]
-  static constexpr int kSmInfo = kSmScale + (PTH ? kScales * (2 * 128 + 4) * 4 : 0);
+  static constexpr int kSmScale = kSmRaw + kRaws * kRaw;
+  static constexpr int kSmInfo = kSmScale + (PTH ? kScales * kScaleWords * 4 : 0);
   static constexpr int kSmBars = kSmInfo + kInfos * (int)sizeof(BlockInfo);
   // kv full / empty, raw full / empty, q full / empty, info full, scales full;
   // per tile: s_full, p_full and pv_done of the two halves, s_read, o_free, drained;
@@ -103,7 +111,6 @@ struct TcCfg {
 constexpr uint32_t kTmemCols = 512;
 __device__ __forceinline__ uint32_t col_s(int t) { return 128u * t; }
 __device__ __forceinline__ uint32_t col_o(int t) { return 256u + 128u * t; }
-constexpr float kSlack = 8.f;
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
@@ -115,10 +122,11 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 }
 
 // largest of 64 logits and acc (of their negations when NEG), those with a set
-// bit only when MASKED, each times its token's factor ks when PTH
-template <bool NEG, bool MASKED, bool PTH>
+// bit only when MASKED, each times its token's factor ks when PTH, plus lv when EXACT
+template <bool NEG, bool MASKED, bool PTH, bool EXACT = false>
 __device__ __forceinline__ float max64(const uint32_t (&r)[64], float acc, uint32_t vis0,
-                                       uint32_t vis1, const float* ks) {
+                                       uint32_t vis1, const float* ks,
+                                       const float* lv = nullptr) {
   float g[8] = {acc, acc, acc, acc, acc, acc, acc, acc};
 #pragma unroll
   for (int t = 0; t < 64; t += 2) {
@@ -126,6 +134,10 @@ __device__ __forceinline__ float max64(const uint32_t (&r)[64], float acc, uint3
     if (PTH) {
       const float2 k = *reinterpret_cast<const float2*>(ks + t);
       mul2v(a, b, k.x, k.y);
+    }
+    if (EXACT) {
+      a += lv[t];
+      b += lv[t + 1];
     }
     if (NEG) {
       a = -a;
@@ -185,17 +197,6 @@ __device__ __forceinline__ float exp64(const uint32_t (&r)[64], uint32_t pa, flo
     tc::tmem_st16(pa + 16 * q, w);
   }
   return ((l[0] + l[1]) + (l[2] + l[3])) + ((l[4] + l[5]) + (l[6] + l[7]));
-}
-
-// largest |v scale| of the tokens with a set bit
-__device__ __noinline__ float seen_max(const float* vs, uint4 vis) {
-  float m = 0.f;
-#pragma unroll 1
-  for (int w = 0; w < 4; ++w)
-    for (uint32_t left = w == 0 ? vis.x : w == 1 ? vis.y : w == 2 ? vis.z : vis.w; left; left &= left - 1)
-      m = fmaxf(m, fabsf(vs[32 * w + __ffs(left) - 1]));
-  __syncwarp();
-  return m;
 }
 
 // O += P V of a block for the row of this thread, the tokens with a set bit of vis
@@ -707,18 +708,21 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
         if constexpr (PTH) {
           // the block's scales (a thread per token), k's with the softmax's own
           float ks = 0.f, vs = 0.f;
-          if (!(fl & kNoData) && bi.t0 + ct < bi.seq) {
+          const bool data = !(fl & kNoData) && bi.t0 + ct < bi.seq;
+          if (data) {
             const long long at = (long long)bi.page * kBlock + ct;
             ks = __ldg(p.k_scale + at) * (p.softmax_scale * kTreeLog2e);
             vs = __ldg(p.v_scale + at);
           }
-          float* sc = reinterpret_cast<float*>(smem + C::kSmScale) + (n % kScales) * (2 * 128 + 4);
+          float* sc = reinterpret_cast<float*>(smem + C::kSmScale) + (n % kScales) * kScaleWords;
           sc[ct] = ks;
-          sc[128 + ct] = vs;
-          float mx = fabsf(vs);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          if (lane == 0) sc[256 + warp - 12] = mx;
+          sc[kSoV + ct] = vs;
+          sc[kSoLog + ct] = log2_scale(vs);
+          const uint32_t mag = scale_bits(vs);
+          const uint32_t hi = __reduce_max_sync(0xffffffffu, data ? mag : 0u);
+          const uint32_t lo = __reduce_min_sync(0xffffffffu, data ? mag : ~0u);
+          if (lane == 0)
+            reinterpret_cast<float2*>(sc + kSoRange)[warp - 12] = make_float2(bits_log2(hi), bits_log2(lo));
           __syncwarp();
           if (lane == 0) mbar_arrive(&sc_full[n % kScales]);
         }
@@ -788,9 +792,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
       }
       const float sink = p.sinks ? __ldg(p.sinks + head) : 0.f;
       float m_run = -INFINITY, l_run = 0.f;
-      // PTH: P carries its token's v scale over a power of two that only grows,
-      // so that it keeps its range in 16 bits whatever the scales
-      float vref = 0.f;
+      constexpr float kHead = FP8 ? kHalfHead : 0.f;
       bool bad = false, ok = true;
       for (int n = 0;; ++n) {
         ok = warp_wait(&info_full[n % kInfos], (n / kInfos) & 1);
@@ -802,7 +804,6 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
         if (fl & kFirst) {
           m_run = -INFINITY;
           l_run = 0.f;
-          vref = 0.f;
           bad = false;
         }
         bad |= (fl & (kBadPage | kPoison)) != 0;
@@ -828,22 +829,19 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
         bool hand = false;
         float moved = 1.f;  // what the second half scaled the first one's P by
         const float* ks = nullptr;
-        float grow = 1.f;  // what O is scaled by for a larger vref
+        // (PTH, by half) log2 of the largest v scale; whether the scales lie too far apart for it
+        float near0 = 0.f, near1 = 0.f;
+        bool exact0 = false, exact1 = false;
         if (PTH && work) {
           ok = warp_wait(&sc_full[n % kScales], (n / kScales) & 1);
           if (!ok) break;
-          ks = reinterpret_cast<const float*>(smem + C::kSmScale) + (n % kScales) * (2 * 128 + 4);
-          float vm = fmaxf(fmaxf(ks[256], ks[257]), fmaxf(ks[258], ks[259]));
-          if (masked && __any_sync(0xffffffffu, vm > vref)) {
-            // of the tokens that this row sees: another's scale must not cost it its range
-            vm = seen_max(ks + 128, make_uint4(vis[0], vis[1], vis[2], vis[3]));
-          }
-          if (vm > vref) {
-            // the next power of two above vm (its exponent field, plus one)
-            const float nr = __uint_as_float(min((__float_as_uint(vm) & 0x7f800000u) + 0x00800000u, 0x7e800000u));
-            grow = vref > 0.f ? vref / nr : 1.f;
-            vref = nr;
-          }
+          ks = reinterpret_cast<const float*>(smem + C::kSmScale) + (n % kScales) * kScaleWords;
+          const float4 r0 = *reinterpret_cast<const float4*>(ks + kSoRange);
+          const float4 r1 = *reinterpret_cast<const float4*>(ks + kSoRange + 4);
+          near0 = fmaxf(r0.x, r0.z);
+          near1 = fmaxf(r1.x, r1.z);
+          exact0 = near0 - fminf(r0.y, r0.w) > kNear;
+          exact1 = near1 - fminf(r1.y, r1.w) > kNear;
         }
         if (!kAhead) ok = warp_wait(&s_full[2 * t], n & 1);
         if (!ok) break;
@@ -865,15 +863,20 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
             }
             // (with PTH the tokens' factors carry the softmax scale and its sign)
             const float sg = PTH ? 1.f : scale2;
+            const bool exact = PTH && (half ? exact1 : exact0);
+            const float near = half ? near1 : near0;
             float mx;
-            if (masked)
+            if (exact)
+              mx = max64<false, true, PTH, true>(r, -INFINITY, v0, v1, kh, kh + kSoLog);
+            else if (masked)
               mx = sg >= 0.f ? max64<false, true, PTH>(r, -INFINITY, v0, v1, kh) * sg
                              : max64<true, true, PTH>(r, -INFINITY, v0, v1, kh) * -sg;
             else
               mx = sg >= 0.f ? max64<false, false, PTH>(r, -INFINITY, v0, v1, kh) * sg
                              : max64<true, false, PTH>(r, -INFINITY, v0, v1, kh) * -sg;
+            mx += exact ? -kHead : near - kHead;
             const bool move = mx > m_run + kSlack || (m_run == -INFINITY && mx > -INFINITY);
-            if (__any_sync(0xffffffffu, move || grow != 1.f)) {
+            if (__any_sync(0xffffffffu, move)) {
               float al = 1.f;
               if (mx > m_run) {
                 al = m_run == -INFINITY ? 1.f : ex2_ftz(m_run - mx);
@@ -881,8 +884,6 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
               }
               l_run *= al;
               if (half) moved = al;
-              al *= grow;
-              grow = 1.f;
               // (a row without a reference has an all-zero O: nothing to rescale)
               if (!((fl & kFirst) && half == 0) && __any_sync(0xffffffffu, al != 1.f)) {
                 ok = half ? warp_wait(&pv_done[2 * t], n & 1) : warp_wait(&pv_done[2 * t + 1], (n - 1) & 1);
@@ -898,17 +899,12 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
                 }
               }
             }
-            float base = m_run == -INFINITY ? 0.f : m_run, unit = 1.f;
-            if constexpr (PTH) {
-              // 2^(x - log2 vref): the sum is taken back by the same power of two
-              unit = vref > 0.f ? vref : 1.f;
-              base += (float)((int)(__float_as_uint(unit) >> 23) - 127);
-            }
-            const float* vh = PTH ? kh + 128 : nullptr;
+            const float base = m_run == -INFINITY ? 0.f : m_run;
+            const float* vh = PTH ? kh + kSoV : nullptr;
             // P of the halves side by side, over logits that have been read
             const uint32_t pa = tmem + lanes + col_s(t) + (kAhead ? 64 * (n & 1) : 0) + 32 * half;
-            l_run += unit * (masked ? exp64<true, FP8, PTH>(r, pa, scale2, base, v0, v1, kh, vh)
-                                    : exp64<false, FP8, PTH>(r, pa, scale2, base, v0, v1, kh, vh));
+            l_run += masked ? exp64<true, FP8, PTH>(r, pa, scale2, base, v0, v1, kh, vh)
+                            : exp64<false, FP8, PTH>(r, pa, scale2, base, v0, v1, kh, vh);
             tc::tmem_wait_st();
             tc::fence_before();
           } else if (kAhead && half && lane == 0) {
@@ -943,9 +939,8 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
           if (!ok) break;
           tc::fence_after();
           const bool none = bad || (m_run == -INFINITY && l_run == 0.f);
-          const float back = PTH ? vref : 1.f;
           const TreeRowEnd e = tree_row_end(none ? -INFINITY : m_run, none ? 0.f : l_run,
-                                            p.sinks != nullptr, sink * kTreeLog2e, PTH ? back : vs);
+                                            p.sinks != nullptr, sink * kTreeLog2e, vs);
           const bool have = (t == 0 || (fl & kTwo)) && !(fl & kPoison);
           const long long r = (long long)(bi.row0 + tok) * H + head;  // row x head in the batch
           const int pm = t * tpt * H + m;  // row of the pair
@@ -972,10 +967,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
                 uint4* dst = reinterpret_cast<uint4*>(p.part_o) + ((long long)bi.slot * 32 + c / 4) * 256 + pm;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                  dst[256 * i] = make_uint4(__float_as_uint(__uint_as_float(v[4 * i]) * back),
-                                      __float_as_uint(__uint_as_float(v[4 * i + 1]) * back),
-                                      __float_as_uint(__uint_as_float(v[4 * i + 2]) * back),
-                                      __float_as_uint(__uint_as_float(v[4 * i + 3]) * back));
+                  dst[256 * i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
               }
               __syncwarp();
             }

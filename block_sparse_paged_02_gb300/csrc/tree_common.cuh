@@ -156,6 +156,25 @@ __device__ __forceinline__ float ex2_ftz(float x) {
   return y;
 }
 
+// What P, rounded to 16 bits, is kept relative to: 2^m with m the largest exponent met
+// so far (log2 units), moved only when one exceeds it by more than kSlack.  Where P is
+// f16 it is kept kHalfHead above that, so that f16's full steps (from 2^-14) reach weights
+// of 2^-21 of the row's largest; kHalfHead + kSlack stays below f16's 2^16.
+constexpr float kSlack = 8.f;
+constexpr float kHalfHead = 7.f;
+
+// With a scale per token P carries it, so the exponent is that of the product, s +
+// log2 |v_scale|: a token of little weight cannot cost the others their range, however
+// large its scale.  The same 2^m divides the sum of the weights, which is fp32 and has
+// room for it: scales below 2^-40 (0 among them) count as 2^-40 here, which keeps 2^(s - m)
+// below 2^56.  The log2 is the exponent field with the mantissa as its fraction, low by
+// 0.09 at most; infinities and NaN give a finite value.
+__device__ __forceinline__ uint32_t scale_bits(float x) {
+  return max(__float_as_uint(x) & 0x7fffffffu, __float_as_uint(0x1p-40f));
+}
+__device__ __forceinline__ float bits_log2(uint32_t b) { return (float)b * 0x1p-23f - 127.f; }
+__device__ __forceinline__ float log2_scale(float x) { return bits_log2(scale_bits(x)); }
+
 // two products a * b + c in one instruction
 __device__ __forceinline__ void fma2(float& x0, float& x1, float b, float c) {
   asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"

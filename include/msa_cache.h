@@ -72,7 +72,11 @@ size_t msa_tree_attn_workspace_size(int32_t num_reqs, int32_t num_rows, int32_t 
  *             MSA_TREE_MAX_ROWS; 0: not known, taken as min(num_rows,
  *             MSA_TREE_MAX_ROWS)); a request with more rows is poisoned
  *   batch->min_q_len  as elsewhere: requests with fewer rows are poisoned
- *   attn      as for msa_sparse_paged_attn (num_rows, num_pages as in batch)
+ *   attn      as for msa_sparse_paged_attn (num_rows, num_pages as in batch).
+ *             exp(s_t - m) times a v_scale per token is rounded to 16 bits
+ *             relative to the row's largest such product, whatever the scale
+ *             of a token of less weight; magnitudes from 2^-40 to 2^80, and 0,
+ *             keep that precision
  * A poisoned request (MSA_DEV_BAD_PAGE, _BAD_LEN, _MALFORMED) gets the
  * outputs of empty rows.  Supported: as msa_sparse_paged_attn (one KV head,
  * head_dim 128, 1..16 heads); topk <= 2048. */
