@@ -34,6 +34,13 @@ __device__ __forceinline__ bool bad_pages(const msa_cache_view& c, int r, int nb
   return __syncthreads_or(bad) != 0;
 }
 
+// The cluster's barrier behind code in which a warp's lanes went different ways: its
+// instructions want the whole warp at once.
+__device__ __forceinline__ void joined_cluster_sync() {
+  __syncwarp();
+  cluster_sync();
+}
+
 __device__ __forceinline__ void red_dsmem_add(uint32_t addr, int v) {
   asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -74,7 +81,7 @@ __global__ void __launch_bounds__(EvCfg<KEYS>::kThreads, KEYS > 0 ? 2 : 1)
   }
   if (tid == 0) s_bad = 0;
   // every CTA of the cluster runs and is cleared before another adds to it
-  if (C > 1) cluster_sync();
+  if (C > 1) joined_cluster_sync();
   else __syncthreads();
 
   // ---- this warp's run of tokens, [w0, w1): whole groups of 32
@@ -180,7 +187,7 @@ __global__ void __launch_bounds__(EvCfg<KEYS>::kThreads, KEYS > 0 ? 2 : 1)
         }
       }
     }
-    if (C > 1) cluster_sync();
+    if (C > 1) joined_cluster_sync();
     else __syncthreads();
     if (pass == 0) {
       // (every CTA's pages have been looked at)
@@ -196,7 +203,7 @@ __global__ void __launch_bounds__(EvCfg<KEYS>::kThreads, KEYS > 0 ? 2 : 1)
         for (int i = me; i < L; i += everyone) keep[i] = i;
       if (why || L <= p.budget) {
         // no CTA leaves while another may still add to it
-        if (C > 1) cluster_sync();
+        if (C > 1) joined_cluster_sync();
         return;
       }
     }
@@ -236,7 +243,7 @@ __global__ void __launch_bounds__(EvCfg<KEYS>::kThreads, KEYS > 0 ? 2 : 1)
           st_dsmem_s32(mapa_shared(smem_u32(&s_left), tid), s_left);
         }
       }
-      cluster_sync();
+      joined_cluster_sync();
     } else {
       __syncthreads();
     }
@@ -278,7 +285,7 @@ __global__ void __launch_bounds__(EvCfg<KEYS>::kThreads, KEYS > 0 ? 2 : 1)
       s_count[0] = above_cta;
       s_count[1] = eq_cta;
     }
-    cluster_sync();
+    joined_cluster_sync();
     // lane c reads CTA c's counts (C <= 16)
     int a = 0, e = 0;
     if (lane < rank) {
@@ -300,7 +307,7 @@ __global__ void __launch_bounds__(EvCfg<KEYS>::kThreads, KEYS > 0 ? 2 : 1)
     eq += __popc(be);
   });
   // no CTA leaves while another reads its counts
-  if (C > 1) cluster_sync();
+  if (C > 1) joined_cluster_sync();
 }
 
 // ------------------------------------------------------------------- move
@@ -328,6 +335,7 @@ __device__ __forceinline__ void loads_done_cluster_sync(uint32_t x) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %0, 0x9e3779b9;\n\t@p nanosleep.u32 0;\n\t}" ::"r"(x)
       : "memory");
+  __syncwarp();  // (a lane may have had nothing to load)
   asm volatile(
       "barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::
           : "memory");

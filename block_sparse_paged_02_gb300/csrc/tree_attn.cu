@@ -583,6 +583,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 if (o1 && ((vis[1] >> t) & 1u)) o[j][2 + e] += p1 * x;
               }
           }
+          __syncwarp();
         }
       }
     }

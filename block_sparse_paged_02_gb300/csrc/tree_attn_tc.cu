@@ -918,6 +918,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
           }
           __syncwarp();
           if (lane == 0 && !(hand && half)) mbar_arrive(&p_full[2 * t + half]);
+          __syncwarp();
         }
         if (!ok) break;
         if (hand) {
@@ -945,6 +946,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
           const long long r = (long long)(bi.row0 + tok) * H + head;  // row x head in the batch
           const int pm = t * tpt * H + m;  // row of the pair
           const long long pr = (long long)bi.slot * 256 + pm;
+          __syncwarp();
           if (have) {
 #pragma unroll 1
             for (int c = 0; c < 128; c += 16) {

@@ -116,3 +116,35 @@ def test_one_long_request(kv, scale, hq, ql):
     w = make(62, [ql], [45000], hq, kv, scale, True)
     assert (45000 + ql) // 128 > 300
     run_both(w)
+
+
+@pytest.mark.parametrize("kv,hkv", [(W.KV_BF16, 1), (W.KV_FP8, 3)])
+@pytest.mark.parametrize("stays", [1, 17, 63, 255, 2049])
+def test_move_where_lanes_of_a_warp_differ(kv, hkv, stays):
+    # the tokens that stay, and the list's end, divide warps; some requests move nothing, one token,
+    # or their last token alone
+    rng = np.random.default_rng(stays)
+    lens = [6000, 4097, 2100, 2100, 5000]
+    bt, pages = tables(rng, lens)
+    n = stays + 1303
+    keep = np.full((5, n), -1, np.int32)
+    for r in (0, 1):
+        keep[r, :stays] = np.arange(stays)
+        keep[r, stays:] = stays + 1 + np.sort(rng.permutation(lens[r] - stays - 1)[:1303])
+    keep[2, :stays] = keep[3, :stays] = np.arange(stays)
+    keep[3, stays - 1] = 2099
+    keep[4, :stays] = np.arange(1, stays + 1)
+    move(pool_set(rng, pages, kv, hkv, kv == W.KV_FP8, 1, 128, True, True), kv, lens, bt, keep, [n, n, stays, stays, stays])
+
+
+@pytest.mark.parametrize("lens,budget", [([1], 1), ([33], 32), ([4129, 1], 4128), ([20001, 31], 31)])
+def test_select_where_lanes_of_a_warp_differ(lens, budget):
+    # lengths that end inside a warp's run, on one CTA and on clusters
+    rng = np.random.default_rng(budget)
+    bt, pages = tables(rng, lens)
+    m = masses(rng, pages, "near")
+    for stride in (bt.shape[1], 200, 2000):
+        if stride >= bt.shape[1]:
+            got = select(lens, wide(bt, stride), m, budget, 0, min(budget, 3))
+            want = T.evict(lens, bt, m, budget, 0, min(budget, 3))
+            assert np.array_equal(got[1], want[1]) and np.array_equal(got[0], want[0])
