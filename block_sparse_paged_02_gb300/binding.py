@@ -170,6 +170,13 @@ def _p(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _one_device(*tensors: Optional[torch.Tensor]):
+    """The tensors of one argument structure live on one device."""
+    there = {t.device for t in tensors if t is not None}
+    if len(there) > 1:
+        raise ValueError(f"tensors on different devices: {', '.join(sorted(map(str, there)))}")
+
+
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -187,6 +194,7 @@ def make_batch(cu_seqlens_q, cu_seqlens_k, context_lens, block_table, num_pages:
     for t in (cu_seqlens_q, cu_seqlens_k, context_lens, block_table):
         if t.dtype != torch.int32:
             raise ValueError("batch geometry arrays are int32")
+    _one_device(cu_seqlens_q, cu_seqlens_k, context_lens, block_table)
     b = msa_batch(_p(cu_seqlens_q), _p(cu_seqlens_k), _p(context_lens), _p(block_table),
                   int(block_table.shape[1]), int(context_lens.shape[0]),
                   int(num_rows if num_rows is not None else 0), int(num_pages), int(max_q_len),
@@ -211,6 +219,7 @@ def check_sinks(sinks: Optional[torch.Tensor], num_heads: int):
 def make_index_cache(k_cache, dtype: int = MSA_KV_BF16, k_scale=None) -> msa_index_cache:
     """The paged index-K cache [P, 128, heads, dim] (bf16, or e4m3 codes with
     optional fp32 per-token scales [P, 128, heads])."""
+    _one_device(k_cache, k_scale)
     x = msa_index_cache(_p(k_cache), _p(k_scale), int(dtype), int(k_cache.shape[2]),
                         int(k_cache.shape[3]))
     x._keep = (k_cache, k_scale)
@@ -221,6 +230,7 @@ def make_attn_args(q, k_cache, v_cache, kv_dtype: int, num_pages: int, out, lse,
                    scale_mode: int = MSA_SCALE_NONE, k_scale=None, v_scale=None, sinks=None,
                    softmax_scale: float) -> msa_attn_args:
     check_sinks(sinks, int(q.shape[1]))
+    _one_device(q, k_cache, v_cache, out, lse, k_scale, v_scale, sinks)
     a = msa_attn_args(_p(q), int(q.shape[0]), int(q.shape[1]), int(k_cache.shape[-2]),
                       int(q.shape[2]), _p(k_cache), _p(v_cache), int(kv_dtype), int(num_pages),
                       int(scale_mode), _p(k_scale), _p(v_scale), _p(sinks),
@@ -358,9 +368,11 @@ def _on(stream, *tensors: Optional[torch.Tensor]) -> int:
 
 
 def _first(struct) -> Optional[torch.Tensor]:
-    """The first tensor behind an argument structure that this module made."""
-    keep = getattr(struct, "_keep", None)
-    return keep[0] if keep else None
+    """A tensor behind an argument structure that this module made (all are on its device)."""
+    for t in getattr(struct, "_keep", ()):
+        if t is not None:
+            return t
+    return None
 
 
 def _calls() -> ctypes.CDLL:
@@ -374,6 +386,7 @@ def make_tree(mask: Optional[torch.Tensor] = None,
     row's selected blocks; None: the whole context)."""
     _typed("mask", mask, (torch.int32, torch.uint32), (None, None))
     _typed("topk_idx", topk_idx, (torch.int32,), (None, None))
+    _one_device(mask, topk_idx)
     t = msa_tree(_p(mask), int(mask.shape[1]) if mask is not None else 0, _p(topk_idx),
                  int(topk_idx.shape[1]) if topk_idx is not None else 0)
     t._keep = (mask, topk_idx)
@@ -405,7 +418,7 @@ def msa_tree_attn(batch: msa_batch, tree: msa_tree, attn: msa_attn_args, workspa
     ws, st = _ptr(workspace), _ptr(dev_status)
     _check("msa_tree_attn", _calls().msa_tree_attn(
         ctypes.byref(batch), ctypes.byref(tree), ctypes.byref(attn), ws, _bytes(workspace), st,
-        _on(stream, dev_status, workspace, _first(batch), _first(attn))))
+        _on(stream, dev_status, workspace, _first(batch), _first(tree), _first(attn))))
 
 
 def msa_attn_mass(batch: msa_batch, tree: msa_tree, attn: msa_attn_args, mass, workspace,
@@ -417,13 +430,14 @@ def msa_attn_mass(batch: msa_batch, tree: msa_tree, attn: msa_attn_args, mass, w
     m, ws, st = _ptr(mass), _ptr(workspace), _ptr(dev_status)
     _check("msa_attn_mass", _calls().msa_attn_mass(
         ctypes.byref(batch), ctypes.byref(tree), ctypes.byref(attn), m, ws, _bytes(workspace), st,
-        _on(stream, dev_status, workspace, mass, _first(batch), _first(attn))))
+        _on(stream, dev_status, workspace, mass, _first(batch), _first(tree), _first(attn))))
 
 
 def make_cache_view(lens, block_table, num_pages: int) -> msa_cache_view:
     """The cached tokens of a set of requests: int32 lens [R], block_table [R, bt_stride]."""
     _typed("lens", lens, (torch.int32,), (None,))
     _typed("block_table", block_table, (torch.int32,), (int(lens.shape[0]), None))
+    _one_device(lens, block_table)
     c = msa_cache_view(_p(lens), _p(block_table), int(block_table.shape[1]), int(lens.shape[0]),
                        int(num_pages))
     c._keep = (lens, block_table)
@@ -458,6 +472,7 @@ def make_kv_pools(k_cache, v_cache, kv_dtype: int, *, scale_mode: int = MSA_SCAL
     _typed("mass", mass, (torch.float32,), (pages, 128))
     if index is not None and int(index._keep[0].shape[0]) != pages:
         raise ValueError(f"the index cache has {index._keep[0].shape[0]} pages, K has {pages}")
+    _one_device(k_cache, v_cache, k_scale, v_scale, mass, *(index._keep if index is not None else ()))
     x = msa_kv_pools(_p(k_cache), _p(v_cache), int(kv_dtype), hkv, dim, int(scale_mode),
                      _p(k_scale), _p(v_scale),
                      ctypes.cast(ctypes.pointer(index), ctypes.c_void_p) if index is not None else None,
