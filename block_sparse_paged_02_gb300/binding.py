@@ -470,8 +470,13 @@ def make_kv_pools(k_cache, v_cache, kv_dtype: int, *, scale_mode: int = MSA_SCAL
         _typed("k_scale", k_scale, (torch.float32,), (pages, 128, hkv))
         _typed("v_scale", v_scale, (torch.float32,), (pages, 128, hkv))
     _typed("mass", mass, (torch.float32,), (pages, 128))
-    if index is not None and int(index._keep[0].shape[0]) != pages:
-        raise ValueError(f"the index cache has {index._keep[0].shape[0]} pages, K has {pages}")
+    if index is not None:
+        ik, iscale = index._keep
+        if int(ik.shape[0]) != pages:
+            raise ValueError(f"the index cache has {ik.shape[0]} pages, K has {pages}")
+        of = (torch.uint8, torch.float8_e4m3fn) if index.dtype == MSA_KV_FP8_E4M3 else (torch.bfloat16,)
+        _typed("index k_cache", ik, of, (pages, 128, index.heads, index.dim))
+        _typed("index k_scale", iscale, (torch.float32,), (pages, 128, index.heads))
     _one_device(k_cache, v_cache, k_scale, v_scale, mass, *(index._keep if index is not None else ()))
     x = msa_kv_pools(_p(k_cache), _p(v_cache), int(kv_dtype), hkv, dim, int(scale_mode),
                      _p(k_scale), _p(v_scale),

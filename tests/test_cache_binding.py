@@ -1,5 +1,6 @@
 """What the binding of include/msa_cache.h refuses before a call: tensors that do not live on the
-current device (on stand-ins, as one GPU or none is there)."""
+current device, index caches of another shape or type than they are named (on stand-ins, as one
+GPU or none is there)."""
 import pytest
 import torch
 
@@ -91,3 +92,26 @@ def test_calls_with_tensors_on_another_device(B):
             B.msa_kv_compact(c, None, k, n, pools(B), st)
     with pytest.raises(ValueError, match="is current"):
         B.msa_kv_compact(view(), None, keep, kl, pools(B, 1, 1, 1, 1), st)
+
+
+@pytest.mark.parametrize("dtype,tensor,scale", [
+    (0, ((9, 128, 1, 64), U8), None),               # e4m3 codes named as bf16: rows of twice their bytes
+    (1, ((9, 128, 1, 64), BF), None),
+    (0, ((9, 64, 1, 128), BF), None),
+    (1, ((9, 128, 1, 64), U8), ((9, 128), F32)),
+    (1, ((9, 128, 2, 64), U8), ((9, 128, 1), F32)),  # a scale for one head of two
+    (1, ((9, 128, 1, 64), U8), ((8, 128, 1), F32)),
+    (1, ((9, 128, 1, 64), U8), ((9, 128, 1), BF))])
+def test_index_cache_of_another_shape_or_type(B, dtype, tensor, scale):
+    index = B.make_index_cache(Stub(*tensor), dtype, None if scale is None else Stub(*scale))
+    kv = Stub((9, 128, 1, 128), BF)
+    with pytest.raises(ValueError, match="index k_"):
+        B.make_kv_pools(kv, kv, B.MSA_KV_BF16, index=index)
+
+
+def test_index_caches_that_move(B):
+    kv = Stub((9, 128, 1, 128), BF)
+    for index in (B.make_index_cache(Stub((9, 128, 1, 128), BF), B.MSA_KV_BF16),
+                  B.make_index_cache(Stub((9, 128, 2, 64), U8), B.MSA_KV_FP8_E4M3, Stub((9, 128, 2), F32)),
+                  B.make_index_cache(Stub((9, 128, 1, 64), torch.float8_e4m3fn), B.MSA_KV_FP8_E4M3)):
+        B.make_kv_pools(kv, kv, B.MSA_KV_BF16, index=index)
