@@ -59,7 +59,7 @@ struct TaCfg {
   static constexpr int kM = 16 * MW;            // rows of a tile
   static constexpr int kNW = kConsWarps / MW;   // token groups
   static constexpr int kTile = kStageTok * kHeadDim * (FP8 ? 1 : 2);
-  static constexpr int kStages = FP8 ? 8 : (MW == 8 ? 5 : 5);
+  static constexpr int kStages = FP8 ? 8 : 5;
   static constexpr int kSmK = 0;
   static constexpr int kSmV = kSmK + kStages * kTile;
   static constexpr int kSmQ = kSmV + kStages * kTile;
@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                      const __grid_constant__ CUtensorMap vmap) {
   using C = TaCfg<FP8, MW>;
   constexpr int NW = C::kNW, M = C::kM;
+  static_assert(!FP8 || NW > 1, "e4m3 pools: tiles of 32 rows at most, wider ones are tree_attn_tc.cu's");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -703,42 +704,19 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             const bool none = bad || (m_run[hh] == -INFINITY && l_run[hh] == 0.f);
             if (c == 0) p.lse[r] = p.sinks && none ? __ldg(p.sinks + m % H) : e.lse;
             uint16_t* dst = p.out + r * kHeadDim;
-            if constexpr (FP8) {
 #pragma unroll
-              for (int e2 = 0; e2 < 2; ++e2) {
-                uint32_t w[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  w[j] = none ? 0u : pack_bf16x2(o[2 * j][2 * hh + e2] * e.f, o[2 * j + 1][2 * hh + e2] * e.f);
-                uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * c + 16 * e2);
-                d4[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                d4[1] = make_uint4(w[4], w[5], w[6], w[7]);
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                *reinterpret_cast<uint32_t*>(dst + 8 * j + 2 * c) =
-                    none ? 0u : pack_bf16x2(o[j][2 * hh] * e.f, o[j][2 * hh + 1] * e.f);
-            }
+            for (int j = 0; j < 16; ++j)
+              *reinterpret_cast<uint32_t*>(dst + 8 * j + 2 * c) =
+                  none ? 0u : pack_bf16x2(o[j][2 * hh] * e.f, o[j][2 * hh + 1] * e.f);
           } else {
             if (m == 0 && c == 0) p.part_bad[slot] = bad ? 1 : 0;
             if (c == 0) p.part_ml[(long long)slot * M + m] = make_float2(m_run[hh], l_run[hh]);
             // [4-dim group][row][4 dims]: rows of a group are contiguous
             float* dst = p.part_o + ((long long)slot * (kHeadDim / 4) * M + m) * 4;
-            if constexpr (FP8) {
 #pragma unroll
-              for (int e2 = 0; e2 < 2; ++e2)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  *reinterpret_cast<float4*>(dst + (8 * c + 4 * e2 + j) * M * 4) =
-                      make_float4(o[4 * j][2 * hh + e2], o[4 * j + 1][2 * hh + e2],
-                                  o[4 * j + 2][2 * hh + e2], o[4 * j + 3][2 * hh + e2]);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                *reinterpret_cast<float2*>(dst + (2 * j + (c >> 1)) * M * 4 + 2 * (c & 1)) =
-                    make_float2(o[j][2 * hh], o[j][2 * hh + 1]);
-            }
+            for (int j = 0; j < 16; ++j)
+              *reinterpret_cast<float2*>(dst + (2 * j + (c >> 1)) * M * 4 + 2 * (c & 1)) =
+                  make_float2(o[j][2 * hh], o[j][2 * hh + 1]);
           }
         }
       }
