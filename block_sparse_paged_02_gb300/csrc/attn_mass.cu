@@ -11,14 +11,14 @@
 // lanes of tensor memory, so each thread adds up its own token's columns and
 // nothing crosses threads.  Per element one packed multiply-add, one 2^x, one
 // packed add.  With few rows the stream of K bounds it (64 requests of one row x 16
-// heads, 134 MB, in 31 us: 4.3 TB/s), with many the issue of the sums, two warps to
-// a scheduler (8 windows of 32 rows x 16 heads over 8191..65000 e4m3 tokens in 43 us,
-// 693 TFLOP/s; 39 without the 2^x or with an eighth of the products).  A quarter of
-// the 2^x as a polynomial took 54 us where 49 were; 16 columns at a time 47 against 43.
+// heads, 134 MB, in 32 us: 4.2 TB/s), with many the issue of the sums, two warps to
+// a scheduler (8 windows of 32 rows x 16 heads over 8191..65000 e4m3 tokens in 43.6 us,
+// 690 TFLOP/s, where 118 M exponentials alone would take 25; 16 columns at a time 47).
+// A quarter of the 2^x as a polynomial cost a tenth more.
 //
 // Blocks go in groups of two, one per epilogue warpgroup, so that one's sums
 // overlap the other's products, and each has two buffers of 128 columns, so that
-// its own next product runs meanwhile (49.5 us before, 46 then).  A request of at most two chunks of rows
+// its own next product runs meanwhile.  A request of at most two chunks of rows
 // keeps its queries in shared memory for all its blocks; more chunks stream
 // through two buffers, each used by the group's two blocks.  e4m3 keys are
 // converted to f16 (exact) by the four loader warps.
@@ -37,8 +37,8 @@ constexpr int kRaw = 128 * 128;    // 128 keys of e4m3
 constexpr int kInfos = 16;
 constexpr int kLoaders = 4;        // warps 12 .. 15
 // Blocks that a request's start and end count as when the work is split: its queries
-// come in, its last blocks are masked by row (window 53 us with 0, 50.5 with 2, 47.4
-// with 4 and with 6 before the loads ahead; decode 32.6, 31.1, 31.2, 31.6)
+// come in, its last blocks are masked by row (windows 47.6 us with 0, 45.3 with 2, 43.6
+// with 4, 43.4 with 6; decode 32.7, 31.4, 32.1, 31.9)
 constexpr int kStart = 4;
 constexpr int kPiece = 128;        // rows x heads of a product; four of them in tensor memory
 
@@ -536,9 +536,8 @@ cudaError_t launch_mass(const TreeLaunch& p, cudaStream_t stream) {
 template <bool FP8>
 cudaError_t launch_rows(const TreeLaunch& p, cudaStream_t stream) {
   // rows of a chunk: one token's leave the shared memory to the stream of keys.  16
-  // requests of 16384 tokens, us, chunks of 16 / 64 / 256: 16 rows x heads bf16
-  // 20.5 / 23.9 / 21.7, e4m3 18.6 / 24.6 / 22.4; 64: bf16 - / 22.9 / 21.0; 128: bf16
-  // - / 28.1 / 24.8
+  // requests of 16384 tokens, us, chunks of 16 / 256: 16 rows x heads bf16 20.7 / 21.7,
+  // e4m3 17.1 / 22.4; chunks of 256: 64 rows x heads 21.2 and 18.9, 128 25.2 and 21.6
   const int rows = p.max_rows * p.num_heads;
   return rows <= 16 ? launch_mass<FP8, 16>(p, stream) : launch_mass<FP8, 256>(p, stream);
 }

@@ -48,8 +48,8 @@ __device__ __forceinline__ void red_dsmem_add(uint32_t addr, int v) {
 // grid: (cluster, requests), one cluster per request.  KEYS: keys a thread
 // holds in registers (a CTA's share has at most its threads * KEYS tokens);
 // kInShared: in shared memory; 0: none, they are read again in every pass.  Shares
-// that fit registers: 22 us there, 31 in shared memory, 44 read again (64 requests
-// of up to 32768 tokens); beyond: 36 in shared memory, 75 read again (500009 tokens).
+// that fit registers: 22 us there, 30 in shared memory, 44 read again (64 requests
+// of up to 32768 tokens); beyond: 36 in shared memory, 74 read again (500009 tokens).
 constexpr int kInShared = -1;
 constexpr int kSharedKeys = 44 * 1024;
 template <int KEYS>
@@ -317,11 +317,13 @@ __global__ void __launch_bounds__(EvCfg<KEYS>::kThreads, KEYS > 0 ? 2 : 1)
 // consecutive destinations, a chunk's destinations lie below every later
 // chunk's sources; so whoever reads a whole chunk before any of it is written
 // never overwrites a token that is still to be read.  The pools are cut into
-// columns of a token's row (whole rows up to 256 bytes, which DRAM likes: 64-byte
-// columns moved 32 x 4096 tokens at 3.3 TB/s), and a cluster of CTAs moves one
-// column of one request, a barrier of the cluster between a chunk's reads and
-// its writes: no two clusters touch the same bytes.  Bound by the copy: 32 x 4096
-// tokens of K, V, index keys and masses, 203 MB read and written in 51 us (4.0 TB/s).
+// columns of a token's row (of 256 bytes; with 128 the same within 2%), and a cluster
+// of CTAs moves one column of one request, a barrier of the cluster between a chunk's
+// reads and its writes: no two clusters touch the same bytes.  32 x 4096 tokens of K, V,
+// index keys and masses, 203 MB read and written, take 52 us (3.9 TB/s, 58% of a copy's
+// rate): a CTA has 16 KB of a chunk in flight and 16 KB of the next, and each of the 16
+// chunks ends in a barrier.  A single request has four CTAs to each column and nothing
+// else to fill the GPU with: 16384 tokens in 85 us, where their 25 MB would stream in 4.
 constexpr int kCpThreads = 256;
 constexpr int kCpColumn = 256;  // bytes of a column
 constexpr int kCpParts = 4;     // CTAs of a cluster (long lists)
@@ -473,9 +475,9 @@ __global__ void __launch_bounds__(kCpThreads) kv_compact_kernel(const CompactLau
 
 // CTAs per request: as many as leave each 2048 tokens or more while the grid
 // fits the GPU at once; 16 (beyond the portable 8) where the device can place
-// such a cluster.  64 requests of up to 32768 tokens: 30 us with one CTA each, 21
-// with two, 22 with four; one of 500009: 891 us with one, 241 with four, 129 with
-// eight, 36 with sixteen (whose shares fit shared memory).
+// such a cluster.  64 requests of up to 32768 tokens: 30 us with one CTA each, 22
+// with two and with four; one of 500009: 898 us with one, 459 with two, 240 with four,
+// 129 with eight, 36 with sixteen (whose shares fit shared memory).
 template <int KEYS>
 cudaError_t launch_evict(const EvictLaunch& p, int C, long long share, cudaStream_t stream,
                          bool* placed) {
@@ -534,8 +536,9 @@ cudaError_t launch_kv_compact(const CompactLaunch& p, cudaStream_t stream) {
   for (int i = 0; i < kCompactPools; ++i)
     if (p.pool[i].base) cols += (p.pool[i].row + kCpColumn - 1) / kCpColumn;
   if (cols == 0) return cudaSuccess;
-  // a short list (an accepted path) is one chunk of one CTA: 16 paths of up to 8 rows
-  // 3.9 us, with the cluster 6.0; 32 x 4096 tokens 75 us with one CTA, 50 with four
+  // A short list (an accepted path) is a few chunks of 64 tokens at most, for one CTA:
+  // 16 paths of up to 8 rows 3.8 us, with the cluster 5.6; 32 x 4096 tokens 78 us with
+  // one CTA, 52 with four
   const int parts = p.keep_stride > 256 ? kCpParts : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cols * parts, p.cache.num_reqs);

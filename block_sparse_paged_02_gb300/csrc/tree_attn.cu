@@ -735,10 +735,11 @@ constexpr int kMgSets = kMgThreads / 32;  // sets of 32 threads, 4 dims a thread
 constexpr int kMgLoads = 4;               // partials that a thread has in flight
 
 // Sets that share a row's partials.  Two rows or more to a unit fill the 32-byte
-// sectors of a partial (a row to a unit: 119 us against 113 for 2 requests of 33 rows
-// x 12 heads over 131K tokens, 39 partials to a row); a row alone is for tiles that
-// most of the GPU shared.  Eight loads in flight took 100 registers and as many us
-// more as the fewer resident CTAs cost (wide trees 84 -> 88).
+// sectors of a partial (a row to a unit from 17 partials on: 110 us against 103 for 2
+// requests of 33 rows x 12 heads over 131K tokens, 39 partials to a row); a row alone
+// is for tiles that most of the GPU shared.  Eight loads in flight, at two CTAs an SM,
+// help small trees (24.8 us against 26.6) and cost wide ones (84.9 against 82.5, 105
+// against 103).
 __device__ __forceinline__ int merge_parts(int n) {
   return n <= 8 ? 1 : n <= 16 ? 2 : n <= 64 ? 4 : 8;
 }
@@ -990,14 +991,20 @@ cudaError_t launch_main(const TreeLaunch& p, cudaStream_t stream) {
   return e != cudaSuccess ? e : launch_merge(p, grid, C::kM, stream);
 }
 
-// Up to 32 rows x heads per request (one token of up to 16 heads, two of 16) the
-// stream of K and V bounds both kernels and warp MMA starts sooner; above, the
-// 5th-generation tensor cores, whose tiles of 128 rows cost the same however few
-// are used.  16 requests of 16384 tokens, us, this kernel / tree_attn_tc.cu:
-//   rows x heads         32          64          128
-//   bf16              39.6 / 40.7  61.7 / 41.0  86.9 / 44.8
-//   e4m3, scales      46.4 / 58.9  71.4 / 60.9   121 / 66.7
-// bf16 pools with a scale per token, which the latter does not take, stay here.
+// Up to 32 rows x heads per request (one token of up to 16 heads, two of 16) warp MMA,
+// which starts sooner; above, the 5th-generation tensor cores, whose tiles of 128 rows
+// cost the same however few are used.  The rule goes by the batch's largest request.
+// 16 requests of 16384 tokens, us, this kernel / tree_attn_tc.cu (the stream of K and V
+// would take 20 for bf16, 10 for e4m3):
+//   rows x heads      16        32          64          128
+//   bf16            33.9 /  39.7 / 40.7  61.0 / 40.9  87.0 / 44.3
+//   e4m3            31.4 /  40.4 / 46.6  62.3 / 46.9  96.8 / 51.1
+//   e4m3, scales    33.1 /  44.8 / 55.7  66.8 / 57.4   107 / 63.1
+// What is above the stream here is its start and the merge (11 us for one request of 700
+// tokens), ~14 blocks a CTA, and with 32 rows the products, two tiles of 16 rows by eight
+// warps that read every fragment of K and V from shared memory twice.
+// bf16 pools with a scale per token, which the latter does not take, stay here (35.2,
+// 43.4, 67.5, 100).
 // The tile is the smallest that holds a request's rows, so that short trees do not
 // carry empty rows through the products (one token of 16 heads: tile 16).
 template <bool FP8, bool PTH>

@@ -19,8 +19,9 @@
 // (bf16 pools with a scale per token stay on tree_attn.cu.)
 //
 // Measured: 8 requests of 48..64 rows x 16 heads over 8192..32768 bf16 tokens 83 us,
-// 65 GFLOP (780 TFLOP/s; 34 us at cuBLAS's rate); 2 of 33 rows x 12 heads over 131K
-// e4m3 tokens with scales 102 us; 16 of 16..32 rows that select 16 blocks each 42 us.
+// 65 GFLOP (780 TFLOP/s; 34 us at cuBLAS's rate, 27 for its 126 M exponentials at 16 a
+// clock and SM); 2 of 33 rows x 12 heads over 131K e4m3 tokens with scales 102 us; 16 of
+// 16..32 rows that select 16 blocks each 42 us.
 // Bound by the chain of a block through S, softmax and P V at two tiles a CTA: the
 // wide trees take 79 us without the 2^x, 81 with a quarter of the products, 64
 // without both, of which 5 go by before the first product and 11 in the merge.
@@ -67,14 +68,14 @@ constexpr int kSoV = 128, kSoLog = 2 * 128, kSoRange = 3 * 128, kScaleWords = 3 
 // With a scale per token P is kept relative to max(s + log2 |v scale|).  Where the 64
 // tokens' scales lie within 2^kNear, max(s) + max(log2 |v scale|) stands for it, at most that
 // much above: the exact maximum needs a second word per token from shared memory for every
-// row (2 requests of 33 rows x 12 heads over 131K tokens: 109 us with it everywhere, 105 so).
+// row (2 requests of 33 rows x 12 heads over 131K tokens: 107 us with it everywhere, 102 so).
 constexpr float kNear = 4.f;
 constexpr int kConv = 4;    // converting warps (e4m3 pools)
 
 // e4m3: 512 threads are launched with 128 registers each; the softmax warpgroups take
 // 24 more from the two others (104 + 152 + 152 + 104 = 4 * 128), which ends their
-// spills: 120 us without, 103 with it for 2 requests of 33 rows x 12 heads over 131K
-// tokens with scales; 160 and 96 are the same to 0.1 us
+// spills: 117 us without, 102.5 with it for 2 requests of 33 rows x 12 heads over 131K
+// tokens with scales, 103 with 160 and 96
 constexpr int kRegsFew = 104, kRegsMore = 152;
 template <int N>
 __device__ __forceinline__ void regs_fewer() {
@@ -525,9 +526,8 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
       // kAhead (bf16): S in two products of 64 tokens.  The first goes over the
       // second half's logits as soon as they are in registers, so that the softmax
       // goes on while P V runs; the second goes over P.  In one product, behind P V,
-      // 8 requests of 48..64 rows x 16 heads took 101 us against 84.  e4m3 (2 requests
-      // of 33 rows x 12 heads over 131K tokens): 106 us in one product, 118 in two
-      // (before registers were moved to the softmax).
+      // 8 requests of 48..64 rows x 16 heads took a fifth longer; e4m3, whose keys are
+      // converted on the way and leave a ring of three tiles, a tenth less so.
       const int t = warp - 1;
       if (lane == 0) {
         const uint64_t qd = tc::desc_kmajor_sw128(smem_u32(smem + kSmQ + t * kTile));
@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
             uint8_t* tile = smem + kSmKv + b * kTile;
             // tokens past the request's end are not data: zeros
             const int there = min(kBlock, bi.seq - bi.t0);
-            // (two at a time: eight took 114 us where two took 105, the softmax's
+            // (two at a time: eight took 106.7 us where two took 102.5, the softmax's
             // instructions wait behind them)
 #pragma unroll 2
             for (int i = ct; i < kRaw / 16; i += kConv * 32) {

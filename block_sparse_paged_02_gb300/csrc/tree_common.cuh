@@ -342,9 +342,9 @@ __device__ __forceinline__ TreeSlice tree_slice(const TreeLaunch& p, Cost cost, 
 }
 
 // A tile counts its blocks and kTreeTileCost items more, for what its start and
-// end cost (queries in, sums joined and written).  64 requests of one row took 70 us
-// without it, 56 with one item, 53 with three or four, 54.5 with seven; wide trees
-// (8 requests of 48..64 rows x 16 heads) 85 with one, 82 with four, 83 with seven.
+// end cost (queries in, sums joined and written).  64 requests of one row: 56 us with
+// one item, 53 with four, 54.5 with seven; wide trees (8 requests of 48..64 rows x 16
+// heads) 83.6, 82.5, 83.7.
 constexpr int kTreeTileCost = 4;
 
 // The part of a tile that the slice holds from item `it` on, in request items
