@@ -70,13 +70,17 @@ size_t msa_tree_attn_workspace_size(int32_t num_reqs, int32_t num_rows, int32_t 
  * per request this is single-token decode over the whole cache.
  *   batch->max_q_len  upper bound of any request's q_len (at most
  *             MSA_TREE_MAX_ROWS; 0: not known, taken as min(num_rows,
- *             MSA_TREE_MAX_ROWS)); a request with more rows is poisoned
+ *             MSA_TREE_MAX_ROWS)); a request with more rows is poisoned.  The
+ *             kernel for the whole batch is chosen by it: give the exact
+ *             bound, and batches of single rows apart from wide trees, for
+ *             speed (the workspace size takes the same value)
  *   batch->min_q_len  as elsewhere: requests with fewer rows are poisoned
  *   attn      as for msa_sparse_paged_attn (num_rows, num_pages as in batch).
  *             exp(s_t - m) times a v_scale per token is rounded to 16 bits
  *             relative to the row's largest such product, whatever the scale
  *             of a token of less weight; magnitudes from 2^-40 to 2^80, and 0,
- *             keep that precision
+ *             keep that precision.  With e4m3 pools q is converted to fp16,
+ *             so |q| must stay below 65504 (msa_attn_mass likewise)
  * A poisoned request (MSA_DEV_BAD_PAGE, _BAD_LEN, _MALFORMED) gets the
  * outputs of empty rows.  Supported: as msa_sparse_paged_attn (one KV head,
  * head_dim 128, 1..16 heads); topk <= 2048. */
@@ -93,7 +97,9 @@ msa_status msa_tree_attn(const msa_batch* batch, const msa_tree* tree, const msa
  *   mass[i] = w_t            for the step's own tokens, whose slots are new
  * with s_t and the visibility of msa_tree_attn, and lse as that call wrote it
  * (a row whose lse is -inf gives nothing).  Slots of no visited token are
- * left as they are.  The sum over rows and heads is taken in fp32 in a fixed
+ * left as they are, and so are those of tokens that a step writes without
+ * calling this: they hold what an evicted token left there, and the caller
+ * clears them before the next call counts them as cached.  The sum over rows and heads is taken in fp32 in a fixed
  * order: the same inputs give the same bits.
  *   attn      q, k_cache, k_scale and lse are read; v_cache, v_scale, sinks
  *             and out are not used and may be NULL
