@@ -26,7 +26,9 @@ EXPORTED = ("msa_index_score", "msa_topk_build_table", "msa_sparse_paged_attn", 
             "msa_kv_insert", "msa_sparse_mla_decode", "msa_sparse_mla_workspace_size",
             "msa_workspace_size", "msa_status_string", "msa_check_bounded_wait",
             "msa_tree_attn_workspace_size", "msa_tree_attn", "msa_attn_mass", "msa_evict_select",
-            "msa_kv_compact")
+            "msa_kv_compact", "msa_qk_rope_insert", "msa_prompt_attn_workspace_size",
+            "msa_prompt_attn", "msa_page_fork", "msa_page_copy")
+MSA_DEV_BAD_POS, MSA_DEV_NO_PAGES = 32, 64
 MSA_CHECK_WAIT_TMEM, MSA_CHECK_WAIT_COPY = 1, 2
 
 
@@ -92,6 +94,32 @@ class msa_kv_pools(ctypes.Structure):
                 ("index", ctypes.c_void_p), ("mass", ctypes.c_void_p)]
 
 
+class msa_rope(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("max_pos", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("positions", ctypes.c_void_p)]
+
+
+class msa_qkv(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("idx_q", ctypes.c_void_p), ("idx_k", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("idx_q_stride", ctypes.c_int64),
+                ("idx_k_stride", ctypes.c_int64), ("num_heads", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
+                ("idx_q_norm", ctypes.c_void_p), ("idx_k_norm", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("norm_shift", ctypes.c_float),
+                ("q_out", ctypes.c_void_p), ("idx_q_out", ctypes.c_void_p)]
+
+
+class msa_page_set(ctypes.Structure):
+    _fields_ = [("lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p), ("copy_src", ctypes.c_void_p),
+                ("copy_dst", ctypes.c_void_p), ("copy_tokens", ctypes.c_void_p),
+                ("bt_stride", ctypes.c_int32), ("num_reqs", ctypes.c_int32)]
+
+
 class msa_trace(ctypes.Structure):
     _fields_ = [("after_score", ctypes.c_void_p), ("after_topk", ctypes.c_void_p),
                 ("after_attn", ctypes.c_void_p), ("kernels", ctypes.c_int32)]
@@ -147,6 +175,16 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
             L.msa_evict_select.argtypes = [P, P, i32, i32, i32, P, P, P, P]
             L.msa_kv_compact.restype = ctypes.c_int
             L.msa_kv_compact.argtypes = [P, P, P, i32, P, P, P, P]
+            L.msa_qk_rope_insert.restype = ctypes.c_int
+            L.msa_qk_rope_insert.argtypes = [P, P, P, P, P, P]
+            L.msa_prompt_attn_workspace_size.restype = ctypes.c_size_t
+            L.msa_prompt_attn_workspace_size.argtypes = [i32, i32]
+            L.msa_prompt_attn.restype = ctypes.c_int
+            L.msa_prompt_attn.argtypes = [P, P, P, ctypes.c_size_t, P, P]
+            L.msa_page_fork.restype = ctypes.c_int
+            L.msa_page_fork.argtypes = [P, P, P, P, P, P, P]
+            L.msa_page_copy.restype = ctypes.c_int
+            L.msa_page_copy.argtypes = [P, i32, i32, P, P, P, i32, P, P]
             L.msa_status_string.restype = ctypes.c_char_p
             L.msa_status_string.argtypes = [ctypes.c_int]
             _lib = L
@@ -500,6 +538,160 @@ def msa_kv_compact(cache: msa_cache_view, base, keep, keep_len, pools: msa_kv_po
     _check("msa_kv_compact", _calls().msa_kv_compact(
         ctypes.byref(cache), b, k, keep.shape[1], n, ctypes.byref(pools), st,
         _on(stream, dev_status, base, keep, keep_len, _first(cache), _first(pools))))
+
+
+# -------------------------------- prompts and shared pages (msa_prompt.h)
+
+def _rows_of(name: str, t: Optional[torch.Tensor], heads=None, dim=None):
+    """Pointer, row stride and shape of bf16 vectors [N, heads, dim] whose rows may lie apart (a
+    slice of a projection's output); a row's heads are packed."""
+    if t is None:
+        return None, 0
+    _typed(name, t, (torch.bfloat16,), (None, heads, dim))
+    if not t.is_cuda:
+        raise ValueError("libmsa takes device tensors")
+    n, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the heads of a row must be packed, got strides {t.stride()}")
+    return t.data_ptr(), t.stride(0) if n > 1 else h * d
+
+
+def make_rope(cos_sin: Optional[torch.Tensor], *, interleaved: bool = False,
+              positions: Optional[torch.Tensor] = None) -> msa_rope:
+    """The rotation: cos_sin fp32 [max_pos, rotary_dim] (cosines, then sines; None: none),
+    `interleaved` pairs neighbours instead of halves, positions int32 [num_rows] (None: the
+    rows' places in the cache)."""
+    _typed("cos_sin", cos_sin, (torch.float32,), (None, None))
+    _typed("positions", positions, (torch.int32,), (None,))
+    _one_device(cos_sin, positions)
+    r = msa_rope(_p(cos_sin), int(cos_sin.shape[0]) if cos_sin is not None else 0,
+                 int(cos_sin.shape[1]) if cos_sin is not None else 0, int(bool(interleaved)),
+                 _p(positions))
+    r._keep = (cos_sin, positions)
+    return r
+
+
+def make_qkv(q, k, v, q_out, *, idx_q=None, idx_k=None, idx_q_out=None, q_norm=None, k_norm=None,
+             idx_q_norm=None, idx_k_norm=None, eps: float = 1e-6, norm_shift: float = 0.0) -> msa_qkv:
+    """The new tokens' vectors: q [N, H, 128], k and v [N, Hkv, 128], idx_q and idx_k [N, Hi, Di]
+    bf16 (rows may lie apart), their RMS-norm weights bf16 [dim] (None: not normed), and the
+    packed outputs q_out, idx_q_out bf16 (q_out may be a packed q itself)."""
+    n, h, d = (int(x) for x in q.shape)
+    hk = int(k.shape[1])
+    if k.shape[0] != n:
+        raise ValueError(f"k has {k.shape[0]} rows, q {n}")
+    qp, qs = _rows_of("q", q)
+    kp, ks = _rows_of("k", k, None, d)
+    vp, vs = _rows_of("v", v, hk, d)
+    _typed("q_out", q_out, (torch.bfloat16,), (n, h, d))
+    _typed("v", v, (torch.bfloat16,), (n, hk, d))
+    ip = jp = None
+    istr = jstr = 0
+    if (idx_q is None) != (idx_k is None) or (idx_q is None) != (idx_q_out is None):
+        raise ValueError("idx_q, idx_k and idx_q_out come together")
+    if idx_q is not None:
+        hi, di = int(idx_q.shape[1]), int(idx_q.shape[2])
+        _typed("idx_q", idx_q, (torch.bfloat16,), (n, hi, di))
+        _typed("idx_k", idx_k, (torch.bfloat16,), (n, hi, di))
+        _typed("idx_q_out", idx_q_out, (torch.bfloat16,), (n, hi, di))
+        ip, istr = _rows_of("idx_q", idx_q)
+        jp, jstr = _rows_of("idx_k", idx_k)
+        for name, w in (("idx_q_norm", idx_q_norm), ("idx_k_norm", idx_k_norm)):
+            _typed(name, w, (torch.bfloat16,), (di,))
+    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+        _typed(name, w, (torch.bfloat16,), (d,))
+    for src, stride, out in ((q, qs, q_out), (idx_q, istr, idx_q_out)):
+        if src is not None and n > 1 and out.data_ptr() == src.data_ptr() and stride != src.shape[1] * src.shape[2]:
+            raise ValueError("an output in place of its input needs packed rows")
+    _one_device(q, k, v, q_out, idx_q, idx_k, idx_q_out, q_norm, k_norm, idx_q_norm, idx_k_norm)
+    x = msa_qkv(qp, kp, vp, ip, jp, qs, ks, vs, istr, jstr, h, hk, d, _p(q_norm), _p(k_norm),
+                _p(idx_q_norm), _p(idx_k_norm), float(eps), float(norm_shift), _p(q_out), _p(idx_q_out))
+    x._keep = (q, k, v, q_out, idx_q, idx_k, idx_q_out, q_norm, k_norm, idx_q_norm, idx_k_norm)
+    x._rows = n
+    x._index = None if idx_q is None else tuple(idx_q.shape[1:])
+    return x
+
+
+def msa_qk_rope_insert(batch: msa_batch, qkv: msa_qkv, rope: msa_rope, pools: msa_kv_pools, dev_status,
+                       stream=None):
+    """Norm, rotation and insertion of the rows' vectors in one pass (see msa_prompt.h); `pools`
+    as make_kv_pools makes them (an e4m3 pool with one scale takes fp32 [1] k_scale and v_scale)."""
+    if qkv._rows != batch.num_rows:
+        raise ValueError(f"the vectors have {qkv._rows} rows, the batch {batch.num_rows}")
+    positions = rope._keep[1]
+    if positions is not None and positions.shape[0] != batch.num_rows:
+        raise ValueError(f"positions has {positions.shape[0]} rows, the batch {batch.num_rows}")
+    if pools._pages != batch.num_pages:
+        raise ValueError(f"the pools have {pools._pages} pages, the batch {batch.num_pages}")
+    k_scale, v_scale, index = pools._keep[2:5]
+    if pools.scale_mode == MSA_SCALE_SCALAR:
+        _typed("k_scale", k_scale, (torch.float32,), (1,))
+        _typed("v_scale", v_scale, (torch.float32,), (1,))
+    if index is not None and qkv._index != (index.heads, index.dim):
+        raise ValueError(f"index vectors {qkv._index}, index cache {(index.heads, index.dim)}")
+    st = _ptr(dev_status)
+    _check("msa_qk_rope_insert", _calls().msa_qk_rope_insert(
+        ctypes.byref(batch), ctypes.byref(qkv), ctypes.byref(rope), ctypes.byref(pools), st,
+        _on(stream, dev_status, _first(batch), _first(qkv), _first(rope), _first(pools))))
+
+
+def msa_prompt_attn_workspace_size(num_heads, num_kv_heads) -> int:
+    return int(lib().msa_prompt_attn_workspace_size(int(num_heads), int(num_kv_heads)))
+
+
+def msa_prompt_attn(batch: msa_batch, attn: msa_attn_args, workspace, dev_status, stream=None):
+    """Causal attention of whole prompts or their chunks over the cache (see msa_prompt.h)."""
+    ws, st = _ptr(workspace), _ptr(dev_status)
+    _check("msa_prompt_attn", _calls().msa_prompt_attn(
+        ctypes.byref(batch), ctypes.byref(attn), ws, _bytes(workspace), st,
+        _on(stream, dev_status, workspace, _first(batch), _first(attn))))
+
+
+def make_page_set(lens, block_table, refs, copy_src, copy_dst, copy_tokens) -> msa_page_set:
+    """What msa_page_fork writes: int32 lens [R], block_table [R, bt_stride], refs [num_pages] and
+    the pages to copy, copy_src, copy_dst, copy_tokens [R]."""
+    n = int(lens.shape[0])
+    _typed("lens", lens, (torch.int32,), (None,))
+    _typed("block_table", block_table, (torch.int32,), (n, None))
+    _typed("refs", refs, (torch.int32,), (None,))
+    for name, t in (("copy_src", copy_src), ("copy_dst", copy_dst), ("copy_tokens", copy_tokens)):
+        _typed(name, t, (torch.int32,), (n,))
+    every = (lens, block_table, refs, copy_src, copy_dst, copy_tokens)
+    _one_device(*every)
+    x = msa_page_set(*(_p(t) for t in every), int(block_table.shape[1]), n)
+    x._keep = every
+    return x
+
+
+def msa_page_fork(cache: msa_cache_view, refs, parent, grow, to: msa_page_set, dev_status, stream=None):
+    """The requests that go on and their pages: request i of `to` continues request parent[i] of
+    `cache` (-1: a new one) and is about to write grow[i] tokens (see msa_prompt.h)."""
+    _typed("refs", refs, (torch.int32,), (cache.num_pages,))
+    _typed("parent", parent, (torch.int32,), (to.num_reqs,))
+    _typed("grow", grow, (torch.int32,), (to.num_reqs,))
+    if to._keep[2].shape[0] != cache.num_pages:
+        raise ValueError(f"the set counts {to._keep[2].shape[0]} pages, the cache view {cache.num_pages}")
+    r, p, g, st = _ptr(refs), _ptr(parent), _ptr(grow), _ptr(dev_status)
+    _check("msa_page_fork", _calls().msa_page_fork(
+        ctypes.byref(cache), r, p, g, ctypes.byref(to), st,
+        _on(stream, dev_status, refs, parent, grow, _first(cache), _first(to))))
+
+
+def msa_page_copy(layers, src, dst, tokens, dev_status, stream=None):
+    """Copy the first tokens[i] slots of page src[i] to page dst[i] (int32 [n]) in the pools of
+    every layer (a sequence of make_kv_pools structs of as many pages each)."""
+    layers = list(layers)
+    pages = {x._pages for x in layers}
+    if len(pages) > 1:
+        raise ValueError(f"layers of different numbers of pages: {sorted(pages)}")
+    _typed("src", src, (torch.int32,), (None,))
+    n = src.shape[0]
+    _typed("dst", dst, (torch.int32,), (n,))
+    _typed("tokens", tokens, (torch.int32,), (n,))
+    s, d, t, st = _ptr(src), _ptr(dst), _ptr(tokens), _ptr(dev_status)
+    _check("msa_page_copy", _calls().msa_page_copy(
+        (msa_kv_pools * len(layers))(*layers), len(layers), pages.pop() if pages else 0, s, d, t, n, st,
+        _on(stream, dev_status, src, dst, tokens, *(_first(x) for x in layers))))
 
 
 def make_trace(after_score=None, after_topk=None, after_attn=None) -> msa_trace:

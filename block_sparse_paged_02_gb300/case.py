@@ -200,11 +200,11 @@ class DeviceCase:
                 self._tree_ws[key] = ws
             return ws
 
-    def kv_pools(self, mass=None):
+    def kv_pools(self, mass=None, index: bool = True):
         """The pools whose tokens msa_kv_compact moves together."""
         return B.make_kv_pools(self.k, self.v, self.w.kv_dtype, scale_mode=self.w.scale_mode,
-                               k_scale=self.k_scale, v_scale=self.v_scale, index=self.index,
-                               mass=mass)
+                               k_scale=self.k_scale, v_scale=self.v_scale,
+                               index=self.index if index else None, mass=mass)
 
     def evict_select(self, lens, mass, budget: int, keep_first: int = 0, keep_recent: int = 0,
                      stream=None):
@@ -221,6 +221,46 @@ class DeviceCase:
         """Move the kept tokens together in every pool of the case (and `mass`)."""
         B.msa_kv_compact(B.make_cache_view(lens, self.bt, self.w.num_pages), base, keep, keep_len,
                          self.kv_pools(mass), self.status, stream)
+
+    # -- prompts into the cache, and the sharing of its pages
+    def qk_rope_insert(self, qkv, rope, skip_index: bool = False, mass=None, stream=None):
+        """msa_qk_rope_insert of the batch's rows (make_qkv, make_rope) into the case's pools."""
+        B.msa_qk_rope_insert(self.batch, qkv, rope, self.kv_pools(mass, not skip_index), self.status,
+                             stream)
+
+    def prompt_attn(self, stream=None):
+        """msa_prompt_attn of the batch's rows."""
+        B.msa_prompt_attn(self.batch, self.attn, self._prompt_workspace(stream), self.status, stream)
+
+    def _prompt_workspace(self, stream):
+        # (as for the tree attention: one per stream, a captured call's own from its graph's pool)
+        with _allocating_on(stream):
+            captured = torch.cuda.is_current_stream_capturing()
+            key = (torch.cuda.current_stream().cuda_stream, "prompt")
+            if not captured and key in self._tree_ws:
+                return self._tree_ws[key]
+            need = B.msa_prompt_attn_workspace_size(self.w.hq, self.w.hkv)
+            ws = torch.empty((max(need, 16),), dtype=torch.uint8, device=self.device)
+            if not captured:
+                self._tree_ws[key] = ws
+            return ws
+
+    def page_fork(self, lens, refs, parent, grow=None, bt_stride: Optional[int] = None, stream=None):
+        """msa_page_fork of requests that hold `lens` tokens under the case's block table: the new
+        set (lens, block table [len(parent), bt_stride] with -1 behind the blocks, refs and the
+        pages to copy) as a make_page_set struct, tensors of the call's stream in its _keep."""
+        n, width = int(parent.shape[0]), int(bt_stride or self.w.bt_stride)
+        with _allocating_on(stream):
+            new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=self.device)
+            to = B.make_page_set(new(n), torch.full((n, width), -1, dtype=torch.int32, device=self.device),
+                                 new(self.w.num_pages), new(n), new(n), new(n))
+        B.msa_page_fork(B.make_cache_view(lens, self.bt, self.w.num_pages), refs, parent, grow, to,
+                        self.status, stream)
+        return to
+
+    def page_copy(self, src, dst, tokens, mass=None, stream=None):
+        """msa_page_copy in the case's pools (and `mass`)."""
+        B.msa_page_copy([self.kv_pools(mass)], src, dst, tokens, self.status, stream)
 
     def fetch(self):
         torch.cuda.synchronize()

@@ -519,6 +519,20 @@ bool encode_map_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_map_3d(CUtensorMap* map, CUtensorMapDataType type, const void* base, long long inner,
+                   long long rows, long long planes, long long row_stride_bytes,
+                   long long plane_stride_bytes, int box_inner, int box_rows, int box_planes) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)planes};
+  const cuuint64_t strides[2] = {(cuuint64_t)row_stride_bytes, (cuuint64_t)plane_stride_bytes};
+  const cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows, (cuuint32_t)box_planes};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, type, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool tc_score_supported(int index_heads, int index_dim) {
   return index_heads == 1 && (index_dim == 64 || index_dim == 128) && tensor_maps_available();
 }

@@ -152,6 +152,16 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// The same of a 3-D map (box at x, y, z)
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // ---- thread-block clusters: barrier (release / acquire) and distributed
 // shared-memory loads
 __device__ __forceinline__ void cluster_sync() {
@@ -351,6 +361,10 @@ cudaError_t launch_index_score(const ScoreLaunch& p, cudaStream_t stream);
 bool tensor_maps_available();
 bool encode_map_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, long long inner,
                    long long rows, long long row_stride_bytes, int box_inner, int box_rows);
+// The same for [planes][rows][inner]
+bool encode_map_3d(CUtensorMap* map, CUtensorMapDataType type, const void* base, long long inner,
+                   long long rows, long long planes, long long row_stride_bytes,
+                   long long plane_stride_bytes, int box_inner, int box_rows, int box_planes);
 cudaError_t launch_index_score_tc(const ScoreLaunch& p, cudaStream_t stream);
 bool tc_score_supported(int index_heads, int index_dim);
 struct KvInsertLaunch {
