@@ -43,15 +43,15 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
-// largest of 64 logits and acc (of their negations when NEG), those with a set
+// largest of N logits and acc (of their negations when NEG), those with a set
 // bit only when MASKED, each times its token's factor ks when PTH, plus lv when EXACT
-template <bool NEG, bool MASKED, bool PTH, bool EXACT = false>
-__device__ __forceinline__ float max64(const uint32_t (&r)[64], float acc, uint32_t vis0,
-                                       uint32_t vis1, const float* ks,
-                                       const float* lv = nullptr) {
+template <bool NEG, bool MASKED, bool PTH, bool EXACT = false, int N>
+__device__ __forceinline__ float row_max(const uint32_t (&r)[N], float acc, uint32_t vis0,
+                                         uint32_t vis1, const float* ks,
+                                         const float* lv = nullptr) {
   float g[8] = {acc, acc, acc, acc, acc, acc, acc, acc};
 #pragma unroll
-  for (int t = 0; t < 64; t += 2) {
+  for (int t = 0; t < N; t += 2) {
     float a = __uint_as_float(r[t]), b = __uint_as_float(r[t + 1]);
     if (PTH) {
       const float2 k = *reinterpret_cast<const float2*>(ks + t);
@@ -75,18 +75,18 @@ __device__ __forceinline__ float max64(const uint32_t (&r)[64], float acc, uint3
   return fmax3(fmax3(g[0], g[1], g[2]), fmax3(g[3], g[4], g[5]), fmaxf(g[6], g[7]));
 }
 
-// P = 2^(s * scale2 - m) of 64 logits as 16-bit pairs into the 32 columns at pa
+// P = 2^(s * scale2 - m) of N logits as 16-bit pairs into the N / 2 columns at pa
 // (with PTH the token's ks in the place of scale2, and P times its vs); returns
 // the fp32 sum of the 2^...
-template <bool MASKED, bool FP8, bool PTH>
-__device__ __forceinline__ float exp64(const uint32_t (&r)[64], uint32_t pa, float scale2, float m,
-                                       uint32_t vis0, uint32_t vis1, const float* ks,
-                                       const float* vs) {
+template <bool MASKED, bool FP8, bool PTH, int N>
+__device__ __forceinline__ float row_exp(const uint32_t (&r)[N], uint32_t pa, float scale2, float m,
+                                         uint32_t vis0, uint32_t vis1, const float* ks,
+                                         const float* vs) {
   // (eight sums: with four, the packed adds' latency bound the softmax, 900
   // cycles for a warp's 64 columns against 390)
   float l[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
+  for (int q = 0; q < N / 32; ++q) {
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
@@ -121,15 +121,15 @@ __device__ __forceinline__ float exp64(const uint32_t (&r)[64], uint32_t pa, flo
   return ((l[0] + l[1]) + (l[2] + l[3])) + ((l[4] + l[5]) + (l[6] + l[7]));
 }
 
-// O += P V of a block for the row of this thread, the tokens with a set bit of vis
-// alone; P (that of the first 64 tokens times f0) at pa and O at oa in tensor memory,
-// V at v, `words` x 32 tokens; O starts with it when fresh
+// Columns [c0, c1) of O += P V of a block for the row of this thread, the tokens with a
+// set bit of vis alone; P of the first 64 tokens (times f0) at pa, of the others at pa2, and O at
+// oa in tensor memory, V at v, `words` x 32 tokens; O starts with it when fresh
 template <bool FP8>
-__device__ __noinline__ void pv_by_hand(uint32_t oa, uint32_t pa, const uint8_t* v, uint4 vis4,
-                                        int words, float f0, bool fresh) {
+__device__ __noinline__ void pv_by_hand(uint32_t oa, int c0, int c1, uint32_t pa, uint32_t pa2,
+                                        const uint8_t* v, uint4 vis4, int words, float f0, bool fresh) {
   tc::tmem_wait_st();
 #pragma unroll 1
-  for (int c = 0; c < 128; c += 16) {
+  for (int c = c0; c < c1; c += 16) {
     uint32_t o[16];
     if (!fresh) tc::tmem_ld16(oa + c, o);
     float acc[16];
@@ -138,7 +138,7 @@ __device__ __noinline__ void pv_by_hand(uint32_t oa, uint32_t pa, const uint8_t*
 #pragma unroll 1
     for (int w = 0; w < words; ++w) {
       uint32_t pr[16];
-      tc::tmem_ld16(pa + 16 * w, pr);
+      tc::tmem_ld16(w < 2 ? pa + 16 * w : pa2 + 16 * (w - 2), pr);
       const uint32_t vis = w == 0 ? vis4.x : w == 1 ? vis4.y : w == 2 ? vis4.z : vis4.w;
       const float f = w < 2 ? f0 : 1.f;
 #pragma unroll

@@ -35,28 +35,27 @@
 namespace msa {
 namespace {
 
-constexpr int kInfos = 8;
-constexpr int kLooks = 4;
-constexpr int kConv = 4;  // converting warps (e4m3 pools)
-// flags of a block
-constexpr int kFirst = 1, kLast = 2, kWhole = 4, kNoData = 8, kPoison = 16, kEnd = 32, kMixed = 64,
-              kTwo = 128, kHalves = 256, kWork0 = 512, kWork1 = 1024;
+constexpr int kInfos = 8;   // segments announced
+constexpr int kPages = 8;   // blocks whose page numbers are held
+constexpr int kLooks = 4;   // blocks to look over
+constexpr int kConv = 4;    // converting warps (e4m3 pools)
+// flags of a segment
+constexpr int kWhole = 1, kTwo = 2, kPoison = 4, kEnd = 8;
 
 // What a tile pair's start and end cost, in tokens
-constexpr int kPairCost = 256;
+constexpr int kPairCost = 384;
 // Least tokens of a CTA's slice (two boundaries of blocks at least)
 constexpr long long kMinSlice = 512;
 
-struct BlockInfo {
+// A segment: blocks [b0, b0 + nb) of a tile pair that the CTA's slice holds
+struct Segment {
   int flags;
   int row0, ntok, pos0;  // the pair's rows: first in the batch, count, position of the first
-  int seq, t0;           // tokens of the request; position of the block's first
+  int seq, b0, nb;       // tokens of the request; blocks
   int slot, head;        // partial slot; KV head
   uint32_t bad;
-  int page;
 };
 
-constexpr int kRegsFew = 104, kRegsMore = 152;
 
 template <bool FP8, bool PTH>
 struct PaCfg {
@@ -67,19 +66,52 @@ struct PaCfg {
   static constexpr int kSmRaw = kSmQ + 2 * kTile;
   static constexpr int kSmScale = kSmRaw + kRaws * kRaw;
   static constexpr int kSmInfo = kSmScale + (PTH ? kScales * kScaleWords * 4 : 0);
-  static constexpr int kSmBars = kSmInfo + kInfos * (int)sizeof(BlockInfo);
+  static constexpr int kSmBars = kSmInfo + kInfos * (int)sizeof(Segment);
   // kv full / empty, raw full / empty, q full / empty, infos, scales; per tile s_full,
-  // p_full of two halves, pv_half, pv_done, o_free; fill, drained, looked
-  static constexpr int kNumBars = 2 * kBufs + 2 * kRaws + 2 + kInfos + kScales + 12 + 2 + kLooks;
+  // p_full of two halves, pv_done, o_free, drained, turn; fill; to look over, looked
+  static constexpr int kNumBars = 2 * kBufs + 2 * kRaws + 2 + kInfos + kScales + 12 + 1 + 2 * kLooks + 2;
   static constexpr int kSmMisc = kSmBars + kNumBars * 8;
-  static constexpr int kBytes = kSmMisc + 64;
+  static constexpr int kBytes = kSmMisc + 192;
   static_assert(kBytes <= 227 * 1024, "shared memory");
-  static_assert(sizeof(BlockInfo) % 8 == 0 && kSmBars % 8 == 0, "alignment");
+  static_assert(sizeof(Segment) % 8 == 0 && kSmBars % 8 == 0, "alignment");
 };
 
 constexpr uint32_t kTmemCols = 512;
 __device__ __forceinline__ uint32_t col_s(int t) { return 128u * t; }
 __device__ __forceinline__ uint32_t col_o(int t) { return 256u + 128u * t; }
+
+// word g of lane j of four becomes word j of lane g
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int lane) {
+  const bool b0 = lane & 1, b1 = lane & 2;
+  const uint32_t x0 = __shfl_xor_sync(0xffffffffu, b0 ? w[0] : w[1], 1);
+  const uint32_t x1 = __shfl_xor_sync(0xffffffffu, b0 ? w[2] : w[3], 1);
+  w[0] = b0 ? x0 : w[0];
+  w[1] = b0 ? w[1] : x0;
+  w[2] = b0 ? x1 : w[2];
+  w[3] = b0 ? w[3] : x1;
+  const uint32_t y0 = __shfl_xor_sync(0xffffffffu, b1 ? w[0] : w[2], 2);
+  const uint32_t y1 = __shfl_xor_sync(0xffffffffu, b1 ? w[1] : w[3], 2);
+  w[0] = b1 ? y0 : w[0];
+  w[2] = b1 ? w[2] : y0;
+  w[1] = b1 ? y1 : w[1];
+  w[3] = b1 ? w[3] : y1;
+}
+
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// Steps of 16 tokens from t0 on that hold one which the rows up to position `last` see; one
+// at least, which starts O in a segment's first block
+__device__ __forceinline__ int steps_to(int last, int t0) { return min(8, max(1, (last - t0 + 16) >> 4)); }
+// The tokens of the mixed block at t0 that some product reads and some row does not see:
+// first | end << 8
+__device__ __forceinline__ int looks_of(const Segment& sg, int t0) {
+  return max(0, sg.pos0 + 1 - t0) | 16 * steps_to(sg.pos0 + sg.ntok - 1, t0) << 8;
+}
 
 struct PromptReq {
   int q0, qlen, ctx, nb;
@@ -211,25 +243,29 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
   uint64_t* sc_full = info_full + kInfos;
   uint64_t* s_full = sc_full + kScales;  // [tile]
   uint64_t* p_full = s_full + 2;         // [tile][half]
-  uint64_t* pv_half = p_full + 4;        // [tile]: P V of the first half
-  uint64_t* pv_done = pv_half + 2;       // [tile]
+  uint64_t* pv_done = p_full + 4;        // [tile]
   uint64_t* o_free = pv_done + 2;        // [tile]
-  uint64_t* fill = o_free + 2;
-  uint64_t* drained = fill + 1;
-  uint64_t* looked = drained + 1;        // [kLooks]
-  BlockInfo* info = reinterpret_cast<BlockInfo*>(smem + C::kSmInfo);
-  // [0] timeout, [4 + n % kLooks] n + 1: odd values in block n's V
-  int* misc = reinterpret_cast<int*>(smem + C::kSmMisc);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 8);
+  uint64_t* drained = o_free + 2;        // [tile]
+  uint64_t* fill = drained + 2;
+  uint64_t* to_look = fill + 1;          // [kLooks]
+  uint64_t* looked = to_look + kLooks;   // [kLooks]
+  uint64_t* turn = looked + kLooks;      // [tile]: its products may go out
+  Segment* info = reinterpret_cast<Segment*>(smem + C::kSmInfo);
+  // [0] timeout; [4 + j % kLooks] block to look over (-1: none any more), then whether its V
+  // holds odd values; [16 + n % kPages] page of block n; [24 + j % kLooks] tokens to look over; [32 + 4 (j % kLooks)] as [8], a word
+  // a converting warp
+  volatile int* misc = reinterpret_cast<volatile int*>(smem + C::kSmMisc);
+  volatile int *look_at = misc + 4, *look_odd = misc + 8, *pages = misc + 16, *look_from = misc + 24, *odd_fp8 = misc + 32;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kSmMisc) + 12;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int H = p.num_heads, Hk = p.num_kv_heads, G = H / Hk;
   const int tpt = 128 / G;  // tokens per tile
 
   if (tid == 0) {
-    for (int i = 0; i < 8; ++i) misc[i] = 0;
+    misc[0] = 0;
     for (int s = 0; s < kBufs; ++s) {
       mbar_init(&kv_full[s], FP8 ? kConv : 1);
-      mbar_init(&kv_empty[s], FP8 ? 1 : 2);  // the issuer, the warp that looks V over
+      mbar_init(&kv_empty[s], 2);  // the issuers
     }
     for (int s = 0; s < kRaws; ++s) {
       mbar_init(&raw_full[s], 1);
@@ -237,19 +273,22 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
     }
     for (int s = 0; s < kScales; ++s) mbar_init(&sc_full[s], FP8 ? kConv : 1);
     mbar_init(q_full, FP8 ? kConv : 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, 2);
     for (int i = 0; i < kInfos; ++i) mbar_init(&info_full[i], 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
       mbar_init(&p_full[2 * t], 4);
       mbar_init(&p_full[2 * t + 1], 4);
-      mbar_init(&pv_half[t], 1);
       mbar_init(&pv_done[t], 1);
       mbar_init(&o_free[t], 4);
+      mbar_init(&drained[t], 1);
+      mbar_init(&turn[t], 1);
     }
     mbar_init(fill, 1);
-    mbar_init(drained, 1);
-    for (int i = 0; i < kLooks; ++i) mbar_init(&looked[i], 1);
+    for (int i = 0; i < kLooks; ++i) {
+      mbar_init(&to_look[i], 1);
+      mbar_init(&looked[i], FP8 ? kConv : 1);
+    }
     fence_barrier_init();
   }
   if (warp == 1) tc::tmem_alloc(tmem_slot, kTmemCols);
@@ -274,9 +313,7 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
   if (sl.begin < sl.end) {
     const auto copies = [&]() {
       // ---------------------------------------------- copies
-      long long it = sl.begin, pre = sl.pre;
-      int q = sl.q, n = 0, n_seg = 0, x = 0, fills = 0, checked = -1;
-      uint32_t bad = 0;
+      int n = 0, n_seg = 0, looks = 0, x = 0, fills = 0;
       bool ok = true;
       PromptSplit rec;
       rec.nrows = 0;
@@ -289,20 +326,20 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
         ++x;
         return b;
       };
-      BlockInfo bi;
-      bi.page = 0;
+      Segment sg;
       auto announce = [&]() {
         if (lane == 0) {
-          info[n % kInfos] = bi;
-          mbar_arrive(&info_full[n % kInfos]);
+          info[n_seg % kInfos] = sg;
+          mbar_arrive(&info_full[n_seg % kInfos]);
         }
-        ++n;
+        ++n_seg;
       };
-      // A block's K and V (without data they still take their places, so that no block
-      // is announced far ahead of the other roles), announced with its first copy.
-      auto push = [&](int pg) {
-        bi.page = pg;
+      // A block's K and V (without data, pg < 0, they still take their places, so that no
+      // segment is announced far ahead of the other roles)
+      auto push = [&](int pg, int t0, bool mixed) {
         const CUtensorMap* maps[2] = {&kmap, &vmap};
+        if (lane == 0) pages[n % kPages] = pg;
+        ++n;
         if constexpr (FP8) {
           for (int kv = 0; kv < 2; ++kv) {
             const int rb = acquire();
@@ -312,20 +349,20 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
                 mbar_arrive(&raw_full[rb]);
               } else {
                 mbar_arrive_expect_tx(&raw_full[rb], kRaw);
-                tma_load_2d(smem + C::kSmRaw + rb * kRaw, maps[kv], bi.head * kHeadDim, pg * kBlock, &raw_full[rb]);
+                tma_load_2d(smem + C::kSmRaw + rb * kRaw, maps[kv], sg.head * kHeadDim, pg * kBlock, &raw_full[rb]);
               }
             }
-            if (kv == 0) announce();
           }
           return;
         }
-        const int there = min(kBlock, bi.seq - bi.t0);
+        const int there = min(kBlock, sg.seq - t0);
         for (int kv = 0; kv < 2; ++kv) {
           const int b = acquire();
           if (!ok) return;
           uint8_t* dst = smem + b * kTile;
-          // V behind the request's end is not data: zeroed before a product reads it
-          const bool part = kv == 1 && pg >= 0 && there < kBlock;
+          // V behind the request's end is not data: zeroed in the step of 16 tokens that a
+          // product still reads
+          const bool part = kv == 1 && pg >= 0 && (there & 15) && there < kBlock;
           uint64_t* land = part ? fill : &kv_full[b];
           if (lane == 0) {
             if (pg < 0) {
@@ -333,109 +370,134 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
             } else {
               mbar_arrive_expect_tx(land, kTile);
               for (int h = 0; h < 2; ++h)
-                tma_load_2d(dst + h * kHalf, maps[kv], bi.head * kHeadDim + 64 * h, pg * kBlock, land);
+                tma_load_2d(dst + h * kHalf, maps[kv], sg.head * kHeadDim + 64 * h, pg * kBlock, land);
             }
           }
-          if (kv == 0) announce();
           if (part) {
             ok = warp_wait(fill, fills & 1);
             ++fills;
             if (!ok) return;
             uint4* v4 = reinterpret_cast<uint4*>(dst);
-            for (int k = there * 8 + lane; k < kBlock * 8; k += 32)
+            for (int k = there * 8 + lane; k < ((there + 15) & ~15) * 8; k += 32)
               v4[k] = v4[kHalf / 16 + k] = make_uint4(0u, 0u, 0u, 0u);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&kv_full[b]);
           }
+          // (asked for when the place's earlier uses are over, so that the wait for this one
+          // cannot take one of them for it)
+          if (!PTH && kv == 1 && mixed) {
+            if (lane == 0) {
+              look_at[looks % kLooks] = n - 1;
+              look_from[looks % kLooks] = looks_of(sg, t0);
+              mbar_arrive(&to_look[looks % kLooks]);
+            }
+            ++looks;
+          }
         }
       };
-      while (ok && it < sl.end) {
-        const PromptReq rq = prompt_request(p.batch, q);
-        const Pairs pr = pairs_of(rq, 2 * tpt);
-        const long long one = pr.before(pr.tiles), cost = rq.qlen > 0 ? one * Hk : 0;
-        if (it >= pre + cost) {
-          pre += cost;
-          ++q;
-          continue;
+      // The next segment's Q, once the products have read the last one's (e4m3: the converting
+      // warps bring the queries)
+      const auto queries = [&]() {
+        if (FP8 || !ok) return;
+        if (n_seg > 1) ok = warp_wait(q_empty, (n_seg - 2) & 1);
+        if (!ok || lane != 0) return;
+        if (sg.flags & kPoison) {
+          mbar_arrive(q_full);
+          return;
         }
-        const int32_t* table = p.batch.block_table + (long long)q * p.batch.bt_stride;
-        if (checked != q) {  // every page of the request, once
-          checked = q;
-          bad = rq.bad;
-          bool odd = false;
-#pragma unroll 4
-          for (int b = lane; b < rq.nb; b += 32) {
-            const int page = __ldg(table + b);
-            odd |= page < 0 || page >= p.batch.num_pages;
-          }
-          if (!bad && __any_sync(0xffffffffu, odd)) bad = MSA_DEV_BAD_PAGE;
+        const int tiles = sg.flags & kTwo ? 2 : 1;
+        mbar_arrive_expect_tx(q_full, 2u * tiles * qbytes);
+        for (int t = 0; t < tiles; ++t)
+          for (int h = 0; h < 2; ++h)
+            tma_load_3d(smem + kSmQ + t * kTile + h * kHalf, &qmap, 64 * h, sg.head * G, sg.row0 + t * tpt, q_full);
+      };
+      int q = sl.q, tile = 0;
+      PromptReq rq;
+      Pairs pr;
+      const int32_t* table = nullptr;
+      int page0 = 0;  // the request's first 32 pages, one a lane
+      uint32_t bad = 0;
+      const auto request = [&]() {  // request q: lengths, every page looked at
+        rq = prompt_request(p.batch, q);
+        pr = pairs_of(rq, 2 * tpt);
+        table = p.batch.block_table + (long long)q * p.batch.bt_stride;
+        bad = rq.bad;
+        bool odd = false;
+        page0 = lane < rq.nb ? __ldg(table + lane) : 0;
+#pragma unroll 8
+        for (int b = lane; b < rq.nb; b += 32) {
+          const int page = __ldg(table + b);
+          odd |= page < 0 || page >= p.batch.num_pages;
         }
-        const long long rel = it - pre;
-        bi.head = (int)(rel / one);
-        const int tile = pr.at(rel % one);
-        const long long start = pre + bi.head * one + pr.before(tile);
+        if (!bad && __any_sync(0xffffffffu, odd)) bad = MSA_DEV_BAD_PAGE;
+      };
+      request();
+      const long long one = pr.before(pr.tiles);  // of a KV head
+      sg.head = (int)((sl.begin - sl.pre) / one);
+      long long start = sl.pre + sg.head * one;
+      tile = pr.at(sl.begin - start);
+      start += pr.before(tile);
+      while (ok && start < sl.end) {
         const int seen = pr.seen(tile), nv = (seen + kBlock - 1) / kBlock;
         // blocks of the pair in the slice: block b is the CTA's whose slice holds
         // token kPairCost + 128 b of the pair
+        const long long first = start + kPairCost, stop = first + seen;
         const auto block_at = [&](long long u) {
-          const long long in = u - start;
-          return in <= kPairCost ? 0 : min((long long)nv, (in - kPairCost + kBlock - 1) / kBlock);
+          return u <= first ? 0 : (int)min((long long)nv, (u - first + kBlock - 1) / kBlock);
         };
-        const long long stop = start + kPairCost + seen;
-        const int b0 = (int)block_at(it), nb = (int)(stop <= sl.end ? nv : block_at(sl.end)) - b0;
-        const long long first = start + kPairCost;
-        it = min(stop, sl.end);
-        if (nb <= 0) continue;
-        const int j0 = tile * 2 * tpt;
-        bi.ntok = min(2 * tpt, rq.qlen - j0);
-        bi.row0 = rq.q0 + j0;
-        bi.pos0 = rq.ctx + j0;
-        bi.seq = rq.ctx + rq.qlen;
-        bi.slot = 2 * blockIdx.x + (b0 > 0 ? 0 : 1);
-        bi.bad = bad;
-        const int both = (nb == nv ? kWhole : 0) | (bi.ntok > tpt ? kTwo : 0);
-        const auto owner = [&](long long u) { return ((u + 1) * sl.ctas - 1) / sl.total; };
-        if (b0 > 0 && owner(first) == (long long)blockIdx.x - 1) {
-          rec.nrows = bi.ntok * G;
-          rec.row0 = bi.row0;
-          rec.head = bi.head;
-          rec.last = (int)owner(first + (long long)(nv - 1) * kBlock);
+        sg.b0 = block_at(sl.begin);
+        sg.nb = (stop <= sl.end ? nv : block_at(sl.end)) - sg.b0;
+        if (sg.nb > 0) {
+          const int j0 = tile * 2 * tpt;
+          sg.ntok = min(2 * tpt, rq.qlen - j0);
+          sg.row0 = rq.q0 + j0;
+          sg.pos0 = rq.ctx + j0;
+          sg.seq = rq.ctx + rq.qlen;
+          sg.slot = 2 * blockIdx.x + (sg.b0 > 0 ? 0 : 1);
+          sg.bad = bad;
+          sg.flags = (sg.nb == nv ? kWhole : 0) | (sg.ntok > tpt ? kTwo : 0) | (bad ? kPoison : 0);
+          if (sg.b0 > 0) {
+            const auto owner = [&](long long u) { return ((u + 1) * sl.ctas - 1) / sl.total; };
+            if (owner(first) == (long long)blockIdx.x - 1) {
+              rec.nrows = sg.ntok * G;
+              rec.row0 = sg.row0;
+              rec.head = sg.head;
+              rec.last = (int)owner(first + (long long)(nv - 1) * kBlock);
+            }
+          }
+          if (bad) sg.nb = 1;
+          announce();
+          // (its first K and V before its Q, whose place is free later than theirs)
+          int page = sg.b0 == 0 ? page0 : 0;
+          for (int i = 0; ok && i < sg.nb; ++i) {
+            if ((i & 31) == 0 && sg.b0 + i > 0)
+              page = !bad && i + lane < sg.nb ? __ldg(table + sg.b0 + i + lane) : 0;
+            const int t0 = kBlock * (sg.b0 + i);
+            push(bad ? -1 : __shfl_sync(0xffffffffu, page, i & 31), t0, !bad && t0 + kBlock - 1 > sg.pos0);
+            if (i == 0) queries();
+          }
         }
-        // (e4m3: the converting warps bring the queries)
-        if (!FP8 && n_seg > 0) ok = warp_wait(q_empty, (n_seg - 1) & 1);
-        if (!ok) break;
-        ++n_seg;
-        if (bad) {
-          bi.flags = kFirst | kLast | kPoison | kNoData | both;
-          bi.t0 = 0;
-          if (!FP8 && lane == 0) mbar_arrive(q_full);
-          push(-1);
-          continue;
-        }
-        if (!FP8 && lane == 0) {
-          const int tiles = both & kTwo ? 2 : 1;
-          mbar_arrive_expect_tx(q_full, 2u * tiles * qbytes);
-          for (int t = 0; t < tiles; ++t)
-            for (int h = 0; h < 2; ++h)
-              tma_load_3d(smem + kSmQ + t * kTile + h * kHalf, &qmap, 64 * h, bi.head * G, bi.row0 + t * tpt, q_full);
-        }
-        const int last0 = bi.pos0 + min(tpt, bi.ntok) - 1, last1 = bi.pos0 + bi.ntok - 1;
-        for (int c0 = 0; ok && c0 < nb; c0 += 32) {
-          int page = 0;
-          if (c0 + lane < nb) page = __ldg(table + b0 + c0 + lane);
-          for (int i = 0; ok && i < min(32, nb - c0); ++i) {
-            const int pg = __shfl_sync(0xffffffffu, page, i);
-            bi.t0 = kBlock * (b0 + c0 + i);
-            bi.flags = both | (c0 + i == 0 ? kFirst : 0) | (c0 + i == nb - 1 ? kLast : 0) |
-                       (bi.t0 + kBlock - 1 > bi.pos0 ? kMixed : 0) | (last1 >= bi.t0 + 64 ? kHalves : 0) |
-                       (c0 + i == 0 || last0 >= bi.t0 ? kWork0 : 0) | (both & kTwo ? kWork1 : 0);
-            push(pg);
+        start = stop;
+        if (++tile == pr.tiles) {
+          tile = 0;
+          if (++sg.head == Hk) {
+            sg.head = 0;
+            if (start < sl.end) {  // (so that requests with rows follow)
+              do {
+                ++q;
+                request();
+              } while (rq.qlen == 0);
+            }
           }
         }
       }
+      if (lane == 0) {
+        look_at[looks % kLooks] = -1;
+        mbar_arrive(&to_look[looks % kLooks]);
+      }
       if (ok) {
-        bi.flags = kEnd;
+        sg.flags = kEnd;
         announce();
       } else {
         misc[0] = 1;
@@ -447,140 +509,139 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
       }
       if (lane == 0) p.split[blockIdx.x] = rec;
     };
-    const auto products = [&]() {
-      // ---------------------------------------------- products
-      // Block by block, tile by tile: P V of the two halves as their softmax is done,
-      // then S of the next block over the same columns.
-      if (lane != 0) return;
-      bool ok = mbar_wait(&info_full[0], 0);
-      int seg = -1, n = 0, fl = ok ? info[0].flags : kEnd;
-      const auto s_of = [&](int t, int blk, int f) {
-        if (f & (t ? kWork1 : kWork0)) {
-          const uint64_t qd = tc::desc_kmajor_sw128(smem_u32(smem + kSmQ + t * kTile));
-          const uint64_t kd = tc::desc_kmajor_sw128(smem_u32(smem + ((2 * blk) % kBufs) * kTile));
-          tc::fence_after();
+    const auto odd_of = [&](int j) {  // odd values in the V of mixed block j
+      if (!FP8) return look_odd[j % kLooks] != 0;
+      const volatile int* o = odd_fp8 + 4 * (j % kLooks);
+      return (o[0] | o[1] | o[2] | o[3]) != 0;
+    };
+    const auto products = [&](int t) {
+      // ---------------------------------------------- products of tile t
+      // Block by block: P V of the two halves as their softmax is done, then S of the
+      // next block over the same columns, which this thread's order keeps apart.
+      if (!elect_one()) return;
+      const uint64_t qd = tc::desc_kmajor_sw128(smem_u32(smem + kSmQ + t * kTile));
+      const uint64_t kd0 = tc::desc_kmajor_sw128(smem_u32(smem));
+      const uint64_t vd0 = tc::desc_mnmajor_sw128(smem_u32(smem), kHalf);
+      const uint32_t sc = tmem + col_s(t), oc = tmem + col_o(t);
+      bool ok = true;
+      int n = 0, mixes = 0;  // blocks, mixed ones
+      for (int seg = 0;; ++seg) {
+        ok = mbar_wait(&info_full[seg % kInfos], (seg / kInfos) & 1);
+        if (!ok) break;
+        const Segment& sg = info[seg % kInfos];
+        const int fl = sg.flags, nb = sg.nb, pos0 = sg.pos0;
+        if (fl & kEnd) break;
+        const int last0 = pos0 + min(tpt, sg.ntok) - 1, last1 = pos0 + sg.ntok - 1;
+        const bool on = !(fl & kPoison) && (t == 0 || (fl & kTwo));
+        int t0 = kBlock * sg.b0;
+        const auto s_of = [&](int i) {
+          const int x = 2 * (n + i), b = x % kBufs;
+          if (!mbar_wait(&kv_full[b], (x / kBufs) & 1)) return false;
+          if (on && (t == 1 || i == 0 || last0 >= t0)) {
+            const uint64_t kd = tc::desc_advance(kd0, b * kTile);
+            tc::fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-            tc::mma_ss(tmem + col_s(t), tc::desc_advance(qd, off), tc::desc_advance(kd, off), kIdescS,
-                       kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+              tc::mma_ss(sc, tc::desc_advance(qd, off), tc::desc_advance(kd, off), kIdescS, kk > 0 ? 1u : 0u);
+            }
           }
-        }
-        tc::commit(&s_full[t]);
-      };
-      const auto open = [&](int blk, int f) {  // K (and Q) of a block are there
-        bool there = true;
-        if (f & kFirst) {
-          ++seg;
-          there = mbar_wait(q_full, seg & 1);
-        }
-        return there && mbar_wait(&kv_full[(2 * blk) % kBufs], ((2 * blk) / kBufs) & 1);
-      };
-      const auto close = [&](int blk, int f) {  // S of both tiles is issued
-        tc::commit(&kv_empty[(2 * blk) % kBufs]);
-        if (f & kLast) tc::commit(q_empty);
-      };
-      if (ok && !(fl & kEnd)) {
-        ok = open(0, fl);
-        if (ok) {
-          s_of(0, 0, fl);
-          s_of(1, 0, fl);
-          close(0, fl);
-        }
-      }
-      while (ok && !(fl & kEnd)) {
-        const int vb = (2 * n + 1) % kBufs, seg_now = seg;
-        const uint64_t vd = tc::desc_mnmajor_sw128(smem_u32(smem + vb * kTile), kHalf);
-        int next = kEnd;
-        ok = mbar_wait(&kv_full[vb], ((2 * n + 1) / kBufs) & 1);
-        for (int t = 0; ok && t < 2; ++t) {
-          const bool work = (fl & (t ? kWork1 : kWork0)) != 0;
+          tc::commit(&s_full[t]);
+          tc::commit(&kv_empty[b]);
+          return true;
+        };
+        ok = mbar_wait(q_full, seg & 1) && s_of(0);
+        if (!ok) break;
+        for (int i = 0; i < nb; ++i, t0 += kBlock) {
+          const int x = 2 * (n + i) + 1, b = x % kBufs;
+          if (i == nb - 1) tc::commit(q_empty);
+          const bool work = on && (t == 1 || i == 0 || last0 >= t0), mixed = on && t0 + kBlock - 1 > pos0;
+          const uint64_t vd = tc::desc_advance(vd0, b * kTile);
+          ok = mbar_wait(&kv_full[b], (x / kBufs) & 1);
           // O of the previous segment has been read
-          if ((fl & kFirst) && seg_now > 0) ok = mbar_wait(&o_free[t], (seg_now - 1) & 1);
-          ok = ok && mbar_wait(&p_full[2 * t], n & 1);
+          if (i == 0 && seg > 0) ok = ok && mbar_wait(&o_free[t], (seg - 1) & 1);
+          // (the softmax writes P of the second half first)
+          ok = ok && mbar_wait(&p_full[2 * t + 1], (n + i) & 1);
+          // (block by block tile 0 first, so that one tile's softmax runs beside the other's products)
+          if (t == 1 || n + i > 0) ok = ok && mbar_wait(&turn[t], (n + i - 1 + t) & 1);
           if (!ok) break;
           // (the softmax adds the block's P V itself)
-          const bool hand = (fl & kMixed) && *reinterpret_cast<volatile int*>(&misc[4 + n % kLooks]) == n + 1;
-          const auto pv = [&](int half) {
-            if (!work || hand || (half && !(fl & kHalves))) return;
+          const bool hand = mixed && odd_of(mixes);
+          const int steps = mixed ? steps_to(t ? last1 : last0, t0) : 8;
+          const auto pv = [&](int half, bool on_top) {
+            if (!work || hand) return;
             tc::fence_after();
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc::mma_ts(tmem + col_o(t), tmem + col_s(t) + half * 32 + kk * 8,
-                         tc::desc_advance(vd, (half * 4 + kk) * 2048), kIdescO,
-                         (kk > 0 || half > 0 || !(fl & kFirst)) ? 1u : 0u);
+              if (4 * half + kk < steps)
+                tc::mma_ts(oc, sc + 64 * half + kk * 8, tc::desc_advance(vd, (4 * half + kk) * 2048), kIdescO,
+                           (kk > 0 || on_top) ? 1u : 0u);
           };
-          pv(0);
-          tc::commit(&pv_half[t]);
-          ok = mbar_wait(&p_full[2 * t + 1], n & 1);
+          pv(1, i > 0);
+          ok = mbar_wait(&p_full[2 * t], (n + i) & 1);
           if (!ok) break;
-          pv(1);
-          tc::commit(&pv_done[t]);
-          if (t == 1) tc::commit(&kv_empty[vb]);
-          if (t == 0) {
-            ok = mbar_wait(&info_full[(n + 1) % kInfos], ((n + 1) / kInfos) & 1);
-            if (!ok) break;
-            next = info[(n + 1) % kInfos].flags;
-            if (!(next & kEnd)) ok = open(n + 1, next);
+          pv(0, i > 0 || steps > 4);
+          if (i == nb - 1) tc::commit(&pv_done[t]);
+          tc::commit(&kv_empty[b]);
+          mixes += !(fl & kPoison) && t0 + kBlock - 1 > pos0;
+          if (i + 1 < nb) {
+            t0 += kBlock;
+            ok = s_of(i + 1);
+            t0 -= kBlock;
             if (!ok) break;
           }
-          if (!(next & kEnd)) s_of(t, n + 1, next);
+          mbar_arrive(&turn[1 - t]);
         }
         if (!ok) break;
-        if (!(next & kEnd)) close(n + 1, next);
-        ++n;
-        fl = next;
+        n += nb;
       }
       if (!ok) misc[0] = 1;
       // every product has completed before the tensor memory is freed
-      tc::commit(drained);
-      if (!mbar_wait(drained, 0)) misc[0] = 1;
+      tc::commit(&drained[t]);
+      if (!mbar_wait(&drained[t], 0)) misc[0] = 1;
+    };
+    // values that are not finite in the V of mixed block j, at place vb (bf16; e4m3: the
+    // converting warps look).  The block's P V waits for the softmax, and that for this.
+    const auto look_over = [&](int j, int vb, int range) {
+      // a row of 64 dims a lane and step
+      const int from = range & 255, rows = (range >> 8) - from;
+      uint32_t odd = 0;
+#pragma unroll 4
+      for (int i = lane; i < 16 * rows; i += 32) {
+        const int row = from + (i >> 4);
+        const uint8_t* src = smem + vb * kTile + ((i >> 3) & 1) * kHalf + row * 128 + (i & 7) * 16;
+        const uint4 v = lds128(src);
+        constexpr uint32_t one = 0x00800080u;  // an exponent's last bit
+        odd |= (v.x & 0x7fff7fffu) + one;
+        odd |= (v.y & 0x7fff7fffu) + one;
+        odd |= (v.z & 0x7fff7fffu) + one;
+        odd |= (v.w & 0x7fff7fffu) + one;
+      }
+      const bool any = __any_sync(0xffffffffu, (odd & 0x80008000u) != 0);
+      if (lane == 0) {
+        look_odd[j % kLooks] = any;
+        mbar_arrive(&looked[j % kLooks]);
+      }
     };
     const auto look = [&]() {
-      // ---------------------------------------------- values that are not finite
-      // in the V of blocks that not every row sees (e4m3: the converting warps look)
+      // ---------------------------------------------- mixed blocks, as they are asked for
       bool ok = true;
-      for (int n = 0;; ++n) {
-        ok = warp_wait(&info_full[n % kInfos], (n / kInfos) & 1);
+      for (int j = 0;; ++j) {
+        ok = warp_wait(&to_look[j % kLooks], (j / kLooks) & 1);
         if (!ok) break;
-        const int fl = info[n % kInfos].flags;
-        if (fl & kEnd) break;
-        // (every use of a place is followed, so that the ring never laps this warp)
-        const int kb = (2 * n) % kBufs, vb = (2 * n + 1) % kBufs;
-        ok = warp_wait(&kv_full[kb], ((2 * n) / kBufs) & 1);
+        const int n = look_at[j % kLooks];
+        if (n < 0) break;
+        ok = warp_wait(&kv_full[(2 * n + 1) % kBufs], ((2 * n + 1) / kBufs) & 1);
         if (!ok) break;
-        if (lane == 0) mbar_arrive(&kv_empty[kb]);
-        ok = warp_wait(&kv_full[vb], ((2 * n + 1) / kBufs) & 1);
-        if (!ok) break;
-        if ((fl & kMixed) && !(fl & kNoData)) {
-          const uint8_t* src = smem + vb * kTile + lane * 16;
-          uint32_t odd = 0;
-#pragma unroll 8
-          for (int i = 0; i < kTile; i += 512) {
-            const uint4 v = lds128(src + i);
-            constexpr uint32_t one = 0x00800080u;  // an exponent's last bit
-            odd |= (v.x & 0x7fff7fffu) + one;
-            odd |= (v.y & 0x7fff7fffu) + one;
-            odd |= (v.z & 0x7fff7fffu) + one;
-            odd |= (v.w & 0x7fff7fffu) + one;
-          }
-          const bool any = __any_sync(0xffffffffu, (odd & 0x80008000u) != 0);
-          if (lane == 0 && any) *reinterpret_cast<volatile int*>(&misc[4 + n % kLooks]) = n + 1;
-        }
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&looked[n % kLooks]);
-          mbar_arrive(&kv_empty[vb]);
-        }
+        look_over(j, (2 * n + 1) % kBufs, look_from[j % kLooks]);
       }
       if (!ok) misc[0] = 1;
     };
     // the scales of token ct of block n (a warp's 32 at a time), k's with the softmax's own
-    const auto scales_of = [&](const BlockInfo& bi, int fl, int n, int ct) {
+    const auto scales_of = [&](int head, bool data, int n, int ct) {
       float ks = 0.f, vs = 0.f;
-      const bool data = !(fl & kNoData) && bi.t0 + ct < bi.seq;
       if (data) {
-        const long long at = ((long long)bi.page * kBlock + ct) * Hk + bi.head;
+        const long long at = ((long long)pages[n % kPages] * kBlock + ct) * Hk + head;
         ks = __ldg(p.k_scale + at) * (p.softmax_scale * kTreeLog2e);
         vs = __ldg(p.v_scale + at);
       }
@@ -595,101 +656,125 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
         reinterpret_cast<float2*>(sc + kSoRange)[ct >> 5] = make_float2(bits_log2(hi), bits_log2(lo));
     };
     const auto scales = [&]() {
-      // ---------------------------------------------- scales per token of bf16 pools
+      // ---------------------------------------------- bf16 pools with a scale per token
+      // The scales of every block, and mixed blocks looked over
       bool ok = true;
-      for (int n = 0;; ++n) {
-        ok = warp_wait(&info_full[n % kInfos], (n / kInfos) & 1);
+      int n = 0, looks = 0;
+      for (int seg = 0;; ++seg) {
+        ok = warp_wait(&info_full[seg % kInfos], (seg / kInfos) & 1);
         if (!ok) break;
-        const BlockInfo& bi = info[n % kInfos];
-        const int fl = bi.flags;
+        const Segment& sg = info[seg % kInfos];
+        const int fl = sg.flags, nb = sg.nb, head = sg.head, seq = sg.seq, pos0 = sg.pos0;
         if (fl & kEnd) break;
-        // (a block is announced when its K has a place, which S of block n - 2 freed: the
-        // softmax is through with this place's block n - 4)
-        for (int i = 0; i < 4; ++i) scales_of(bi, fl, n, 32 * i + lane);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sc_full[n % kScales]);
+        int t0 = sg.b0 * kBlock;
+        for (int i = 0; i < nb; ++i, ++n, t0 += kBlock) {
+          // (K of the block has a place, which S of block n - 2 freed: its page is known, and
+          // the softmax is through with this place's block n - 4)
+          ok = warp_wait(&kv_full[(2 * n) % kBufs], ((2 * n) / kBufs) & 1);
+          if (!ok) break;
+          for (int k = 0; k < 4; ++k)
+            scales_of(head, !(fl & kPoison) && t0 + 32 * k + lane < seq, n, 32 * k + lane);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sc_full[n % kScales]);
+          // (V is followed too, so that no wait is two uses of its place behind)
+          ok = warp_wait(&kv_full[(2 * n + 1) % kBufs], ((2 * n + 1) / kBufs) & 1);
+          if (!ok) break;
+          if (!(fl & kPoison) && t0 + kBlock - 1 > pos0) look_over(looks++, (2 * n + 1) % kBufs, looks_of(sg, t0));
+        }
+        if (!ok) break;
       }
       if (!ok) misc[0] = 1;
     };
     const auto convert = [&]() {
       // ---------------------------------------------- e4m3 tiles to f16, queries
       const int ct = tid - 12 * 32;
-      int x = 0, seg = -1;  // tiles, segments
+      int x = 0, looks = 0;  // tiles, mixed blocks
       bool ok = true;
-      for (int n = 0;; ++n) {
-        ok = warp_wait(&info_full[n % kInfos], (n / kInfos) & 1);
+      for (int seg = 0;; ++seg) {
+        ok = warp_wait(&info_full[seg % kInfos], (seg / kInfos) & 1);
         if (!ok) break;
-        const BlockInfo& bi = info[n % kInfos];
-        const int fl = bi.flags;
+        const Segment& sg = info[seg % kInfos];
+        const int fl = sg.flags, nb = sg.nb, head = sg.head, seq = sg.seq, b0 = sg.b0, pos0 = sg.pos0;
         if (fl & kEnd) break;
-        if (fl & kFirst) {
-          ++seg;
-          if (seg > 0) ok = warp_wait(q_empty, (seg - 1) & 1);
-          if (!ok) break;
-          if (!(fl & kPoison)) {
+        if (seg > 0) ok = warp_wait(q_empty, (seg - 1) & 1);
+        if (!ok) break;
+        if (!(fl & kPoison)) {
+          const int row0 = sg.row0, ntok = sg.ntok;
 #pragma unroll 8
-            for (int i = ct; i < 2 * 128 * 16; i += kConv * 32) {
-              const int t = i >> 11, m = (i >> 4) & 127, ch = i & 15;
-              const int mt = m / G, tok = t * tpt + mt;
-              uint4 v = make_uint4(0u, 0u, 0u, 0u);
-              if (mt < tpt && tok < bi.ntok)
-                v = __ldg(reinterpret_cast<const uint4*>(
-                              p.q + (((long long)bi.row0 + tok) * H + bi.head * G + (m - mt * G)) * kHeadDim) + ch);
-              v.x = pack_f16x2(bf16lo(v.x), bf16hi(v.x));
-              v.y = pack_f16x2(bf16lo(v.y), bf16hi(v.y));
-              v.z = pack_f16x2(bf16lo(v.z), bf16hi(v.z));
-              v.w = pack_f16x2(bf16lo(v.w), bf16hi(v.w));
-              *reinterpret_cast<uint4*>(smem + kSmQ + t * kTile + (ch >> 3) * kHalf + m * 128 +
-                                        (((ch & 7) ^ (m & 7)) << 4)) = v;
-            }
+          for (int i = ct; i < 2 * 128 * 16; i += kConv * 32) {
+            const int t = i >> 11, m = (i >> 4) & 127, ch = i & 15;
+            const int mt = m / G, tok = t * tpt + mt;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (mt < tpt && tok < ntok)
+              v = __ldg(reinterpret_cast<const uint4*>(
+                            p.q + (((long long)row0 + tok) * H + head * G + (m - mt * G)) * kHeadDim) + ch);
+            v.x = pack_f16x2(bf16lo(v.x), bf16hi(v.x));
+            v.y = pack_f16x2(bf16lo(v.y), bf16hi(v.y));
+            v.z = pack_f16x2(bf16lo(v.z), bf16hi(v.z));
+            v.w = pack_f16x2(bf16lo(v.w), bf16hi(v.w));
+            *reinterpret_cast<uint4*>(smem + kSmQ + t * kTile + (ch >> 3) * kHalf + m * 128 +
+                                      (((ch & 7) ^ (m & 7)) << 4)) = v;
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(q_full);
         }
-        if constexpr (PTH) {
-          // (the block's K has an e4m3 place, so V of block n - 2 is converted, over K of block
-          // n - 3 that its S has read: the softmax is through with block n - 4's scales)
-          scales_of(bi, fl, n, ct);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sc_full[n % kScales]);
-        }
-        for (int kv = 0; ok && kv < 2; ++kv, ++x) {
-          const int b = x % kBufs, rb = x % kRaws;
-          if (x >= kBufs) ok = warp_wait(&kv_empty[b], ((x / kBufs) - 1) & 1);
-          ok = ok && warp_wait(&raw_full[rb], (x / kRaws) & 1);
-          if (!ok) break;
-          if (!(fl & kNoData)) {
-            // (rows of 128 bytes, 16-byte chunks swizzled by the copy)
-            const uint8_t* raw = smem + C::kSmRaw + rb * kRaw;
-            uint8_t* tile = smem + b * kTile;
-            const int there = min(kBlock, bi.seq - bi.t0);  // behind it: not data, zeros
-            uint32_t odd = 0;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+        for (int i = 0; ok && i < nb; ++i) {
+          const int t0 = (b0 + i) * kBlock;
+          const bool mixed = !(fl & kPoison) && t0 + kBlock - 1 > pos0;
+          for (int kv = 0; ok && kv < 2; ++kv, ++x) {
+            constexpr int kRing = FP8 ? kRaws : 1;
+            const int b = x % kBufs, rb = x % kRing;
+            ok = warp_wait(&raw_full[rb], (x / kRing) & 1);
+            if (!ok) break;
+            if (PTH && kv == 0) {
+              // (the block's K has an e4m3 place, so V of block n - 2 is converted, over K of block
+              // n - 3 that its S has read: the softmax is through with block n - 4's scales)
+              const int n = x >> 1;
+              scales_of(head, !(fl & kPoison) && t0 + ct < seq, n, ct);
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sc_full[n % kScales]);
+            }
+            if (x >= kBufs) ok = warp_wait(&kv_empty[b], ((x / kBufs) - 1) & 1);
+            if (!ok) break;
+            if (!(fl & kPoison)) {
+              // (rows of 128 bytes, 16-byte chunks swizzled by the copy)
+              const uint8_t* raw = smem + C::kSmRaw + rb * kRaw;
+              uint8_t* tile = smem + b * kTile;
+              const int there = min(kBlock, seq - t0);  // behind it: not data, zeros
+              const int range = kv == 1 && mixed ? looks_of(sg, t0) : kBlock;  // rows to look over
+              uint32_t odd = 0;
 #pragma unroll 2
-            for (int i = ct; i < kRaw / 16; i += kConv * 32) {
-              const int row = i >> 3, c = i & 7, ch = 2 * c;  // 16 codes: f16 chunks ch, ch + 1
-              uint4 v = lds128(raw + row * 128 + ((c ^ (row & 7)) << 4));
-              if (row >= there) v = make_uint4(0u, 0u, 0u, 0u);
-              // (a code of NaN: 0x7f without its sign)
-              odd |= ((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u) |
-                     ((v.z & 0x7f7f7f7fu) + 0x01010101u) | ((v.w & 0x7f7f7f7fu) + 0x01010101u);
-              uint8_t* dst = tile + (ch >> 3) * kHalf + row * 128;
-              *reinterpret_cast<uint4*>(dst + (((ch & 7) ^ (row & 7)) << 4)) =
-                  make_uint4(e4m3x2_to_f16x2((uint16_t)v.x), e4m3x2_to_f16x2((uint16_t)(v.x >> 16)),
-                             e4m3x2_to_f16x2((uint16_t)v.y), e4m3x2_to_f16x2((uint16_t)(v.y >> 16)));
-              *reinterpret_cast<uint4*>(dst + ((((ch & 7) + 1) ^ (row & 7)) << 4)) =
-                  make_uint4(e4m3x2_to_f16x2((uint16_t)v.z), e4m3x2_to_f16x2((uint16_t)(v.z >> 16)),
-                             e4m3x2_to_f16x2((uint16_t)v.w), e4m3x2_to_f16x2((uint16_t)(v.w >> 16)));
+              for (int k = ct; k < kRaw / 16; k += kConv * 32) {
+                const int row = k >> 3, c = k & 7, ch = 2 * c;  // 16 codes: f16 chunks ch, ch + 1
+                uint4 v = lds128(raw + row * 128 + ((c ^ (row & 7)) << 4));
+                if (row >= there) v = make_uint4(0u, 0u, 0u, 0u);
+                if (row >= (range & 255))  // (a code of NaN: 0x7f without its sign)
+                  odd |= ((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u) |
+                         ((v.z & 0x7f7f7f7fu) + 0x01010101u) | ((v.w & 0x7f7f7f7fu) + 0x01010101u);
+                uint8_t* dst = tile + (ch >> 3) * kHalf + row * 128;
+                *reinterpret_cast<uint4*>(dst + (((ch & 7) ^ (row & 7)) << 4)) =
+                    make_uint4(e4m3x2_to_f16x2((uint16_t)v.x), e4m3x2_to_f16x2((uint16_t)(v.x >> 16)),
+                               e4m3x2_to_f16x2((uint16_t)v.y), e4m3x2_to_f16x2((uint16_t)(v.y >> 16)));
+                *reinterpret_cast<uint4*>(dst + ((((ch & 7) + 1) ^ (row & 7)) << 4)) =
+                    make_uint4(e4m3x2_to_f16x2((uint16_t)v.z), e4m3x2_to_f16x2((uint16_t)(v.z >> 16)),
+                               e4m3x2_to_f16x2((uint16_t)v.w), e4m3x2_to_f16x2((uint16_t)(v.w >> 16)));
+              }
+              fence_proxy_async_smem();
+              if (kv == 1 && mixed) {
+                // (a word a warp: the place's last readers are behind this block's K)
+                const bool any = __any_sync(0xffffffffu, (odd & 0x80808080u) != 0);
+                if (lane == 0) odd_fp8[4 * (looks % kLooks) + warp - 12] = any;
+              }
+              __syncwarp();
             }
-            fence_proxy_async_smem();
-            if (kv == 1 && (fl & kMixed) && (odd & 0x80808080u))
-              *reinterpret_cast<volatile int*>(&misc[4 + n % kLooks]) = n + 1;
-            __syncwarp();
+            if (lane == 0) {
+              if (kv == 1 && mixed) mbar_arrive(&looked[looks % kLooks]);
+              mbar_arrive(&raw_empty[rb]);
+              mbar_arrive(&kv_full[b]);
+            }
           }
-          if (lane == 0) {
-            mbar_arrive(&raw_empty[rb]);
-            mbar_arrive(&kv_full[b]);
-          }
+          looks += mixed;
         }
         if (!ok) break;
       }
@@ -707,74 +792,89 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
         scale2 *= __ldg(p.k_scale);
         vs = __ldg(p.v_scale);
       }
-      float m_run = -INFINITY, l_run = 0.f;
       constexpr float kHead = FP8 ? kHalfHead : 0.f;
+      // a factor that is not positive: the logits take its sign (or 0)
+      const bool turned = !PTH && !(scale2 > 0.f);
+      const float flip = scale2 < 0.f ? -1.f : scale2 == 0.f ? 0.f : scale2;
+      if (turned) scale2 = scale2 < 0.f ? -scale2 : 1.f;
+      // one bit for each of 32 tokens of which the first c are seen
+      const auto bits = [](int c) { return c >= 32 ? ~0u : c > 0 ? (1u << c) - 1u : 0u; };
       bool ok = true;
-      for (int n = 0;; ++n) {
-        ok = warp_wait(&info_full[n % kInfos], (n / kInfos) & 1);
+      int n = 0, looks = 0;  // blocks, mixed ones
+      for (int seg = 0;; ++seg) {
+        ok = warp_wait(&info_full[seg % kInfos], (seg / kInfos) & 1);
         if (!ok) break;
-        const BlockInfo& bi = info[n % kInfos];
-        const int fl = bi.flags;
+        const Segment& sg = info[seg % kInfos];
+        const int fl = sg.flags, nb = sg.nb, pos0 = sg.pos0, ntok = sg.ntok;
         if (fl & kEnd) break;
-        const int vb = (2 * n + 1) % kBufs;
-        if (fl & kFirst) {
-          m_run = -INFINITY;
-          l_run = 0.f;
-        }
-        const bool there = mtok < tpt && tok < bi.ntok;
-        const bool work = (fl & (t ? kWork1 : kWork0)) != 0;
-        bool masked = (fl & kMixed) != 0;
-        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-        if (masked) {
-          const int seen = there ? bi.pos0 + tok + 1 - bi.t0 : 0;  // tokens of the block that the row sees
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int c = seen - 32 * w;
-            vis[w] = c >= 32 ? ~0u : c > 0 ? (1u << c) - 1u : 0u;
-          }
-          masked = !__all_sync(0xffffffffu, seen >= kBlock || !there);
-        }
-        bool hand = false;
-        float moved = 1.f;  // what the second half scaled the first one's P by
-        const float* ks = nullptr;
-        // (PTH, by half) log2 of the largest v scale; whether the scales lie too far apart for it
-        float near0 = 0.f, near1 = 0.f;
-        bool exact0 = false, exact1 = false;
-        if (PTH) {
-          ok = warp_wait(&sc_full[n % kScales], (n / kScales) & 1);
-          if (!ok) break;
-          ks = reinterpret_cast<const float*>(smem + C::kSmScale) + (n % kScales) * kScaleWords;
-          const float4 r0 = *reinterpret_cast<const float4*>(ks + kSoRange);
-          const float4 r1 = *reinterpret_cast<const float4*>(ks + kSoRange + 4);
-          near0 = fmaxf(r0.x, r0.z);
-          near1 = fmaxf(r1.x, r1.z);
-          exact0 = near0 - fminf(r0.y, r0.w) > kNear;
-          exact1 = near1 - fminf(r1.y, r1.w) > kNear;
-        }
-        ok = warp_wait(&s_full[t], n & 1);
-        if (!ok) break;
-        tc::fence_after();
+        const bool there = mtok < tpt && tok < ntok;
+        const bool on = !(fl & kPoison) && (t == 0 || (fl & kTwo));
+        const int last0 = pos0 + min(tpt, ntok) - 1;
+        float m_run = -INFINITY, l_run = 0.f;
+        int t0 = kBlock * sg.b0;
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          if (work && (half == 0 || (fl & kHalves))) {
-            const uint32_t v0 = half ? vis[2] : vis[0], v1 = half ? vis[3] : vis[1];
-            const float* kh = PTH ? ks + 64 * half : nullptr;
+        for (int i = 0; i < nb; ++i, ++n, t0 += kBlock) {
+          const bool work = on && (t == 1 || i == 0 || last0 >= t0);
+          const bool mixed = !(fl & kPoison) && t0 + kBlock - 1 > pos0;
+          const int seen = mixed ? (there ? pos0 + tok + 1 - t0 : 0) : kBlock;  // of the block's tokens
+          const float* ks = nullptr;
+          // (PTH, by half) log2 of the largest v scale; whether the scales lie too far apart for it
+          float near[2] = {0.f, 0.f};
+          bool exact[2] = {false, false};
+          if (PTH) {
+            ok = warp_wait(&sc_full[n % kScales], (n / kScales) & 1);
+            if (!ok) break;
+            ks = reinterpret_cast<const float*>(smem + C::kSmScale) + (n % kScales) * kScaleWords;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float4 r = *reinterpret_cast<const float4*>(ks + kSoRange + 4 * h);
+              near[h] = fmaxf(r.x, r.z);
+              exact[h] = near[h] - fminf(r.y, r.w) > kNear;
+            }
+          }
+          ok = warp_wait(&s_full[t], n & 1);
+          if (!ok) break;
+          tc::fence_after();
+          if (work) {
+            // Logits that the row does not see become -inf in place, and a factor that is not
+            // positive goes into them, so that what follows is the same code for every block (a
+            // scale per token, which may be anything where the row does not look, is masked there).
+            if (__builtin_expect((mixed && !PTH) || turned, 0)) {
+              const int least = __reduce_min_sync(0xffffffffu, there ? seen : kBlock);
+              const int most = __reduce_max_sync(0xffffffffu, there ? seen : 0);
+#pragma unroll 1
+              for (int c = turned ? 0 : max(0, least) & ~15; c < 128; c += 16) {
+                uint32_t x[16];
+                if (c < most) {
+                  tc::tmem_ld16(sa + c, x);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k)
+                    x[k] = c + k >= seen ? 0xff800000u : turned ? __float_as_uint(__uint_as_float(x[k]) * flip) : x[k];
+                } else {
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) x[k] = 0xff800000u;
+                }
+                tc::tmem_st16(sa + c, x);
+              }
+              tc::tmem_wait_st();
+            }
             uint32_t r[64];
-            tc::tmem_ld64(sa + 64 * half, r);
-            // (with PTH the tokens' factors carry the softmax scale and its sign)
-            const float sg = PTH ? 1.f : scale2;
-            const bool exact = PTH && (half ? exact1 : exact0);
-            const float near = half ? near1 : near0;
-            float mx;
-            if (exact)
-              mx = max64<false, true, PTH, true>(r, -INFINITY, v0, v1, kh, kh + kSoLog);
-            else if (masked)
-              mx = sg >= 0.f ? max64<false, true, PTH>(r, -INFINITY, v0, v1, kh) * sg
-                             : max64<true, true, PTH>(r, -INFINITY, v0, v1, kh) * -sg;
-            else
-              mx = sg >= 0.f ? max64<false, false, PTH>(r, -INFINITY, v0, v1, kh) * sg
-                             : max64<true, false, PTH>(r, -INFINITY, v0, v1, kh) * -sg;
-            mx += exact ? -kHead : near - kHead;
+            const auto largest = [&](int h, float acc) {
+              if constexpr (PTH) {  // (the tokens' factors carry the softmax scale)
+                const float* kh = ks + 64 * h;
+                const uint32_t v0 = bits(seen - 64 * h), v1 = bits(seen - 64 * h - 32);
+                if (exact[h]) return fmaxf(acc, row_max<false, true, PTH, true>(r, -INFINITY, v0, v1, kh, kh + kSoLog));
+                if (mixed) return fmaxf(acc, row_max<false, true, PTH>(r, -INFINITY, v0, v1, kh) + near[h]);
+                return fmaxf(acc, row_max<false, false, PTH>(r, -INFINITY, 0, 0, kh) + near[h]);
+              } else {
+                return row_max<false, false, PTH>(r, acc, 0, 0, ks);
+              }
+            };
+            tc::tmem_ld64(sa, r);
+            float mx = largest(0, -INFINITY);
+            tc::tmem_ld64(sa + 64, r);
+            mx = largest(1, mx);
+            mx = PTH ? mx - kHead : mx * scale2 - kHead;
             const bool move = there && (mx > m_run + kSlack || (m_run == -INFINITY && mx > -INFINITY));
             if (__any_sync(0xffffffffu, move)) {
               float al = 1.f;
@@ -783,138 +883,146 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
                 m_run = mx;
               }
               l_run *= al;
-              if (half) moved = al;
               // (a row without a reference has an all-zero O: nothing to rescale.  P V of
               // the block before is complete: this block's S came behind it)
-              if (!((fl & kFirst) && half == 0) && __any_sync(0xffffffffu, al != 1.f)) {
-                if (half) {
-                  ok = warp_wait(&pv_half[t], n & 1);
-                  if (!ok) break;
-                }
-                tc::fence_after();
+              if (i > 0 && __any_sync(0xffffffffu, al != 1.f)) {
 #pragma unroll 1
                 for (int c = 0; c < 128; c += 16) {
                   uint32_t x[16];
                   tc::tmem_ld16(oa + c, x);
 #pragma unroll
-                  for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * al);
+                  for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * al);
                   tc::tmem_st16(oa + c, x);
                 }
               }
             }
             const float base = m_run == -INFINITY ? 0.f : m_run;
-            const float* vh = PTH ? kh + kSoV : nullptr;
-            // P of the halves side by side, over logits that have been read
-            const uint32_t pa = sa + 32 * half;
-            l_run += masked ? exp64<true, FP8, PTH>(r, pa, scale2, base, v0, v1, kh, vh)
-                            : exp64<false, FP8, PTH>(r, pa, scale2, base, v0, v1, kh, vh);
-            tc::tmem_wait_st();
-            tc::fence_before();
+            bool hand = false;
+            if (__builtin_expect(mixed, 0)) {
+              ok = warp_wait(&looked[looks % kLooks], (looks / kLooks) & 1);
+              if (!ok) break;
+              hand = odd_of(looks);
+            }
+            // P of each half over its own logits, the second first: its logits are at hand, and
+            // the first's are read again (128 at once took a fifth longer with what else lives in
+            // 168 registers)
+            const auto weights = [&](int h) {
+              const float *kh = PTH ? ks + 64 * h : nullptr, *vh = PTH ? kh + kSoV : nullptr;
+              if (PTH && mixed)
+                l_run += row_exp<true, FP8, PTH>(r, sa + 64 * h, scale2, base, bits(seen - 64 * h), bits(seen - 64 * h - 32), kh, vh);
+              else
+                l_run += row_exp<false, FP8, PTH>(r, sa + 64 * h, scale2, base, 0, 0, kh, vh);
+              tc::tmem_wait_st();
+            };
+            const auto announce = [&](int h) {
+              tc::fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&p_full[2 * t + h]);
+            };
+            weights(1);
+            announce(1);
+            tc::tmem_ld64(sa, r);
+            weights(0);
+            if (__builtin_expect(hand, 0)) {
+              pv_by_hand<FP8>(oa, 0, 128, sa, sa + 64, smem + ((2 * n + 1) % kBufs) * kTile,
+                              make_uint4(bits(seen), bits(seen - 32), bits(seen - 64), bits(seen - 96)), 4, 1.f, i == 0);
+              tc::tmem_wait_st();
+            }
+            announce(0);
+          } else {
+            if (mixed) {
+              ok = warp_wait(&looked[looks % kLooks], (looks / kLooks) & 1);
+              if (!ok) break;
+            }
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&p_full[2 * t]);
+              mbar_arrive(&p_full[2 * t + 1]);
+            }
           }
-          if (half == 0 && (fl & kMixed) && !(fl & kNoData)) {
-            ok = FP8 ? warp_wait(&kv_full[vb], ((2 * n + 1) / kBufs) & 1)
-                     : warp_wait(&looked[n % kLooks], (n / kLooks) & 1);
-            if (!ok) break;
-            hand = *reinterpret_cast<volatile int*>(&misc[4 + n % kLooks]) == n + 1;
-          }
-          __syncwarp();
-          if (lane == 0 && !(hand && half)) mbar_arrive(&p_full[2 * t + half]);
-          __syncwarp();
+          looks += mixed;
         }
         if (!ok) break;
-        if (hand) {
-          if (work) {
-            tc::fence_after();
-            pv_by_hand<FP8>(oa, sa, smem + vb * kTile, make_uint4(vis[0], vis[1], vis[2], vis[3]),
-                            fl & kHalves ? 4 : 2, moved, (fl & kFirst) != 0);
-            tc::tmem_wait_st();
-            tc::fence_before();
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[2 * t + 1]);
-        }
-        if (fl & kLast) {
-          ok = warp_wait(&pv_done[t], n & 1);
-          if (!ok) break;
-          tc::fence_after();
-          const int hh = bi.head * G + (m - mtok * G);
-          const float sink = p.sinks && there ? __ldg(p.sinks + hh) : 0.f;
-          const bool none = (fl & kPoison) || (m_run == -INFINITY && l_run == 0.f);
-          const TreeRowEnd e = tree_row_end(none ? -INFINITY : m_run, none ? 0.f : l_run,
-                                            p.sinks != nullptr, sink * kTreeLog2e, vs);
-          const bool have = (t == 0 || (fl & kTwo)) && !(fl & kPoison);
-          const long long r = ((long long)bi.row0 + tok) * H + hh;  // row x head in the batch
-          const int pm = t * tpt * G + m;  // row of the pair
-          const long long pr = (long long)bi.slot * 256 + pm;
-          __syncwarp();
-          if (have) {
+        // ---- the segment's end: O out of tensor memory, to the rows or to a partial
+        ok = warp_wait(&pv_done[t], seg & 1);
+        if (!ok) break;
+        tc::fence_after();
+        const int hh = sg.head * G + (m - mtok * G);
+        const float sink = p.sinks && there ? __ldg(p.sinks + hh) : 0.f;
+        const bool none = (fl & kPoison) || (m_run == -INFINITY && l_run == 0.f);
+        const TreeRowEnd e = tree_row_end(none ? -INFINITY : m_run, none ? 0.f : l_run, p.sinks != nullptr,
+                                          sink * kTreeLog2e, vs);
+        const long long r = ((long long)sg.row0 + tok) * H + hh;  // row x head in the batch
+        const int pm = t * tpt * G + m;                           // row of the pair
+        if (on && (fl & kWhole)) {
+          // A lane holds two columns of a row in every eight; the four lanes of a row trade theirs
+          // for eight columns each, so that a store's lines are eight rows' and not 32.
+          const int rel = there ? tok * H + hh : -1;  // place behind the pair's first row
+          uint16_t* const out = p.out + (long long)sg.row0 * H * kHeadDim + 8 * (lane & 3);
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 16) {
-              uint32_t v[16];
-              tc::tmem_ld16(oa + c, v);
-              if (there && (fl & kWhole)) {
-                uint4* dst = reinterpret_cast<uint4*>(p.out + r * kHeadDim + c);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  uint32_t w[4];
-#pragma unroll
-                  for (int k = 0; k < 4; ++k)
-                    w[k] = none ? 0u
-                                : pack_bf16x2(__uint_as_float(v[8 * i + 2 * k]) * e.f,
-                                              __uint_as_float(v[8 * i + 2 * k + 1]) * e.f);
-                  dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-              } else if (there) {
-                // [4-dim group][row][4 dims]: the warp's rows are contiguous
-                uint4* dst = reinterpret_cast<uint4*>(p.part_o) + ((long long)bi.slot * 32 + c / 4) * 256 + pm;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  dst[256 * i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-              }
+          for (int g = 0; g < 8; ++g) {
+            const int upper = g >> 2, c = 32 * (g & 3);  // rows 16 * upper .. + 15, columns c .. + 31
+            uint32_t v[16];
+            tc::tmem_ld16x256(oa + ((uint32_t)(16 * upper) << 16) + c, v);
+            if (g == 7) {
+              tc::fence_before();
               __syncwarp();
+              if (lane == 0) mbar_arrive(&o_free[t]);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int row = 16 * upper + 8 * k + (lane >> 2);
+              const float f = __shfl_sync(0xffffffffu, none ? 0.f : e.f, row);
+              const int at = __shfl_sync(0xffffffffu, rel, row);
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[i] = f == 0.f ? 0u : pack_bf16x2(__uint_as_float(v[4 * i + 2 * k]) * f, __uint_as_float(v[4 * i + 2 * k + 1]) * f);
+              quad_transpose(w, lane);
+              if (at >= 0) *reinterpret_cast<uint4*>(out + (long long)at * kHeadDim + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        } else {
+          if (on) {
+            // [4-dim group][row][4 dims]: the warp's rows are contiguous
+            uint4* dst = reinterpret_cast<uint4*>(p.part_o) + (long long)sg.slot * 32 * 256 + pm;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 64) {
+              uint32_t v[64];
+              tc::tmem_ld64(oa + c, v);
+              if (there) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                  dst[256 * (c / 4 + k)] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+              }
             }
           } else if (there) {  // a poisoned request's rows
             uint4* dst = reinterpret_cast<uint4*>(p.out + r * kHeadDim);
-            for (int i = 0; i < kHeadDim / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+            for (int k = 0; k < kHeadDim / 8; ++k) dst[k] = make_uint4(0u, 0u, 0u, 0u);
           }
           tc::fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&o_free[t]);
-          if (there) {
-            if (fl & (kWhole | kPoison)) p.lse[r] = none ? (p.sinks ? sink : -INFINITY) : e.lse;
-            else p.part_ml[pr] = make_float2(m_run, l_run);
-          }
-          if (t == 0 && m == 0) {
-            if (!(fl & kWhole)) p.part_bad[bi.slot] = fl & kPoison ? 1 : 0;
-            if (bi.bad) atomicOr(p.status, bi.bad);
-          }
+        }
+        if (there) {
+          if (fl & (kWhole | kPoison)) p.lse[r] = none ? (p.sinks ? sink : -INFINITY) : e.lse;
+          else p.part_ml[(long long)sg.slot * 256 + pm] = make_float2(m_run, l_run);
+        }
+        if (t == 0 && m == 0) {
+          if (!(fl & kWhole)) p.part_bad[sg.slot] = fl & kPoison ? 1 : 0;
+          if (sg.bad) atomicOr(p.status, sg.bad);
         }
       }
       if (!ok) misc[0] = 1;
     };
-    if constexpr (FP8) {
-      // (a warpgroup's warps give and take registers together)
-      if (warp < 4) {
-        regs_fewer<kRegsFew>();
-        if (warp == 0) copies();
-        else if (warp == 1) products();
-      } else if (warp >= 12) {
-        regs_fewer<kRegsFew>();
-        convert();
-      } else {
-        regs_more<kRegsMore>();
-        softmax();
-      }
-    } else if (warp == 0) {
-      copies();
-    } else if (warp == 1) {
-      products();
-    } else if (warp == 2) {
-      if (PTH) scales();
-    } else if (warp == 3) {
-      look();
-    } else {
+    if (warp == 0) copies();
+    else if (warp < 3) products(warp - 1);
+    else if (warp == 3) {
+      if (!FP8) PTH ? scales() : look();
+    } else if (warp < 12) {
       softmax();
+    } else {
+      convert();
     }
   }
   tc::fence_before();

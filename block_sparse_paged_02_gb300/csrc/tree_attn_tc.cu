@@ -702,13 +702,13 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
             const float near = half ? near1 : near0;
             float mx;
             if (exact)
-              mx = max64<false, true, PTH, true>(r, -INFINITY, v0, v1, kh, kh + kSoLog);
+              mx = row_max<false, true, PTH, true>(r, -INFINITY, v0, v1, kh, kh + kSoLog);
             else if (masked)
-              mx = sg >= 0.f ? max64<false, true, PTH>(r, -INFINITY, v0, v1, kh) * sg
-                             : max64<true, true, PTH>(r, -INFINITY, v0, v1, kh) * -sg;
+              mx = sg >= 0.f ? row_max<false, true, PTH>(r, -INFINITY, v0, v1, kh) * sg
+                             : row_max<true, true, PTH>(r, -INFINITY, v0, v1, kh) * -sg;
             else
-              mx = sg >= 0.f ? max64<false, false, PTH>(r, -INFINITY, v0, v1, kh) * sg
-                             : max64<true, false, PTH>(r, -INFINITY, v0, v1, kh) * -sg;
+              mx = sg >= 0.f ? row_max<false, false, PTH>(r, -INFINITY, v0, v1, kh) * sg
+                             : row_max<true, false, PTH>(r, -INFINITY, v0, v1, kh) * -sg;
             mx += exact ? -kHead : near - kHead;
             const bool move = mx > m_run + kSlack || (m_run == -INFINITY && mx > -INFINITY);
             if (__any_sync(0xffffffffu, move)) {
@@ -738,8 +738,8 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
             const float* vh = PTH ? kh + kSoV : nullptr;
             // P of the halves side by side, over logits that have been read
             const uint32_t pa = tmem + lanes + col_s(t) + (kAhead ? 64 * (n & 1) : 0) + 32 * half;
-            l_run += masked ? exp64<true, FP8, PTH>(r, pa, scale2, base, v0, v1, kh, vh)
-                            : exp64<false, FP8, PTH>(r, pa, scale2, base, v0, v1, kh, vh);
+            l_run += masked ? row_exp<true, FP8, PTH>(r, pa, scale2, base, v0, v1, kh, vh)
+                            : row_exp<false, FP8, PTH>(r, pa, scale2, base, v0, v1, kh, vh);
             tc::tmem_wait_st();
             tc::fence_before();
           } else if (kAhead && half && lane == 0) {
@@ -760,7 +760,8 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
           if (work) {
             // (P V of the blocks before is complete: this block's S waited for it)
             tc::fence_after();
-            pv_by_hand<FP8>(oa, tmem + lanes + col_s(t) + (kAhead ? 64 * (n & 1) : 0),
+            pv_by_hand<FP8>(oa, 0, 128, tmem + lanes + col_s(t) + (kAhead ? 64 * (n & 1) : 0),
+                            tmem + lanes + col_s(t) + (kAhead ? 64 * (n & 1) : 0) + 32,
                             smem + kSmKv + vb * kTile, make_uint4(vis[0], vis[1], vis[2], vis[3]),
                             fl & kHalves ? 4 : 2, moved, (fl & kFirst) != 0);
             tc::tmem_wait_st();
