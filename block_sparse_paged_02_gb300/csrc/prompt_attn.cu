@@ -126,17 +126,20 @@ __device__ __forceinline__ PromptReq prompt_request(const msa_batch& b, int q) {
   return r;
 }
 
-// The pairs of one KV head of a request: `wide` rows each
+// The pairs of one KV head of a request: `wide` rows each.  `whole`: the list counts pairs
 struct Pairs {
   int tiles, wide, qlen, ctx;
+  bool whole;
   // tokens before pair i (all of them for i = tiles)
   __device__ __forceinline__ long long before(int i) const {
+    if (whole) return i;
     const long long n = (long long)i * (kPairCost + ctx) + (long long)wide * i * (i + 1) / 2;
     return i < tiles ? n : n - ((long long)tiles * wide - qlen);
   }
   __device__ __forceinline__ int seen(int i) const { return ctx + min((i + 1) * wide, qlen); }
   // the pair that holds token u of the list
   __device__ __forceinline__ int at(long long u) const {
+    if (whole) return (int)u;
     const float a = 0.5f * (float)wide, b = (float)(kPairCost + ctx) + a, f = (float)u;
     int i = (int)(2.f * f / (b + sqrtf(b * b + 4.f * a * f)));
     i = max(0, min(i, tiles - 1));
@@ -145,8 +148,8 @@ struct Pairs {
     return i;
   }
 };
-__device__ __forceinline__ Pairs pairs_of(const PromptReq& r, int wide) {
-  return {(int)(((long long)r.qlen + wide - 1) / wide), wide, r.qlen, r.ctx};
+__device__ __forceinline__ Pairs pairs_of(const PromptReq& r, int wide, bool whole) {
+  return {(int)(((unsigned)r.qlen + wide - 1) / wide), wide, r.qlen, r.ctx, whole};
 }
 
 // The CTA's slice [begin, end) of the list; every thread takes part; s_ll: 40
@@ -173,7 +176,7 @@ __device__ __forceinline__ PromptSlice prompt_slice(const PromptLaunch& p, int w
       const PromptReq r = prompt_request(p.batch, q);
       ok &= r.qlen >= 0 && (q > 0 || r.q0 == 0) && (q < R - 1 || r.q0 + r.qlen == p.batch.num_rows);
       if (ok && r.qlen > 0) {
-        const Pairs a = pairs_of(r, wide);
+        const Pairs a = pairs_of(r, wide, p.whole);
         c = a.before(a.tiles) * p.num_kv_heads;
       }
     }
@@ -192,8 +195,11 @@ __device__ __forceinline__ PromptSlice prompt_slice(const PromptLaunch& p, int w
     for (int w = 0; w < NT / 32; ++w) s.total += s_ll[w];
     if (q0 + NT < R) __syncthreads();
   }
-  s.ctas = (int)max(1ll, min((long long)gridDim.x, s.total / kMinSlice));
-  if ((int)blockIdx.x < s.ctas) {
+  s.ctas = (int)max(1ll, min((long long)gridDim.x, p.whole ? s.total : s.total / kMinSlice));
+  if (p.whole && (int)blockIdx.x < s.total) {  // (the grid holds every pair)
+    s.begin = blockIdx.x;
+    s.end = s.begin + 1;
+  } else if (!p.whole && (int)blockIdx.x < s.ctas) {
     s.begin = s.total * blockIdx.x / s.ctas;
     s.end = s.total * (blockIdx.x + 1) / s.ctas;
   }
@@ -261,35 +267,32 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
   const int H = p.num_heads, Hk = p.num_kv_heads, G = H / Hk;
   const int tpt = 128 / G;  // tokens per tile
 
-  if (tid == 0) {
-    misc[0] = 0;
-    for (int s = 0; s < kBufs; ++s) {
-      mbar_init(&kv_full[s], FP8 ? kConv : 1);
-      mbar_init(&kv_empty[s], 2);  // the issuers
-    }
-    for (int s = 0; s < kRaws; ++s) {
-      mbar_init(&raw_full[s], 1);
-      mbar_init(&raw_empty[s], kConv);
-    }
-    for (int s = 0; s < kScales; ++s) mbar_init(&sc_full[s], FP8 ? kConv : 1);
-    mbar_init(q_full, FP8 ? kConv : 1);
-    mbar_init(q_empty, 2);
-    for (int i = 0; i < kInfos; ++i) mbar_init(&info_full[i], 1);
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[2 * t], 4);
-      mbar_init(&p_full[2 * t + 1], 4);
-      mbar_init(&pv_done[t], 1);
-      mbar_init(&o_free[t], 4);
-      mbar_init(&drained[t], 1);
-      mbar_init(&turn[t], 1);
-    }
-    mbar_init(fill, 1);
-    for (int i = 0; i < kLooks; ++i) {
-      mbar_init(&to_look[i], 1);
-      mbar_init(&looked[i], FP8 ? kConv : 1);
-    }
-    fence_barrier_init();
+  // (a barrier a thread)
+  const auto barriers = [&](uint64_t* first, int n, int count) {
+    if (warp == 3 && lane < n) mbar_init(first + lane, count);
+  };
+  if (tid == 0) misc[0] = 0;
+  barriers(kv_full, kBufs, FP8 ? kConv : 1);
+  barriers(kv_empty, kBufs, 2);  // the issuers
+  barriers(raw_full, kRaws, 1);
+  barriers(raw_empty, kRaws, kConv);
+  barriers(q_full, 1, FP8 ? kConv : 1);
+  barriers(q_empty, 1, 2);
+  barriers(info_full, kInfos, 1);
+  barriers(sc_full, kScales, FP8 ? kConv : 1);
+  barriers(s_full, 2, 1);
+  barriers(p_full, 4, 4);
+  barriers(pv_done, 2, 1);
+  barriers(o_free, 2, 4);
+  barriers(drained, 2, 1);
+  barriers(fill, 1, 1);
+  barriers(to_look, kLooks, 1);
+  barriers(looked, kLooks, FP8 ? kConv : 1);
+  barriers(turn, 2, 1);
+  if (warp == 3) fence_barrier_init();
+  if (tid < 3 && !(FP8 && tid == 0)) {
+    const CUtensorMap* maps[3] = {&qmap, &kmap, &vmap};
+    asm volatile("prefetch.tensormap [%0];" ::"l"(maps[tid]) : "memory");
   }
   if (warp == 1) tc::tmem_alloc(tmem_slot, kTmemCols);
   const PromptSlice sl = prompt_slice<kThreads>(p, 2 * tpt, reinterpret_cast<long long*>(smem));
@@ -420,7 +423,7 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
       uint32_t bad = 0;
       const auto request = [&]() {  // request q: lengths, every page looked at
         rq = prompt_request(p.batch, q);
-        pr = pairs_of(rq, 2 * tpt);
+        pr = pairs_of(rq, 2 * tpt, p.whole);
         table = p.batch.block_table + (long long)q * p.batch.bt_stride;
         bad = rq.bad;
         bool odd = false;
@@ -434,7 +437,7 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
       };
       request();
       const long long one = pr.before(pr.tiles);  // of a KV head
-      sg.head = (int)((sl.begin - sl.pre) / one);
+      sg.head = Hk == 1 ? 0 : p.whole ? (int)(sl.begin - sl.pre) / pr.tiles : (int)((sl.begin - sl.pre) / one);
       long long start = sl.pre + sg.head * one;
       tile = pr.at(sl.begin - start);
       start += pr.before(tile);
@@ -442,11 +445,11 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
         const int seen = pr.seen(tile), nv = (seen + kBlock - 1) / kBlock;
         // blocks of the pair in the slice: block b is the CTA's whose slice holds
         // token kPairCost + 128 b of the pair
-        const long long first = start + kPairCost, stop = first + seen;
+        const long long first = start + kPairCost, stop = p.whole ? start + 1 : first + seen;
         const auto block_at = [&](long long u) {
           return u <= first ? 0 : (int)min((long long)nv, (u - first + kBlock - 1) / kBlock);
         };
-        sg.b0 = block_at(sl.begin);
+        sg.b0 = p.whole ? 0 : block_at(sl.begin);
         sg.nb = (stop <= sl.end ? nv : block_at(sl.end)) - sg.b0;
         if (sg.nb > 0) {
           const int j0 = tile * 2 * tpt;
@@ -960,11 +963,11 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
           const int rel = there ? tok * H + hh : -1;  // place behind the pair's first row
           uint16_t* const out = p.out + (long long)sg.row0 * H * kHeadDim + 8 * (lane & 3);
 #pragma unroll 1
-          for (int g = 0; g < 8; ++g) {
-            const int upper = g >> 2, c = 32 * (g & 3);  // rows 16 * upper .. + 15, columns c .. + 31
-            uint32_t v[16];
+          for (int g = 0; g < 4; ++g) {
+            const int upper = g >> 1, c = 64 * (g & 1);  // rows 16 * upper .. + 15, columns c .. + 63
+            uint32_t v[32];
             tc::tmem_ld16x256(oa + ((uint32_t)(16 * upper) << 16) + c, v);
-            if (g == 7) {
+            if (g == 3) {
               tc::fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(&o_free[t]);
@@ -974,12 +977,18 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
               const int row = 16 * upper + 8 * k + (lane >> 2);
               const float f = __shfl_sync(0xffffffffu, none ? 0.f : e.f, row);
               const int at = __shfl_sync(0xffffffffu, rel, row);
-              uint32_t w[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                w[i] = f == 0.f ? 0u : pack_bf16x2(__uint_as_float(v[4 * i + 2 * k]) * f, __uint_as_float(v[4 * i + 2 * k + 1]) * f);
-              quad_transpose(w, lane);
-              if (at >= 0) *reinterpret_cast<uint4*>(out + (long long)at * kHeadDim + c) = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int x = 0; x < 2; ++x) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int y = 16 * x + 4 * i + 2 * k;
+                  w[i] = f == 0.f ? 0u : pack_bf16x2(__uint_as_float(v[y]) * f, __uint_as_float(v[y + 1]) * f);
+                }
+                quad_transpose(w, lane);
+                if (at >= 0)
+                  *reinterpret_cast<uint4*>(out + (long long)at * kHeadDim + c + 32 * x) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
             }
           }
         } else {
@@ -1194,7 +1203,7 @@ cudaError_t launch(const PromptLaunch& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   kern<<<grid, C::kThreads, C::kBytes, stream>>>(p, qmap, kmap, vmap);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.whole) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(3 * grid);
   cfg.blockDim = dim3(kJoinThreads);
@@ -1209,7 +1218,15 @@ cudaError_t launch(const PromptLaunch& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_prompt_attn(const PromptLaunch& p, cudaStream_t stream) {
+// Short prompts, of few pairs and blocks: a pair to a CTA, with nothing to join behind.
+// TODO figures
+constexpr int kWholeBlocks = 16;
+
+cudaError_t launch_prompt_attn(const PromptLaunch& given, cudaStream_t stream) {
+  PromptLaunch p = given;
+  const int wide = 2 * (128 / (p.num_heads / p.num_kv_heads));
+  const long long pairs = ((long long)p.batch.num_rows / wide + min(p.batch.num_rows, p.batch.num_reqs)) * p.num_kv_heads;
+  p.whole = pairs <= device_sm_count() && p.batch.bt_stride <= kWholeBlocks;
   const bool pth = p.scale_mode == MSA_SCALE_PER_TOKEN_HEAD;
   if (p.kv_fp8) return pth ? launch<true, true>(p, stream) : launch<true, false>(p, stream);
   return pth ? launch<false, true>(p, stream) : launch<false, false>(p, stream);

@@ -34,6 +34,7 @@ struct PromptLaunch {
   uint16_t* out;
   float* lse;
   uint32_t* status;
+  bool whole;          // a pair to a CTA, none split
   PromptSplit* split;  // [grid]
   int32_t* part_bad;   // [2 * grid]
   float2* part_ml;     // [2 * grid, 256]
