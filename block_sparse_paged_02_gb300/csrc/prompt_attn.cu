@@ -67,9 +67,9 @@ struct PaCfg {
   static constexpr int kSmScale = kSmRaw + kRaws * kRaw;
   static constexpr int kSmInfo = kSmScale + (PTH ? kScales * kScaleWords * 4 : 0);
   static constexpr int kSmBars = kSmInfo + kInfos * (int)sizeof(Segment);
-  // kv full / empty, raw full / empty, q full / empty, infos, scales; per tile s_full,
+  // kv full / empty, raw full / empty, q full / empty / raw, infos, scales; per tile s_full,
   // p_full of two halves, pv_done, o_free, drained, turn; fill; to look over, looked
-  static constexpr int kNumBars = 2 * kBufs + 2 * kRaws + 2 + kInfos + kScales + 12 + 1 + 2 * kLooks + 2;
+  static constexpr int kNumBars = 2 * kBufs + 2 * kRaws + 3 + kInfos + kScales + 12 + 1 + 2 * kLooks + 2;
   static constexpr int kSmMisc = kSmBars + kNumBars * 8;
   static constexpr int kBytes = kSmMisc + 192;
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -245,7 +245,8 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
   uint64_t* raw_empty = raw_full + kRaws;
   uint64_t* q_full = raw_empty + kRaws;
   uint64_t* q_empty = q_full + 1;
-  uint64_t* info_full = q_empty + 1;
+  uint64_t* q_raw = q_empty + 1;         // (e4m3) Q in bf16
+  uint64_t* info_full = q_raw + 1;
   uint64_t* sc_full = info_full + kInfos;
   uint64_t* s_full = sc_full + kScales;  // [tile]
   uint64_t* p_full = s_full + 2;         // [tile][half]
@@ -278,6 +279,7 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
   barriers(raw_empty, kRaws, kConv);
   barriers(q_full, 1, FP8 ? kConv : 1);
   barriers(q_empty, 1, 2);
+  barriers(q_raw, 1, 1);
   barriers(info_full, kInfos, 1);
   barriers(sc_full, kScales, FP8 ? kConv : 1);
   barriers(s_full, 2, 1);
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
   barriers(looked, kLooks, FP8 ? kConv : 1);
   barriers(turn, 2, 1);
   if (warp == 3) fence_barrier_init();
-  if (tid < 3 && !(FP8 && tid == 0)) {
+  if (tid < 3) {
     const CUtensorMap* maps[3] = {&qmap, &kmap, &vmap};
     asm volatile("prefetch.tensormap [%0];" ::"l"(maps[tid]) : "memory");
   }
@@ -321,14 +323,6 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
       PromptSplit rec;
       rec.nrows = 0;
       const uint32_t qbytes = 2u * 64u * (uint32_t)(G * tpt);  // of one box of Q
-      auto acquire = [&]() -> int {
-        constexpr int ring = FP8 ? kRaws : kBufs;
-        uint64_t* freed = FP8 ? raw_empty : kv_empty;
-        const int b = x % ring;
-        if (x >= ring) ok = ok && warp_wait(&freed[b], ((x / ring) - 1) & 1);
-        ++x;
-        return b;
-      };
       Segment sg;
       auto announce = [&]() {
         if (lane == 0) {
@@ -339,81 +333,79 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
       };
       // A block's K and V (without data, pg < 0, they still take their places, so that no
       // segment is announced far ahead of the other roles)
-      auto push = [&](int pg, int t0, bool mixed) {
-        const CUtensorMap* maps[2] = {&kmap, &vmap};
-        if (lane == 0) pages[n % kPages] = pg;
-        ++n;
+      auto push = [&](int kv, int pg, int t0, bool mixed) {
+        const CUtensorMap* map = kv ? &vmap : &kmap;
+        constexpr int ring = FP8 ? kRaws : kBufs;
+        if (kv == 0 && lane == 0) pages[n % kPages] = pg;
+        n += kv;
+        const int b = x % ring;
+        if (x >= ring) ok = warp_wait(&(FP8 ? raw_empty : kv_empty)[b], ((x / ring) - 1) & 1);
+        if (!ok) return;
+        ++x;
         if constexpr (FP8) {
-          for (int kv = 0; kv < 2; ++kv) {
-            const int rb = acquire();
-            if (!ok) return;
-            if (lane == 0) {
-              if (pg < 0) {
-                mbar_arrive(&raw_full[rb]);
-              } else {
-                mbar_arrive_expect_tx(&raw_full[rb], kRaw);
-                tma_load_2d(smem + C::kSmRaw + rb * kRaw, maps[kv], sg.head * kHeadDim, pg * kBlock, &raw_full[rb]);
-              }
+          if (lane == 0) {
+            if (pg < 0) {
+              mbar_arrive(&raw_full[b]);
+            } else {
+              mbar_arrive_expect_tx(&raw_full[b], kRaw);
+              tma_load_2d(smem + C::kSmRaw + b * kRaw, map, sg.head * kHeadDim, pg * kBlock, &raw_full[b]);
             }
           }
           return;
         }
         const int there = min(kBlock, sg.seq - t0);
-        for (int kv = 0; kv < 2; ++kv) {
-          const int b = acquire();
+        uint8_t* dst = smem + b * kTile;
+        // V behind the request's end is not data: zeroed in the step of 16 tokens that a
+        // product still reads
+        const bool part = kv == 1 && pg >= 0 && (there & 15) && there < kBlock;
+        uint64_t* land = part ? fill : &kv_full[b];
+        if (lane == 0) {
+          if (pg < 0) {
+            mbar_arrive(land);
+          } else {
+            mbar_arrive_expect_tx(land, kTile);
+            for (int h = 0; h < 2; ++h)
+              tma_load_2d(dst + h * kHalf, map, sg.head * kHeadDim + 64 * h, pg * kBlock, land);
+          }
+        }
+        if (part) {
+          ok = warp_wait(fill, fills & 1);
+          ++fills;
           if (!ok) return;
-          uint8_t* dst = smem + b * kTile;
-          // V behind the request's end is not data: zeroed in the step of 16 tokens that a
-          // product still reads
-          const bool part = kv == 1 && pg >= 0 && (there & 15) && there < kBlock;
-          uint64_t* land = part ? fill : &kv_full[b];
+          uint4* v4 = reinterpret_cast<uint4*>(dst);
+          for (int k = there * 8 + lane; k < ((there + 15) & ~15) * 8; k += 32)
+            v4[k] = v4[kHalf / 16 + k] = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&kv_full[b]);
+        }
+        // (asked for when the place's earlier uses are over, so that the wait for this one
+        // cannot take one of them for it)
+        if (!PTH && kv == 1 && mixed) {
           if (lane == 0) {
-            if (pg < 0) {
-              mbar_arrive(land);
-            } else {
-              mbar_arrive_expect_tx(land, kTile);
-              for (int h = 0; h < 2; ++h)
-                tma_load_2d(dst + h * kHalf, maps[kv], sg.head * kHeadDim + 64 * h, pg * kBlock, land);
-            }
+            look_at[looks % kLooks] = n - 1;
+            look_from[looks % kLooks] = looks_of(sg, t0);
+            mbar_arrive(&to_look[looks % kLooks]);
           }
-          if (part) {
-            ok = warp_wait(fill, fills & 1);
-            ++fills;
-            if (!ok) return;
-            uint4* v4 = reinterpret_cast<uint4*>(dst);
-            for (int k = there * 8 + lane; k < ((there + 15) & ~15) * 8; k += 32)
-              v4[k] = v4[kHalf / 16 + k] = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&kv_full[b]);
-          }
-          // (asked for when the place's earlier uses are over, so that the wait for this one
-          // cannot take one of them for it)
-          if (!PTH && kv == 1 && mixed) {
-            if (lane == 0) {
-              look_at[looks % kLooks] = n - 1;
-              look_from[looks % kLooks] = looks_of(sg, t0);
-              mbar_arrive(&to_look[looks % kLooks]);
-            }
-            ++looks;
-          }
+          ++looks;
         }
       };
       // The next segment's Q, once the products have read the last one's (e4m3: the converting
-      // warps bring the queries)
+      // warps turn it into f16 in its place)
       const auto queries = [&]() {
-        if (FP8 || !ok) return;
+        uint64_t* land = FP8 ? q_raw : q_full;
+        if (!ok) return;
         if (n_seg > 1) ok = warp_wait(q_empty, (n_seg - 2) & 1);
         if (!ok || lane != 0) return;
         if (sg.flags & kPoison) {
-          mbar_arrive(q_full);
+          mbar_arrive(land);
           return;
         }
         const int tiles = sg.flags & kTwo ? 2 : 1;
-        mbar_arrive_expect_tx(q_full, 2u * tiles * qbytes);
+        mbar_arrive_expect_tx(land, 2u * tiles * qbytes);
         for (int t = 0; t < tiles; ++t)
           for (int h = 0; h < 2; ++h)
-            tma_load_3d(smem + kSmQ + t * kTile + h * kHalf, &qmap, 64 * h, sg.head * G, sg.row0 + t * tpt, q_full);
+            tma_load_3d(smem + kSmQ + t * kTile + h * kHalf, &qmap, 64 * h, sg.head * G, sg.row0 + t * tpt, land);
       };
       int q = sl.q, tile = 0;
       PromptReq rq;
@@ -471,14 +463,16 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
           }
           if (bad) sg.nb = 1;
           announce();
-          // (its first K and V before its Q, whose place is free later than theirs)
+          // (its first K before its Q, whose place is free later)
           int page = sg.b0 == 0 ? page0 : 0;
           for (int i = 0; ok && i < sg.nb; ++i) {
             if ((i & 31) == 0 && sg.b0 + i > 0)
               page = !bad && i + lane < sg.nb ? __ldg(table + sg.b0 + i + lane) : 0;
             const int t0 = kBlock * (sg.b0 + i);
-            push(bad ? -1 : __shfl_sync(0xffffffffu, page, i & 31), t0, !bad && t0 + kBlock - 1 > sg.pos0);
+            const int pg = bad ? -1 : __shfl_sync(0xffffffffu, page, i & 31);
+            push(0, pg, t0, false);
             if (i == 0) queries();
+            if (ok) push(1, pg, t0, !bad && t0 + kBlock - 1 > sg.pos0);
           }
         }
         start = stop;
@@ -508,7 +502,7 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
         const int ring = FP8 ? kRaws : kBufs;
         uint64_t* bars = FP8 ? raw_full : kv_full;
         for (int i = max(0, x - ring); i < x; ++i) mbar_wait(&bars[i % ring], (i / ring) & 1);
-        if (!FP8 && n_seg > 0) mbar_wait(q_full, (n_seg - 1) & 1);
+        if (n_seg > 0) mbar_wait(FP8 ? q_raw : q_full, (n_seg - 1) & 1);
       }
       if (lane == 0) p.split[blockIdx.x] = rec;
     };
@@ -699,24 +693,19 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
         const Segment& sg = info[seg % kInfos];
         const int fl = sg.flags, nb = sg.nb, head = sg.head, seq = sg.seq, b0 = sg.b0, pos0 = sg.pos0;
         if (fl & kEnd) break;
-        if (seg > 0) ok = warp_wait(q_empty, (seg - 1) & 1);
+        ok = warp_wait(q_raw, seg & 1);
         if (!ok) break;
         if (!(fl & kPoison)) {
-          const int row0 = sg.row0, ntok = sg.ntok;
+          // (in place, whatever lies in rows without a query)
+          uint4* at = reinterpret_cast<uint4*>(smem + kSmQ) + ct;
 #pragma unroll 8
-          for (int i = ct; i < 2 * 128 * 16; i += kConv * 32) {
-            const int t = i >> 11, m = (i >> 4) & 127, ch = i & 15;
-            const int mt = m / G, tok = t * tpt + mt;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (mt < tpt && tok < ntok)
-              v = __ldg(reinterpret_cast<const uint4*>(
-                            p.q + (((long long)row0 + tok) * H + head * G + (m - mt * G)) * kHeadDim) + ch);
+          for (int i = 0; i < (fl & kTwo ? 2 : 1) * kTile / 16; i += kConv * 32) {
+            uint4 v = at[i];
             v.x = pack_f16x2(bf16lo(v.x), bf16hi(v.x));
             v.y = pack_f16x2(bf16lo(v.y), bf16hi(v.y));
             v.z = pack_f16x2(bf16lo(v.z), bf16hi(v.z));
             v.w = pack_f16x2(bf16lo(v.w), bf16hi(v.w));
-            *reinterpret_cast<uint4*>(smem + kSmQ + t * kTile + (ch >> 3) * kHalf + m * 128 +
-                                      (((ch & 7) ^ (m & 7)) << 4)) = v;
+            at[i] = v;
           }
         }
         fence_proxy_async_smem();
@@ -741,25 +730,31 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
             if (x >= kBufs) ok = warp_wait(&kv_empty[b], ((x / kBufs) - 1) & 1);
             if (!ok) break;
             if (!(fl & kPoison)) {
-              // (rows of 128 bytes, 16-byte chunks swizzled by the copy)
-              const uint8_t* raw = smem + C::kSmRaw + rb * kRaw;
-              uint8_t* tile = smem + b * kTile;
-              const int there = min(kBlock, seq - t0);  // behind it: not data, zeros
-              const int range = kv == 1 && mixed ? looks_of(sg, t0) : kBlock;  // rows to look over
+              // Rows of 128 bytes, 16-byte chunks swizzled by the copy; a thread takes chunk ct % 8 of
+              // every 16th row, which becomes two chunks of a half tile's row
+              const int row0 = ct >> 3, c = ct & 7, sw = row0 & 7;
+              const uint8_t* from = smem + C::kSmRaw + rb * kRaw + row0 * 128 + ((c ^ sw) << 4);
+              uint8_t* to = smem + b * kTile + (c >> 2) * kHalf + row0 * 128;
+              const int even = (((2 * c) & 7) ^ sw) << 4, odd_at = (((2 * c + 1) & 7) ^ sw) << 4;
+              const int there = seq - t0;  // behind it: not data, zeros
+              // rows to look over
+              const int first = kv == 1 && mixed ? looks_of(sg, t0) & 255 : kBlock;
+              const bool edge = there < kBlock || first < kBlock;
               uint32_t odd = 0;
-#pragma unroll 2
-              for (int k = ct; k < kRaw / 16; k += kConv * 32) {
-                const int row = k >> 3, c = k & 7, ch = 2 * c;  // 16 codes: f16 chunks ch, ch + 1
-                uint4 v = lds128(raw + row * 128 + ((c ^ (row & 7)) << 4));
-                if (row >= there) v = make_uint4(0u, 0u, 0u, 0u);
-                if (row >= (range & 255))  // (a code of NaN: 0x7f without its sign)
-                  odd |= ((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u) |
-                         ((v.z & 0x7f7f7f7fu) + 0x01010101u) | ((v.w & 0x7f7f7f7fu) + 0x01010101u);
-                uint8_t* dst = tile + (ch >> 3) * kHalf + row * 128;
-                *reinterpret_cast<uint4*>(dst + (((ch & 7) ^ (row & 7)) << 4)) =
+#pragma unroll 4
+              for (int k = 0; k < 8; ++k) {
+                uint4 v = lds128(from + 2048 * k);
+                if (edge) {
+                  const int row = row0 + 16 * k;
+                  if (row >= there) v = make_uint4(0u, 0u, 0u, 0u);
+                  if (row >= first)  // (a code of NaN: 0x7f without its sign)
+                    odd |= ((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u) |
+                           ((v.z & 0x7f7f7f7fu) + 0x01010101u) | ((v.w & 0x7f7f7f7fu) + 0x01010101u);
+                }
+                *reinterpret_cast<uint4*>(to + even + 2048 * k) =
                     make_uint4(e4m3x2_to_f16x2((uint16_t)v.x), e4m3x2_to_f16x2((uint16_t)(v.x >> 16)),
                                e4m3x2_to_f16x2((uint16_t)v.y), e4m3x2_to_f16x2((uint16_t)(v.y >> 16)));
-                *reinterpret_cast<uint4*>(dst + ((((ch & 7) + 1) ^ (row & 7)) << 4)) =
+                *reinterpret_cast<uint4*>(to + odd_at + 2048 * k) =
                     make_uint4(e4m3x2_to_f16x2((uint16_t)v.z), e4m3x2_to_f16x2((uint16_t)(v.z >> 16)),
                                e4m3x2_to_f16x2((uint16_t)v.w), e4m3x2_to_f16x2((uint16_t)(v.w >> 16)));
               }
@@ -1187,15 +1182,14 @@ cudaError_t launch(const PromptLaunch& p, cudaStream_t stream) {
   using C = PaCfg<FP8, PTH>;
   const int G = p.num_heads / p.num_kv_heads, tpt = 128 / G;
   CUtensorMap qmap, kmap, vmap;
-  memset(&qmap, 0, sizeof(qmap));
   const long long toks = max(1ll, (long long)p.batch.num_pages) * kBlock;
   const long long inner = (long long)p.num_kv_heads * kHeadDim;
   const auto type = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int size = FP8 ? 1 : 2, box = 128 / size;  // 128 bytes
   if (!encode_map_2d(&kmap, type, p.k, inner, toks, inner * size, box, kBlock) ||
       !encode_map_2d(&vmap, type, p.v, inner, toks, inner * size, box, kBlock) ||
-      (!FP8 && !encode_map_3d(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.q, kHeadDim, p.num_heads,
-                              p.batch.num_rows, kHeadDim * 2, (long long)p.num_heads * kHeadDim * 2, 64, G, tpt)))
+      !encode_map_3d(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.q, kHeadDim, p.num_heads,
+                              p.batch.num_rows, kHeadDim * 2, (long long)p.num_heads * kHeadDim * 2, 64, G, tpt))
     return cudaErrorInvalidValue;
   const int grid = device_sm_count();
   auto kern = prompt_attn_kernel<FP8, PTH>;
