@@ -76,9 +76,9 @@ __device__ __forceinline__ float row_max(const uint32_t (&r)[N], float acc, uint
 }
 
 // P = 2^(s * scale2 - m) of N logits as 16-bit pairs into the N / 2 columns at pa
-// (with PTH the token's ks in the place of scale2, and P times its vs); returns
-// the fp32 sum of the 2^...
-template <bool MASKED, bool FP8, bool PTH, int N>
+// (with PTH the token's ks in the place of scale2, which SCALED logits carry already, and P
+// times its vs); returns the fp32 sum of the 2^...
+template <bool MASKED, bool FP8, bool PTH, bool SCALED = false, int N>
 __device__ __forceinline__ float row_exp(const uint32_t (&r)[N], uint32_t pa, float scale2, float m,
                                          uint32_t vis0, uint32_t vis1, const float* ks,
                                          const float* vs) {
@@ -88,11 +88,14 @@ __device__ __forceinline__ float row_exp(const uint32_t (&r)[N], uint32_t pa, fl
 #pragma unroll
   for (int q = 0; q < N / 32; ++q) {
     uint32_t w[16];
+    float4 four = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
       const int t = 32 * q + i;
       float a = __uint_as_float(r[t]), b = __uint_as_float(r[t + 1]);
-      if (PTH) {
+      if (SCALED) {
+        add2(a, b, -m, -m);
+      } else if (PTH) {
         const float2 k = *reinterpret_cast<const float2*>(ks + t);
         fma2p(a, b, k.x, k.y, -m);
       } else {
@@ -107,7 +110,13 @@ __device__ __forceinline__ float row_exp(const uint32_t (&r)[N], uint32_t pa, fl
       }
       add2(l[i & 6], l[(i & 6) + 1], a, b);
       if (PTH) {
-        const float2 x = *reinterpret_cast<const float2*>(vs + t);
+        float2 x;
+        if (SCALED) {
+          if ((i & 2) == 0) four = *reinterpret_cast<const float4*>(vs + t);
+          x = (i & 2) == 0 ? make_float2(four.x, four.y) : make_float2(four.z, four.w);
+        } else {
+          x = *reinterpret_cast<const float2*>(vs + t);
+        }
         mul2v(a, b, x.x, x.y);
         if (MASKED) {  // (the scale of a token that the row does not see may be anything)
           a = (v >> i) & 1u ? a : 0.f;

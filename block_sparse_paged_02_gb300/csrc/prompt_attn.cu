@@ -634,19 +634,22 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
       }
       if (!ok) misc[0] = 1;
     };
-    // the scales of token ct of block n (a warp's 32 at a time), k's with the softmax's own
+    // The scales of token ct of block n: asked for, then put in place (a warp's 32 at a time), k's
+    // with the softmax's own
     const auto scales_of = [&](int head, bool data, int n, int ct) {
-      float ks = 0.f, vs = 0.f;
+      float2 x = make_float2(0.f, 0.f);
       if (data) {
         const long long at = ((long long)pages[n % kPages] * kBlock + ct) * Hk + head;
-        ks = __ldg(p.k_scale + at) * (p.softmax_scale * kTreeLog2e);
-        vs = __ldg(p.v_scale + at);
+        x = make_float2(__ldg(p.k_scale + at), __ldg(p.v_scale + at));
       }
+      return x;
+    };
+    const auto scales_in = [&](float2 x, bool data, int n, int ct) {
       float* sc = reinterpret_cast<float*>(smem + C::kSmScale) + (n % kScales) * kScaleWords;
-      sc[ct] = ks;
-      sc[kSoV + ct] = vs;
-      sc[kSoLog + ct] = log2_scale(vs);
-      const uint32_t mag = scale_bits(vs);
+      sc[ct] = x.x * (p.softmax_scale * kTreeLog2e);
+      sc[kSoV + ct] = x.y;
+      sc[kSoLog + ct] = log2_scale(x.y);
+      const uint32_t mag = scale_bits(x.y);
       const uint32_t hi = __reduce_max_sync(0xffffffffu, data ? mag : 0u);
       const uint32_t lo = __reduce_min_sync(0xffffffffu, data ? mag : ~0u);
       if (lane == 0)
@@ -669,8 +672,11 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
           // the softmax is through with this place's block n - 4)
           ok = warp_wait(&kv_full[(2 * n) % kBufs], ((2 * n) / kBufs) & 1);
           if (!ok) break;
-          for (int k = 0; k < 4; ++k)
-            scales_of(head, !(fl & kPoison) && t0 + 32 * k + lane < seq, n, 32 * k + lane);
+          float2 x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = scales_of(head, !(fl & kPoison) && t0 + 32 * k + lane < seq, n, 32 * k + lane);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) scales_in(x[k], !(fl & kPoison) && t0 + 32 * k + lane < seq, n, 32 * k + lane);
           __syncwarp();
           if (lane == 0) mbar_arrive(&sc_full[n % kScales]);
           // (V is followed too, so that no wait is two uses of its place behind)
@@ -719,14 +725,12 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
             const int b = x % kBufs, rb = x % kRing;
             ok = warp_wait(&raw_full[rb], (x / kRing) & 1);
             if (!ok) break;
-            if (PTH && kv == 0) {
-              // (the block's K has an e4m3 place, so V of block n - 2 is converted, over K of block
-              // n - 3 that its S has read: the softmax is through with block n - 4's scales)
-              const int n = x >> 1;
-              scales_of(head, !(fl & kPoison) && t0 + ct < seq, n, ct);
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sc_full[n % kScales]);
-            }
+            // (the block's scales are asked for before its K is converted and put in place after: K has
+            // an e4m3 place, so V of block n - 2 is converted, over K of block n - 3 that its S has
+            // read: the softmax is through with block n - 4's)
+            const bool data = !(fl & kPoison) && t0 + ct < seq;
+            float2 scale = make_float2(0.f, 0.f);
+            if (PTH && kv == 0) scale = scales_of(head, data, x >> 1, ct);
             if (x >= kBufs) ok = warp_wait(&kv_empty[b], ((x / kBufs) - 1) & 1);
             if (!ok) break;
             if (!(fl & kPoison)) {
@@ -765,6 +769,11 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
                 if (lane == 0) odd_fp8[4 * (looks % kLooks) + warp - 12] = any;
               }
               __syncwarp();
+            }
+            if (PTH && kv == 0) {
+              scales_in(scale, data, x >> 1, ct);
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sc_full[(x >> 1) % kScales]);
             }
             if (lane == 0) {
               if (kv == 1 && mixed) mbar_arrive(&looked[looks % kLooks]);
@@ -857,20 +866,46 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
               tc::tmem_wait_st();
             }
             uint32_t r[64];
-            const auto largest = [&](int h, float acc) {
-              if constexpr (PTH) {  // (the tokens' factors carry the softmax scale)
-                const float* kh = ks + 64 * h;
-                const uint32_t v0 = bits(seen - 64 * h), v1 = bits(seen - 64 * h - 32);
-                if (exact[h]) return fmaxf(acc, row_max<false, true, PTH, true>(r, -INFINITY, v0, v1, kh, kh + kSoLog));
-                if (mixed) return fmaxf(acc, row_max<false, true, PTH>(r, -INFINITY, v0, v1, kh) + near[h]);
-                return fmaxf(acc, row_max<false, false, PTH>(r, -INFINITY, 0, 0, kh) + near[h]);
-              } else {
-                return row_max<false, false, PTH>(r, acc, 0, 0, ks);
+            // Half h's logits; with a scale per token times the token's factor (which carries the
+            // softmax scale), -inf where the row does not look, whatever that factor is
+            const auto logits = [&](int h) {
+              tc::tmem_ld64(sa + 64 * h, r);
+              if constexpr (PTH) {
+#pragma unroll
+                for (int k = 0; k < 64; k += 4) {
+                  const float4 f = *reinterpret_cast<const float4*>(ks + 64 * h + k);
+                  float* x = reinterpret_cast<float*>(r + k);
+                  mul2v(x[0], x[1], f.x, f.y);
+                  mul2v(x[2], x[3], f.z, f.w);
+                }
+                if (__builtin_expect(mixed, 0)) {
+#pragma unroll
+                  for (int k = 0; k < 64; ++k)
+                    if (64 * h + k >= seen) r[k] = 0xff800000u;
+                }
               }
             };
-            tc::tmem_ld64(sa, r);
+            const auto largest = [&](int h, float acc) {
+              if constexpr (PTH) {
+                if (exact[h]) {
+                  float m4[4] = {acc, acc, acc, acc};
+#pragma unroll
+                  for (int k = 0; k < 64; k += 4) {
+                    const float4 l = *reinterpret_cast<const float4*>(ks + kSoLog + 64 * h + k);
+                    const float x[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], __uint_as_float(r[k + e]) + x[e]);
+                  }
+                  return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                }
+                return fmaxf(acc, row_max<false, false, false>(r, -INFINITY, 0, 0, nullptr) + near[h]);
+              } else {
+                return row_max<false, false, false>(r, acc, 0, 0, nullptr);
+              }
+            };
+            logits(0);
             float mx = largest(0, -INFINITY);
-            tc::tmem_ld64(sa + 64, r);
+            logits(1);
             mx = largest(1, mx);
             mx = PTH ? mx - kHead : mx * scale2 - kHead;
             const bool move = there && (mx > m_run + kSlack || (m_run == -INFINITY && mx > -INFINITY));
@@ -905,11 +940,11 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
             // the first's are read again (128 at once took a fifth longer with what else lives in
             // 168 registers)
             const auto weights = [&](int h) {
-              const float *kh = PTH ? ks + 64 * h : nullptr, *vh = PTH ? kh + kSoV : nullptr;
+              const float* vh = PTH ? ks + kSoV + 64 * h : nullptr;
               if (PTH && mixed)
-                l_run += row_exp<true, FP8, PTH>(r, sa + 64 * h, scale2, base, bits(seen - 64 * h), bits(seen - 64 * h - 32), kh, vh);
+                l_run += row_exp<true, FP8, PTH, PTH>(r, sa + 64 * h, scale2, base, bits(seen - 64 * h), bits(seen - 64 * h - 32), nullptr, vh);
               else
-                l_run += row_exp<false, FP8, PTH>(r, sa + 64 * h, scale2, base, 0, 0, kh, vh);
+                l_run += row_exp<false, FP8, PTH, PTH>(r, sa + 64 * h, scale2, base, 0, 0, nullptr, vh);
               tc::tmem_wait_st();
             };
             const auto announce = [&](int h) {
@@ -919,7 +954,7 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
             };
             weights(1);
             announce(1);
-            tc::tmem_ld64(sa, r);
+            logits(0);
             weights(0);
             if (__builtin_expect(hand, 0)) {
               pv_by_hand<FP8>(oa, 0, 128, sa, sa + 64, smem + ((2 * n + 1) % kBufs) * kTile,
