@@ -6,10 +6,10 @@
 // counted; (2) each old request's pages gain children - 1 holders (a partial last page
 // only those children that do not grow), so that requests with one child touch no
 // count; (3) of the requests that go on writing a partial page that nobody else holds,
-// the lowest keeps it (an atomic minimum of a negative number in its count); (4) pages
-// needed per request and their prefix sum, free pages per CTA; (5) the lowest free
-// pages found in order by ballots and written to the tables.  Counts are integers, so
-// their order does not matter.
+// the lowest keeps it: every CTA finds these for itself in a table in shared memory, as
+// it does the pages needed per request and their prefix sum, and counts the free pages
+// of its slice; (4) tables, and the lowest free pages, found in order by a scan.  Counts
+// are integers, so their order does not matter.
 #include "prompt_common.cuh"
 
 namespace msa {
@@ -18,47 +18,39 @@ namespace {
 constexpr int kFkThreads = 1024, kFkWarps = kFkThreads / 32, kFkCtas = 8;
 constexpr unsigned kAll = 0xffffffffu;
 
+constexpr int kFkRows = kMaxReqs / kFkThreads;  // new requests of a thread
+
+// Shared memory behind the fixed part: children[R] (then place[N]), off[N + 1], and the
+// table of pages that may be kept, keys[slots] and lowest[slots]
 struct FkShared {
-  int children[kMaxReqs];   // of an old request: all, and those that grow << 16
-  int off[kMaxReqs + 1];    // first new page of a new request; the total behind them
-  int warp[kFkWarps];
+  int warp[2][kFkWarps];
   int flags[kFkCtas], free_pages[kFkCtas];
 };
+__host__ __device__ __forceinline__ int fk_slots(int n) {
+  int s = 64;
+  while (s < 2 * n) s *= 2;
+  return s;
+}
+__host__ __device__ __forceinline__ int fk_longer(int r, int n) { return r > n ? r : n; }
+size_t fk_bytes(int r, int n) { return sizeof(FkShared) + 4ull * (fk_longer(r, n) + n + 1 + 2 * fk_slots(n)); }
 
-// A new request: its tokens, blocks held, full ones, the page it would write on with
-// (-1: none), blocks with its growth; wrong: status bits
+// A new request: its parent, tokens, growth, and the partial page it would write on (-1: none)
 struct FkNew {
-  int n, have, full, last, blocks;
-  bool partial;  // its last page is partial and it grows
-  uint32_t wrong;
+  int parent, n, grow, last;
+  __device__ __forceinline__ int have() const { return (n + kBlock - 1) / kBlock; }
+  __device__ __forceinline__ int full() const { return n / kBlock; }
+  __device__ __forceinline__ int blocks() const { return (n + grow + kBlock - 1) / kBlock; }
 };
 
-__device__ __forceinline__ FkNew fk_new(const ForkLaunch& p, int i) {
-  FkNew x;
-  x.n = x.have = x.full = x.blocks = 0;
-  x.last = -1;
-  x.partial = false;
-  x.wrong = 0;
-  const int parent = __ldg(p.parent + i), grow = p.grow ? __ldg(p.grow + i) : 0;
-  if (parent < -1 || parent >= p.from.num_reqs || grow < 0) {
-    x.wrong = MSA_DEV_MALFORMED;
-    return x;
-  }
-  if (parent >= 0) x.n = __ldg(p.from.lens + parent);
-  const long long most = (long long)x.n + grow;
-  if (x.n < 0 || x.n > (long long)kBlock * p.from.bt_stride || most > (long long)kBlock * p.to.bt_stride) {
-    x.wrong = MSA_DEV_MALFORMED;
-    return x;
-  }
-  x.have = (x.n + kBlock - 1) / kBlock;
-  x.full = x.n / kBlock;
-  x.blocks = (int)((most + kBlock - 1) / kBlock);
-  x.partial = grow > 0 && x.have > x.full;
-  if (x.partial) x.last = __ldg(p.from.block_table + (long long)parent * p.from.bt_stride + x.full);
-  return x;
+// sum over the block of v; s_warp is free again after the next barrier
+__device__ __forceinline__ int block_sum(int v, int* s_warp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = __reduce_add_sync(kAll, v);
+  if (lane == 0) s_warp[warp] = v;
+  __syncthreads();
+  return __reduce_add_sync(kAll, s_warp[lane]);
 }
-
-// exclusive sum over the block; the total in *sum
+// exclusive sum; the total in *sum
 __device__ __forceinline__ int block_scan(int v, int* s_warp, int* sum) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
@@ -67,23 +59,26 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* sum) {
     const int y = __shfl_up_sync(kAll, x, o);
     if (lane >= o) x += y;
   }
-  __syncthreads();
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < kFkWarps; ++w) {
-    if (w < warp) before += s_warp[w];
-    all += s_warp[w];
-  }
-  *sum = all;
+  const int w = s_warp[lane];
+  *sum = __reduce_add_sync(kAll, w);
+  const int before = __reduce_add_sync(kAll, lane < warp ? w : 0);
   return before + x - v;
 }
 
 __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
     page_fork_kernel(const __grid_constant__ ForkLaunch p) {
-  __shared__ FkShared s;
+  extern __shared__ __align__(16) uint8_t fk_smem[];
+  FkShared& s = *reinterpret_cast<FkShared*>(fk_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x;
-  const int R = p.from.num_reqs, N = p.to.num_reqs, P = p.from.num_pages;
+  const int R = p.from.num_reqs, N = p.to.num_reqs, P = p.from.num_pages, slots = fk_slots(N);
+  int* children = reinterpret_cast<int*>(&s + 1);  // of an old request: all, and those that grow << 16
+  // of a new request: its parent << 16 | whether it copies a page << 15 | blocks shared
+  int* place = children;
+  int* off = children + fk_longer(R, N);           // first new page of a new request; the total behind them
+  int* keys = off + N + 1;
+  int* lowest = keys + slots;
   int32_t* refs = p.to.refs;
   const int gwarp = rank * kFkWarps + warp;
   constexpr int kGridWarps = kFkCtas * kFkWarps;
@@ -116,17 +111,43 @@ __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
   };
 
   // ---- (1) checks and the children of each old request (every CTA counts them all)
-  for (int i = tid; i < R; i += kFkThreads) s.children[i] = 0;
-  __syncthreads();
+  FkNew x[kFkRows];
   uint32_t wrong = 0;
-  for (int i = tid; i < N; i += kFkThreads) {
-    const FkNew x = fk_new(p, i);
-    wrong |= x.wrong;
-    const int parent = __ldg(p.parent + i);
-    if (!x.wrong && parent >= 0)
-      atomicAdd(&s.children[parent], 1 + (p.grow && __ldg(p.grow + i) > 0 ? 1 << 16 : 0));
+#pragma unroll
+  for (int k = 0; k < kFkRows; ++k) {
+    const int i = tid + k * kFkThreads;
+    x[k].parent = -1;
+    x[k].n = x[k].grow = 0;
+    x[k].last = -1;
+    if (i >= N) continue;
+    x[k].parent = __ldg(p.parent + i);
+    x[k].grow = p.grow ? __ldg(p.grow + i) : 0;
+    if (x[k].parent < -1 || x[k].parent >= R || x[k].grow < 0) {
+      wrong |= MSA_DEV_MALFORMED;
+      x[k].parent = -1;
+    }
+  }
+  for (int i = tid; i < R; i += kFkThreads) children[i] = 0;
+  for (int i = tid; i < slots; i += kFkThreads) {
+    keys[i] = -1;
+    lowest[i] = N;
   }
   copy_refs();
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kFkRows; ++k) {
+    if (tid + k * kFkThreads >= N) continue;
+    if (x[k].parent >= 0) {
+      x[k].n = __ldg(p.from.lens + x[k].parent);
+      atomicAdd(&children[x[k].parent], 1 + (x[k].grow > 0 ? 1 << 16 : 0));
+    }
+    if (x[k].n < 0 || x[k].n > (long long)kBlock * p.from.bt_stride ||
+        (long long)x[k].n + x[k].grow > (long long)kBlock * p.to.bt_stride) {
+      wrong |= MSA_DEV_MALFORMED;
+    } else if (x[k].grow > 0 && x[k].n % kBlock) {
+      x[k].last = __ldg(p.from.block_table + (long long)x[k].parent * p.from.bt_stride + x[k].full());
+    }
+  }
   // warps of the cluster to old requests: several a request when these are few
   const int wpo = max(1, kGridWarps / max(1, R)), wpn = max(1, kGridWarps / max(1, N));
   for (int r = gwarp / wpo; r < R; r += kGridWarps / wpo) {
@@ -143,13 +164,11 @@ __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
     }
   }
   wrong = __reduce_or_sync(kAll, wrong);
-  if (lane == 0) s.warp[warp] = (int)wrong;
+  if (lane == 0) s.warp[0][warp] = (int)wrong;
   __syncthreads();
-  wrong = 0;
-  for (int w = 0; w < kFkWarps; ++w) wrong |= (uint32_t)s.warp[w];
+  wrong = __reduce_or_sync(kAll, (uint32_t)s.warp[0][lane]);
   exchange(s.flags, (int)wrong);
-  wrong = 0;
-  for (int c = 0; c < kFkCtas; ++c) wrong |= (uint32_t)s.flags[c];
+  wrong = __reduce_or_sync(kAll, lane < kFkCtas ? (uint32_t)s.flags[lane] : 0u);
   if (wrong) {
     refuse(wrong);
     return;
@@ -157,9 +176,11 @@ __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
 
   // ---- (2) holders gained and lost
   for (int r = gwarp / wpo; r < R; r += kGridWarps / wpo) {
+    const int all = children[r] & 0xffff, grown = children[r] >> 16;
+    if (all == 1 && grown == 0) continue;
     const int n = __ldg(p.from.lens + r), full = n / kBlock, nb = (n + kBlock - 1) / kBlock;
-    const int all = s.children[r] & 0xffff, grown = s.children[r] >> 16;
-    for (int b = (gwarp % wpo) * 32 + lane; b < nb; b += 32 * wpo) {
+    // (with one child only a partial last page may change)
+    for (int b = (all == 1 ? full : 0) + (gwarp % wpo) * 32 + lane; b < nb; b += 32 * wpo) {
       const int d = (b < full ? all : all - grown) - 1;
       if (d) atomicAdd(refs + __ldg(p.from.block_table + (long long)r * p.from.bt_stride + b), d);
     }
@@ -167,86 +188,93 @@ __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
   __syncthreads();
   cluster_sync();
 
-  // ---- (3) who keeps a partial page
-  for (int i = rank * kFkThreads + tid; i < N; i += kFkCtas * kFkThreads) {
-    const FkNew x = fk_new(p, i);
-    if (x.partial && __ldcg(refs + x.last) <= 0) atomicMin(refs + x.last, -(N - i));
+  // ---- (3) who keeps a partial page: the lowest of those that go on writing one without holders
+  const auto slot_of = [&](int page) { return (int)(((uint32_t)page * 2654435761u) >> 8) & (slots - 1); };
+  bool wants[kFkRows];
+#pragma unroll
+  for (int k = 0; k < kFkRows; ++k) {
+    const int page = x[k].last;
+    wants[k] = page >= 0 && __ldcg(refs + page) <= 0;
+    if (!wants[k]) continue;
+    int at = slot_of(page);
+    while (true) {  // (half the table stays empty)
+      const int was = atomicCAS(&keys[at], -1, page);
+      if (was == -1 || was == page) break;
+      at = (at + 1) & (slots - 1);
+    }
+    atomicMin(&lowest[at], tid + k * kFkThreads);
   }
   __syncthreads();
-  cluster_sync();
-
-  // ---- (4) new pages per request (every CTA for all), free pages
-  const auto keeps = [&](const FkNew& x, int i) { return x.partial && __ldcg(refs + x.last) == -(N - i); };
-  int total = 0;
-  for (int i0 = 0; i0 < N; i0 += kFkThreads) {
-    const int i = i0 + tid;
+  // pages needed and their prefix sum (every CTA for all), free pages of the slice
+  int total = 0, kept_here = 0;
+#pragma unroll
+  for (int k = 0; k < kFkRows; ++k) {
+    if (k * kFkThreads >= N) break;
+    const int i = tid + k * kFkThreads;
     int need = 0;
     if (i < N) {
-      const FkNew x = fk_new(p, i);
-      const bool copy = x.partial && !keeps(x, i);
-      need = x.blocks - x.have + (copy ? 1 : 0);
+      const int page = x[k].last;
+      bool keeps = wants[k];
+      if (keeps) {
+        int at = slot_of(page);
+        while (keys[at] != page) at = (at + 1) & (slots - 1);
+        keeps = lowest[at] == i;
+      }
+      wants[k] = keeps;
+      const bool copy = page >= 0 && !keeps;
+      if (keeps && page >= p0 && page < p1 && __ldcg(refs + page) == 0) ++kept_here;
+      need = x[k].blocks() - x[k].have() + (copy ? 1 : 0);
+      place[i] = max(x[k].parent, 0) << 16 | (copy ? 1 << 15 | x[k].full() : x[k].have());
       if (i % kFkCtas == rank) {
-        p.to.lens[i] = x.n;
-        p.to.copy_src[i] = copy ? x.last : -1;
-        p.to.copy_tokens[i] = copy ? x.n % kBlock : 0;
+        p.to.lens[i] = x[k].n;
+        p.to.copy_src[i] = copy ? page : -1;
+        p.to.copy_tokens[i] = copy ? x[k].n % kBlock : 0;
         if (!copy) p.to.copy_dst[i] = -1;
       }
     }
     int sum;
-    const int before = block_scan(need, s.warp, &sum);
-    if (i < N) s.off[i] = total + before;
+    const int before = block_scan(need, s.warp[k & 1], &sum);
+    if (i < N) off[i] = total + before;
     total += sum;
   }
-  if (tid == 0) s.off[N] = total;
-  int zeros = 0;
+  if (tid == 0) off[N] = total;
+  int zeros = -kept_here;
   for (int i = p0 + tid; i < p1; i += kFkThreads) zeros += __ldcg(refs + i) == 0;
-  zeros = __reduce_add_sync(kAll, zeros);
   __syncthreads();
-  if (lane == 0) s.warp[warp] = zeros;
-  __syncthreads();
-  int mine = 0;
-  for (int w = 0; w < kFkWarps; ++w) mine += s.warp[w];
-  exchange(s.free_pages, mine);
-  int at = 0, avail = 0;
-  for (int c = 0; c < kFkCtas; ++c) {
-    if (c < rank) at += s.free_pages[c];
-    avail += s.free_pages[c];
-  }
-  if (avail < total) {
+  exchange(s.free_pages, block_sum(zeros, s.warp[0]));
+  const int free_of = lane < kFkCtas ? s.free_pages[lane] : 0;
+  int at = __reduce_add_sync(kAll, lane < rank ? free_of : 0);
+  if ((int)__reduce_add_sync(kAll, free_of) < total) {
     copy_refs();
     refuse(MSA_DEV_NO_PAGES);
     return;
   }
 
-  // ---- (5) tables
+  // ---- (4) tables
+#pragma unroll
+  for (int k = 0; k < kFkRows; ++k)
+    if (wants[k] && x[k].last >= p0 && x[k].last < p1) refs[x[k].last] = 1;
+  __syncthreads();  // (before the slice's free pages are looked for)
   for (int i = gwarp / wpn; i < N; i += kGridWarps / wpn) {
-    const FkNew x = fk_new(p, i);
-    const int parent = __ldg(p.parent + i);
-    // (a kept page's count is negative until it becomes 1 below, a copied one's is not)
-    const int count = s.off[i + 1] - s.off[i];
-    const bool copy = count > x.blocks - x.have;
-    const int shared = copy ? x.full : x.have;
+    const int parent = place[i] >> 16, shared = place[i] & 0x7fff;
     for (int b = (gwarp % wpn) * 32 + lane; b < shared; b += 32 * wpn)
       p.to.block_table[(long long)i * p.to.bt_stride + b] =
           __ldg(p.from.block_table + (long long)parent * p.from.bt_stride + b);
-    if (x.partial && !copy && gwarp % wpn == 0 && lane == 0) refs[x.last] = 1;
   }
-  for (int i0 = p0; i0 < p1 && at < total; i0 += kFkThreads) {
+  for (int i0 = p0, turn = 0; i0 < p1 && at < total; i0 += kFkThreads, turn ^= 1) {
     const int page = i0 + tid;
     const bool free_page = page < p1 && __ldcg(refs + page) == 0;
     int sum;
-    const int k = at + block_scan(free_page ? 1 : 0, s.warp, &sum);
+    const int k = at + block_scan(free_page ? 1 : 0, s.warp[turn], &sum);
     if (free_page && k < total) {
       int lo = 0, hi = N - 1;  // the last request whose first new page is k or before
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (s.off[mid] <= k) lo = mid; else hi = mid - 1;
+        if (off[mid] <= k) lo = mid; else hi = mid - 1;
       }
-      const FkNew x = fk_new(p, lo);
-      const bool copy = s.off[lo + 1] - s.off[lo] > x.blocks - x.have;
-      const int j = k - s.off[lo];
-      p.to.block_table[(long long)lo * p.to.bt_stride + (copy ? x.full : x.have) + j] = page;
-      if (copy && j == 0) p.to.copy_dst[lo] = page;
+      const int j = k - off[lo];
+      p.to.block_table[(long long)lo * p.to.bt_stride + (place[lo] & 0x7fff) + j] = page;
+      if (j == 0 && (place[lo] >> 15 & 1)) p.to.copy_dst[lo] = page;
       refs[page] = 1;
     }
     at += sum;
@@ -294,7 +322,12 @@ __global__ void __launch_bounds__(kCpThreads) page_copy_kernel(const __grid_cons
 }  // namespace
 
 cudaError_t launch_page_fork(const ForkLaunch& p, cudaStream_t stream) {
-  page_fork_kernel<<<kFkCtas, kFkThreads, 0, stream>>>(p);
+  const size_t bytes = fk_bytes(p.from.num_reqs, p.to.num_reqs);
+  if (bytes > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(page_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+  }
+  page_fork_kernel<<<kFkCtas, kFkThreads, bytes, stream>>>(p);
   return cudaGetLastError();
 }
 
