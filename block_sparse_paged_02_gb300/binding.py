@@ -690,7 +690,7 @@ def msa_page_copy(layers, src, dst, tokens, dev_status, stream=None):
     _typed("tokens", tokens, (torch.int32,), (n,))
     s, d, t, st = _ptr(src), _ptr(dst), _ptr(tokens), _ptr(dev_status)
     _check("msa_page_copy", _calls().msa_page_copy(
-        (msa_kv_pools * len(layers))(*layers), len(layers), pages.pop() if pages else 0, s, d, t, n, st,
+        b"".join(layers), len(layers), pages.pop() if pages else 0, s, d, t, n, st,
         _on(stream, dev_status, src, dst, tokens, *(_first(x) for x in layers))))
 
 

@@ -111,6 +111,11 @@ __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
   };
 
   // ---- (1) checks and the children of each old request (every CTA counts them all)
+  // Warps of the cluster to old requests: several a request when these are few.  The loads go out
+  // in stages, each one's in flight together: lengths, parents; pages; their counts.
+  const int wpo = max(1, kGridWarps / max(1, R)), wpn = max(1, kGridWarps / max(1, N));
+  const int r0 = gwarp / wpo, b0 = (gwarp % wpo) * 32 + lane;
+  const int n0 = r0 < R ? __ldg(p.from.lens + r0) : 0;
   FkNew x[kFkRows];
   uint32_t wrong = 0;
 #pragma unroll
@@ -132,6 +137,9 @@ __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
     keys[i] = -1;
     lowest[i] = N;
   }
+  int page0 = 0;  // of block b0 of request r0
+  const bool there0 = n0 >= 0 && n0 <= (long long)kBlock * p.from.bt_stride && b0 < (n0 + kBlock - 1) / kBlock;
+  if (there0) page0 = __ldg(p.from.block_table + (long long)r0 * p.from.bt_stride + b0);
   copy_refs();
   __syncthreads();
 #pragma unroll
@@ -148,17 +156,15 @@ __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
       x[k].last = __ldg(p.from.block_table + (long long)x[k].parent * p.from.bt_stride + x[k].full());
     }
   }
-  // warps of the cluster to old requests: several a request when these are few
-  const int wpo = max(1, kGridWarps / max(1, R)), wpn = max(1, kGridWarps / max(1, N));
-  for (int r = gwarp / wpo; r < R; r += kGridWarps / wpo) {
-    const int n = __ldg(p.from.lens + r);
+  for (int r = r0; r < R; r += kGridWarps / wpo) {
+    const int n = r == r0 ? n0 : __ldg(p.from.lens + r);
     if (n < 0 || n > (long long)kBlock * p.from.bt_stride) {
       wrong |= MSA_DEV_MALFORMED;
       continue;
     }
     const int nb = (n + kBlock - 1) / kBlock;
-    for (int b = (gwarp % wpo) * 32 + lane; b < nb; b += 32 * wpo) {
-      const int page = __ldg(p.from.block_table + (long long)r * p.from.bt_stride + b);
+    for (int b = b0; b < nb; b += 32 * wpo) {
+      const int page = r == r0 && b == b0 ? page0 : __ldg(p.from.block_table + (long long)r * p.from.bt_stride + b);
       if (page < 0 || page >= P) wrong |= MSA_DEV_BAD_PAGE;
       else if (__ldg(p.refs + page) < 1) wrong |= MSA_DEV_BAD_TABLE;
     }
@@ -175,14 +181,14 @@ __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
   }
 
   // ---- (2) holders gained and lost
-  for (int r = gwarp / wpo; r < R; r += kGridWarps / wpo) {
+  for (int r = r0; r < R; r += kGridWarps / wpo) {
     const int all = children[r] & 0xffff, grown = children[r] >> 16;
     if (all == 1 && grown == 0) continue;
-    const int n = __ldg(p.from.lens + r), full = n / kBlock, nb = (n + kBlock - 1) / kBlock;
-    // (with one child only a partial last page may change)
-    for (int b = (all == 1 ? full : 0) + (gwarp % wpo) * 32 + lane; b < nb; b += 32 * wpo) {
+    const int n = r == r0 ? n0 : __ldg(p.from.lens + r), full = n / kBlock, nb = (n + kBlock - 1) / kBlock;
+    for (int b = b0; b < nb; b += 32 * wpo) {
       const int d = (b < full ? all : all - grown) - 1;
-      if (d) atomicAdd(refs + __ldg(p.from.block_table + (long long)r * p.from.bt_stride + b), d);
+      if (d == 0) continue;
+      atomicAdd(refs + (r == r0 && b == b0 ? page0 : __ldg(p.from.block_table + (long long)r * p.from.bt_stride + b)), d);
     }
   }
   __syncthreads();
