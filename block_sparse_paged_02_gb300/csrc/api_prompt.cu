@@ -11,10 +11,10 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 msa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MSA_OK : MSA_ERR_CUDA; }
 
 struct PromptWs {
-  size_t flags, part_ml, part_o, total;
+  size_t split, part_bad, part_ml, part_o, total;
 };
 
-// The flags and the partials: two pairs of 128-row tiles a CTA
+// The records and the partials: two pairs of 128-row tiles a CTA
 PromptWs prompt_layout() {
   PromptWs w;
   size_t off = 0;
@@ -23,8 +23,9 @@ PromptWs prompt_layout() {
     off = round_up(off + bytes, 256);
     return at;
   };
-  const size_t grid = (size_t)prompt_grid();
-  w.flags = take(prompt_flag_bytes((int)grid));
+  const size_t grid = (size_t)device_sm_count();
+  w.split = take(grid * sizeof(PromptSplit));
+  w.part_bad = take(2 * grid * 4);
   w.part_ml = take(2 * grid * 256 * 8);
   w.part_o = take(2 * grid * 256 * kHeadDim * 4);
   w.total = off;
@@ -203,7 +204,8 @@ msa_status msa_prompt_attn(const msa_batch* batch, const msa_attn_args* a, void*
   p.out = static_cast<uint16_t*>(a->out);
   p.lse = a->lse;
   p.status = dev_status;
-  p.flags = reinterpret_cast<int32_t*>(ws + w.flags);
+  p.split = reinterpret_cast<PromptSplit*>(ws + w.split);
+  p.part_bad = reinterpret_cast<int32_t*>(ws + w.part_bad);
   p.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
   p.part_o = reinterpret_cast<float*>(ws + w.part_o);
   return cuda_status(launch_prompt_attn(p, stream));

@@ -20,8 +20,8 @@
 // The work is the list (request, KV head, tile pair), each pair counted as the
 // tokens it sees and kPairCost more; it is cut into equal contiguous slices, one
 // per CTA, at block boundaries.  A pair that several CTAs share goes through
-// partial results (O, m, l in fp32), joined by twos in a fixed order by whichever
-// CTA comes last, without any waiting; results do not depend on timing.
+// partial results (O, m, l in fp32) that a second kernel joins in CTA order, so
+// that results do not depend on timing.
 //
 // A block that not every row sees whole (the diagonal) takes a masked softmax,
 // and its V is looked over: a value that is not finite would reach rows that
@@ -48,12 +48,11 @@ constexpr int kPairCost = 384;
 constexpr long long kMinSlice = 512;
 
 // A segment: blocks [b0, b0 + nb) of a tile pair that the CTA's slice holds
-struct alignas(8) Segment {
+struct Segment {
   int flags;
   int row0, ntok, pos0;  // the pair's rows: first in the batch, count, position of the first
   int seq, b0, nb;       // tokens of the request; blocks
-  int head;              // KV head
-  int c0, parts;         // a pair cut over several CTAs: the first of them, how many
+  int slot, head;        // partial slot; KV head
   uint32_t bad;
 };
 
@@ -61,7 +60,7 @@ struct alignas(8) Segment {
 template <bool FP8, bool PTH>
 struct PaCfg {
   static constexpr int kThreads = FP8 ? 512 : 384;
-  static constexpr int kBufs = 3;  // ring of 16-bit K and V tiles, alternating
+  static constexpr int kBufs = FP8 ? 3 : PTH ? 4 : 5;  // ring of 16-bit K and V tiles, alternating
   static constexpr int kRaws = FP8 ? 3 : 0;            // ring of e4m3 tiles
   static constexpr int kSmQ = kBufs * kTile;
   static constexpr int kSmRaw = kSmQ + 2 * kTile;
@@ -304,6 +303,8 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *tmem_slot;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0 && sl.begin >= sl.end) p.split[blockIdx.x].nrows = 0;
   if (!sl.tiled) {  // every row of an unusable batch, as empty rows
     const long long n = (long long)p.batch.num_rows * H, step = (long long)gridDim.x * kThreads;
     const long long at = (long long)blockIdx.x * kThreads + tid;
@@ -319,6 +320,8 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
       // ---------------------------------------------- copies
       int n = 0, n_seg = 0, looks = 0, x = 0, fills = 0;
       bool ok = true;
+      PromptSplit rec;
+      rec.nrows = 0;
       const uint32_t qbytes = 2u * 64u * (uint32_t)(G * tpt);  // of one box of Q
       Segment sg;
       auto announce = [&]() {
@@ -446,12 +449,17 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
           sg.row0 = rq.q0 + j0;
           sg.pos0 = rq.ctx + j0;
           sg.seq = rq.ctx + rq.qlen;
+          sg.slot = 2 * blockIdx.x + (sg.b0 > 0 ? 0 : 1);
           sg.bad = bad;
           sg.flags = (sg.nb == nv ? kWhole : 0) | (sg.ntok > tpt ? kTwo : 0) | (bad ? kPoison : 0);
-          if (sg.nb < nv) {
-            const auto owner = [&](long long u) { return (int)(((u + 1) * sl.ctas - 1) / sl.total); };
-            sg.c0 = owner(first);
-            sg.parts = owner(first + (long long)(nv - 1) * kBlock) - sg.c0 + 1;
+          if (sg.b0 > 0) {
+            const auto owner = [&](long long u) { return ((u + 1) * sl.ctas - 1) / sl.total; };
+            if (owner(first) == (long long)blockIdx.x - 1) {
+              rec.nrows = sg.ntok * G;
+              rec.row0 = sg.row0;
+              rec.head = sg.head;
+              rec.last = (int)owner(first + (long long)(nv - 1) * kBlock);
+            }
           }
           if (bad) sg.nb = 1;
           announce();
@@ -496,6 +504,7 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
         for (int i = max(0, x - ring); i < x; ++i) mbar_wait(&bars[i % ring], (i / ring) & 1);
         if (n_seg > 0) mbar_wait(FP8 ? q_raw : q_full, (n_seg - 1) & 1);
       }
+      if (lane == 0) p.split[blockIdx.x] = rec;
     };
     const auto odd_of = [&](int j) {  // odd values in the V of mixed block j
       if (!FP8) return look_odd[j % kLooks] != 0;
@@ -511,27 +520,51 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
       const uint64_t kd0 = tc::desc_kmajor_sw128(smem_u32(smem));
       const uint64_t vd0 = tc::desc_mnmajor_sw128(smem_u32(smem), kHalf);
       const uint32_t sc = tmem + col_s(t), oc = tmem + col_o(t);
-      bool ok = true, on = false, any = false;  // the tile has rows; the segment has data
-      // block n of all, i of nb of segment seg, at t0; mixed blocks so far
-      int n = -1, seg = -1, i = -1, nb = 0, t0 = 0, mixes = 0, pos0 = 0, last = 0, last0 = 0;
-      while (true) {
-        const bool next_seg = i + 1 >= nb;
-        if (n >= 0) {
-          // ---- P V of the block
-          const int x = 2 * n + 1, b = x % kBufs;
+      bool ok = true;
+      int n = 0, mixes = 0;  // blocks, mixed ones
+      for (int seg = 0;; ++seg) {
+        ok = mbar_wait(&info_full[seg % kInfos], (seg / kInfos) & 1);
+        if (!ok) break;
+        const Segment& sg = info[seg % kInfos];
+        const int fl = sg.flags, nb = sg.nb, pos0 = sg.pos0;
+        if (fl & kEnd) break;
+        const int last0 = pos0 + min(tpt, sg.ntok) - 1, last1 = pos0 + sg.ntok - 1;
+        const bool on = !(fl & kPoison) && (t == 0 || (fl & kTwo));
+        int t0 = kBlock * sg.b0;
+        const auto s_of = [&](int i) {
+          const int x = 2 * (n + i), b = x % kBufs;
+          if (!mbar_wait(&kv_full[b], (x / kBufs) & 1)) return false;
+          if (on && (t == 1 || i == 0 || last0 >= t0)) {
+            const uint64_t kd = tc::desc_advance(kd0, b * kTile);
+            tc::fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+              tc::mma_ss(sc, tc::desc_advance(qd, off), tc::desc_advance(kd, off), kIdescS, kk > 0 ? 1u : 0u);
+            }
+          }
+          tc::commit(&s_full[t]);
+          tc::commit(&kv_empty[b]);
+          return true;
+        };
+        ok = mbar_wait(q_full, seg & 1) && s_of(0);
+        if (!ok) break;
+        for (int i = 0; i < nb; ++i, t0 += kBlock) {
+          const int x = 2 * (n + i) + 1, b = x % kBufs;
+          if (i == nb - 1) tc::commit(q_empty);
           const bool work = on && (t == 1 || i == 0 || last0 >= t0), mixed = on && t0 + kBlock - 1 > pos0;
           const uint64_t vd = tc::desc_advance(vd0, b * kTile);
           ok = mbar_wait(&kv_full[b], (x / kBufs) & 1);
           // O of the previous segment has been read
           if (i == 0 && seg > 0) ok = ok && mbar_wait(&o_free[t], (seg - 1) & 1);
           // (the softmax writes P of the second half first)
-          ok = ok && mbar_wait(&p_full[2 * t + 1], n & 1);
+          ok = ok && mbar_wait(&p_full[2 * t + 1], (n + i) & 1);
           // (block by block tile 0 first, so that one tile's softmax runs beside the other's products)
-          if (t == 1 || n > 0) ok = ok && mbar_wait(&turn[t], (n - 1 + t) & 1);
+          if (t == 1 || n + i > 0) ok = ok && mbar_wait(&turn[t], (n + i - 1 + t) & 1);
           if (!ok) break;
           // (the softmax adds the block's P V itself)
           const bool hand = mixed && odd_of(mixes);
-          const int steps = mixed ? steps_to(last, t0) : 8;
+          const int steps = mixed ? steps_to(t ? last1 : last0, t0) : 8;
           const auto pv = [&](int half, bool on_top) {
             if (!work || hand) return;
             tc::fence_after();
@@ -542,51 +575,22 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
                            (kk > 0 || on_top) ? 1u : 0u);
           };
           pv(1, i > 0);
-          ok = mbar_wait(&p_full[2 * t], n & 1);
+          ok = mbar_wait(&p_full[2 * t], (n + i) & 1);
           if (!ok) break;
           pv(0, i > 0 || steps > 4);
-          if (next_seg) tc::commit(&pv_done[t]);
+          if (i == nb - 1) tc::commit(&pv_done[t]);
           tc::commit(&kv_empty[b]);
-          mixes += any && t0 + kBlock - 1 > pos0;
-          // (the other tile does not wait for the next segment's Q)
-          if (next_seg) mbar_arrive(&turn[1 - t]);
-        }
-        // ---- S of the next block
-        ++i;
-        t0 += kBlock;
-        if (next_seg) {
-          ++seg;
-          ok = mbar_wait(&info_full[seg % kInfos], (seg / kInfos) & 1);
-          if (!ok) break;
-          const Segment& sg = info[seg % kInfos];
-          if (sg.flags & kEnd) break;
-          nb = sg.nb;
-          pos0 = sg.pos0;
-          i = 0;
-          t0 = kBlock * sg.b0;
-          any = !(sg.flags & kPoison);
-          on = any && (t == 0 || (sg.flags & kTwo));
-          last0 = pos0 + min(tpt, sg.ntok) - 1;
-          last = t ? pos0 + sg.ntok - 1 : last0;
-          ok = mbar_wait(q_full, seg & 1);
-        }
-        ++n;
-        const int x = 2 * n, b = x % kBufs;
-        ok = ok && mbar_wait(&kv_full[b], (x / kBufs) & 1);
-        if (!ok) break;
-        if (on && (t == 1 || i == 0 || last0 >= t0)) {
-          const uint64_t kd = tc::desc_advance(kd0, b * kTile);
-          tc::fence_after();
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-            tc::mma_ss(sc, tc::desc_advance(qd, off), tc::desc_advance(kd, off), kIdescS, kk > 0 ? 1u : 0u);
+          mixes += !(fl & kPoison) && t0 + kBlock - 1 > pos0;
+          if (i + 1 < nb) {
+            t0 += kBlock;
+            ok = s_of(i + 1);
+            t0 -= kBlock;
+            if (!ok) break;
           }
+          mbar_arrive(&turn[1 - t]);
         }
-        tc::commit(&s_full[t]);
-        tc::commit(&kv_empty[b]);
-        if (i == nb - 1) tc::commit(q_empty);
-        if (!next_seg) mbar_arrive(&turn[1 - t]);
+        if (!ok) break;
+        n += nb;
       }
       if (!ok) misc[0] = 1;
       // every product has completed before the tensor memory is freed
@@ -782,71 +786,6 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
         if (!ok) break;
       }
       if (!ok) misc[0] = 1;
-    };
-    // where CTA c0 + i of a shared pair keeps its partial: a CTA shares its last pair with those
-    // behind it (i = 0) and its first with those before
-    const auto slot_of = [&](const Segment& sg, int i) { return 2 * (sg.c0 + i) + (i == 0 ? 1 : 0); };
-    // The partials of a warp's 32 rows of a shared pair, joined by twos: of two neighbouring ranges
-    // of CTAs the one that ends last joins both into the left one's place, and the last two
-    // become the rows.  Which are joined does not depend on who comes last, so neither do the bits.
-    const auto join = [&](const Segment& sg, int t, float vs) {
-      const int n = sg.parts, quarter = warp & 3, grid = gridDim.x;
-      asm volatile("griddepcontrol.wait;" ::: "memory");  // (the flags are cleared)
-      int i = blockIdx.x - sg.c0;
-#pragma unroll 1
-      for (int k = 0; (1 << k) < n; ++k) {
-        const int left = i >> (k + 1) << (k + 1), right = left + (1 << k);
-        i = left;
-        if (right >= n) continue;
-        __threadfence();
-        __syncwarp();
-        int before = 0;
-        if (lane == 0)
-          before = atomicAdd(p.flags + (((left ? kJoinLevels : 0) + k) * grid + sg.c0 + left) * 8 + 4 * t + quarter, 1);
-        if (__shfl_sync(0xffffffffu, before, 0) == 0) return;
-        __threadfence();
-        const bool last = (2 << k) >= n;  // (left is 0 then)
-        const long long sl_ = slot_of(sg, left), sr = slot_of(sg, right);
-#pragma unroll 1
-        for (int rs = 0; rs < 4; ++rs) {
-          // four lanes a row, every fourth group of dims each
-          const int m = quarter * 32 + 8 * rs + (lane >> 2), mtok = m / G, tok = t * tpt + mtok;
-          const bool there = mtok < tpt && tok < sg.ntok;
-          const int hh = sg.head * G + (m - mtok * G);
-          const float2 a = __ldcg(p.part_ml + sl_ * 256 + 128 * t + m), b = __ldcg(p.part_ml + sr * 256 + 128 * t + m);
-          const float M = fmaxf(a.x, b.x), ref = M == -INFINITY ? 0.f : M;
-          float fa = a.x == -INFINITY ? 1.f : ex2_ftz(a.x - ref), fb = b.x == -INFINITY ? 1.f : ex2_ftz(b.x - ref);
-          const float L = a.y * fa + b.y * fb;
-          const float sink = p.sinks && there ? __ldg(p.sinks + hh) : 0.f;
-          const bool none = M == -INFINITY && L == 0.f;
-          const TreeRowEnd e = tree_row_end(M, L, p.sinks != nullptr, sink * kTreeLog2e, vs);
-          const long long r = ((long long)sg.row0 + tok) * H + hh;
-          if (last) {
-            fa *= e.f;
-            fb *= e.f;
-          }
-          float4* oa = reinterpret_cast<float4*>(p.part_o) + (sl_ * 32 + (lane & 3)) * 256 + 128 * t + m;
-          const float4* ob = reinterpret_cast<const float4*>(p.part_o) + (sr * 32 + (lane & 3)) * 256 + 128 * t + m;
-          uint16_t* out = p.out + r * kHeadDim + 4 * (lane & 3);
-#pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            const float4 x = __ldcg(oa + 4 * g * 256), y = __ldcg(ob + 4 * g * 256);
-            const float4 z = make_float4(x.x * fa + y.x * fb, x.y * fa + y.y * fb, x.z * fa + y.z * fb, x.w * fa + y.w * fb);
-            if (!last) {
-              oa[4 * g * 256] = z;
-            } else if (there) {
-              *reinterpret_cast<uint2*>(out + 16 * g) =
-                  none ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(z.x, z.y), pack_bf16x2(z.z, z.w));
-            }
-          }
-          __syncwarp();  // (every lane has read its row's weights before they change)
-          if ((lane & 3) == 0) {
-            if (!last) p.part_ml[sl_ * 256 + 128 * t + m] = make_float2(M, L);
-            else if (there) p.lse[r] = e.lse;
-          }
-        }
-        if (last) return;
-      }
     };
     const auto softmax = [&]() {
       // ---------------------------------------------- softmax of tile t
@@ -1047,6 +986,7 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
         const TreeRowEnd e = tree_row_end(none ? -INFINITY : m_run, none ? 0.f : l_run, p.sinks != nullptr,
                                           sink * kTreeLog2e, vs);
         const long long r = ((long long)sg.row0 + tok) * H + hh;  // row x head in the batch
+        const int pm = t * tpt * G + m;                           // row of the pair
         if (on && (fl & kWhole)) {
           // A lane holds two columns of a row in every eight; the four lanes of a row trade theirs
           // for eight columns each, so that a store's lines are eight rows' and not 32.
@@ -1083,8 +1023,8 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
           }
         } else {
           if (on) {
-            // a partial [4-dim group][row][4 dims]: the warp's rows are contiguous
-            uint4* dst = reinterpret_cast<uint4*>(p.part_o) + (long long)slot_of(sg, blockIdx.x - sg.c0) * 32 * 256 + 128 * t + m;
+            // [4-dim group][row][4 dims]: the warp's rows are contiguous
+            uint4* dst = reinterpret_cast<uint4*>(p.part_o) + (long long)sg.slot * 32 * 256 + pm;
 #pragma unroll 1
             for (int c = 0; c < 128; c += 64) {
               uint32_t v[64];
@@ -1103,11 +1043,13 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&o_free[t]);
         }
-        if (there && (fl & (kWhole | kPoison))) p.lse[r] = none ? (p.sinks ? sink : -INFINITY) : e.lse;
-        if (t == 0 && m == 0 && sg.bad) atomicOr(p.status, sg.bad);
-        if (on && !(fl & kWhole)) {
-          p.part_ml[(long long)slot_of(sg, blockIdx.x - sg.c0) * 256 + 128 * t + m] = make_float2(m_run, l_run);
-          join(sg, t, vs);
+        if (there) {
+          if (fl & (kWhole | kPoison)) p.lse[r] = none ? (p.sinks ? sink : -INFINITY) : e.lse;
+          else p.part_ml[(long long)sg.slot * 256 + pm] = make_float2(m_run, l_run);
+        }
+        if (t == 0 && m == 0) {
+          if (!(fl & kWhole)) p.part_bad[sg.slot] = fl & kPoison ? 1 : 0;
+          if (sg.bad) atomicOr(p.status, sg.bad);
         }
       }
       if (!ok) misc[0] = 1;
@@ -1131,11 +1073,143 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
   }
 }
 
-// The flags of shared pairs, before the attention that counts in them (it starts beside
-// this, and waits for it where it first joins).
-__global__ void __launch_bounds__(1024) prompt_clear_kernel(uint4* flags, int n) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  for (int i = threadIdx.x; i < n; i += 1024) flags[i] = make_uint4(0u, 0u, 0u, 0u);
+// ------------------------------------------------------------------ join
+
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+constexpr int kMaxMainCtas = 512;  // (the main kernel runs one CTA per SM)
+
+// Threads x 4 dims that share a row's partials: a unit is 8 / parts rows
+__device__ __forceinline__ int join_parts(int n) {
+  return n <= 8 ? 1 : n <= 16 ? 2 : n <= 64 ? 4 : 8;
+}
+
+// Joins the partials of the pairs that several CTAs share.
+__global__ void __launch_bounds__(kJoinThreads, 3)
+    prompt_join_kernel(const __grid_constant__ PromptLaunch p, int grid_main) {
+  __shared__ float4 s_o[kJoinThreads];
+  __shared__ float s_m[8], s_l[8];
+  __shared__ int s_bad[8], s_sum[kJoinWarps], s_base[kMaxMainCtas];
+  __shared__ PromptSplit s_rec[kMaxMainCtas];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int H = p.num_heads, G = H / p.num_kv_heads;
+  const float vs = p.scale_mode == MSA_SCALE_SCALAR ? __ldg(p.v_scale) : 1.f;
+  // the split pairs' work units, by a prefix sum over the records
+  int total = 0;
+  for (int c0 = 0; c0 < grid_main; c0 += kJoinThreads) {
+    const int c = c0 + threadIdx.x;
+    PromptSplit rec;
+    rec.nrows = 0;
+    rec.last = c;
+    if (c > 0 && c < grid_main) rec = p.split[c];
+    const int per = 8 / join_parts(rec.last - c + 2);
+    const int units = (rec.nrows + per - 1) / per;
+    int x = units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_sum[warp] = x;
+    __syncthreads();
+    if (c < grid_main) {
+      int before = x - units;
+      for (int w = 0; w < warp; ++w) before += s_sum[w];
+      s_base[c] = total + before;
+      s_rec[c] = rec;
+    }
+    for (int w = 0; w < kJoinWarps; ++w) total += s_sum[w];
+    __syncthreads();
+  }
+  for (int unit = blockIdx.x; unit < total; unit += gridDim.x) {
+    int lo = 0, hi = grid_main - 1;  // last record whose first unit is <= unit
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_base[mid] <= unit) lo = mid; else hi = mid - 1;
+    }
+    const int c = lo;
+    const PromptSplit rec = s_rec[c];
+    const int n = rec.last - c + 2;  // partials: CTAs c - 1 .. last
+    const int parts = join_parts(n), per = 8 / parts;
+    // neighbouring threads take the unit's rows, then the 4-dim groups, then the parts
+    const int row = threadIdx.x & (per - 1), x = threadIdx.x / per;
+    const int g = x & 31, part = x >> 5;
+    const int m = (unit - s_base[c]) * per + row;
+    const bool live = m < rec.nrows;
+    float M = -INFINITY, L = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    int bad = 0;
+    constexpr int kLoads = 4;  // partials that a thread has in flight
+    if (live) {
+      for (int i0 = part; i0 < n; i0 += kLoads * parts) {
+        float2 ml[kLoads];
+        float4 v[kLoads];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          const int i = i0 + u * parts;
+          ml[u] = make_float2(-INFINITY, 0.f);
+          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < n) {
+            const long long slot = 2ll * (c - 1 + i) + (i == 0 ? 1 : 0);
+            bad |= p.part_bad[slot];
+            ml[u] = p.part_ml[slot * 256 + m];
+            v[u] = reinterpret_cast<const float4*>(p.part_o)[(slot * 32 + g) * 256 + m];
+          }
+        }
+        float mn = M;
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) mn = fmaxf(mn, ml[u].x);
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        const float f0 = M == -INFINITY ? 1.f : ex2_ftz(M - ref);
+        L *= f0;
+        a.x *= f0; a.y *= f0; a.z *= f0; a.w *= f0;
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          const float f = ml[u].x == -INFINITY ? 1.f : ex2_ftz(ml[u].x - ref);
+          L += ml[u].y * f;
+          a.x += v[u].x * f; a.y += v[u].y * f; a.z += v[u].z * f; a.w += v[u].w * f;
+        }
+        M = mn;
+      }
+    }
+    if (parts > 1) {
+      __syncthreads();  // the previous unit's sums have been read
+      s_o[threadIdx.x] = a;
+      if (g == 0) {
+        s_m[part * per + row] = M;
+        s_l[part * per + row] = L;
+        s_bad[part * per + row] = bad;
+      }
+      __syncthreads();
+      if (part == 0) {
+        for (int k = 1; k < parts; ++k) {
+          bad |= s_bad[k * per + row];
+          M = fmaxf(M, s_m[k * per + row]);
+        }
+        const float ref = M == -INFINITY ? 0.f : M;
+        L = 0.f;
+        a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < parts; ++k) {
+          const float mk = s_m[k * per + row], f = mk == -INFINITY ? 1.f : ex2_ftz(mk - ref);
+          const float4 o = s_o[k * 32 * per + threadIdx.x];
+          L += s_l[k * per + row] * f;
+          a.x += o.x * f; a.y += o.y * f; a.z += o.z * f; a.w += o.w * f;
+        }
+      }
+      __syncthreads();  // read before the next unit overwrites them
+    }
+    if (live && part == 0) {
+      const bool none = bad || (M == -INFINITY && L == 0.f);
+      const int h = rec.head * G + m % G;
+      const float sink = p.sinks ? __ldg(p.sinks + h) : 0.f;
+      const TreeRowEnd e = tree_row_end(M, L, p.sinks != nullptr, sink * kTreeLog2e, vs);
+      const long long r = ((long long)rec.row0 + m / G) * H + h;
+      uint2 w = make_uint2(pack_bf16x2(a.x * e.f, a.y * e.f), pack_bf16x2(a.z * e.f, a.w * e.f));
+      if (none) w = make_uint2(0u, 0u);
+      *reinterpret_cast<uint2*>(p.out + r * kHeadDim + 4 * g) = w;
+      if (g == 0) p.lse[r] = none ? (p.sinks ? sink : -INFINITY) : e.lse;
+    }
+  }
 }
 
 template <bool FP8, bool PTH>
@@ -1152,26 +1226,23 @@ cudaError_t launch(const PromptLaunch& p, cudaStream_t stream) {
       !encode_map_3d(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.q, kHeadDim, p.num_heads,
                               p.batch.num_rows, kHeadDim * 2, (long long)p.num_heads * kHeadDim * 2, 64, G, tpt))
     return cudaErrorInvalidValue;
-  const int grid = prompt_grid();
+  const int grid = device_sm_count();
   auto kern = prompt_attn_kernel<FP8, PTH>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (e != cudaSuccess) return e;
+  kern<<<grid, C::kThreads, C::kBytes, stream>>>(p, qmap, kmap, vmap);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.whole) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kBytes;
+  cfg.gridDim = dim3(3 * grid);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  if (!p.whole) {
-    prompt_clear_kernel<<<1, 1024, 0, stream>>>(reinterpret_cast<uint4*>(p.flags), (int)(prompt_flag_bytes(grid) / 16));
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    cfg.numAttrs = 1;
-  }
-  return cudaLaunchKernelEx(&cfg, kern, p, qmap, kmap, vmap);
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prompt_join_kernel, p, grid);
 }
 
 }  // namespace
@@ -1184,7 +1255,7 @@ cudaError_t launch_prompt_attn(const PromptLaunch& given, cudaStream_t stream) {
   PromptLaunch p = given;
   const int wide = 2 * (128 / (p.num_heads / p.num_kv_heads));
   const long long pairs = ((long long)p.batch.num_rows / wide + min(p.batch.num_rows, p.batch.num_reqs)) * p.num_kv_heads;
-  p.whole = pairs <= prompt_grid() && p.batch.bt_stride <= kWholeBlocks;
+  p.whole = pairs <= device_sm_count() && p.batch.bt_stride <= kWholeBlocks;
   const bool pth = p.scale_mode == MSA_SCALE_PER_TOKEN_HEAD;
   if (p.kv_fp8) return pth ? launch<true, true>(p, stream) : launch<true, false>(p, stream);
   return pth ? launch<false, true>(p, stream) : launch<false, false>(p, stream);

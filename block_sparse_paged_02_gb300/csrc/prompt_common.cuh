@@ -11,16 +11,14 @@ namespace msa {
 constexpr int kMaxGroup = 128;
 constexpr int kMaxKvHeads = 64;
 
-// A pair of tiles cut over CTAs is joined by twos: levels of that (2^8 CTAs at most), for the
-// pair that a CTA shares with those behind it and for the one it shares with those before
-constexpr int kJoinLevels = 8;
-// CTAs of the attention: one an SM
-inline int prompt_grid() {
-  const int n = device_sm_count();
-  return n < (1 << kJoinLevels) ? n : 1 << kJoinLevels;
-}
-// a flag for each, and for each warp of the softmax
-inline size_t prompt_flag_bytes(int grid) { return (size_t)2 * kJoinLevels * grid * 8 * 4; }
+// One tile pair whose blocks are shared by several CTAs (written by the second
+// of them): partials of CTAs c - 1 .. last.
+struct PromptSplit {
+  int32_t nrows;  // rows x group; 0: none
+  int32_t row0;   // first row in the batch
+  int32_t head;   // KV head
+  int32_t last;
+};
 
 struct PromptLaunch {
   msa_batch batch;
@@ -37,7 +35,8 @@ struct PromptLaunch {
   float* lse;
   uint32_t* status;
   bool whole;          // a pair to a CTA, none split
-  int32_t* flags;      // [2, kJoinLevels, grid, 8]
+  PromptSplit* split;  // [grid]
+  int32_t* part_bad;   // [2 * grid]
   float2* part_ml;     // [2 * grid, 256]
   float* part_o;       // [2 * grid, 32, 256, 4]
 };
