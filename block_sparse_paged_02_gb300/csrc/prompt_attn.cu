@@ -60,7 +60,7 @@ struct Segment {
 template <bool FP8, bool PTH>
 struct PaCfg {
   static constexpr int kThreads = FP8 ? 512 : 384;
-  static constexpr int kBufs = FP8 ? 3 : PTH ? 4 : 5;  // ring of 16-bit K and V tiles, alternating
+  static constexpr int kBufs = 3;  // ring of 16-bit K and V tiles, alternating
   static constexpr int kRaws = FP8 ? 3 : 0;            // ring of e4m3 tiles
   static constexpr int kSmQ = kBufs * kTile;
   static constexpr int kSmRaw = kSmQ + 2 * kTile;
@@ -68,8 +68,8 @@ struct PaCfg {
   static constexpr int kSmInfo = kSmScale + (PTH ? kScales * kScaleWords * 4 : 0);
   static constexpr int kSmBars = kSmInfo + kInfos * (int)sizeof(Segment);
   // kv full / empty, raw full / empty, q full / empty / raw, infos, scales; per tile s_full,
-  // p_full of two halves, pv_done, o_free, drained, turn; fill; to look over, looked
-  static constexpr int kNumBars = 2 * kBufs + 2 * kRaws + 3 + kInfos + kScales + 12 + 1 + 2 * kLooks + 2;
+  // p_full of two halves, pv_done, o_free, drained, turn; fill; to look over, looked; pages
+  static constexpr int kNumBars = 2 * kBufs + 2 * kRaws + 3 + kInfos + kScales + 12 + 1 + 2 * kLooks + 2 + kPages;
   static constexpr int kSmMisc = kSmBars + kNumBars * 8;
   static constexpr int kBytes = kSmMisc + 192;
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
   uint64_t* to_look = fill + 1;          // [kLooks]
   uint64_t* looked = to_look + kLooks;   // [kLooks]
   uint64_t* turn = looked + kLooks;      // [tile]: its products may go out
+  uint64_t* page_in = turn + 2;          // [kPages] (bf16 with a scale per token) the block's page is known
   Segment* info = reinterpret_cast<Segment*>(smem + C::kSmInfo);
   // [0] timeout; [4 + j % kLooks] block to look over (-1: none any more), then whether its V
   // holds odd values; [16 + n % kPages] page of block n; [24 + j % kLooks] tokens to look over; [32 + 4 (j % kLooks)] as [8], a word
@@ -291,6 +292,7 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
   barriers(to_look, kLooks, 1);
   barriers(looked, kLooks, FP8 ? kConv : 1);
   barriers(turn, 2, 1);
+  barriers(page_in, kPages, 1);
   if (warp == 3) fence_barrier_init();
   if (tid < 3) {
     const CUtensorMap* maps[3] = {&qmap, &kmap, &vmap};
@@ -336,12 +338,15 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
       auto push = [&](int kv, int pg, int t0, bool mixed) {
         const CUtensorMap* map = kv ? &vmap : &kmap;
         constexpr int ring = FP8 ? kRaws : kBufs;
-        if (kv == 0 && lane == 0) pages[n % kPages] = pg;
-        n += kv;
         const int b = x % ring;
         if (x >= ring) ok = warp_wait(&(FP8 ? raw_empty : kv_empty)[b], ((x / ring) - 1) & 1);
         if (!ok) return;
         ++x;
+        if (PTH && kv == 0 && lane == 0) {
+          pages[n % kPages] = pg;
+          if (!FP8) mbar_arrive(&page_in[n % kPages]);
+        }
+        n += kv;
         if constexpr (FP8) {
           if (lane == 0) {
             if (pg < 0) {
@@ -381,7 +386,7 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
         }
         // (asked for when the place's earlier uses are over, so that the wait for this one
         // cannot take one of them for it)
-        if (!PTH && kv == 1 && mixed) {
+        if (kv == 1 && mixed) {
           if (lane == 0) {
             look_at[looks % kLooks] = n - 1;
             look_from[looks % kLooks] = looks_of(sg, t0);
@@ -520,51 +525,27 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
       const uint64_t kd0 = tc::desc_kmajor_sw128(smem_u32(smem));
       const uint64_t vd0 = tc::desc_mnmajor_sw128(smem_u32(smem), kHalf);
       const uint32_t sc = tmem + col_s(t), oc = tmem + col_o(t);
-      bool ok = true;
-      int n = 0, mixes = 0;  // blocks, mixed ones
-      for (int seg = 0;; ++seg) {
-        ok = mbar_wait(&info_full[seg % kInfos], (seg / kInfos) & 1);
-        if (!ok) break;
-        const Segment& sg = info[seg % kInfos];
-        const int fl = sg.flags, nb = sg.nb, pos0 = sg.pos0;
-        if (fl & kEnd) break;
-        const int last0 = pos0 + min(tpt, sg.ntok) - 1, last1 = pos0 + sg.ntok - 1;
-        const bool on = !(fl & kPoison) && (t == 0 || (fl & kTwo));
-        int t0 = kBlock * sg.b0;
-        const auto s_of = [&](int i) {
-          const int x = 2 * (n + i), b = x % kBufs;
-          if (!mbar_wait(&kv_full[b], (x / kBufs) & 1)) return false;
-          if (on && (t == 1 || i == 0 || last0 >= t0)) {
-            const uint64_t kd = tc::desc_advance(kd0, b * kTile);
-            tc::fence_after();
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-              tc::mma_ss(sc, tc::desc_advance(qd, off), tc::desc_advance(kd, off), kIdescS, kk > 0 ? 1u : 0u);
-            }
-          }
-          tc::commit(&s_full[t]);
-          tc::commit(&kv_empty[b]);
-          return true;
-        };
-        ok = mbar_wait(q_full, seg & 1) && s_of(0);
-        if (!ok) break;
-        for (int i = 0; i < nb; ++i, t0 += kBlock) {
-          const int x = 2 * (n + i) + 1, b = x % kBufs;
-          if (i == nb - 1) tc::commit(q_empty);
+      bool ok = true, on = false, any = false;  // the tile has rows; the segment has data
+      // block n of all, i of nb of segment seg, at t0; mixed blocks so far
+      int n = -1, seg = -1, i = -1, nb = 0, t0 = 0, mixes = 0, pos0 = 0, last = 0, last0 = 0;
+      while (true) {
+        const bool next_seg = i + 1 >= nb;
+        if (n >= 0) {
+          // ---- P V of the block
+          const int x = 2 * n + 1, b = x % kBufs;
           const bool work = on && (t == 1 || i == 0 || last0 >= t0), mixed = on && t0 + kBlock - 1 > pos0;
           const uint64_t vd = tc::desc_advance(vd0, b * kTile);
           ok = mbar_wait(&kv_full[b], (x / kBufs) & 1);
           // O of the previous segment has been read
           if (i == 0 && seg > 0) ok = ok && mbar_wait(&o_free[t], (seg - 1) & 1);
           // (the softmax writes P of the second half first)
-          ok = ok && mbar_wait(&p_full[2 * t + 1], (n + i) & 1);
+          ok = ok && mbar_wait(&p_full[2 * t + 1], n & 1);
           // (block by block tile 0 first, so that one tile's softmax runs beside the other's products)
-          if (t == 1 || n + i > 0) ok = ok && mbar_wait(&turn[t], (n + i - 1 + t) & 1);
+          if (t == 1 || n > 0) ok = ok && mbar_wait(&turn[t], (n - 1 + t) & 1);
           if (!ok) break;
           // (the softmax adds the block's P V itself)
           const bool hand = mixed && odd_of(mixes);
-          const int steps = mixed ? steps_to(t ? last1 : last0, t0) : 8;
+          const int steps = mixed ? steps_to(last, t0) : 8;
           const auto pv = [&](int half, bool on_top) {
             if (!work || hand) return;
             tc::fence_after();
@@ -575,22 +556,51 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
                            (kk > 0 || on_top) ? 1u : 0u);
           };
           pv(1, i > 0);
-          ok = mbar_wait(&p_full[2 * t], (n + i) & 1);
+          ok = mbar_wait(&p_full[2 * t], n & 1);
           if (!ok) break;
           pv(0, i > 0 || steps > 4);
-          if (i == nb - 1) tc::commit(&pv_done[t]);
+          if (next_seg) tc::commit(&pv_done[t]);
           tc::commit(&kv_empty[b]);
-          mixes += !(fl & kPoison) && t0 + kBlock - 1 > pos0;
-          if (i + 1 < nb) {
-            t0 += kBlock;
-            ok = s_of(i + 1);
-            t0 -= kBlock;
-            if (!ok) break;
-          }
-          mbar_arrive(&turn[1 - t]);
+          mixes += any && t0 + kBlock - 1 > pos0;
+          // (the other tile does not wait for the next segment's Q)
+          if (next_seg) mbar_arrive(&turn[1 - t]);
         }
+        // ---- S of the next block
+        ++i;
+        t0 += kBlock;
+        if (next_seg) {
+          ++seg;
+          ok = mbar_wait(&info_full[seg % kInfos], (seg / kInfos) & 1);
+          if (!ok) break;
+          const Segment& sg = info[seg % kInfos];
+          if (sg.flags & kEnd) break;
+          nb = sg.nb;
+          pos0 = sg.pos0;
+          i = 0;
+          t0 = kBlock * sg.b0;
+          any = !(sg.flags & kPoison);
+          on = any && (t == 0 || (sg.flags & kTwo));
+          last0 = pos0 + min(tpt, sg.ntok) - 1;
+          last = t ? pos0 + sg.ntok - 1 : last0;
+          ok = mbar_wait(q_full, seg & 1);
+        }
+        ++n;
+        const int x = 2 * n, b = x % kBufs;
+        ok = ok && mbar_wait(&kv_full[b], (x / kBufs) & 1);
         if (!ok) break;
-        n += nb;
+        if (on && (t == 1 || i == 0 || last0 >= t0)) {
+          const uint64_t kd = tc::desc_advance(kd0, b * kTile);
+          tc::fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+            tc::mma_ss(sc, tc::desc_advance(qd, off), tc::desc_advance(kd, off), kIdescS, kk > 0 ? 1u : 0u);
+          }
+        }
+        tc::commit(&s_full[t]);
+        tc::commit(&kv_empty[b]);
+        if (i == nb - 1) tc::commit(q_empty);
+        if (!next_seg) mbar_arrive(&turn[1 - t]);
       }
       if (!ok) misc[0] = 1;
       // every product has completed before the tensor memory is freed
@@ -620,19 +630,24 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
         mbar_arrive(&looked[j % kLooks]);
       }
     };
+    // the j-th mixed block, once it is asked for; false without one, or when a wait ran out
+    const auto look_next = [&](int j) {
+      if (!warp_wait(&to_look[j % kLooks], (j / kLooks) & 1)) {
+        misc[0] = 1;
+        return false;
+      }
+      const int n = look_at[j % kLooks];
+      if (n < 0) return false;
+      if (!warp_wait(&kv_full[(2 * n + 1) % kBufs], ((2 * n + 1) / kBufs) & 1)) {
+        misc[0] = 1;
+        return false;
+      }
+      look_over(j, (2 * n + 1) % kBufs, look_from[j % kLooks]);
+      return true;
+    };
     const auto look = [&]() {
       // ---------------------------------------------- mixed blocks, as they are asked for
-      bool ok = true;
-      for (int j = 0;; ++j) {
-        ok = warp_wait(&to_look[j % kLooks], (j / kLooks) & 1);
-        if (!ok) break;
-        const int n = look_at[j % kLooks];
-        if (n < 0) break;
-        ok = warp_wait(&kv_full[(2 * n + 1) % kBufs], ((2 * n + 1) / kBufs) & 1);
-        if (!ok) break;
-        look_over(j, (2 * n + 1) % kBufs, look_from[j % kLooks]);
-      }
-      if (!ok) misc[0] = 1;
+      for (int j = 0; look_next(j);) ++j;
     };
     // The scales of token ct of block n: asked for, then put in place (a warp's 32 at a time), k's
     // with the softmax's own
@@ -668,9 +683,9 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
         if (fl & kEnd) break;
         int t0 = sg.b0 * kBlock;
         for (int i = 0; i < nb; ++i, ++n, t0 += kBlock) {
-          // (K of the block has a place, which S of block n - 2 freed: its page is known, and
-          // the softmax is through with this place's block n - 4)
-          ok = warp_wait(&kv_full[(2 * n) % kBufs], ((2 * n) / kBufs) & 1);
+          // (the block's K has a place, that of V of block n - 2: its page is known, and the
+          // softmax is through with that block, so with block n - 4 of this place too)
+          ok = warp_wait(&page_in[n % kPages], (n / kPages) & 1);
           if (!ok) break;
           float2 x[4];
 #pragma unroll
@@ -679,10 +694,10 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
           for (int k = 0; k < 4; ++k) scales_in(x[k], !(fl & kPoison) && t0 + 32 * k + lane < seq, n, 32 * k + lane);
           __syncwarp();
           if (lane == 0) mbar_arrive(&sc_full[n % kScales]);
-          // (V is followed too, so that no wait is two uses of its place behind)
-          ok = warp_wait(&kv_full[(2 * n + 1) % kBufs], ((2 * n + 1) / kBufs) & 1);
-          if (!ok) break;
-          if (!(fl & kPoison) && t0 + kBlock - 1 > pos0) look_over(looks++, (2 * n + 1) % kBufs, looks_of(sg, t0));
+          if (!(fl & kPoison) && t0 + kBlock - 1 > pos0) {
+            ok = look_next(looks++);
+            if (!ok) break;
+          }
         }
         if (!ok) break;
       }
@@ -825,19 +840,10 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
           const bool mixed = !(fl & kPoison) && t0 + kBlock - 1 > pos0;
           const int seen = mixed ? (there ? pos0 + tok + 1 - t0 : 0) : kBlock;  // of the block's tokens
           const float* ks = nullptr;
-          // (PTH, by half) log2 of the largest v scale; whether the scales lie too far apart for it
-          float near[2] = {0.f, 0.f};
-          bool exact[2] = {false, false};
           if (PTH) {
             ok = warp_wait(&sc_full[n % kScales], (n / kScales) & 1);
             if (!ok) break;
             ks = reinterpret_cast<const float*>(smem + C::kSmScale) + (n % kScales) * kScaleWords;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float4 r = *reinterpret_cast<const float4*>(ks + kSoRange + 4 * h);
-              near[h] = fmaxf(r.x, r.z);
-              exact[h] = near[h] - fminf(r.y, r.w) > kNear;
-            }
           }
           ok = warp_wait(&s_full[t], n & 1);
           if (!ok) break;
@@ -866,11 +872,13 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
               tc::tmem_wait_st();
             }
             uint32_t r[64];
-            // Half h's logits; with a scale per token times the token's factor (which carries the
-            // softmax scale), -inf where the row does not look, whatever that factor is
-            const auto logits = [&](int h) {
-              tc::tmem_ld64(sa + 64 * h, r);
-              if constexpr (PTH) {
+            float mx = -INFINITY;
+            if constexpr (PTH) {
+              // Logits times their tokens' factors (which carry the softmax scale), -inf where the row
+              // does not look, whatever the factor is; the first half's go back into their place
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h) {
+                tc::tmem_ld64(sa + 64 * h, r);
 #pragma unroll
                 for (int k = 0; k < 64; k += 4) {
                   const float4 f = *reinterpret_cast<const float4*>(ks + 64 * h + k);
@@ -883,30 +891,30 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
                   for (int k = 0; k < 64; ++k)
                     if (64 * h + k >= seen) r[k] = 0xff800000u;
                 }
-              }
-            };
-            const auto largest = [&](int h, float acc) {
-              if constexpr (PTH) {
-                if (exact[h]) {
-                  float m4[4] = {acc, acc, acc, acc};
+                if (h == 0) tc::tmem_st64(sa, r);
+                // log2 of the largest v scale stands for every token's where they lie near
+                const float4 g = *reinterpret_cast<const float4*>(ks + kSoRange + 4 * h);
+                const float near = fmaxf(g.x, g.z);
+                if (__builtin_expect(near - fminf(g.y, g.w) > kNear, 0)) {
+                  float m2[2] = {mx, mx};
 #pragma unroll
                   for (int k = 0; k < 64; k += 4) {
                     const float4 l = *reinterpret_cast<const float4*>(ks + kSoLog + 64 * h + k);
-                    const float x[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], __uint_as_float(r[k + e]) + x[e]);
+                    m2[0] = fmax3(m2[0], __uint_as_float(r[k]) + l.x, __uint_as_float(r[k + 1]) + l.y);
+                    m2[1] = fmax3(m2[1], __uint_as_float(r[k + 2]) + l.z, __uint_as_float(r[k + 3]) + l.w);
                   }
-                  return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                  mx = fmaxf(m2[0], m2[1]);
+                } else {
+                  mx = fmaxf(mx, row_max<false, false, false>(r, -INFINITY, 0, 0, nullptr) + near);
                 }
-                return fmaxf(acc, row_max<false, false, false>(r, -INFINITY, 0, 0, nullptr) + near[h]);
-              } else {
-                return row_max<false, false, false>(r, acc, 0, 0, nullptr);
               }
-            };
-            logits(0);
-            float mx = largest(0, -INFINITY);
-            logits(1);
-            mx = largest(1, mx);
+              tc::tmem_wait_st();
+            } else {
+              tc::tmem_ld64(sa, r);
+              mx = row_max<false, false, false>(r, mx, 0, 0, nullptr);
+              tc::tmem_ld64(sa + 64, r);
+              mx = row_max<false, false, false>(r, mx, 0, 0, nullptr);
+            }
             mx = PTH ? mx - kHead : mx * scale2 - kHead;
             const bool move = there && (mx > m_run + kSlack || (m_run == -INFINITY && mx > -INFINITY));
             if (__any_sync(0xffffffffu, move)) {
@@ -941,11 +949,22 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
             // 168 registers)
             const auto weights = [&](int h) {
               const float* vh = PTH ? ks + kSoV + 64 * h : nullptr;
-              if (PTH && mixed)
-                l_run += row_exp<true, FP8, PTH, PTH>(r, sa + 64 * h, scale2, base, bits(seen - 64 * h), bits(seen - 64 * h - 32), nullptr, vh);
-              else
-                l_run += row_exp<false, FP8, PTH, PTH>(r, sa + 64 * h, scale2, base, 0, 0, nullptr, vh);
+              l_run += row_exp<false, FP8, PTH, PTH>(r, sa + 64 * h, scale2, base, 0, 0, nullptr, vh);
               tc::tmem_wait_st();
+              if (PTH && __builtin_expect(mixed, 0)) {  // (0 times a hidden token's scale, which may be anything)
+#pragma unroll 1
+                for (int c = 0; c < 32; c += 16) {
+                  uint32_t x[16];
+                  tc::tmem_ld16(sa + 64 * h + c, x);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) {
+                    const int left = seen - 64 * h - 2 * (c + k);
+                    x[k] &= left > 1 ? ~0u : left == 1 ? 0xffffu : 0u;
+                  }
+                  tc::tmem_st16(sa + 64 * h + c, x);
+                }
+                tc::tmem_wait_st();
+              }
             };
             const auto announce = [&](int h) {
               tc::fence_before();
@@ -954,7 +973,7 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
             };
             weights(1);
             announce(1);
-            logits(0);
+            tc::tmem_ld64(sa, r);
             weights(0);
             if (__builtin_expect(hand, 0)) {
               pv_by_hand<FP8>(oa, 0, 128, sa, sa + 64, smem + ((2 * n + 1) % kBufs) * kTile,
