@@ -260,8 +260,15 @@ msa_status msa_page_copy(const msa_kv_pools* layers, int32_t num_layers, int32_t
   p.num_copies = num_copies;
   p.num_pages = num_pages;
   p.status = dev_status;
+  cudaError_t error = cudaSuccess;
+  const auto flush = [&]() {
+    if (error == cudaSuccess && p.num_pools > 0) error = launch_page_copy(p, stream);
+    p.num_pools = 0;
+  };
   const auto add = [&](void* base, int row) {
-    if (base) p.pool[p.num_pools++] = {static_cast<uint8_t*>(base), row};
+    if (!base) return;
+    if (p.num_pools == kCopyPools) flush();
+    p.pool[p.num_pools++] = {static_cast<uint8_t*>(base), row};
   };
   for (int i = 0; i < num_layers; ++i) {
     const msa_kv_pools& l = layers[i];
@@ -278,13 +285,9 @@ msa_status msa_page_copy(const msa_kv_pools* layers, int32_t num_layers, int32_t
       if (x.dtype == MSA_KV_FP8_E4M3) add(x.k_scale, 4 * x.heads);
     }
     add(l.mass, 4);
-    if (p.num_pools + 7 > kCopyPools || i == num_layers - 1) {
-      const cudaError_t e = launch_page_copy(p, stream);
-      if (e != cudaSuccess) return MSA_ERR_CUDA;
-      p.num_pools = 0;
-    }
   }
-  return MSA_OK;
+  flush();
+  return cuda_status(error);
 }
 
 }  // extern "C"

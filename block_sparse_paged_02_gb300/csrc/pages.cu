@@ -10,11 +10,17 @@
 // it does the pages needed per request and their prefix sum, and counts the free pages
 // of its slice; (4) tables, and the lowest free pages, found in order by a scan.  Counts
 // are integers, so their order does not matter.
+//
+// The tables and counts are a megabyte at most in use: it is bound by latency, the
+// cluster barriers and the chains of dependent loads between them (64 requests of 4 beams
+// each, contexts to 8192: 10.5 us).
 #include "prompt_common.cuh"
 
 namespace msa {
 namespace {
 
+// (clusters of 8, 4, 2 and 1 CTAs: 10.9, 13.1, 16.9 and 22.7 us: the counts and the tables are
+// shared out, the barriers stay)
 constexpr int kFkThreads = 1024, kFkWarps = kFkThreads / 32, kFkCtas = 8;
 constexpr unsigned kAll = 0xffffffffu;
 
@@ -289,7 +295,12 @@ __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
 
 // ------------------------------------------------------------------ copies
 
-constexpr int kCpThreads = 256;
+// 16 bytes a thread and load.  120 pages in 40 layers of e4m3 with scales, 245 MB both ways, in
+// one launch: 40.9 us (6.0 TB/s, 88 % of the copy rate: bound by memory).  In two launches it took
+// 43.4, with 256 and 512 threads 44.8 and 67.7, with 2 loads of a thread in flight in place of 4
+// 46.3, with 8 60.2 (the last four at two launches, 2 and 8 loads at 256 threads).  96 pages of
+// one layer: 3.2 us (3.7 with 2 loads), a launch and two dependent loads.
+constexpr int kCpThreads = 128;
 
 // One array's part of one page per CTA
 __global__ void __launch_bounds__(kCpThreads) page_copy_kernel(const __grid_constant__ CopyLaunch p) {

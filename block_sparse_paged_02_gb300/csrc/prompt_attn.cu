@@ -9,11 +9,11 @@
 // heads (one 3-D tensor copy of Q); two tiles share every block of 128 tokens'
 // K and V, which is a page, and while one is in its softmax the tensor cores work
 // on the other.  S and P V are tcgen05.mma M128 N128 of the same shape from one
-// issuing thread, so they run in the order of issue: S of the next block goes
+// issuing thread a tile, so they run in the order of issue: S of the next block goes
 // out right behind P V of this one, over the same tensor memory, without a
 // wait between them.
-// Roles: warp 0 issues the copies; one thread of warp 1 all products; warp 2
-// brings the scales per token of bf16 pools; warp 3 looks bf16 V over (below);
+// Roles: warp 0 issues the copies; a thread of warps 1 and 2 each the products of a
+// tile; warp 3 looks bf16 V over (below) and brings the scales per token of bf16 pools;
 // warps 4-7 and 8-11 are the tiles' softmax, a thread per row.  With e4m3
 // pools warps 12-15 turn the tiles into f16 (exact) and the products run in f16.
 //
@@ -27,6 +27,17 @@
 // and its V is looked over: a value that is not finite would reach rows that
 // do not see it through 0 * V, so that block's P V is then added row by row,
 // from the visible tokens alone.  V behind the request's end is zeroed.
+//
+// P is rounded to bf16 (f16 with e4m3 pools), the operand of its product; the sum l
+// takes it in fp32 before that.  What bounds it: 4 * 128 * H operations a visible pair of
+// tokens on the tensor cores, and beside them an exponential a pair and head (32 a clock
+// and SM), about half as long; a block of a tile pair measures 2900 clocks against the
+// products' 2048, the rest being the hand-over between softmax and products, which two
+// tiles a CTA do not hide wholly.  Measured (16 heads, bf16): 16384 rows 671 us, 1640
+// TFLOP/s of the 1842 that a library product reaches; 8 x 2048 rows 130 us; a 512-row chunk
+// behind 30000 tokens 93 us.  With a scale per token the factors' way from shared memory
+// (128 bits a thread and four tokens, for each row) nearly doubles the softmax: 8192 rows 311
+// us against 200.
 #include <string.h>
 
 #include "attn_tc.cuh"
@@ -42,9 +53,11 @@ constexpr int kConv = 4;    // converting warps (e4m3 pools)
 // flags of a segment
 constexpr int kWhole = 1, kTwo = 2, kPoison = 4, kEnd = 8;
 
-// What a tile pair's start and end cost, in tokens
+// What a tile pair's start and end cost, in tokens (8 x 2048 rows: 157, 130, 137 us with
+// 128, 384, 768; 16 ragged prompts 192, 152, 166)
 constexpr int kPairCost = 384;
-// Least tokens of a CTA's slice (two boundaries of blocks at least)
+// Least tokens of a CTA's slice: two boundaries of blocks at least (256 and 1024 measured
+// the same)
 constexpr long long kMinSlice = 512;
 
 // A segment: blocks [b0, b0 + nb) of a tile pair that the CTA's slice holds
@@ -60,7 +73,8 @@ struct Segment {
 template <bool FP8, bool PTH>
 struct PaCfg {
   static constexpr int kThreads = FP8 ? 512 : 384;
-  static constexpr int kBufs = 3;  // ring of 16-bit K and V tiles, alternating
+  // ring of 16-bit K and V tiles, alternating (4 and 5 measured the same: 16384 rows, 8 x 2048)
+  static constexpr int kBufs = 3;
   static constexpr int kRaws = FP8 ? 3 : 0;            // ring of e4m3 tiles
   static constexpr int kSmQ = kBufs * kTile;
   static constexpr int kSmRaw = kSmQ + 2 * kTile;
@@ -740,9 +754,8 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
             const int b = x % kBufs, rb = x % kRing;
             ok = warp_wait(&raw_full[rb], (x / kRing) & 1);
             if (!ok) break;
-            // (the block's scales are asked for before its K is converted and put in place after: K has
-            // an e4m3 place, so V of block n - 2 is converted, over K of block n - 3 that its S has
-            // read: the softmax is through with block n - 4's)
+            // (the block's scales are asked for before its K is converted and put in place after: K
+            // goes over V of block n - 2, so the softmax is through with block n - 4's)
             const bool data = !(fl & kPoison) && t0 + ct < seq;
             float2 scale = make_float2(0.f, 0.f);
             if (PTH && kv == 0) scale = scales_of(head, data, x >> 1, ct);
@@ -1266,15 +1279,20 @@ cudaError_t launch(const PromptLaunch& p, cudaStream_t stream) {
 
 }  // namespace
 
-// Short prompts, of few pairs and blocks: a pair to a CTA, with nothing to join behind.
-// TODO figures
-constexpr int kWholeBlocks = 16;
+// What the join takes (its launch, the partials' way through L2), in blocks of a pair
+constexpr int kJoinBlocks = 8;
 
 cudaError_t launch_prompt_attn(const PromptLaunch& given, cudaStream_t stream) {
   PromptLaunch p = given;
   const int wide = 2 * (128 / (p.num_heads / p.num_kv_heads));
   const long long pairs = ((long long)p.batch.num_rows / wide + min(p.batch.num_rows, p.batch.num_reqs)) * p.num_kv_heads;
-  p.whole = pairs <= device_sm_count() && p.batch.bt_stride <= kWholeBlocks;
+  // A pair to a CTA, with nothing to join, where the deepest pair takes less than its slice of an
+  // even split and the join behind that (one prompt, 16 heads: 200 rows 12.3 us against 16.1,
+  // 1000 rows 20.5 against 24.4, 2048 rows 31.9 against 40.0, 2400 rows 36.4 against 44.2;
+  // behind cached tokens the split wins: 64 rows after 1900 tokens 19.1 against 31.6, 512 rows
+  // after 1500 26.1 against 32.4).  The table's width stands for the depth.
+  const long long deepest = p.batch.bt_stride, sms = device_sm_count();
+  p.whole = pairs <= sms && deepest <= kJoinBlocks + pairs * (deepest + kPairCost / kBlock) / sms;
   const bool pth = p.scale_mode == MSA_SCALE_PER_TOKEN_HEAD;
   if (p.kv_fp8) return pth ? launch<true, true>(p, stream) : launch<true, false>(p, stream);
   return pth ? launch<false, true>(p, stream) : launch<false, false>(p, stream);
