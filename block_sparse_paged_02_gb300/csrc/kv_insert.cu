@@ -9,8 +9,8 @@
 // index-K go to page block_table[q, pos/128], slot pos%128.  FP8 caches take
 // OCP e4m3 codes: with a scalar scale the value is divided by it; with
 // per-token-head scales the scale is max|x|/448 of that token and KV head (1
-// for an all-zero vector), written beside the page.  (The norm and RoPE parts
-// of the fused op need model weights and are not part of this library.)
+// for an all-zero vector), written beside the page.  (The vectors come
+// normed and rotated; qk_rope.cu has the form that does both on the way.)
 //
 // One warp per row: lanes own 4 consecutive head dims; the amax is a warp
 // max-reduce; division is IEEE fp32 and the codes come from the hardware

@@ -304,8 +304,8 @@ msa_status msa_decode(const msa_batch* batch, const void* idx_q, const msa_index
  * q/k-norm + RoPE + KV insert with skip_index, so index-reuse layers skip the
  * index-cache write; item 5: separate K and V pools].  Every query row of the
  * batch is a new token at its own position pos = context_lens[q] + j; its
- * vectors go to page block_table[q, pos/128], slot pos%128 (the q/k norm and
- * RoPE need model weights and stay with the caller).
+ * vectors go to page block_table[q, pos/128], slot pos%128, as they come
+ * (msa_prompt.h has the form that norms and rotates them on the way).
  *   k_new, v_new [num_rows, num_kv_heads, head_dim] bf16
  *   k_cache, v_cache  pools [P, 128, num_kv_heads, head_dim] of kv_dtype
  *   idx_new      [num_rows, index->heads, index->dim] bf16
