@@ -1280,19 +1280,21 @@ cudaError_t launch(const PromptLaunch& p, cudaStream_t stream) {
 }  // namespace
 
 // What the join takes (its launch, the partials' way through L2), in blocks of a pair
-constexpr int kJoinBlocks = 8;
+static constexpr int kJoinBlocks = 8;
 
 cudaError_t launch_prompt_attn(const PromptLaunch& given, cudaStream_t stream) {
   PromptLaunch p = given;
   const int wide = 2 * (128 / (p.num_heads / p.num_kv_heads));
   const long long pairs = ((long long)p.batch.num_rows / wide + min(p.batch.num_rows, p.batch.num_reqs)) * p.num_kv_heads;
-  // A pair to a CTA, with nothing to join, where the deepest pair takes less than its slice of an
-  // even split and the join behind that (one prompt, 16 heads: 200 rows 12.3 us against 16.1,
+  // A pair to a CTA, with nothing to join, where the deepest pair takes less than a CTA's share of
+  // an even split and the join behind that (one prompt, 16 heads: 200 rows 12.3 us against 16.1,
   // 1000 rows 20.5 against 24.4, 2048 rows 31.9 against 40.0, 2400 rows 36.4 against 44.2;
   // behind cached tokens the split wins: 64 rows after 1900 tokens 19.1 against 31.6, 512 rows
-  // after 1500 26.1 against 32.4).  The table's width stands for the depth.
+  // after 1500 26.1 against 32.4).  The table's width stands for the depth, half of it for the
+  // mean, as in a prompt from its start: 22 blocks at most, so that one deep request among
+  // short ones does not hold a CTA for long.
   const long long deepest = p.batch.bt_stride, sms = device_sm_count();
-  p.whole = pairs <= sms && deepest <= kJoinBlocks + pairs * (deepest + kPairCost / kBlock) / sms;
+  p.whole = pairs <= sms && deepest <= kJoinBlocks + pairs * (deepest / 2 + kPairCost / kBlock) / sms;
   const bool pth = p.scale_mode == MSA_SCALE_PER_TOKEN_HEAD;
   if (p.kv_fp8) return pth ? launch<true, true>(p, stream) : launch<true, false>(p, stream);
   return pth ? launch<false, true>(p, stream) : launch<false, false>(p, stream);
