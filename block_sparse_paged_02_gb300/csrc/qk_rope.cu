@@ -14,13 +14,13 @@
 // keys, values, index vectors) goes through a second form that picks source, weights
 // and destination by lane group.  Weights, cosines and sines lie in shared memory:
 // held in registers they cost the occupancy that hides the loads (12.6 K rows, below:
-// 36 us at two CTAs an SM, 31.4 at four).
+// 36 us at two CTAs an SM, 31.4 at four).  A warp of many rows asks for the next four
+// heads before it turns these (31.2 us without, 28.5 with).
 //
-// Measured (graph, 16 heads, bf16 pools, two index heads of 64, rotary 64): one row 4.6
-// us, 64 rows over e4m3 with scales 5.5, both a launch and a chain of loads; 12.6 K
-// rows of neighbours' rotation 31.4 us, 133 MB at 4.2 TB/s (62 % of the copy rate),
-// bound by issue and load latency together (of it ~7 us start and chain, ~18 the
-// queries, ~10 the rest of a row where it does not overlap).
+// Measured (graph, 16 heads, bf16 pools, two index heads of 64, rotary 64): one row 4.4
+// us, 64 rows over e4m3 with scales 5.3, both a launch and a chain of loads; 12.6 K
+// rows of neighbours' rotation 28.5 us, 133 MB at 4.7 TB/s (69 % of the copy rate),
+// bound by load latency: 2.6 rows a warp, each a chain of angles, heads, rest.
 #include "prompt_common.cuh"
 
 namespace msa {
@@ -238,18 +238,33 @@ __global__ void __launch_bounds__(kWarps * 32, 4) qk_rope_kernel(const __grid_co
     }
     const float* table = p.cos_sin + (long long)rot * p.rotary;
     float* mine = s_cs[warp];
+    // (the first heads are asked for before the angles are waited for, where a warp takes
+    // several; with one the angles go first)
+    const uint16_t* src = p.q.src + (long long)r * p.q.stride + group * kHeadDim;
+    uint4 na = make_uint4(0u, 0u, 0u, 0u), nc = na;
+    if (WPR < kWarps && warp % WPR < quads) {
+      na = *reinterpret_cast<const uint4*>(src + warp % WPR * 4 * kHeadDim + ca);
+      nc = *reinterpret_cast<const uint4*>(src + warp % WPR * 4 * kHeadDim + cb);
+    }
     __syncwarp();  // the row before has been turned
     if (4 * lane < p.rotary)
       *reinterpret_cast<float4*>(mine + 4 * lane) = __ldg(reinterpret_cast<const float4*>(table) + lane);
     __syncwarp();
 
     // ---- four query heads at a time
-    const uint16_t* src = p.q.src + (long long)r * p.q.stride + group * kHeadDim;
     uint16_t* dst = p.q_out + ((long long)r * H + group) * kHeadDim;
     for (int s0 = warp % WPR; s0 < quads; s0 += WPR) {
       const int at = s0 * 4 * kHeadDim;
       Lane16 v;
-      v.unpack(*reinterpret_cast<const uint4*>(src + at + ca), *reinterpret_cast<const uint4*>(src + at + cb));
+      if (WPR == kWarps) {
+        na = *reinterpret_cast<const uint4*>(src + at + ca);
+        nc = *reinterpret_cast<const uint4*>(src + at + cb);
+      }
+      v.unpack(na, nc);
+      if (WPR < kWarps && s0 + WPR < quads) {
+        na = *reinterpret_cast<const uint4*>(src + at + 4 * WPR * kHeadDim + ca);
+        nc = *reinterpret_cast<const uint4*>(src + at + 4 * WPR * kHeadDim + cb);
+      }
       if (p.q.norm) {
         const float f = rsqrtf(group_sum(v.squares(), true) * (1.f / kHeadDim) + p.eps);
         v.scale8(0, f, s_w[0] + ca);
