@@ -130,15 +130,15 @@ __device__ __forceinline__ float row_exp(const uint32_t (&r)[N], uint32_t pa, fl
   return ((l[0] + l[1]) + (l[2] + l[3])) + ((l[4] + l[5]) + (l[6] + l[7]));
 }
 
-// Columns [c0, c1) of O += P V of a block for the row of this thread, the tokens with a
-// set bit of vis alone; P of the first 64 tokens (times f0) at pa, of the others at pa2, and O at
-// oa in tensor memory, V at v, `words` x 32 tokens; O starts with it when fresh
-template <bool FP8>
-__device__ __noinline__ void pv_by_hand(uint32_t oa, int c0, int c1, uint32_t pa, uint32_t pa2,
-                                        const uint8_t* v, uint4 vis4, int words, float f0, bool fresh) {
+// O += P V of a block for the row of this thread, the tokens with a set bit of vis
+// alone; P of the first 64 tokens (times f0) at pa, of the others kNext behind it, and O at oa in
+// tensor memory, V at v, `words` x 32 tokens; O starts with it when fresh
+template <bool FP8, int kNext = 32>
+__device__ __noinline__ void pv_by_hand(uint32_t oa, uint32_t pa, const uint8_t* v, uint4 vis4,
+                                        int words, float f0, bool fresh) {
   tc::tmem_wait_st();
 #pragma unroll 1
-  for (int c = c0; c < c1; c += 16) {
+  for (int c = 0; c < 128; c += 16) {
     uint32_t o[16];
     if (!fresh) tc::tmem_ld16(oa + c, o);
     float acc[16];
@@ -147,7 +147,7 @@ __device__ __noinline__ void pv_by_hand(uint32_t oa, int c0, int c1, uint32_t pa
 #pragma unroll 1
     for (int w = 0; w < words; ++w) {
       uint32_t pr[16];
-      tc::tmem_ld16(w < 2 ? pa + 16 * w : pa2 + 16 * (w - 2), pr);
+      tc::tmem_ld16(pa + 16 * w + (w < 2 ? 0 : kNext - 32), pr);
       const uint32_t vis = w == 0 ? vis4.x : w == 1 ? vis4.y : w == 2 ? vis4.z : vis4.w;
       const float f = w < 2 ? f0 : 1.f;
 #pragma unroll

@@ -38,8 +38,6 @@
 // behind 30000 tokens 93 us.  With a scale per token the factors' way from shared memory
 // (128 bits a thread and four tokens, for each row) nearly doubles the softmax: 8192 rows 311
 // us against 200.
-#include <string.h>
-
 #include "attn_tc.cuh"
 #include "prompt_common.cuh"
 
@@ -68,7 +66,6 @@ struct Segment {
   int slot, head;        // partial slot; KV head
   uint32_t bad;
 };
-
 
 template <bool FP8, bool PTH>
 struct PaCfg {
@@ -989,7 +986,7 @@ __global__ void __launch_bounds__(PaCfg<FP8, PTH>::kThreads, 1)
             tc::tmem_ld64(sa, r);
             weights(0);
             if (__builtin_expect(hand, 0)) {
-              pv_by_hand<FP8>(oa, 0, 128, sa, sa + 64, smem + ((2 * n + 1) % kBufs) * kTile,
+              pv_by_hand<FP8, 64>(oa, sa, smem + ((2 * n + 1) % kBufs) * kTile,
                               make_uint4(bits(seen), bits(seen - 32), bits(seen - 64), bits(seen - 96)), 4, 1.f, i == 0);
               tc::tmem_wait_st();
             }

@@ -760,8 +760,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, PTH>::kThreads, 1)
           if (work) {
             // (P V of the blocks before is complete: this block's S waited for it)
             tc::fence_after();
-            pv_by_hand<FP8>(oa, 0, 128, tmem + lanes + col_s(t) + (kAhead ? 64 * (n & 1) : 0),
-                            tmem + lanes + col_s(t) + (kAhead ? 64 * (n & 1) : 0) + 32,
+            pv_by_hand<FP8>(oa, tmem + lanes + col_s(t) + (kAhead ? 64 * (n & 1) : 0),
                             smem + kSmKv + vb * kTile, make_uint4(vis[0], vis[1], vis[2], vis[3]),
                             fl & kHalves ? 4 : 2, moved, (fl & kFirst) != 0);
             tc::tmem_wait_st();
