@@ -34,13 +34,6 @@ __device__ __forceinline__ bool bad_pages(const msa_cache_view& c, int r, int nb
   return __syncthreads_or(bad) != 0;
 }
 
-// The cluster's barrier behind code in which a warp's lanes went different ways: its
-// instructions want the whole warp at once.
-__device__ __forceinline__ void joined_cluster_sync() {
-  __syncwarp();
-  cluster_sync();
-}
-
 __device__ __forceinline__ void red_dsmem_add(uint32_t addr, int v) {
   asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }

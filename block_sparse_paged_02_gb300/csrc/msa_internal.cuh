@@ -169,6 +169,21 @@ __device__ __forceinline__ void cluster_sync() {
                    : "memory");
 }
 // the address of the same shared-memory location in CTA `rank` of the cluster
+// The cluster's barrier behind code in which a warp's lanes went different ways: its
+// instructions want the whole warp at once.
+__device__ __forceinline__ void joined_cluster_sync() {
+  __syncwarp();
+  cluster_sync();
+}
+// "This CTA runs", and the wait until every CTA of the cluster does: another CTA's shared
+// memory may be written only behind it.  Nothing is published by it.
+__device__ __forceinline__ void cluster_started() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_started() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
 __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
   uint32_t out;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(out) : "r"(addr), "r"(rank));

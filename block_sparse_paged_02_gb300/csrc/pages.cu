@@ -76,6 +76,7 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* sum) {
 __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
     page_fork_kernel(const __grid_constant__ ForkLaunch p) {
   extern __shared__ __align__(16) uint8_t fk_smem[];
+  cluster_started();  // (waited for behind part (1), whose loads take longer)
   FkShared& s = *reinterpret_cast<FkShared*>(fk_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x;
   const int R = p.from.num_reqs, N = p.to.num_reqs, P = p.from.num_pages, slots = fk_slots(N);
@@ -105,7 +106,7 @@ __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
   const auto exchange = [&](int* to, int value) {
     if (tid < kFkCtas) st_dsmem_s32(mapa_shared(smem_u32(to + rank), tid), value);
     __syncthreads();
-    cluster_sync();
+    joined_cluster_sync();
   };
   const auto refuse = [&](uint32_t bits) {
     for (int i = rank * kFkThreads + tid; i < N; i += kFkCtas * kFkThreads) {
@@ -179,6 +180,7 @@ __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
   if (lane == 0) s.warp[0][warp] = (int)wrong;
   __syncthreads();
   wrong = __reduce_or_sync(kAll, (uint32_t)s.warp[0][lane]);
+  cluster_wait_started();
   exchange(s.flags, (int)wrong);
   wrong = __reduce_or_sync(kAll, lane < kFkCtas ? (uint32_t)s.flags[lane] : 0u);
   if (wrong) {
@@ -198,7 +200,7 @@ __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
     }
   }
   __syncthreads();
-  cluster_sync();
+  joined_cluster_sync();
 
   // ---- (3) who keeps a partial page: the lowest of those that go on writing one without holders
   const auto slot_of = [&](int page) { return (int)(((uint32_t)page * 2654435761u) >> 8) & (slots - 1); };
