@@ -343,7 +343,9 @@ __global__ void __launch_bounds__(kCpThreads) page_copy_kernel(const __grid_cons
 cudaError_t launch_page_fork(const ForkLaunch& p, cudaStream_t stream) {
   const size_t bytes = fk_bytes(p.from.num_reqs, p.to.num_reqs);
   if (bytes > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(page_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    // (what any call may need: the limit is the process's, and another thread's call sets it too)
+    const cudaError_t e = cudaFuncSetAttribute(page_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)fk_bytes(kMaxReqs, kMaxReqs));
     if (e != cudaSuccess) return e;
   }
   page_fork_kernel<<<kFkCtas, kFkThreads, bytes, stream>>>(p);

@@ -1,4 +1,7 @@
 """msa_page_fork called many times at once: CTAs of a cluster that start late, host threads."""
+import ctypes
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -66,3 +69,52 @@ def test_refused_and_good_ones_beside_other_work(msa):
     assert sum(isinstance(c.want, int) for c in calls) == 32
     for c in calls:
         c.check()
+
+
+def two_sizes(msa, each=1):
+    rng = np.random.default_rng(4)
+    calls = []
+    for n in (2100, 4096) * each:
+        lens, table, refs = state(rng, n, 2, 6000, share=False)
+        calls.append(Call(msa, lens, table, refs, rng.integers(-1, n, n), rng.integers(0, 90, n), 4))
+    torch.cuda.synchronize()
+    return calls
+
+
+def test_host_threads_with_other_numbers_of_requests(msa):
+    """Calls of two sizes from several threads, each on a stream of its own: none is refused by what the others
+    need of shared memory."""
+    calls = two_sizes(msa, 4)
+    start, codes = threading.Barrier(len(calls)), []
+
+    def many(c):
+        stream = torch.cuda.Stream()
+        cache, refs, parent, grow, to = c.args
+        args = (ctypes.byref(cache), refs.data_ptr(), parent.data_ptr(), grow.data_ptr(), ctypes.byref(to),
+                c.status.data_ptr(), stream.cuda_stream)
+        fork = msa.lib().msa_page_fork
+        start.wait()
+        codes.append({fork(*args) for _ in range(4000)})
+        stream.synchronize()
+
+    threads = [threading.Thread(target=many, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert codes == [{0}] * len(calls)
+    for c in calls:
+        c.check()
+
+
+def test_two_sizes_in_one_graph(msa):
+    small, large = two_sizes(msa)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        large.run()
+        small.run()
+    graph.replay()
+    torch.cuda.synchronize()
+    small.check()
+    large.check()
