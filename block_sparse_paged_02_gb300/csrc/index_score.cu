@@ -633,8 +633,10 @@ cudaError_t launch_cfg(const ScoreLaunch& p, cudaStream_t stream) {
                         kBlock);
     if (rows > 0x7fffffffll || !ok) return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  // (the limit is the process's, and another thread's call sets it too: what any call may need)
+  cudaError_t e = cudaFuncSetAttribute(
+      kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      (int)min(kMaxDynSmem, ScoreSmem<DI, HI, KIND, BUDGET>::bytes(kMaxReqs)));
   if (e != cudaSuccess) return e;
   kern<<<device_sm_count(), C::kThreads, smem, stream>>>(p, kmap);
   return cudaGetLastError();

@@ -473,8 +473,9 @@ cudaError_t launch_tc(const ScoreLaunch& p, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   const size_t smem = TcCfg<DI>::bytes(p.batch.num_reqs);
   auto kern = index_score_tc_kernel<DI>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // (the limit is the process's, and another thread's call sets it too: what any call may need)
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)TcCfg<DI>::bytes(kMaxReqs));
   if (e != cudaSuccess) return e;
   kern<<<device_sm_count(), kTcThreads, smem, stream>>>(p, kmap);
   return cudaGetLastError();

@@ -549,8 +549,9 @@ cudaError_t launch_warp(const TopkLaunch& p, cudaStream_t stream, bool programma
   auto kern = topk_table_kernel_warp<KPL>;
   const size_t smem = (size_t)(p.batch.num_reqs + 1 + kWarpRows * p.topk) * sizeof(int);
   if (smem > 48 * 1024) {
-    cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (the limit is the process's, and another thread's call sets it too: what any call may need)
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)((kMaxReqs + 1 + kWarpRows * kWarpTopkMax) * sizeof(int)));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -577,8 +578,8 @@ cudaError_t launch_kpt(const TopkLaunch& p, cudaStream_t stream, bool programmat
     kern = topk_table_kernel_multi<KPT>;
   const size_t smem = (size_t)(p.topk + p.batch.bt_stride) * sizeof(int);
   if (smem > 48 * 1024) {
-    cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)((kMaxTopk + kMaxBlocksPerRow) * sizeof(int)));  // (as above)
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};

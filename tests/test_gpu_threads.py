@@ -1,5 +1,6 @@
 """The library called from several host threads."""
 import ctypes
+import dataclasses
 import threading
 
 import numpy as np
@@ -47,3 +48,76 @@ def test_first_cuda_call_of_a_thread(msa, op, kv, scale):
     torch.cuda.synchronize()
     assert codes == [0] * 4
     assert torch.equal(out, want) and int(c.status.item()) == 0
+
+
+def together(works, times=4000):
+    """works: functions of a stream that return a call's status; each runs in a thread of its own."""
+    start, codes = threading.Barrier(len(works)), []
+
+    def many(work):
+        stream = torch.cuda.Stream()
+        start.wait()
+        codes.append({work(stream.cuda_stream) for _ in range(times)})
+        stream.synchronize()
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=many, args=(w,)) for w in works]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert codes == [{0}] * len(works)
+
+
+@pytest.mark.parametrize("fp8,q", [(False, 1), (True, 1), (False, 64)])
+def test_scores_of_few_and_many_requests(msa, fp8, q):
+    def case(n):
+        w = W.custom(n, [q] * n, [79 + q] * n, hq=4, topk=4)
+        c = msa.DeviceCase(W.fp8_index(w, n) if fp8 else w)
+        c.scores.zero_()
+        return c
+
+    cases = [case(n) for n in (3, 1500) * 3]
+
+    def work(c):
+        args = (ctypes.byref(c.batch), c.idx_q.data_ptr(), ctypes.byref(c.index), c.scores.data_ptr(), c.w.bt_stride,
+                c.status.data_ptr())
+        return lambda stream: msa.lib().msa_index_score(*args, stream)
+
+    alone = []
+    for c in cases:
+        assert work(c)(None) == 0
+        torch.cuda.synchronize()
+        alone.append(c.scores.clone())
+        c.scores.zero_()
+    together([work(c) for c in cases])
+    for c, want in zip(cases, alone):
+        assert torch.equal(c.scores, want) and int(c.status.item()) == 0
+
+
+def test_topk_of_wide_and_wider_tables(msa):
+    def case(n, width):
+        w = W.custom(n, [1] * n, [700] * n, hq=4, topk=4)
+        table = np.zeros((n, width), w.block_table.dtype)
+        table[:, :w.block_table.shape[1]] = w.block_table
+        c = msa.DeviceCase(dataclasses.replace(w, block_table=table))
+        c.scores.copy_(torch.arange(c.scores.numel(), device="cuda").view_as(c.scores) % 7919)
+        return c
+
+    cases = [case(2, width) for width in (12500, 16384) * 3]
+
+    def work(c):
+        args = (ctypes.byref(c.batch), c.scores.data_ptr(), c.w.bt_stride, c.topk, c.topk_idx.data_ptr(), c.tbl.data_ptr(),
+                c.tbl_stride, c.sparse_len.data_ptr(), c.status.data_ptr())
+        return lambda stream: msa.lib().msa_topk_build_table(*args, stream)
+
+    alone = []
+    for c in cases:
+        assert work(c)(None) == 0
+        torch.cuda.synchronize()
+        alone.append(c.topk_idx.clone())
+        c.topk_idx.fill_(-7)
+    together([work(c) for c in cases])
+    for c, want in zip(cases, alone):
+        assert torch.equal(c.topk_idx, want) and int(c.status.item()) == 0
