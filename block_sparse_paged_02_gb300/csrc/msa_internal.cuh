@@ -287,19 +287,21 @@ __device__ __forceinline__ uint32_t score_key(float s) {
 // --------------------------------------------------- batch geometry checks
 
 // Request q's lengths.  Returns 0 if usable, else MSA_DEV_BAD_LEN or
-// MSA_DEV_MALFORMED; *nb = ceil(seq_len/128) when usable.
+// MSA_DEV_MALFORMED; *nb = ceil(seq_len/128) when usable.  *q_len is -1 where the entries of
+// cu_seqlens_q fall: by a difference alone, entries 2^31 apart would pass as a length.  So
+// where every q_len is 0 or more, the first entry 0 and the last num_rows, all lie between.
 __device__ __forceinline__ uint32_t request_lengths(const msa_batch& b, int q, int* q_begin,
                                                     int* q_len, int* ctx, int* nb) {
   const int c0 = b.cu_seqlens_q[q], c1 = b.cu_seqlens_q[q + 1];
-  const int slen = b.cu_seqlens_k[q + 1] - b.cu_seqlens_k[q];
+  const int slen = (int)((uint32_t)b.cu_seqlens_k[q + 1] - (uint32_t)b.cu_seqlens_k[q]);
   *q_begin = c0;
-  *q_len = c1 - c0;
+  *q_len = c1 < c0 ? -1 : (int)((uint32_t)c1 - (uint32_t)c0);
   *ctx = b.context_lens[q];
   *nb = 0;
   if (slen < *q_len || *ctx < 0 || (long long)slen > (long long)kBlock * b.bt_stride ||
       *q_len < b.min_q_len)
     return MSA_DEV_MALFORMED;
-  if (*ctx + *q_len != slen) return MSA_DEV_BAD_LEN;
+  if ((long long)*ctx + *q_len != slen) return MSA_DEV_BAD_LEN;
   *nb = (slen + kBlock - 1) / kBlock;
   return 0u;
 }
