@@ -181,6 +181,11 @@ __global__ void __launch_bounds__(kThreads, FP8 ? MSA_ATTN_CTAS_FP8 : (PUSH ? 1 
       bulk_g2s(smem + C::kQ, p.q + (long long)r * p.num_heads * kHeadDim, q_bytes, qbar);
     }
   }
+  // (every CTA of the row's cluster passes here; waited for before the first push)
+  if constexpr (CL && (FP8 || PUSH)) {
+    __syncwarp();
+    cluster_started();
+  }
 
   // this warp's page-16 entries are split*pps + warp + 4*i, one per lane; the
   // table load does not depend on the length, so both are in flight together
@@ -566,6 +571,7 @@ __global__ void __launch_bounds__(kThreads, FP8 ? MSA_ATTN_CTAS_FP8 : (PUSH ? 1 
     // owner (asynchronous remote stores), one cluster barrier makes all of
     // them visible, and each owner merges its chunks from its own memory:
     // no remote load on the path and no second barrier.
+    cluster_wait_started();
     const uint32_t recv = smem_u32(smem + C::kRecvOff);
     const uint32_t recv_ml = recv + kRecvF4Bytes, recv_fl = recv_ml + kRecvMlBytes;
     {
@@ -584,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, FP8 ? MSA_ATTN_CTAS_FP8 : (PUSH ? 1 
       if (tid < p.splits)  // this split's poison flag, to every CTA of the row
         st_dsmem_s32(mapa_shared(recv_fl, (uint32_t)tid) + 4u * split, (len_bad || cta_bad) ? 1 : 0);
     }
-    cluster_sync();  // every push of the row has landed
+    joined_cluster_sync();  // every push of the row has landed
     const int* fl = reinterpret_cast<const int*>(smem + C::kRecvOff + kRecvF4Bytes + kRecvMlBytes);
     const bool poisoned = __any_sync(full, lane < p.splits && fl[lane] != 0);
     if (poisoned && split == 0 && tid == 0) atomicOr(p.status, MSA_DEV_BAD_TABLE);
@@ -626,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, FP8 ? MSA_ATTN_CTAS_FP8 : (PUSH ? 1 
       cp[kCpL + head] = lh;
     }
     if (tid == 0) reinterpret_cast<int*>(cp)[kCpFlag] = (len_bad || cta_bad) ? 1 : 0;
-    cluster_sync();  // every partial of the row is written and visible
+    joined_cluster_sync();  // every partial of the row is written and visible
     const uint32_t cp_addr = smem_u32(cp);
     int fl = 0;
     if (lane < p.splits) fl = ld_dsmem_s32(mapa_shared(cp_addr + 4u * kCpFlag, (uint32_t)lane));
@@ -664,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, FP8 ? MSA_ATTN_CTAS_FP8 : (PUSH ? 1 
       }
       finalize_out<4, SCALE>(p, sink_s, r, h, d, a, M, L, (i4 & 31) == 0);
     }
-    cluster_sync();  // no CTA leaves while another may still read its partial
+    joined_cluster_sync();  // no CTA leaves while another may still read its partial
     return;
   }
 

@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 2) sparse_mla_kernel(const MlaLaunch
     float* mine = reinterpret_cast<float*>(smem);
     put(mine, o, m_run, l_run);
     if (tid == 0) flags[2] = cta_bad ? 1 : 0;
-    cluster_sync();
+    joined_cluster_sync();
     const uint32_t base = smem_u32(mine);
     int fl = 0;
     if (lane < p.splits) fl = ld_dsmem_s32(mapa_shared(smem_u32(&flags[2]), (uint32_t)lane));
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 2) sparse_mla_kernel(const MlaLaunch
         p.lse[(long long)r * p.num_heads + h_abs] =
             (M == -INFINITY || Lsum <= 0.f) ? -INFINITY : (M + log2f(Lsum)) * kLn2;
     }
-    cluster_sync();
+    joined_cluster_sync();
     return;
   }
 

@@ -121,3 +121,25 @@ def test_topk_of_wide_and_wider_tables(msa):
     together([work(c) for c in cases])
     for c, want in zip(cases, alone):
         assert torch.equal(c.topk_idx, want) and int(c.status.item()) == 0
+
+
+@pytest.mark.parametrize("kv,scale", [(W.KV_BF16, W.SCALE_NONE), (W.KV_FP8, W.SCALE_PER_TOKEN_HEAD)])
+def test_decode_beside_other_work(msa, kv, scale):
+    """The CTAs of a row write into each other's shared memory: the same results however late some of them start."""
+    cases = [msa.DeviceCase(W.custom(n, [1] * n, [3000 + 100 * n] * n, hq=16, topk=16, kv_dtype=kv, scale_mode=scale))
+             for n in (1, 2, 5, 9, 13)]
+    for c in cases:
+        c.decode()
+    torch.cuda.synchronize()
+    want = [c.out.clone() for c in cases]
+    a = torch.randn((1024, 1024), device="cuda")
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(10):
+        for c in cases:
+            c.out.zero_()
+        torch.cuda.synchronize()
+        for c, s in zip(cases, streams):
+            a = (a @ a).clamp(-1, 1)
+            c.decode(stream=s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(c.out, t) and int(c.status.item()) == 0 for c, t in zip(cases, want))
