@@ -79,6 +79,20 @@ bool stride_ok(int64_t stride, int heads, int dim) {
   return stride >= (int64_t)heads * dim && stride % 8 == 0;
 }
 
+// Memory of a call: `rows` runs of `len` bytes, `stride` (at least len) from one to the next
+struct Span {
+  const void* at;
+  long long rows, stride, len;
+};
+Span packed(const void* at, long long bytes) { return {at, at && bytes > 0 ? 1 : 0, bytes, bytes}; }
+// whether a packed span touches any run of the other
+bool touch(const Span& one, const Span& runs) {
+  if (one.rows == 0 || runs.rows == 0 || runs.len == 0) return false;
+  const long long a = (long long)reinterpret_cast<uintptr_t>(one.at) - (long long)reinterpret_cast<uintptr_t>(runs.at);
+  const long long first = a < runs.len ? 0 : (a - runs.len) / runs.stride + 1;  // the first run that ends behind a
+  return first < runs.rows && first * runs.stride < a + one.len;
+}
+
 }  // namespace
 }  // namespace msa
 
@@ -124,6 +138,27 @@ msa_status msa_qk_rope_insert(const msa_batch* batch, const msa_qkv* qkv, const 
   if ((qkv->q_out == qkv->q && qkv->q_stride != (int64_t)qkv->num_heads * kHeadDim) ||
       (x && qkv->idx_q_out == qkv->idx_q && qkv->idx_q_stride != (int64_t)x->heads * x->dim))
     return MSA_ERR_SHAPE;
+  // otherwise the outputs lie apart from each other and from every vector
+  {
+    const long long n = batch->num_rows;
+    const auto rows = [&](const void* src, int64_t stride, int heads, int dim) {
+      return Span{src, n, 2 * (long long)stride, 2ll * heads * dim};
+    };
+    const Span q_out = packed(qkv->q_out, n * qkv->num_heads * kHeadDim * 2);
+    const Span idx_q_out = packed(x ? qkv->idx_q_out : nullptr, x ? n * x->heads * x->dim * 2 : 0);
+    Span in[5] = {rows(qkv->q, qkv->q_stride, qkv->num_heads, kHeadDim), rows(qkv->k, qkv->k_stride, hk, kHeadDim),
+                  rows(qkv->v, qkv->v_stride, hk, kHeadDim), {}, {}};
+    if (x) {
+      in[3] = rows(qkv->idx_q, qkv->idx_q_stride, x->heads, x->dim);
+      in[4] = rows(qkv->idx_k, qkv->idx_k_stride, x->heads, x->dim);
+    }
+    bool shared = touch(q_out, idx_q_out);
+    for (int i = 0; i < 5; ++i) {
+      shared |= (i != 0 || qkv->q_out != qkv->q) && touch(q_out, in[i]);
+      shared |= (i != 3 || qkv->idx_q_out != qkv->idx_q) && touch(idx_q_out, in[i]);
+    }
+    if (shared) return MSA_ERR_SHAPE;
+  }
   RopeLaunch p = {};
   p.batch = *batch;
   const auto vec = [](const void* src, int64_t stride, int heads, int dim, const void* norm) {
@@ -187,6 +222,11 @@ msa_status msa_prompt_attn(const msa_batch* batch, const msa_attn_args* a, void*
     return MSA_ERR_SHAPE;
   const PromptWs w = prompt_layout();
   if (!workspace || workspace_bytes < w.total || !aligned16(workspace)) return MSA_ERR_WORKSPACE;
+  // out may take q's place; nothing else of what is written shares memory with q or out
+  const long long vectors = (long long)a->num_rows * a->num_heads;
+  const Span q = packed(a->q, vectors * kHeadDim * 2), out = packed(a->out, vectors * kHeadDim * 2);
+  const Span lse = packed(a->lse, vectors * 4);
+  if ((a->out != a->q && touch(out, q)) || touch(lse, q) || touch(lse, out)) return MSA_ERR_SHAPE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   PromptLaunch p = {};
   p.batch = *batch;
@@ -229,9 +269,19 @@ msa_status msa_page_fork(const msa_cache_view* from, const int32_t* refs, const 
                          to->copy_src, to->copy_dst, to->copy_tokens};
   for (const void* ptr : every)
     if (!aligned16(ptr)) return MSA_ERR_SHAPE;
-  if ((refs && refs == to->refs) || (from->lens && from->lens == to->lens) ||
-      (from->block_table && from->block_table == to->block_table))
-    return MSA_ERR_SHAPE;
+  const long long n = to->num_reqs, row = 4ll * to->bt_stride;
+  const Span in[] = {packed(from->lens, 4ll * from->num_reqs),
+                     packed(from->block_table, 4ll * from->num_reqs * from->bt_stride),
+                     packed(refs, 4ll * from->num_pages), packed(parent, 4 * n), packed(grow, 4 * n)};
+  const Span out[] = {packed(to->lens, 4 * n),     packed(to->block_table, n * row), packed(to->refs, 4ll * from->num_pages),
+                      packed(to->copy_src, 4 * n), packed(to->copy_dst, 4 * n),      packed(to->copy_tokens, 4 * n)};
+  constexpr int kOut = sizeof(out) / sizeof(out[0]);
+  for (int i = 0; i < kOut; ++i) {
+    for (const Span& x : in)
+      if (touch(out[i], x)) return MSA_ERR_SHAPE;
+    for (int j = 0; j < i; ++j)
+      if (touch(out[i], out[j])) return MSA_ERR_SHAPE;
+  }
   return cuda_status(launch_page_fork({*from, refs, parent, grow, *to, dev_status}, stream));
 }
 

@@ -61,7 +61,9 @@ typedef struct msa_rope {
  *   eps, norm_shift  y = x * (mean(x^2) + eps)^-1/2 * (weight + norm_shift)
  *   q_out     [num_rows, num_heads, head_dim] bf16, may be q itself when
  *             q_stride is num_heads * head_dim
- *   idx_q_out [num_rows, index->heads, index->dim] bf16, likewise */
+ *   idx_q_out [num_rows, index->heads, index->dim] bf16, likewise
+ * Otherwise the outputs share no memory with each other or with any of the
+ * vectors (MSA_ERR_SHAPE). */
 typedef struct msa_qkv {
   const void* q;
   const void* k;
@@ -123,9 +125,11 @@ size_t msa_prompt_attn_workspace_size(int32_t num_heads, int32_t num_kv_heads);
  * not reach its result, whatever their bytes hold.  Any number of rows per
  * request, none among them.
  *   attn      as for msa_tree_attn, with any num_heads that num_kv_heads
- *             divides.  The weights exp(s_t - m) (times a v_scale per token)
- *             are rounded to 16 bits for the product with V; with e4m3 pools q
- *             is converted to fp16, so |q| must stay below 65504
+ *             divides.  out may be q itself; otherwise out and lse share no
+ *             memory with q or each other (MSA_ERR_SHAPE).  The weights
+ *             exp(s_t - m) (times a v_scale per token) are rounded to 16 bits
+ *             for the product with V; with e4m3 pools q is converted to fp16,
+ *             so |q| must stay below 65504
  *   batch->max_q_len  not used
  *   batch->min_q_len  as elsewhere: requests with fewer rows are poisoned
  * A poisoned request (MSA_DEV_BAD_PAGE, _BAD_LEN, _MALFORMED) gets the
@@ -169,7 +173,7 @@ typedef struct msa_page_set {
  *     in refs and stay.
  * Entries of to->block_table behind a request's last block are left as they
  * are.  Nothing of `from` or refs is written, and `to` shares no memory with
- * them: the caller keeps two sets and swaps them.
+ * them (MSA_ERR_SHAPE): the caller keeps two sets and swaps them.
  *   refs      [from->num_pages] int32;  parent, grow  [to->num_reqs] int32
  *             (grow may be NULL: 0, nothing is copied or added)
  * A length outside 0 .. 128 * bt_stride, a parent outside -1 .. from->num_reqs
