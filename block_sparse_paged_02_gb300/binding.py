@@ -83,7 +83,7 @@ class msa_tree(ctypes.Structure):
 class msa_cache_view(ctypes.Structure):
     _fields_ = [("lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
                 ("bt_stride", ctypes.c_int32), ("num_reqs", ctypes.c_int32),
-                ("num_pages", ctypes.c_int32)]
+                ("num_pages", ctypes.c_int32), ("blocks", ctypes.c_void_p)]
 
 
 class msa_kv_pools(ctypes.Structure):
@@ -117,7 +117,8 @@ class msa_page_set(ctypes.Structure):
     _fields_ = [("lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
                 ("refs", ctypes.c_void_p), ("copy_src", ctypes.c_void_p),
                 ("copy_dst", ctypes.c_void_p), ("copy_tokens", ctypes.c_void_p),
-                ("bt_stride", ctypes.c_int32), ("num_reqs", ctypes.c_int32)]
+                ("bt_stride", ctypes.c_int32), ("num_reqs", ctypes.c_int32),
+                ("blocks", ctypes.c_void_p)]
 
 
 class msa_trace(ctypes.Structure):
@@ -471,14 +472,16 @@ def msa_attn_mass(batch: msa_batch, tree: msa_tree, attn: msa_attn_args, mass, w
         _on(stream, dev_status, workspace, mass, _first(batch), _first(tree), _first(attn))))
 
 
-def make_cache_view(lens, block_table, num_pages: int) -> msa_cache_view:
-    """The cached tokens of a set of requests: int32 lens [R], block_table [R, bt_stride]."""
+def make_cache_view(lens, block_table, num_pages: int, blocks=None) -> msa_cache_view:
+    """The cached tokens of a set of requests: int32 lens [R], block_table [R, bt_stride], and for
+    msa_page_fork blocks [R], the pages that each holds (None: those of its tokens)."""
     _typed("lens", lens, (torch.int32,), (None,))
     _typed("block_table", block_table, (torch.int32,), (int(lens.shape[0]), None))
-    _one_device(lens, block_table)
+    _typed("blocks", blocks, (torch.int32,), (int(lens.shape[0]),))
+    _one_device(lens, block_table, blocks)
     c = msa_cache_view(_p(lens), _p(block_table), int(block_table.shape[1]), int(lens.shape[0]),
-                       int(num_pages))
-    c._keep = (lens, block_table)
+                       int(num_pages), _p(blocks))
+    c._keep = (lens, block_table, blocks)
     return c
 
 
@@ -647,19 +650,21 @@ def msa_prompt_attn(batch: msa_batch, attn: msa_attn_args, workspace, dev_status
         _on(stream, dev_status, workspace, _first(batch), _first(attn))))
 
 
-def make_page_set(lens, block_table, refs, copy_src, copy_dst, copy_tokens) -> msa_page_set:
-    """What msa_page_fork writes: int32 lens [R], block_table [R, bt_stride], refs [num_pages] and
-    the pages to copy, copy_src, copy_dst, copy_tokens [R]."""
+def make_page_set(lens, block_table, refs, copy_src, copy_dst, copy_tokens, blocks=None) -> msa_page_set:
+    """What msa_page_fork writes: int32 lens [R], block_table [R, bt_stride], refs [num_pages], the
+    pages to copy, copy_src, copy_dst, copy_tokens [R], and (where given) the pages held, blocks [R]."""
     n = int(lens.shape[0])
     _typed("lens", lens, (torch.int32,), (None,))
     _typed("block_table", block_table, (torch.int32,), (n, None))
     _typed("refs", refs, (torch.int32,), (None,))
-    for name, t in (("copy_src", copy_src), ("copy_dst", copy_dst), ("copy_tokens", copy_tokens)):
+    for name, t in (("copy_src", copy_src), ("copy_dst", copy_dst), ("copy_tokens", copy_tokens),
+                    ("blocks", blocks)):
         _typed(name, t, (torch.int32,), (n,))
     every = (lens, block_table, refs, copy_src, copy_dst, copy_tokens)
-    _one_device(*every)
-    x = msa_page_set(*(_p(t) for t in every), int(block_table.shape[1]), n)
+    _one_device(*every, blocks)
+    x = msa_page_set(*(_p(t) for t in every), int(block_table.shape[1]), n, _p(blocks))
     x._keep = every
+    x._blocks = blocks
     return x
 
 

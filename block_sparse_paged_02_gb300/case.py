@@ -245,16 +245,17 @@ class DeviceCase:
                 self._tree_ws[key] = ws
             return ws
 
-    def page_fork(self, lens, refs, parent, grow=None, bt_stride: Optional[int] = None, stream=None):
-        """msa_page_fork of requests that hold `lens` tokens under the case's block table: the new
-        set (lens, block table [len(parent), bt_stride] with -1 behind the blocks, refs and the
-        pages to copy) as a make_page_set struct, tensors of the call's stream in its _keep."""
+    def page_fork(self, lens, refs, parent, grow=None, bt_stride: Optional[int] = None, stream=None, blocks=None):
+        """msa_page_fork of requests that hold `lens` tokens, and `blocks` pages (None: those of the
+        tokens), under the case's block table: the new set (lens, block table [len(parent),
+        bt_stride] with -1 behind the blocks, refs and the pages to copy) as a make_page_set
+        struct, tensors of the call's stream in its _keep, the pages held in its _blocks."""
         n, width = int(parent.shape[0]), int(bt_stride or self.w.bt_stride)
         with _allocating_on(stream):
             new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=self.device)
             to = B.make_page_set(new(n), torch.full((n, width), -1, dtype=torch.int32, device=self.device),
-                                 new(self.w.num_pages), new(n), new(n), new(n))
-        B.msa_page_fork(B.make_cache_view(lens, self.bt, self.w.num_pages), refs, parent, grow, to,
+                                 new(self.w.num_pages), new(n), new(n), new(n), new(n))
+        B.msa_page_fork(B.make_cache_view(lens, self.bt, self.w.num_pages, blocks), refs, parent, grow, to,
                         self.status, stream)
         return to
 

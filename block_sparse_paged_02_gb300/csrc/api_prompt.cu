@@ -266,15 +266,17 @@ msa_status msa_page_fork(const msa_cache_view* from, const int32_t* refs, const 
                            !to->copy_tokens))
     return MSA_ERR_NULL;
   const void* every[] = {from->lens, from->block_table, refs, parent, grow, to->lens, to->block_table, to->refs,
-                         to->copy_src, to->copy_dst, to->copy_tokens};
+                         to->copy_src, to->copy_dst, to->copy_tokens, from->blocks, to->blocks};
   for (const void* ptr : every)
     if (!aligned16(ptr)) return MSA_ERR_SHAPE;
   const long long n = to->num_reqs, row = 4ll * to->bt_stride;
   const Span in[] = {packed(from->lens, 4ll * from->num_reqs),
                      packed(from->block_table, 4ll * from->num_reqs * from->bt_stride),
-                     packed(refs, 4ll * from->num_pages), packed(parent, 4 * n), packed(grow, 4 * n)};
+                     packed(refs, 4ll * from->num_pages), packed(parent, 4 * n), packed(grow, 4 * n),
+                     packed(from->blocks, 4ll * from->num_reqs)};
   const Span out[] = {packed(to->lens, 4 * n),     packed(to->block_table, n * row), packed(to->refs, 4ll * from->num_pages),
-                      packed(to->copy_src, 4 * n), packed(to->copy_dst, 4 * n),      packed(to->copy_tokens, 4 * n)};
+                      packed(to->copy_src, 4 * n), packed(to->copy_dst, 4 * n),      packed(to->copy_tokens, 4 * n),
+                      packed(to->blocks, 4 * n)};
   constexpr int kOut = sizeof(out) / sizeof(out[0]);
   for (int i = 0; i < kOut; ++i) {
     for (const Span& x : in)

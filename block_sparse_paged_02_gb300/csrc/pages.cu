@@ -5,15 +5,16 @@
 // inside one launch: (1) refs copied, everything checked, children of each old request
 // counted; (2) each old request's pages gain children - 1 holders (a partial last page
 // only those children that do not grow), so that requests with one child touch no
-// count; (3) of the requests that go on writing a partial page that nobody else holds,
-// the lowest keeps it: every CTA finds these for itself in a table in shared memory, as
-// it does the pages needed per request and their prefix sum, and counts the free pages
-// of its slice; (4) tables, and the lowest free pages, found in order by a scan.  Counts
-// are integers, so their order does not matter.
+// count, and those behind the request's tokens lose one; (3) of the requests that go on
+// writing a partial page that nobody else holds, the lowest keeps it: every CTA finds
+// these for itself in a table in shared memory, as it does the pages needed per request
+// and their prefix sum, and counts the free pages of its slice; (4) tables, and the
+// lowest free pages, found in order by a scan.  Counts are integers, so their order does
+// not matter.
 //
-// The tables and counts are a megabyte at most in use: it is bound by latency, the
-// cluster barriers and the chains of dependent loads between them (64 requests of 4 beams
-// each, contexts to 8192: 10.5 us).
+// 64 requests of 4 beams each, contexts to 8192, take 10.9 us (graph).  Their tables and
+// counts are some 60 KB: it is bound by latency, the cluster barriers and the chains of
+// dependent loads between them.
 #include "prompt_common.cuh"
 
 namespace msa {
@@ -111,6 +112,7 @@ __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
   const auto refuse = [&](uint32_t bits) {
     for (int i = rank * kFkThreads + tid; i < N; i += kFkCtas * kFkThreads) {
       p.to.lens[i] = -1;
+      if (p.to.blocks) p.to.blocks[i] = -1;
       p.to.copy_src[i] = p.to.copy_dst[i] = -1;
       p.to.copy_tokens[i] = 0;
     }
@@ -123,6 +125,10 @@ __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
   const int wpo = max(1, kGridWarps / max(1, R)), wpn = max(1, kGridWarps / max(1, N));
   const int r0 = gwarp / wpo, b0 = (gwarp % wpo) * 32 + lane;
   const int n0 = r0 < R ? __ldg(p.from.lens + r0) : 0;
+  const bool fits0 = n0 >= 0 && n0 <= (long long)kBlock * p.from.bt_stride;
+  // pages that an old request holds: those of its tokens, and maybe more
+  const int h0 = r0 < R && p.from.blocks ? __ldg(p.from.blocks + r0) : fits0 ? (n0 + kBlock - 1) / kBlock : 0;
+  const auto held = [&](int r, int have) { return r == r0 ? h0 : p.from.blocks ? __ldg(p.from.blocks + r) : have; };
   FkNew x[kFkRows];
   uint32_t wrong = 0;
 #pragma unroll
@@ -145,8 +151,7 @@ __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
     lowest[i] = N;
   }
   int page0 = 0;  // of block b0 of request r0
-  const bool there0 = n0 >= 0 && n0 <= (long long)kBlock * p.from.bt_stride && b0 < (n0 + kBlock - 1) / kBlock;
-  if (there0) page0 = __ldg(p.from.block_table + (long long)r0 * p.from.bt_stride + b0);
+  if (fits0 && h0 <= p.from.bt_stride && b0 < h0) page0 = __ldg(p.from.block_table + (long long)r0 * p.from.bt_stride + b0);
   copy_refs();
   __syncthreads();
 #pragma unroll
@@ -169,7 +174,11 @@ __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
       wrong |= MSA_DEV_MALFORMED;
       continue;
     }
-    const int nb = (n + kBlock - 1) / kBlock;
+    const int have = (n + kBlock - 1) / kBlock, nb = held(r, have);
+    if (nb < have || nb > p.from.bt_stride) {
+      wrong |= MSA_DEV_MALFORMED;
+      continue;
+    }
     for (int b = b0; b < nb; b += 32 * wpo) {
       const int page = r == r0 && b == b0 ? page0 : __ldg(p.from.block_table + (long long)r * p.from.bt_stride + b);
       if (page < 0 || page >= P) wrong |= MSA_DEV_BAD_PAGE;
@@ -191,10 +200,11 @@ __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
   // ---- (2) holders gained and lost
   for (int r = r0; r < R; r += kGridWarps / wpo) {
     const int all = children[r] & 0xffff, grown = children[r] >> 16;
-    if (all == 1 && grown == 0) continue;
-    const int n = r == r0 ? n0 : __ldg(p.from.lens + r), full = n / kBlock, nb = (n + kBlock - 1) / kBlock;
+    if (all == 1 && grown == 0 && !p.from.blocks) continue;
+    const int n = r == r0 ? n0 : __ldg(p.from.lens + r), full = n / kBlock, have = (n + kBlock - 1) / kBlock;
+    const int nb = held(r, have);
     for (int b = b0; b < nb; b += 32 * wpo) {
-      const int d = (b < full ? all : all - grown) - 1;
+      const int d = (b < full ? all : b < have ? all - grown : 0) - 1;
       if (d == 0) continue;
       atomicAdd(refs + (r == r0 && b == b0 ? page0 : __ldg(p.from.block_table + (long long)r * p.from.bt_stride + b)), d);
     }
@@ -241,6 +251,7 @@ __global__ void __cluster_dims__(kFkCtas, 1, 1) __launch_bounds__(kFkThreads, 1)
       place[i] = max(x[k].parent, 0) << 16 | (copy ? 1 << 15 | x[k].full() : x[k].have());
       if (i % kFkCtas == rank) {
         p.to.lens[i] = x[k].n;
+        if (p.to.blocks) p.to.blocks[i] = x[k].blocks();
         p.to.copy_src[i] = copy ? page : -1;
         p.to.copy_tokens[i] = copy ? x[k].n % kBlock : 0;
         if (!copy) p.to.copy_dst[i] = -1;

@@ -115,13 +115,17 @@ msa_status msa_attn_mass(const msa_batch* batch, const msa_tree* tree, const msa
  *   lens         [num_reqs] tokens in the cache
  *   block_table  [num_reqs, bt_stride] page of each 128-token block; the
  *                first ceil(lens/128) entries of a row are read
- *   num_pages    P, pages in the pools (bounds check) */
+ *   num_pages    P, pages in the pools (bounds check)
+ *   blocks       [num_reqs] pages that a request holds, those that it has no
+ *                tokens in yet or any more among them; NULL: ceil(lens/128).
+ *                Read by msa_page_fork alone (msa_prompt.h) */
 typedef struct msa_cache_view {
   const int32_t* lens;
   const int32_t* block_table;
   int32_t bt_stride;
   int32_t num_reqs;
   int32_t num_pages;
+  const int32_t* blocks;
 } msa_cache_view;
 
 /* The tokens that each request keeps under a budget.  For a request of L =

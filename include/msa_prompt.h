@@ -145,7 +145,8 @@ msa_status msa_prompt_attn(const msa_batch* batch, const msa_attn_args* attn, vo
  *   refs        [num_pages] how many tables (and other holders) name a page
  *   copy_src, copy_dst, copy_tokens  [num_reqs] the pages to copy: the first
  *               copy_tokens[i] slots of page copy_src[i] to copy_dst[i]
- *               (-1, -1, 0 where request i needs none) */
+ *               (-1, -1, 0 where request i needs none)
+ *   blocks      [num_reqs] pages held, ceil((lens + grow) / 128); may be NULL */
 typedef struct msa_page_set {
   int32_t* lens;
   int32_t* block_table;
@@ -155,6 +156,7 @@ typedef struct msa_page_set {
   int32_t* copy_tokens;
   int32_t bt_stride;
   int32_t num_reqs;
+  int32_t* blocks;
 } msa_page_set;
 
 /* The requests of the next step and their pages.  Request i of `to` goes on
@@ -166,23 +168,31 @@ typedef struct msa_page_set {
  *     other holder of that page is left, the lowest such i keeps it, and any
  *     other gets a new page and its copy entry;
  *   - new pages follow, so that n + grow[i] tokens fit;
+ *   - pages that an old request holds behind its tokens (from->blocks) are
+ *     given back, not handed on: the new ones stand for them;
  *   - new pages are the free ones (refs 0) of lowest number, in the order of i
  *     and block; pages that lose their last holder in this call are free;
  *   - to->refs counts the holders after it: refs, less the tables of `from`,
  *     plus those of `to`.  Holders outside the tables (a prefix cache) count
  *     in refs and stay.
+ * grow is what a request may write: where fewer tokens came to be (rejected
+ * drafts, an early stop, an eviction), its table names more pages than lens
+ * tells of, and from->blocks has to say so at the next call (to->blocks of the
+ * call before does): without it, pages behind ceil(lens / 128) keep their
+ * count, which nobody takes off any more.
  * Entries of to->block_table behind a request's last block are left as they
  * are.  Nothing of `from` or refs is written, and `to` shares no memory with
  * them (MSA_ERR_SHAPE): the caller keeps two sets and swaps them.
  *   refs      [from->num_pages] int32;  parent, grow  [to->num_reqs] int32
  *             (grow may be NULL: 0, nothing is copied or added)
- * A length outside 0 .. 128 * bt_stride, a parent outside -1 .. from->num_reqs
- * - 1, a negative grow or one that does not fit to->bt_stride
- * (MSA_DEV_MALFORMED), a page id out of range among a request's blocks
- * (MSA_DEV_BAD_PAGE), one whose refs is below 1 (MSA_DEV_BAD_TABLE), or too
- * few free pages (MSA_DEV_NO_PAGES) stop the whole call: to->lens is -1
- * everywhere, the copy entries are empty, to->refs equals refs and
- * to->block_table is left as it is.  A request may not name a page twice.
+ * A length outside 0 .. 128 * bt_stride, blocks outside ceil(lens / 128) ..
+ * bt_stride, a parent outside -1 .. from->num_reqs - 1, a negative grow or
+ * one that does not fit to->bt_stride (MSA_DEV_MALFORMED), a page id out of
+ * range among a request's blocks (MSA_DEV_BAD_PAGE), one whose refs is below 1
+ * (MSA_DEV_BAD_TABLE), or too few free pages (MSA_DEV_NO_PAGES) stop the whole
+ * call: to->lens (and to->blocks) is -1 everywhere, the copy entries are
+ * empty, to->refs equals refs and to->block_table is left as it is.  A request
+ * may not name a page twice.
  * Supported: num_reqs of both <= 4096, bt_stride of both <= 16384. */
 msa_status msa_page_fork(const msa_cache_view* from, const int32_t* refs, const int32_t* parent,
                          const int32_t* grow, const msa_page_set* to, uint32_t* dev_status,
