@@ -83,7 +83,8 @@ class msa_tree(ctypes.Structure):
 class msa_cache_view(ctypes.Structure):
     _fields_ = [("lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
                 ("bt_stride", ctypes.c_int32), ("num_reqs", ctypes.c_int32),
-                ("num_pages", ctypes.c_int32), ("blocks", ctypes.c_void_p)]
+                ("num_pages", ctypes.c_int32), ("blocks", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p)]
 
 
 class msa_kv_pools(ctypes.Structure):
@@ -472,16 +473,18 @@ def msa_attn_mass(batch: msa_batch, tree: msa_tree, attn: msa_attn_args, mass, w
         _on(stream, dev_status, workspace, mass, _first(batch), _first(tree), _first(attn))))
 
 
-def make_cache_view(lens, block_table, num_pages: int, blocks=None) -> msa_cache_view:
-    """The cached tokens of a set of requests: int32 lens [R], block_table [R, bt_stride], and for
-    msa_page_fork blocks [R], the pages that each holds (None: those of its tokens)."""
+def make_cache_view(lens, block_table, num_pages: int, blocks=None, refs=None) -> msa_cache_view:
+    """The cached tokens of a set of requests: int32 lens [R], block_table [R, bt_stride]; for
+    msa_page_fork blocks [R], the pages that each holds (None: those of its tokens); for
+    msa_kv_compact refs [num_pages], by which requests that share pages are refused."""
     _typed("lens", lens, (torch.int32,), (None,))
     _typed("block_table", block_table, (torch.int32,), (int(lens.shape[0]), None))
     _typed("blocks", blocks, (torch.int32,), (int(lens.shape[0]),))
-    _one_device(lens, block_table, blocks)
+    _typed("refs", refs, (torch.int32,), (int(num_pages),))
+    _one_device(lens, block_table, blocks, refs)
     c = msa_cache_view(_p(lens), _p(block_table), int(block_table.shape[1]), int(lens.shape[0]),
-                       int(num_pages), _p(blocks))
-    c._keep = (lens, block_table, blocks)
+                       int(num_pages), _p(blocks), _p(refs))
+    c._keep = (lens, block_table, blocks, refs)
     return c
 
 

@@ -217,10 +217,11 @@ class DeviceCase:
                            keep_first, keep_recent, keep, keep_len, self.status, stream)
         return keep, keep_len
 
-    def kv_compact(self, lens, keep, keep_len, base=None, mass=None, stream=None):
-        """Move the kept tokens together in every pool of the case (and `mass`)."""
-        B.msa_kv_compact(B.make_cache_view(lens, self.bt, self.w.num_pages), base, keep, keep_len,
-                         self.kv_pools(mass), self.status, stream)
+    def kv_compact(self, lens, keep, keep_len, base=None, mass=None, stream=None, refs=None):
+        """Move the kept tokens together in every pool of the case (and `mass`); with refs, requests
+        are left as they are whose tokens would move into shared pages."""
+        B.msa_kv_compact(B.make_cache_view(lens, self.bt, self.w.num_pages, refs=refs), base, keep,
+                         keep_len, self.kv_pools(mass), self.status, stream)
 
     # -- prompts into the cache, and the sharing of its pages
     def qk_rope_insert(self, qkv, rope, skip_index: bool = False, mass=None, stream=None):

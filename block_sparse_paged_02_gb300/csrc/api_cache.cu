@@ -217,7 +217,7 @@ msa_status msa_kv_compact(const msa_cache_view* cache, const int32_t* base, cons
   if (!keep || !keep_len || !pools->k_cache || !pools->v_cache) return MSA_ERR_NULL;
   if (token_scales && (!pools->k_scale || !pools->v_scale)) return MSA_ERR_NULL;
   if (x && !x->k_cache) return MSA_ERR_NULL;
-  if (!aligned16(pools->k_cache) || !aligned16(pools->v_cache) || !aligned16(keep) ||
+  if (!aligned16(pools->k_cache) || !aligned16(pools->v_cache) || !aligned16(keep) || !aligned16(cache->refs) ||
       !aligned16(pools->mass) || (token_scales && (!aligned16(pools->k_scale) || !aligned16(pools->v_scale))) ||
       (x && (!aligned16(x->k_cache) || !aligned16(x->k_scale))))
     return MSA_ERR_SHAPE;

@@ -419,7 +419,7 @@ __device__ __forceinline__ void move_column(const CompactLaunch& p, int r, int b
 }
 
 __global__ void __launch_bounds__(kCpThreads) kv_compact_kernel(const CompactLaunch p, int parts) {
-  __shared__ int s_page[kCpPages];
+  __shared__ int s_page[kCpPages], s_first;
   const int r = blockIdx.y, tid = threadIdx.x;
   const int n = p.keep_len[r];
   if (n <= 0) return;
@@ -438,6 +438,20 @@ __global__ void __launch_bounds__(kCpThreads) kv_compact_kernel(const CompactLau
     if (__syncthreads_or(list_bad)) bad = MSA_DEV_BAD_TABLE;
   }
   if (!bad && bad_pages(p.cache, r, (L + kBlock - 1) / kBlock, kCpThreads)) bad = MSA_DEV_BAD_PAGE;
+  if (!bad && p.cache.refs) {  // pages that tokens move into: from the first that does not stay on
+    if (tid == 0) s_first = n;
+    __syncthreads();
+    int first = n;
+    for (int i = tid; i < n && first == n; i += kCpThreads)
+      if (__ldg(p.keep + (long long)r * p.keep_stride + i) != i) first = i;
+    if (first < n) atomicMin(&s_first, first);
+    __syncthreads();
+    bool shared = false;
+    if (s_first < n)
+      for (int b = (base + s_first) / kBlock + tid; b <= (base + n - 1) / kBlock; b += kCpThreads)
+        shared |= __ldg(p.cache.refs + __ldg(p.cache.block_table + (long long)r * p.cache.bt_stride + b)) > 1;
+    if (__syncthreads_or(shared)) bad = MSA_DEV_BAD_TABLE;
+  }
   if (bad) {
     if (tid == 0 && blockIdx.x == 0) atomicOr(p.status, bad);
     return;

@@ -105,8 +105,10 @@ msa_status msa_tree_attn(const msa_batch* batch, const msa_tree* tree, const msa
  *             and out are not used and may be NULL
  *   mass      fp32 [num_pages, 128]
  * Requests of one call must not share pages, nor may one name a page twice (a
- * shared slot would be updated by several blocks at once).  Poisoned requests
- * leave mass as it is. */
+ * shared slot would be updated by several blocks at once): requests that a
+ * fork left with common pages (msa_page_fork) go in calls of their own, one
+ * behind another, which add up in the shared slots.  Poisoned requests leave
+ * mass as it is. */
 msa_status msa_attn_mass(const msa_batch* batch, const msa_tree* tree, const msa_attn_args* attn,
                          float* mass, void* workspace, size_t workspace_bytes,
                          uint32_t* dev_status, cudaStream_t stream);
@@ -118,7 +120,9 @@ msa_status msa_attn_mass(const msa_batch* batch, const msa_tree* tree, const msa
  *   num_pages    P, pages in the pools (bounds check)
  *   blocks       [num_reqs] pages that a request holds, those that it has no
  *                tokens in yet or any more among them; NULL: ceil(lens/128).
- *                Read by msa_page_fork alone (msa_prompt.h) */
+ *                Read by msa_page_fork alone (msa_prompt.h)
+ *   refs         [num_pages] how many requests (and other holders) name a
+ *                page, or NULL: not known.  Read by msa_kv_compact alone */
 typedef struct msa_cache_view {
   const int32_t* lens;
   const int32_t* block_table;
@@ -126,6 +130,7 @@ typedef struct msa_cache_view {
   int32_t num_reqs;
   int32_t num_pages;
   const int32_t* blocks;
+  const int32_t* refs;
 } msa_cache_view;
 
 /* The tokens that each request keeps under a budget.  For a request of L =
@@ -181,8 +186,14 @@ typedef struct msa_kv_pools {
  * (keep_len > keep_stride, base + keep >= lens, base < 0) is left as it is
  * and sets MSA_DEV_BAD_TABLE; a length out of range sets MSA_DEV_MALFORMED,
  * a bad page id among the request's blocks MSA_DEV_BAD_PAGE, likewise.
- * Pages of a request must not be shared with another request of the call, nor
- * named twice.
+ * A page that a token moves into (those of positions base[r] + i from the
+ * first i with keep[r, i] != i on) must have no other holder, in the call or
+ * outside it, and a request may not name a page twice.  So requests that share
+ * pages (msa_page_fork) are not compacted after an eviction, unless all that
+ * they share stays where it is; committing a draft tree moves tokens within the
+ * pages that the fork gave the request alone.  With cache->refs such a request
+ * is left as it is and sets MSA_DEV_BAD_TABLE; without, its siblings' tokens
+ * are overwritten.
  * Supported: head_dim 128, 1 <= num_kv_heads <= 64, keep_stride >= 1, the
  * index shapes of msa_index_cache, num_reqs <= 4096, bt_stride <= 16384. */
 msa_status msa_kv_compact(const msa_cache_view* cache, const int32_t* base, const int32_t* keep,

@@ -180,6 +180,9 @@ typedef struct msa_page_set {
  * tells of, and from->blocks has to say so at the next call (to->blocks of the
  * call before does): without it, pages behind ceil(lens / 128) keep their
  * count, which nobody takes off any more.
+ * Shared pages are read by any operator, but none may write them: requests
+ * that share are not compacted after an eviction (msa_kv_compact), and
+ * msa_attn_mass takes them one to a call.
  * Entries of to->block_table behind a request's last block are left as they
  * are.  Nothing of `from` or refs is written, and `to` shares no memory with
  * them (MSA_ERR_SHAPE): the caller keeps two sets and swaps them.
