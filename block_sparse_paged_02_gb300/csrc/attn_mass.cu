@@ -13,7 +13,7 @@
 // packed add.  With few rows the stream of K bounds it (64 requests of one row x 16
 // heads, 134 MB, in 32 us: 4.2 TB/s), with many the issue of the sums, two warps to
 // a scheduler (8 windows of 32 rows x 16 heads over 8191..65000 e4m3 tokens in 43.6 us,
-// 690 TFLOP/s, where 118 M exponentials alone would take 25; 16 columns at a time 47).
+// 690 TFLOP/s, where 118 M exponentials alone would take 12; 16 columns at a time 47).
 // A quarter of the 2^x as a polynomial cost a tenth more.
 //
 // Blocks go in groups of two, one per epilogue warpgroup, so that one's sums

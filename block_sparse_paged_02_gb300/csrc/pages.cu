@@ -12,7 +12,7 @@
 // lowest free pages, found in order by a scan.  Counts are integers, so their order does
 // not matter.
 //
-// 64 requests of 4 beams each, contexts to 8192, take 10.9 us (graph).  Their tables and
+// 64 requests of 4 beams each, contexts to 8192, take 11.0 us (graph).  Their tables and
 // counts are some 60 KB: it is bound by latency, the cluster barriers and the chains of
 // dependent loads between them.
 #include "prompt_common.cuh"
@@ -20,8 +20,8 @@
 namespace msa {
 namespace {
 
-// (clusters of 8, 4, 2 and 1 CTAs: 10.9, 13.1, 16.9 and 22.7 us: the counts and the tables are
-// shared out, the barriers stay)
+// (clusters of 8, 4, 2 and 1 CTAs: 10.9, 13.1, 16.9 and 22.7 us when it was chosen, before the wait
+// for every CTA's start: the counts and the tables are shared out, the barriers stay)
 constexpr int kFkThreads = 1024, kFkWarps = kFkThreads / 32, kFkCtas = 8;
 constexpr unsigned kAll = 0xffffffffu;
 

@@ -1284,12 +1284,13 @@ cudaError_t launch_prompt_attn(const PromptLaunch& given, cudaStream_t stream) {
   const int wide = 2 * (128 / (p.num_heads / p.num_kv_heads));
   const long long pairs = ((long long)p.batch.num_rows / wide + min(p.batch.num_rows, p.batch.num_reqs)) * p.num_kv_heads;
   // A pair to a CTA, with nothing to join, where the deepest pair takes less than a CTA's share of
-  // an even split and the join behind that (one prompt, 16 heads: 200 rows 12.3 us against 16.1,
-  // 1000 rows 20.5 against 24.4, 2048 rows 31.9 against 40.0, 2400 rows 36.4 against 44.2;
+  // an even split and the join behind that (one prompt, 16 heads, in a table no wider than it needs:
+  // 200 rows 11.5 us, split 15.1; 1000 rows 20.2, 23.4; 2048 rows 31.3, 39.4; 2400 rows 36.0, 42.8;
   // behind cached tokens the split wins: 64 rows after 1900 tokens 19.1 against 31.6, 512 rows
-  // after 1500 26.1 against 32.4).  The table's width stands for the depth, half of it for the
-  // mean, as in a prompt from its start: 22 blocks at most, so that one deep request among
-  // short ones does not hold a CTA for long.
+  // after 1500 26.1 against 32.4).  The lengths are on the device, so the table's width stands
+  // for the depth, half of it for the mean, as in a prompt from its start: 22 blocks at most, so
+  // that one deep request among short ones does not hold a CTA for long.  In a table that is wider
+  // than its requests (22, 256 and 8192 blocks measured the same) short prompts are split, too.
   const long long deepest = p.batch.bt_stride, sms = device_sm_count();
   p.whole = pairs <= sms && deepest <= kJoinBlocks + pairs * (deepest / 2 + kPairCost / kBlock) / sms;
   const bool pth = p.scale_mode == MSA_SCALE_PER_TOKEN_HEAD;

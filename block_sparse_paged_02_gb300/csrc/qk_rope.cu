@@ -19,8 +19,14 @@
 //
 // Measured (graph, 16 heads, bf16 pools, two index heads of 64, rotary 64): one row 4.4
 // us, 64 rows over e4m3 with scales 5.3, both a launch and a chain of loads; 12.6 K
-// rows of neighbours' rotation 28.5 us, 133 MB at 4.7 TB/s (69 % of the copy rate),
-// bound by load latency: 2.6 rows a warp, each a chain of angles, heads, rest.
+// rows of neighbours' rotation 28.5 us, 133 MB at 4.7 TB/s (69 % of the copy rate), over
+// e4m3 29.7, with scales 30.1: bound by load latency, 3 rows to each of seven warps (the
+// eighth has none), each a chain of angles, heads, rest.
+//
+// A request's pages are all looked at before one of its rows is written, by every warp
+// that has such a row, so the time grows with the context: one row behind 8 K tokens 4.7
+// us, 131 K 5.2, 1 M 11.5; 64 rows behind 8 K each 5.0, 131 K 5.6; 4096 rows of one
+// request behind 0, 131 K, 500 K and 1 M tokens 10.1, 11.1, 13.8 and 17.5.
 #include "prompt_common.cuh"
 
 namespace msa {

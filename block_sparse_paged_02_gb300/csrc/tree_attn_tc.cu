@@ -19,7 +19,7 @@
 // (bf16 pools with a scale per token stay on tree_attn.cu.)
 //
 // Measured: 8 requests of 48..64 rows x 16 heads over 8192..32768 bf16 tokens 83 us,
-// 65 GFLOP (780 TFLOP/s; 34 us at cuBLAS's rate, 27 for its 126 M exponentials at 16 a
+// 65 GFLOP (780 TFLOP/s; 34 us at cuBLAS's rate, 13 for its 126 M exponentials at 32 a
 // clock and SM); 2 of 33 rows x 12 heads over 131K e4m3 tokens with scales 102 us; 16 of
 // 16..32 rows that select 16 blocks each 42 us.
 // Bound by the chain of a block through S, softmax and P V at two tiles a CTA: the

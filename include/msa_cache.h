@@ -80,7 +80,8 @@ size_t msa_tree_attn_workspace_size(int32_t num_reqs, int32_t num_rows, int32_t 
  *             relative to the row's largest such product, whatever the scale
  *             of a token of less weight; magnitudes from 2^-40 to 2^80, and 0,
  *             keep that precision.  With e4m3 pools q is converted to fp16,
- *             so |q| must stay below 65504 (msa_attn_mass likewise)
+ *             so |q| must stay below 65504, and below 2^-14 it is held to
+ *             2^-25, not to its own size (msa_attn_mass likewise)
  * A poisoned request (MSA_DEV_BAD_PAGE, _BAD_LEN, _MALFORMED) gets the
  * outputs of empty rows.  Supported: as msa_sparse_paged_attn (one KV head,
  * head_dim 128, 1..16 heads); topk <= 2048. */

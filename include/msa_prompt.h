@@ -129,11 +129,15 @@ size_t msa_prompt_attn_workspace_size(int32_t num_heads, int32_t num_kv_heads);
  *             memory with q or each other (MSA_ERR_SHAPE).  The weights
  *             exp(s_t - m) (times a v_scale per token) are rounded to 16 bits
  *             for the product with V; with e4m3 pools q is converted to fp16,
- *             so |q| must stay below 65504
+ *             so |q| must stay below 65504, and below 2^-14 it is held to
+ *             2^-25, not to its own size
  *   batch->max_q_len  not used
  *   batch->min_q_len  as elsewhere: requests with fewer rows are poisoned
  * A poisoned request (MSA_DEV_BAD_PAGE, _BAD_LEN, _MALFORMED) gets the
- * outputs of empty rows: 0, and sink_h or -inf.  Supported: head_dim 128,
+ * outputs of empty rows: 0, and sink_h or -inf.  The same call gives the same
+ * bits; how a row's sums are cut, and so their last bits, goes by the whole
+ * batch, bt_stride (which decides whether pairs of tiles are shared by CTAs)
+ * and the GPU's number of SMs.  Supported: head_dim 128,
  * num_heads / num_kv_heads <= 128, num_kv_heads <= 64, num_reqs <= 4096,
  * bt_stride <= 16384, num_pages < 2^24. */
 msa_status msa_prompt_attn(const msa_batch* batch, const msa_attn_args* attn, void* workspace,
